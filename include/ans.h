@@ -120,6 +120,8 @@ typedef enum {
 #define ANS_STATUS_SMEM_ALIGN 0x8u  /* a fused-GEMM CTA's dynamic shared memory did not start
                                        on the 1024-byte boundary its tensor-core operand
                                        layout assumes (its Y is not valid) */
+#define ANS_STATUS_BAD_INDEX 0x10u  /* an adapter index or a target was past the end of its
+                                       range (that token was taken as having none) */
 
 typedef enum {
   ANS_INT4 = 0,
@@ -384,6 +386,104 @@ ans_status ans_gemm_batched_workspace(const ans_gemm_job* jobs, uint32_t n_jobs,
 ans_status ans_gemm_batched(const ans_gemm_job* jobs, uint32_t n_jobs, uint32_t M,
                             ans_scale_kind scale_kind, uint32_t group_k, void* d_ws,
                             size_t ws_bytes, uint32_t* d_status, ans_stream_t stream);
+
+/* ---- Adapters, gradients and loss on compressed layers ----------------------
+ * What stands next to ans_gemm when the compressed weights are frozen: the
+ * low-rank adapters of many requests beside a projection, the gradients that
+ * train them, and the loss of a compressed vocabulary head.  W is never
+ * changed and has no gradient.  The scale kinds are ans_gemm's, dequantised
+ * weights w(n, k) as there.
+ *
+ * All of these calls take M up to 2^24 tokens (ANS_ERR_UNSUPPORTED above),
+ * write nothing outside the outputs they name and the workspace, and give the
+ * same bits for the same inputs.  Workspaces are 256-byte aligned and, as for
+ * ans_gemm, zero-filled once before their first use with a given layer and
+ * size; after a run that set *d_status zero them again.  Calls that may
+ * overlap on the GPU need a workspace each.
+ *
+ * Rounding.  Activations, adapters and gradients of activations are bf16; loss
+ * and the adapters' gradients are fp32; every sum is fp32.  Products whose
+ * second factor is a computed value (a probability, a gradient under row
+ * scales) round that value once: to f16 under a power of two of its row for the
+ * formats whose values are exact in f16 (all but bf16), to bf16 beside bf16
+ * weights.  bf16 weights without scales take d_dY as it is. */
+
+/* A set of low-rank adapters of one projection (W is N x K): adapter a adds
+ * s_a (x A_a^T) B_a^T to y.  All have one rank (a multiple of 8 up to 128; an
+ * adapter of a smaller one is padded with zeros) and the set holds at most
+ * 256; ANS_ERR_UNSUPPORTED otherwise.  d_A and d_B 16-byte aligned. */
+typedef struct {
+  uint32_t n_adapters;
+  uint32_t rank;
+  const uint16_t* d_A;  /* bf16 [n_adapters][rank][K] */
+  const uint16_t* d_B;  /* bf16 [n_adapters][N][rank] */
+  const float* d_scale; /* fp32 [n_adapters], or NULL: 1 */
+} ans_lora;
+
+/* Bytes of device workspace of ans_gemm_lora (the pointers of `lora` are not
+ * read). */
+ans_status ans_gemm_lora_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind,
+                                   const ans_lora* lora, size_t* bytes);
+
+/* ans_gemm with adapters: Y[m] = X[m] W^T + s_a (X[m] A_a^T) B_a^T with
+ * a = d_ids[m] (int32).  A token with a negative index has no adapter, and its
+ * Y is ans_gemm's to the bit.  An index of n_adapters or more sets
+ * ANS_STATUS_BAD_INDEX and is taken as none.  Tokens may name adapters in any
+ * order.  M == 0 is a no-op. */
+ans_status ans_gemm_lora(const uint16_t* d_X, uint32_t M, const ans_tiles* W,
+                         ans_scale_kind scale_kind, const void* d_scales, uint32_t group_k,
+                         const ans_lora* lora, const int32_t* d_ids, float* d_Y, void* d_ws,
+                         size_t ws_bytes, uint32_t* d_status, ans_stream_t stream);
+
+ans_status ans_gemm_grad_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind,
+                                   size_t* bytes);
+
+/* The gradient of ans_gemm's X: dX[m][k] = sum_n dY[m][n] w(n, k), dY bf16
+ * M x N and dX bf16 M x K, row-major, 16-byte aligned.  The layer is decoded
+ * once into the workspace (2 N K bytes) and meets every token from there.
+ * M == 0 is a no-op. */
+ans_status ans_gemm_grad(const uint16_t* d_dY, uint32_t M, const ans_tiles* W,
+                         ans_scale_kind scale_kind, const void* d_scales, uint32_t group_k,
+                         uint16_t* d_dX, void* d_ws, size_t ws_bytes, uint32_t* d_status,
+                         ans_stream_t stream);
+
+ans_status ans_gemm_lora_grad_workspace(const ans_layout* layout, uint32_t M,
+                                        ans_scale_kind scale_kind, const ans_lora* lora,
+                                        size_t* bytes);
+
+/* The gradients of ans_gemm_lora.  With dH[m] = s_a dY[m] B_a for the tokens of
+ * an adapter a:
+ *   dX[m] = dY[m] W + dH[m] A_a           bf16 M x K; d_dX NULL: not computed
+ *   dA_a = sum over a's tokens of dH[m]^T X[m]              fp32, shaped as A
+ *   dB_a = s_a * sum over a's tokens of dY[m]^T (X[m] A_a^T)  fp32, shaped as B
+ * Every element of dA and dB is written: zeros for an adapter without tokens
+ * (for all of them when M == 0).  Indices as for ans_gemm_lora. */
+ans_status ans_gemm_lora_grad(const uint16_t* d_X, const uint16_t* d_dY, uint32_t M,
+                              const ans_tiles* W, ans_scale_kind scale_kind, const void* d_scales,
+                              uint32_t group_k, const ans_lora* lora, const int32_t* d_ids,
+                              uint16_t* d_dX, float* d_dA, float* d_dB, void* d_ws,
+                              size_t ws_bytes, uint32_t* d_status, ans_stream_t stream);
+
+/* Bytes of device workspace of ans_xent; with_grad: 1 for calls with d_dX. */
+ans_status ans_xent_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind,
+                              int with_grad, size_t* bytes);
+
+/* Softmax cross entropy over a compressed vocabulary head W (N x K), a piece
+ * of the vocabulary at a time: no M x N matrix is ever held.  With
+ * z[m][n] = sum_k X[m][k] w(n, k) for n < vocab (1 <= vocab <= N,
+ * ANS_ERR_SHAPE otherwise; the rows of W from vocab on are padding):
+ *   lse[m] = log sum_n exp z[m][n],   loss[m] = lse[m] - z[m][t],  t = d_targets[m]
+ *   dX[m] = g[m] (sum_n softmax(z[m])_n w(n) - w(t))
+ * X bf16 M x K, targets int32, loss and lse fp32 [M], dX bf16 M x K (NULL: loss
+ * only), g = d_weight fp32 [M] (NULL: 1; read with d_dX only): the gradient of
+ * sum_m g[m] loss[m].  A token with a negative target has loss 0 and a zero dX;
+ * its lse is written.  A target of vocab or more sets ANS_STATUS_BAD_INDEX and
+ * is taken as negative.  M == 0 is a no-op. */
+ans_status ans_xent(const uint16_t* d_X, uint32_t M, const ans_tiles* W, ans_scale_kind scale_kind,
+                    const void* d_scales, uint32_t group_k, uint32_t vocab,
+                    const int32_t* d_targets, float* d_loss, float* d_lse, const float* d_weight,
+                    uint16_t* d_dX, void* d_ws, size_t ws_bytes, uint32_t* d_status,
+                    ans_stream_t stream);
 
 /* ---- Versioned on-disk container of a compressed layer ---------------------
  * "Approaching Shannon Bound", s3.1: the offline stage yields per layer a

@@ -21,6 +21,7 @@ INT4, BF16_SPLIT, FP8_E4M3, INT4_PAIRS, INT8, FP4_E2M1, FP4_PAIRS = 0, 1, 2, 3, 
 BF16_WHOLE = 7   # bf16 as whole 16-bit symbols: the ans_*16 entry points only
 SCALE_NONE, SCALE_ROW_BF16, SCALE_ROW_F32, SCALE_GROUP_BF16 = 0, 1, 2, 3
 STATUS_CORRUPT, STATUS_TIMEOUT, STATUS_BAD_OFFSETS, STATUS_SMEM_ALIGN = 0x1, 0x2, 0x4, 0x8
+STATUS_BAD_INDEX = 0x10
 ALPHABET = {INT4: 16, BF16_SPLIT: 256, FP8_E4M3: 256, INT4_PAIRS: 256, INT8: 256, FP4_E2M1: 16,
             FP4_PAIRS: 256}
 
@@ -30,7 +31,9 @@ EXPORTS = ["ans_status_string", "ans_last_error", "ans_num_tiles", "ans_layout_c
            "ans_encode_tiles", "ans_decode_tiles", "ans_histogram16_host", "ans_build_codebook16",
            "ans_encode_tiles16", "ans_decode_table16", "ans_decode_tiles16", "ans_gemm_workspace", "ans_gemm",
            "ans_gemm_noalloc", "ans_gemm_uncompressed", "ans_gemm_batched_workspace",
-           "ans_gemm_batched", "ans_container_write", "ans_container_read"]
+           "ans_gemm_batched", "ans_gemm_lora_workspace", "ans_gemm_lora", "ans_gemm_grad_workspace",
+           "ans_gemm_grad", "ans_gemm_lora_grad_workspace", "ans_gemm_lora_grad", "ans_xent_workspace",
+           "ans_xent", "ans_container_write", "ans_container_read"]
 MAX_BATCH = 8
 
 
@@ -71,6 +74,11 @@ class AnsGemmJob(C.Structure):
                 ("d_Y", C.c_void_p)]
 
 
+class AnsLora(C.Structure):
+    _fields_ = [("n_adapters", C.c_uint32), ("rank", C.c_uint32), ("d_A", C.c_void_p),
+                ("d_B", C.c_void_p), ("d_scale", C.c_void_p)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -108,6 +116,14 @@ def load():
             L.ans_gemm_uncompressed.argtypes = [P, u32, P, P, i32, P, u32, P, P, sz, P, P]
             L.ans_gemm_batched_workspace.argtypes = [P, u32, u32, i32, P]
             L.ans_gemm_batched.argtypes = [P, u32, u32, i32, u32, P, sz, P, P]
+            L.ans_gemm_lora_workspace.argtypes = [P, u32, i32, P, P]
+            L.ans_gemm_lora.argtypes = [P, u32, P, i32, P, u32, P, P, P, P, sz, P, P]
+            L.ans_gemm_grad_workspace.argtypes = [P, u32, i32, P]
+            L.ans_gemm_grad.argtypes = [P, u32, P, i32, P, u32, P, P, sz, P, P]
+            L.ans_gemm_lora_grad_workspace.argtypes = [P, u32, i32, P, P]
+            L.ans_gemm_lora_grad.argtypes = [P, P, u32, P, i32, P, u32, P, P, P, P, P, P, sz, P, P]
+            L.ans_xent_workspace.argtypes = [P, u32, i32, i32, P]
+            L.ans_xent.argtypes = [P, u32, P, i32, P, u32, u32, P, P, P, P, P, P, sz, P, P]
             L.ans_container_write.argtypes = [P, P, u64, P]
             L.ans_container_read.argtypes = [P, u64, P]
             for name in EXPORTS:
@@ -333,6 +349,73 @@ def ans_gemm_batched(jobs, M: int, scale_kind: int, group_k: int, d_ws, ws_bytes
            "ans_gemm_batched")
 
 
+def ans_gemm_lora_workspace(layout: AnsLayout, M: int, scale_kind: int, lora: AnsLora) -> int:
+    out = C.c_size_t(0)
+    _check(load().ans_gemm_lora_workspace(C.byref(layout), M, scale_kind, C.byref(lora), C.byref(out)),
+           "ans_gemm_lora_workspace")
+    return out.value
+
+
+def ans_gemm_lora(d_X, M: int, tiles: AnsTiles, scale_kind: int, d_scales, group_k: int, lora: AnsLora,
+                  d_ids, d_Y, d_ws, ws_bytes: int, d_status, stream=None):
+    """ans_gemm with the adapter of each token beside it (d_ids: int32, negative = none)."""
+    _check(load().ans_gemm_lora(_ptr(d_X), M, C.byref(tiles), scale_kind, _ptr(d_scales), group_k,
+                                C.byref(lora), _ptr(d_ids), _ptr(d_Y), _ptr(d_ws), ws_bytes,
+                                _ptr(d_status), _stream(stream)),
+           "ans_gemm_lora")
+
+
+def ans_gemm_grad_workspace(layout: AnsLayout, M: int, scale_kind: int = SCALE_NONE) -> int:
+    out = C.c_size_t(0)
+    _check(load().ans_gemm_grad_workspace(C.byref(layout), M, scale_kind, C.byref(out)),
+           "ans_gemm_grad_workspace")
+    return out.value
+
+
+def ans_gemm_grad(d_dY, M: int, tiles: AnsTiles, scale_kind: int, d_scales, group_k: int, d_dX, d_ws,
+                  ws_bytes: int, d_status, stream=None):
+    """dX = dY W of a compressed layer (bf16 in, bf16 out)."""
+    _check(load().ans_gemm_grad(_ptr(d_dY), M, C.byref(tiles), scale_kind, _ptr(d_scales), group_k,
+                                _ptr(d_dX), _ptr(d_ws), ws_bytes, _ptr(d_status), _stream(stream)),
+           "ans_gemm_grad")
+
+
+def ans_gemm_lora_grad_workspace(layout: AnsLayout, M: int, scale_kind: int, lora: AnsLora) -> int:
+    out = C.c_size_t(0)
+    _check(load().ans_gemm_lora_grad_workspace(C.byref(layout), M, scale_kind, C.byref(lora),
+                                               C.byref(out)),
+           "ans_gemm_lora_grad_workspace")
+    return out.value
+
+
+def ans_gemm_lora_grad(d_X, d_dY, M: int, tiles: AnsTiles, scale_kind: int, d_scales, group_k: int,
+                       lora: AnsLora, d_ids, d_dX, d_dA, d_dB, d_ws, ws_bytes: int, d_status, stream=None):
+    """Gradients of ans_gemm_lora: dX (bf16, or None) and the adapters' dA and dB (fp32)."""
+    _check(load().ans_gemm_lora_grad(_ptr(d_X), _ptr(d_dY), M, C.byref(tiles), scale_kind,
+                                     _ptr(d_scales), group_k, C.byref(lora), _ptr(d_ids), _ptr(d_dX),
+                                     _ptr(d_dA), _ptr(d_dB), _ptr(d_ws), ws_bytes, _ptr(d_status),
+                                     _stream(stream)),
+           "ans_gemm_lora_grad")
+
+
+def ans_xent_workspace(layout: AnsLayout, M: int, scale_kind: int = SCALE_NONE,
+                       with_grad: bool = False) -> int:
+    out = C.c_size_t(0)
+    _check(load().ans_xent_workspace(C.byref(layout), M, scale_kind, 1 if with_grad else 0, C.byref(out)),
+           "ans_xent_workspace")
+    return out.value
+
+
+def ans_xent(d_X, M: int, tiles: AnsTiles, scale_kind: int, d_scales, group_k: int, vocab: int, d_targets,
+             d_loss, d_lse, d_weight, d_dX, d_ws, ws_bytes: int, d_status, stream=None):
+    """Cross entropy over a compressed vocabulary head; d_dX (bf16) with the gradient of
+    sum(d_weight * loss), or None for the loss alone."""
+    _check(load().ans_xent(_ptr(d_X), M, C.byref(tiles), scale_kind, _ptr(d_scales), group_k, vocab,
+                           _ptr(d_targets), _ptr(d_loss), _ptr(d_lse), _ptr(d_weight), _ptr(d_dX),
+                           _ptr(d_ws), ws_bytes, _ptr(d_status), _stream(stream)),
+           "ans_xent")
+
+
 def ans_container_write(layout: AnsLayout, prob_bits: int, freq, stream: np.ndarray,
                         offsets: np.ndarray, raw: np.ndarray | None = None) -> np.ndarray:
     """The versioned container of a compressed layer (host arrays) as uint8[]."""
@@ -478,3 +561,21 @@ class CompressedLayer:
         cb = ans_build_codebook(hist, ALPHABET[layout.dtype], 12)
         stream, offsets, raw = ans_encode_tiles(h_w, layout, cb)
         return cls(layout, cb, stream, offsets, raw, device)
+
+
+class LoraAdapters:
+    """A projection's adapters on the device: A bf16 [n, rank, K], B bf16 [n, N, rank], scale fp32 [n]
+    or None.  Holds the tensors, and the ans_lora struct pointing at them in `lora`."""
+
+    def __init__(self, A, B, scale=None):
+        import torch
+        n, rank, _ = A.shape
+        if B.shape[0] != n or B.shape[2] != rank or (scale is not None and tuple(scale.shape) != (n,)):
+            raise AnsError(2, "LoraAdapters", "A, B and scale disagree about the adapters or the rank")
+        if (A.dtype, B.dtype) != (torch.bfloat16, torch.bfloat16) or \
+                (scale is not None and scale.dtype != torch.float32):
+            raise AnsError(1, "LoraAdapters", "A and B are bf16, scale is fp32")
+        if not (A.is_contiguous() and B.is_contiguous() and (scale is None or scale.is_contiguous())):
+            raise AnsError(1, "LoraAdapters", "A, B and scale are contiguous")
+        self.A, self.B, self.scale = A, B, scale
+        self.lora = AnsLora(n, rank, A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr())

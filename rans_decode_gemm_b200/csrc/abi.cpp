@@ -8,6 +8,9 @@
 
 #include "../../include/ans.h"
 #include "cuda/kernels.h"
+#include "cuda/lora.h"
+#include "cuda/operand.h"
+#include "cuda/xent.h"
 #include "host/codec_host.h"
 
 namespace {
@@ -562,6 +565,8 @@ int ansdev_set_wait_budget(long long cycles) {
   if (e == cudaSuccess) e = ansdev::set_live_wait_budget_decode(c);
   if (e == cudaSuccess) e = ansdev::set_live_wait_budget_dense(c);
   if (e == cudaSuccess) e = ansdev::set_live_wait_budget_decode16(c);
+  if (e == cudaSuccess) e = ansdev::set_live_wait_budget_operand(c);
+  if (e == cudaSuccess) e = ansdev::set_live_wait_budget_operand_gemm(c);
   return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ansdev_set_wait_budget");
 }
 
@@ -795,6 +800,324 @@ ans_status ans_container_read(const uint8_t* h_buf, uint64_t bytes, ans_containe
   }
   *layer = c;
   return ANS_OK;
+}
+
+}  // extern "C"
+
+// ---- adapters, gradients and loss ------------------------------------------------
+namespace {
+
+bool misaligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
+
+size_t up1024(size_t n) { return (n + 1023) / 1024 * 1024; }
+
+// Checks of an adapter set against a layer (no device work); pointers only
+// where the call will read them.
+ans_status check_lora(const ans_lora* l, const ans_layout& ly, bool pointers, ansdev::LoraDev* out) {
+  if (!l) return ANS_ERR_ARG;
+  if (l->n_adapters == 0 || l->rank == 0) return ANS_ERR_ARG;
+  if (l->n_adapters > ansdev::kLoraMaxAdapters || l->rank > ansdev::kLoraMaxRank || l->rank % 8 != 0)
+    return ANS_ERR_UNSUPPORTED;
+  if (pointers && (!l->d_A || !l->d_B || misaligned16(l->d_A) || misaligned16(l->d_B) ||
+                   reinterpret_cast<uintptr_t>(l->d_scale) % 4 != 0))
+    return ANS_ERR_ARG;
+  *out = ansdev::LoraDev{l->d_A, l->d_B, l->d_scale, l->n_adapters, l->rank, ly.N, ly.K};
+  return ANS_OK;
+}
+
+// Scale kinds by value (a workspace query has no scales to check).
+ans_status check_scale_kind(const ans_layout& ly, ans_scale_kind kind) {
+  if (kind < ANS_SCALE_NONE || kind > ANS_SCALE_GROUP_BF16) return ANS_ERR_ARG;
+  if (kind == ANS_SCALE_GROUP_BF16 && !is_int4(ly.dtype)) return ANS_ERR_ARG;
+  return ANS_OK;
+}
+
+// Largest token count of these calls: a token is a row of a grid, and tiles
+// are counted in 32 bits.
+constexpr uint32_t kMaxTokens = 1u << 24;
+
+// The gradient through a layer: workspace layout of ans_gemm_grad and
+// ans_gemm_lora_grad.
+struct GradPlan {
+  ansdev::OperandGemmPlan gemm;
+  ansdev::LoraPlan lora;
+  bool prep;  // dY needs a form of its own (f16, or row scales applied)
+  size_t off_images, off_rows, off_factor, off_parts, off_delta, off_lora, bytes;
+};
+
+void make_grad_plan(const ans_layout& ly, uint32_t M, ans_scale_kind kind, const ansdev::LoraDev* lora, int sms,
+                    GradPlan* p) {
+  const bool f16 = ansdev::operand_is_f16(ly.dtype);
+  p->gemm = ansdev::plan_operand_gemm(true, f16, M, ly.N, ly.K, 16, sms);
+  p->prep = f16 || kind == ANS_SCALE_ROW_BF16 || kind == ANS_SCALE_ROW_F32;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += up1024(n);
+    return o;
+  };
+  const size_t MK = static_cast<size_t>(M) * ly.K;
+  p->off_images = take(ansdev::operand_bytes(ly.N, ly.K));
+  p->off_rows = take(p->prep ? static_cast<size_t>(M) * ly.N * 2 : 0);
+  p->off_factor = take(p->prep ? static_cast<size_t>(M) * 4 : 0);
+  p->off_parts = take(p->gemm.splits > 1 ? MK * 4 * p->gemm.splits : 0);
+  p->off_delta = take(lora ? MK * 4 : 0);
+  p->off_lora = at;
+  if (lora) {
+    ansdev::make_lora_plan(M, *lora, true, sms, &p->lora);
+    at += up1024(p->lora.bytes);
+  }
+  p->bytes = at;
+}
+
+// dX = dY W (+ delta, for the tokens of an adapter).
+cudaError_t launch_grad_x(const GradPlan& p, const ansdev::LayerDev& L, const uint16_t* d_dY, uint32_t M,
+                          ans_scale_kind kind, const void* d_scales, uint32_t group_k, const float* delta,
+                          const int32_t* ids, uint32_t n_ids, uint16_t* d_dX, uint8_t* ws, uint32_t* d_status,
+                          int sms, cudaStream_t stream) {
+  const void* rows = d_dY;
+  const float* factor = nullptr;
+  cudaError_t e;
+  if (p.prep) {
+    const bool f16 = ansdev::operand_is_f16(L.dtype);
+    uint16_t* r = reinterpret_cast<uint16_t*>(ws + p.off_rows);
+    float* f = reinterpret_cast<float*>(ws + p.off_factor);
+    e = ansdev::launch_row_prep(d_dY, M, L.N, kind, d_scales, f16, r, f, stream);
+    if (e != cudaSuccess) return e;
+    rows = r;
+    factor = f;
+  }
+  uint8_t* images = ws + p.off_images;
+  e = ansdev::launch_operand_decode(L, 0, L.N, kind, d_scales, group_k, images, d_status, sms, stream);
+  if (e != cudaSuccess) return e;
+  ansdev::OperandGemmOut out;
+  out.ld = L.K;
+  if (p.gemm.splits == 1) {
+    out.out16 = d_dX;
+    out.beta = factor;
+    out.add = delta;
+    out.ids = ids;
+    out.n_ids = n_ids;
+    return ansdev::launch_operand_gemm(p.gemm, images, rows, out, d_status, stream);
+  }
+  out.out32 = reinterpret_cast<float*>(ws + p.off_parts);
+  out.split_stride = static_cast<uint64_t>(M) * L.K;
+  e = ansdev::launch_operand_gemm(p.gemm, images, rows, out, d_status, stream);
+  if (e != cudaSuccess) return e;
+  return ansdev::launch_sum_splits(out.out32, p.gemm.splits, out.split_stride, M, L.K, factor, delta, ids, n_ids, d_dX,
+                                   stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+ans_status ans_gemm_lora_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind,
+                                   const ans_lora* lora, size_t* bytes) {
+  if (!bytes) return ANS_ERR_ARG;
+  size_t base = 0;
+  ans_status st = ans_gemm_workspace(layout, M, scale_kind, &base);
+  if (st != ANS_OK) return st;
+  ansdev::LoraDev A;
+  st = check_lora(lora, *layout, false, &A);
+  if (st != ANS_OK) return st;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (M == 0) return ANS_OK;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ansdev::LoraPlan p;
+  ansdev::make_lora_plan(M, A, false, sms, &p);
+  *bytes = up1024(base) + p.bytes;
+  return ANS_OK;
+}
+
+ans_status ans_gemm_lora(const uint16_t* d_X, uint32_t M, const ans_tiles* W, ans_scale_kind scale_kind,
+                         const void* d_scales, uint32_t group_k, const ans_lora* lora, const int32_t* d_ids,
+                         float* d_Y, void* d_ws, size_t ws_bytes, uint32_t* d_status, ans_stream_t stream) {
+  ans_status st = check_gemm_tiles(W, scale_kind, d_scales, group_k);
+  if (st != ANS_OK) return st;
+  ansdev::LoraDev A;
+  st = check_lora(lora, W->layout, true, &A);
+  if (st != ANS_OK) return st;
+  if (M == 0) return ANS_OK;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  st = check_gemm_io(d_X, d_Y, d_status, d_scales);
+  if (st != ANS_OK) return st;
+  if (!d_ids || reinterpret_cast<uintptr_t>(d_ids) % 4 != 0) return ANS_ERR_ARG;
+  if (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0) return ANS_ERR_ARG;
+  ansdev::LayerDev L;
+  fill_layer(W, &L);
+  ansdev::GemmPlan plan;
+  st = plan_gemm(L, M, scale_kind, true, &plan);
+  if (st != ANS_OK) return st;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ansdev::LoraPlan p;
+  ansdev::make_lora_plan(M, A, false, sms, &p);
+  // the base product's workspace comes first: its counters are the part that
+  // has to be zero before the first call
+  const size_t base = up1024(plan.ws_bytes);
+  if (ws_bytes < base + p.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
+  st = launch_planned(plan, d_X, L, true, nullptr, scale_kind, d_scales, group_k, d_Y, d_ws, d_status, stream);
+  if (st != ANS_OK) return st;
+  cudaError_t e = ansdev::launch_lora_forward(p, A, d_X, d_ids, d_Y, static_cast<uint8_t*>(d_ws) + base, d_status,
+                                              reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gemm_lora");
+}
+
+ans_status ans_gemm_grad_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind, size_t* bytes) {
+  if (!bytes) return ANS_ERR_ARG;
+  ans_status st = check_layout(layout);
+  if (st != ANS_OK) return st;
+  st = check_scale_kind(*layout, scale_kind);
+  if (st != ANS_OK) return st;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (M == 0) return ANS_OK;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  GradPlan p;
+  make_grad_plan(*layout, M, scale_kind, nullptr, sms, &p);
+  *bytes = p.bytes;
+  return ANS_OK;
+}
+
+ans_status ans_gemm_grad(const uint16_t* d_dY, uint32_t M, const ans_tiles* W, ans_scale_kind scale_kind,
+                         const void* d_scales, uint32_t group_k, uint16_t* d_dX, void* d_ws, size_t ws_bytes,
+                         uint32_t* d_status, ans_stream_t stream) {
+  ans_status st = check_gemm_tiles(W, scale_kind, d_scales, group_k);
+  if (st != ANS_OK) return st;
+  if (M == 0) return ANS_OK;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  if (!d_dY || !d_dX || !d_status || misaligned16(d_dY) || misaligned16(d_dX) || misaligned16(d_scales))
+    return ANS_ERR_ARG;
+  if (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0) return ANS_ERR_ARG;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ansdev::LayerDev L;
+  fill_layer(W, &L);
+  GradPlan p;
+  make_grad_plan(W->layout, M, scale_kind, nullptr, sms, &p);
+  if (ws_bytes < p.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
+  cudaError_t e = launch_grad_x(p, L, d_dY, M, scale_kind, d_scales, group_k, nullptr, nullptr, 0, d_dX,
+                                static_cast<uint8_t*>(d_ws), d_status, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gemm_grad");
+}
+
+ans_status ans_gemm_lora_grad_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind,
+                                        const ans_lora* lora, size_t* bytes) {
+  if (!bytes) return ANS_ERR_ARG;
+  ans_status st = check_layout(layout);
+  if (st != ANS_OK) return st;
+  st = check_scale_kind(*layout, scale_kind);
+  if (st != ANS_OK) return st;
+  ansdev::LoraDev A;
+  st = check_lora(lora, *layout, false, &A);
+  if (st != ANS_OK) return st;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (M == 0) return ANS_OK;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  GradPlan p;
+  make_grad_plan(*layout, M, scale_kind, &A, sms, &p);
+  *bytes = p.bytes;
+  return ANS_OK;
+}
+
+ans_status ans_gemm_lora_grad(const uint16_t* d_X, const uint16_t* d_dY, uint32_t M, const ans_tiles* W,
+                              ans_scale_kind scale_kind, const void* d_scales, uint32_t group_k,
+                              const ans_lora* lora, const int32_t* d_ids, uint16_t* d_dX, float* d_dA, float* d_dB,
+                              void* d_ws, size_t ws_bytes, uint32_t* d_status, ans_stream_t stream) {
+  ans_status st = check_gemm_tiles(W, scale_kind, d_scales, group_k);
+  if (st != ANS_OK) return st;
+  ansdev::LoraDev A;
+  st = check_lora(lora, W->layout, true, &A);
+  if (st != ANS_OK) return st;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  if (!d_dA || !d_dB || misaligned16(d_dA) || misaligned16(d_dB)) return ANS_ERR_ARG;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    // no tokens: the adapters' gradients are zero, and are written
+    cudaError_t e = cudaMemsetAsync(d_dA, 0, static_cast<size_t>(A.n) * A.rank * A.K * 4, cs);
+    if (e == cudaSuccess) e = cudaMemsetAsync(d_dB, 0, static_cast<size_t>(A.n) * A.rank * A.N * 4, cs);
+    return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gemm_lora_grad");
+  }
+  if (!d_X || !d_dY || !d_ids || !d_status || misaligned16(d_X) || misaligned16(d_dY) || misaligned16(d_dX) ||
+      misaligned16(d_scales) || reinterpret_cast<uintptr_t>(d_ids) % 4 != 0)
+    return ANS_ERR_ARG;
+  if (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0) return ANS_ERR_ARG;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ansdev::LayerDev L;
+  fill_layer(W, &L);
+  GradPlan p;
+  make_grad_plan(W->layout, M, scale_kind, &A, sms, &p);
+  if (ws_bytes < p.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
+  uint8_t* ws = static_cast<uint8_t*>(d_ws);
+  float* delta = d_dX ? reinterpret_cast<float*>(ws + p.off_delta) : nullptr;
+  cudaError_t e = ansdev::launch_lora_grad(p.lora, A, d_X, d_dY, d_ids, d_dA, d_dB, delta, ws + p.off_lora, d_status, cs);
+  if (e == cudaSuccess && d_dX)
+    e = launch_grad_x(p, L, d_dY, M, scale_kind, d_scales, group_k, delta, d_ids, A.n, d_dX, ws, d_status, sms, cs);
+  return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gemm_lora_grad");
+}
+
+ans_status ans_xent_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind, int with_grad,
+                              size_t* bytes) {
+  if (!bytes) return ANS_ERR_ARG;
+  ans_status st = check_layout(layout);
+  if (st != ANS_OK) return st;
+  st = check_scale_kind(*layout, scale_kind);
+  if (st != ANS_OK) return st;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (M == 0) return ANS_OK;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ansdev::LayerDev L;
+  fill_layer_plain(layout, &L);
+  ansdev::XentPlan p;
+  ansdev::make_xent_plan(L, M, with_grad != 0, sms, &p);
+  *bytes = p.bytes;
+  return ANS_OK;
+}
+
+ans_status ans_xent(const uint16_t* d_X, uint32_t M, const ans_tiles* W, ans_scale_kind scale_kind,
+                    const void* d_scales, uint32_t group_k, uint32_t vocab, const int32_t* d_targets, float* d_loss,
+                    float* d_lse, const float* d_weight, uint16_t* d_dX, void* d_ws, size_t ws_bytes,
+                    uint32_t* d_status, ans_stream_t stream) {
+  ans_status st = check_gemm_tiles(W, scale_kind, d_scales, group_k);
+  if (st != ANS_OK) return st;
+  if (vocab == 0 || vocab > W->layout.N) return ANS_ERR_SHAPE;
+  if (M == 0) return ANS_OK;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  if (!d_X || !d_targets || !d_loss || !d_lse || !d_status || misaligned16(d_X) || misaligned16(d_dX) ||
+      misaligned16(d_scales))
+    return ANS_ERR_ARG;
+  for (const void* p : {static_cast<const void*>(d_targets), static_cast<const void*>(d_loss),
+                        static_cast<const void*>(d_lse), static_cast<const void*>(d_weight)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return ANS_ERR_ARG;
+  if (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0) return ANS_ERR_ARG;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ansdev::LayerDev L;
+  fill_layer(W, &L);
+  ansdev::XentPlan plan;
+  ansdev::make_xent_plan(L, M, d_dX != nullptr, sms, &plan);
+  if (ws_bytes < plan.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
+  const ansdev::XentArgs a{d_X, static_cast<uint32_t>(scale_kind), d_scales, group_k, vocab, d_targets, d_loss, d_lse,
+                           d_weight, d_dX, d_status};
+  cudaError_t e = ansdev::launch_xent(plan, L, a, d_ws, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_xent");
 }
 
 }  // extern "C"

@@ -990,7 +990,7 @@ bool make_gemm_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool dec
 
 // ---- tensor maps (2-D, tiled, one destination CTA), encoded through the driver
 // entry point the runtime hands out (no link-time dependence on libcuda)
-static cudaError_t encode_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* base,
+cudaError_t encode_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* base,
                                uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                                uint32_t box_outer, CUtensorMapSwizzle swizzle) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

@@ -1,0 +1,52 @@
+// lora.h -- low-rank adapters of many requests beside a projection: plans and
+// launch entry points (lora.cu).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace ansdev {
+
+constexpr uint32_t kLoraMaxRank = 128;
+constexpr uint32_t kLoraMaxAdapters = 256;
+
+struct LoraDev {
+  const uint16_t* A;   // bf16 n x rank x K
+  const uint16_t* B;   // bf16 n x N x rank
+  const float* scale;  // n, or null: 1
+  uint32_t n, rank, N, K;
+};
+
+// Tokens grouped by adapter, in device memory: the sorted order `perm` (tokens
+// without an adapter left out), adapter a's tokens at [off[a], off[a + 1]),
+// and tiles of at most tm tokens of one adapter each.
+struct LoraGroups {
+  uint32_t* n_tiles;
+  uint32_t* off;
+  uint32_t* perm;
+  uint32_t* tile_adapter;
+  uint32_t* tile_start;
+  uint32_t* tile_count;
+};
+
+struct LoraPlan {
+  uint32_t M, tm, max_tiles;
+  uint32_t splits_k, len_k;  // ranges of a sum over K, and their length
+  uint32_t splits_n, len_n;  // of a sum over N
+  size_t off_groups, off_part, off_h, off_dh, bytes;
+};
+void make_lora_plan(uint32_t M, const LoraDev& L, bool grad, int sms, LoraPlan* plan);
+
+// Y[m][n] += s_a sum_j (sum_k X[m][k] A_a[j][k]) B_a[n][j]
+cudaError_t launch_lora_forward(const LoraPlan& plan, const LoraDev& L, const uint16_t* X,
+                                const int32_t* ids, float* Y, void* ws, uint32_t* status,
+                                cudaStream_t stream);
+// dH[m][j] = s_a sum_n dY[m][n] B_a[n][j];  dA_a = sum_m dH[m]^T X[m];
+// dB_a = s_a sum_m dY[m]^T (X[m] A_a^T);  delta[m] = dH[m] A_a where delta is
+// given (fp32 M x K, rows of tokens with an adapter only).
+cudaError_t launch_lora_grad(const LoraPlan& plan, const LoraDev& L, const uint16_t* X,
+                             const uint16_t* dY, const int32_t* ids, float* dA, float* dB,
+                             float* delta, void* ws, uint32_t* status, cudaStream_t stream);
+
+}  // namespace ansdev

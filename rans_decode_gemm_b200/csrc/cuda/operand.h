@@ -1,0 +1,91 @@
+// operand.h -- decoding a range of a compressed layer into 16-bit tensor-core
+// operands, and GEMMs that read those operands either way round.  Host-side
+// plans and launch entry points shared by the gradient, adapter and loss
+// operators.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "kernels.h"
+
+namespace ansdev {
+
+// Operand images: the weights of a range of W rows as 16-bit values, 4 KB per
+// 128 rows x 16 columns (row r at byte 32 r, its two 16-byte halves swapped
+// where bit 2 of r is set: the 32-byte shared-memory swizzle), the image of
+// the range's rows 128 b .. + 127 and columns 16 j .. + 15 at byte
+// (b * K / 16 + j) * 4096.  bf16 weights stay bf16.  Every other format's
+// values are exact in f16 (int4 with group scales: q * s, exact for scales in
+// [2^-14, 2^12]; row scales are not part of the image).
+inline bool operand_is_f16(uint32_t dtype) { return dtype != 1; }
+inline size_t operand_bytes(uint64_t rows, uint32_t K) { return static_cast<size_t>(rows) * K * 2; }
+
+// Decodes row blocks [row0, row0 + rows) (multiples of tile_n) into images.
+cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t rows,
+                                  uint32_t scale_kind, const void* scales, uint32_t group_k,
+                                  uint8_t* images, uint32_t* status, int sms, cudaStream_t stream);
+
+// Rows of a bf16 matrix as f16 under a power of two of their own: out[m][c] =
+// f16(in[m][c] * s[c] * 2^e), factor[m] = 2^-e, with e such that the row's
+// largest finite magnitude lands in [2^14, 2^15).  scale_kind: s[c] as bf16 (1)
+// or fp32 (2), else 1.  f16 false: out[m][c] = bf16(in[m][c] * s[c]), factor 1
+// (for bf16 weights that carry row scales).
+cudaError_t launch_row_prep(const uint16_t* in, uint32_t M, uint32_t C, uint32_t scale_kind,
+                            const void* scales, bool f16, uint16_t* out, float* factor, cudaStream_t stream);
+
+// One GEMM on operand images of `rows` W rows and K columns, X and G 16-bit
+// row-major, fp32 sums:
+//   forward:     out[m][n] = s_n * sum_k X[m][k] W[n][k]        (n < rows)
+//   transposed:  out[m][k] = sum_n G[m][n] W[n][k]              (k < K)
+// The transposed sum may be cut into `splits` ranges of n.
+struct OperandGemmPlan {
+  uint32_t trans, f16;
+  uint32_t M, rows, K;
+  uint32_t bn;       // tokens of one tile
+  uint32_t splits;   // ranges of the sum (transposed only)
+  uint32_t sms;
+};
+// max_splits 1: never cut.
+OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t rows, uint32_t K,
+                                  uint32_t max_splits, int sms);
+
+// What happens to the sums (v[m][c], c = n or k).
+struct OperandGemmOut {
+  // forward: out32[m * ld + n] = v * s_n.
+  // transposed with out16: out16[m * ld + k] = bf16(beta[m] * v + add[m * ld + k]),
+  //   the addend taken for rows with 0 <= ids[m] < n_ids only (add may be null).
+  // transposed with out32: out32[split][m * ld + k] = alpha[m] * (its old value) +
+  //   beta[m] * v; alpha null: the old value is not read.  beta null: 1.
+  float* out32 = nullptr;
+  uint16_t* out16 = nullptr;
+  uint64_t split_stride = 0;  // elements between the splits' out32
+  uint32_t ld = 0;
+  const float* alpha = nullptr;
+  const float* beta = nullptr;
+  const float* add = nullptr;
+  const int32_t* ids = nullptr;
+  uint32_t n_ids = 0;
+  uint32_t scale_kind = 0;
+  const void* scales = nullptr;
+};
+cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* images, const void* rows16,
+                                const OperandGemmOut& out, uint32_t* status, cudaStream_t stream);
+
+// out[m][k] = bf16(beta[m] * sum over splits of part[split][m][k] + add[m][k])
+// (the addend as in OperandGemmOut).
+cudaError_t launch_sum_splits(const float* part, uint32_t splits, uint64_t split_stride, uint32_t M,
+                              uint32_t K, const float* beta, const float* add, const int32_t* ids,
+                              uint32_t n_ids, uint16_t* out, cudaStream_t stream);
+
+cudaError_t set_live_wait_budget_operand(long long cycles);
+cudaError_t set_live_wait_budget_operand_gemm(long long cycles);
+
+// 2-D tiled tensor map (gemm.cu).
+cudaError_t encode_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner,
+                        uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                        CUtensorMapSwizzle swizzle);
+
+}  // namespace ansdev

@@ -1,0 +1,458 @@
+// operand_gemm.cu -- tcgen05 GEMMs on operand images (operand.h), either way
+// round, and the row kernels beside them.
+//
+//   forward      D[n][m] = sum_k W[n][k] X[m][k]    (the logits of a vocabulary piece)
+//   transposed   D[k][m] = sum_n W[n][k] G[m][n]    (a gradient that leaves the layer)
+//
+// One layout of W serves both.  An image is 128 rows of 32 bytes under the
+// 32-byte swizzle.  Read as rows n with 16 consecutive k it is a K-major
+// operand; read as 16 consecutive output features k by 8-row groups of n it is
+// the canonical MN-major one (atoms of 16 k x 8 n, 256 bytes apart along n),
+// so the transposed product needs neither a second copy of W nor a
+// transposing load.  Tokens are the MMA's N dimension in both: 128 rows of W
+// (or of W^T) by up to 256 tokens, fp32 accumulators in two TMEM sets so that
+// the stores of a tile overlap the MMAs of the next.
+//
+// A stage holds 64 steps of the sum: 16 KB of W by bulk copies (forward: four
+// consecutive images, one copy; transposed: half of each of eight images) and
+// a 64 x bn box of the tokens by TMA under the 128-byte swizzle.  Four K = 16
+// MMAs and one commit a stage.
+// Warps: 0 loads, 1 MMA issue (and TMEM owner), 2-5 epilogue.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "gemm_common.cuh"
+#include "launch.h"
+#include "operand.h"
+#include "rans_core.cuh"
+
+namespace ansdev {
+
+constexpr uint32_t kOgBM = 128, kOgBK = 64;
+constexpr uint32_t kOgABytes = kOgBM * kOgBK * 2;  // 16 KB
+constexpr uint32_t kOgThreads = 6 * 32;
+constexpr uint32_t kOgMaxStages = 8;
+constexpr uint32_t kOgSmemTiles = 200 * 1024;  // stages
+constexpr uint32_t kOgSmem = kOgSmemTiles + 1024;
+
+struct OperandGemmDev {
+  const uint8_t* images;
+  CUtensorMap tmap_b;  // tokens: 64 x b_box_rows boxes, 128-byte swizzle
+  OperandGemmOut out;
+  uint32_t* status;
+  uint32_t M, bn, m_blocks, n_tiles, splits;
+  uint32_t k_slabs;      // images per 128-row block (K / 16)
+  uint32_t out_cols;     // rows of D that exist: rows of W, or K (transposed)
+  uint32_t n_kb;         // stages of the whole sum
+  uint32_t b_box_rows, stages, stage_bytes;
+  uint32_t idesc, idesc_tail;
+};
+
+template <bool kTrans>
+__global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __grid_constant__ OperandGemmDev P) {
+  extern __shared__ __align__(1024) uint8_t dsmem_raw[];
+  __shared__ __align__(8) uint64_t full[kOgMaxStages], empty[kOgMaxStages];
+  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t abort_flag;
+
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // stages on a 1024-byte boundary (the 128-byte swizzle atom)
+  const uint32_t smem_s = (smem_u32(dsmem_raw) + 1023u) & ~1023u;
+  const uint32_t n_st = P.stages;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (uint32_t i = 0; i < kOgMaxStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);  // one arrival per epilogue warp
+    }
+    mbar_init(&mma_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  } else if (warp == 0 && lane == 0) {
+    prefetch_tmap(&P.tmap_b);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  volatile uint32_t* abort = &abort_flag;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // tile t: row block ab, token block mb, range sp of the sum.  Row block
+  // major, so that the CTAs running at one time share W through L2.
+  const uint32_t per_ab = P.m_blocks * P.splits;
+  auto tile_of = [&](uint32_t t, uint32_t& ab, uint32_t& mb, uint32_t& sp, uint32_t& kb0, uint32_t& kb1) {
+    ab = t / per_ab;
+    const uint32_t r = t - ab * per_ab;
+    sp = r / P.m_blocks;
+    mb = r - sp * P.m_blocks;
+    kb0 = cta_begin(P.n_kb, P.splits, sp);
+    kb1 = cta_begin(P.n_kb, P.splits, sp + 1);
+  };
+
+  if (warp == 0) {
+    // ======================= loads =======================
+    if (lane == 0) {
+      uint32_t it = 0, s = 0, ph = 1;  // the first pass over the ring finds it free
+      bool live = true;
+      for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x) {
+        uint32_t ab, mb, sp, kb0, kb1;
+        tile_of(t, ab, mb, sp, kb0, kb1);
+        // transposed: images of this tile's k that exist (the last block may
+        // hold fewer than 8; its missing rows of D are never stored)
+        const uint32_t n_img = min(8u, P.k_slabs - min(P.k_slabs, 8 * ab));
+        for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+          if (it >= n_st && !wait_live(&empty[s], ph, abort, P.status, 20)) {
+            live = false;
+            break;
+          }
+          const uint32_t bar = smem_u32(&full[s]);
+          const uint32_t a_s = smem_s + s * P.stage_bytes, b_s = a_s + kOgABytes;
+          if (kTrans) {
+            mbar_arrive_expect_tx_s(bar, n_img * 2048u + P.b_box_rows * kOgBK * 2);
+            const uint8_t* src = P.images + (static_cast<uint64_t>(kb >> 1) * P.k_slabs + 8 * ab) * kSlabBytes +
+                                 (kb & 1u) * 2048u;
+            for (uint32_t j = 0; j < n_img; ++j) bulk_g2s_s(a_s + j * 2048u, src + j * kSlabBytes, 2048u, bar);
+          } else {
+            const uint32_t cnt = min(4u, P.k_slabs - 4 * kb);
+            mbar_arrive_expect_tx_s(bar, cnt * kSlabBytes + P.b_box_rows * kOgBK * 2);
+            bulk_g2s_s(a_s, P.images + (static_cast<uint64_t>(ab) * P.k_slabs + 4 * kb) * kSlabBytes,
+                       cnt * kSlabBytes, bar);
+          }
+          tma_load_2d_s(b_s, &P.tmap_b, static_cast<int32_t>(kb * kOgBK), static_cast<int32_t>(mb * P.bn), bar);
+          if (++s == n_st) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // loads still in flight (only after an abort) land before exit
+      const uint32_t first = it > n_st ? it - n_st : 0;
+      for (uint32_t q = first; q < it; ++q) wait_drain(&full[q % n_st], (q / n_st) & 1u, P.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ======================= MMA issue =======================
+    if (lane == 0) {
+      // forward A: K-major, 8-row groups 256 B apart (SBO), image j of a stage
+      // is its K = 16 slice j.  Transposed A: MN-major, atoms of 16 k 2 KB
+      // apart (LBO), 8-row groups of n 256 B apart (SBO); the K = 16 slice j
+      // starts 16 rows (512 B) further.  B: 128-byte swizzle, 8-row groups
+      // 1024 B apart, slice j 32 j bytes into each row.
+      const uint64_t da = (kTrans ? (128ull << 16) : (1ull << 16)) | (16ull << 32) | (1ull << 46) | (6ull << 61);
+      const uint64_t db = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+      uint32_t s = 0, ph = 0, acc = 0;
+      bool live = true;
+      for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x, ++acc) {
+        uint32_t ab, mb, sp, kb0, kb1;
+        tile_of(t, ab, mb, sp, kb0, kb1);
+        const uint32_t b = acc & 1u;
+        if (acc >= 2 && !wait_live(&acc_empty[b], ((acc >> 1) + 1) & 1u, abort, P.status, 21)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + b * 256;
+        // the last token block is narrower when M is not a multiple of bn
+        const uint32_t idesc = mb == P.m_blocks - 1 ? P.idesc_tail : P.idesc;
+        for (uint32_t kb = kb0; kb < kb1; ++kb) {
+          if (!wait_live(&full[s], ph, abort, P.status, 22)) {
+            live = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a16 = (smem_s + s * P.stage_bytes) >> 4, b16 = a16 + (kOgABytes >> 4);
+          const uint32_t cnt = kTrans ? 4u : min(4u, P.k_slabs - 4 * kb);
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j)
+            if (j < cnt)
+              umma_f16(d_tmem, da | (a16 + j * ((kTrans ? 512u : kSlabBytes) >> 4)), db | (b16 + 2 * j), idesc,
+                       (kb != kb0 || j != 0) ? 1u : 0u);
+          umma_commit(&empty[s]);
+          if (++s == n_st) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (live) umma_commit(&acc_full[b]);
+      }
+      umma_commit(&mma_done);
+      wait_drain(&mma_done, 0, P.status);
+    }
+    __syncwarp();
+  } else {
+    // ======================= epilogue (warps 2-5) =======================
+    const uint32_t quad = warp & 3u;
+    const OperandGemmOut& O = P.out;
+    uint32_t acc = 0;
+    for (uint32_t t = blockIdx.x; t < P.n_tiles; t += gridDim.x, ++acc) {
+      uint32_t ab, mb, sp, kb0, kb1;
+      tile_of(t, ab, mb, sp, kb0, kb1);
+      const uint32_t b = acc & 1u;
+      const bool ok = wait_live(&acc_full[b], (acc >> 1) & 1u, abort, P.status, 23, 64);
+      tc_fence_after();
+      const uint32_t c = ab * kOgBM + 32 * quad + lane;  // this thread's column of the output
+      const uint32_t m0 = mb * P.bn;
+      const uint32_t cols = min(P.bn, P.M - m0);
+      float scale = 1.0f;
+      if (!kTrans && c < P.out_cols) {
+        if (O.scale_kind == 1) scale = bf16_to_f32(__ldg(static_cast<const uint16_t*>(O.scales) + c));
+        else if (O.scale_kind == 2) scale = __ldg(static_cast<const float*>(O.scales) + c);
+      }
+      if (ok) {
+        for (uint32_t c0 = 0; c0 < cols; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem_base + ((32 * quad) << 16) + b * 256 + c0, v);
+          const uint64_t at = static_cast<uint64_t>(m0 + c0) * O.ld + c;
+          float old[32];
+          if (kTrans && O.out32 != nullptr && O.alpha != nullptr) {
+#pragma unroll
+            for (uint32_t j = 0; j < 32; ++j)
+              old[j] = (c0 + j < cols && c < P.out_cols)
+                           ? __ldcg(O.out32 + sp * O.split_stride + at + static_cast<uint64_t>(j) * O.ld) : 0.0f;
+          }
+          tmem_ld_wait();
+          if (c < P.out_cols) {
+#pragma unroll
+            for (uint32_t j = 0; j < 32; ++j) {
+              if (c0 + j >= cols) break;
+              const uint32_t m = m0 + c0 + j;
+              const uint64_t i = at + static_cast<uint64_t>(j) * O.ld;
+              float x = __uint_as_float(v[j]);
+              if (!kTrans) {
+                O.out32[i] = x * scale;
+              } else {
+                if (O.beta != nullptr) x *= __ldcg(O.beta + m);
+                if (O.out32 != nullptr) {
+                  if (O.alpha != nullptr) x = fmaf(__ldcg(O.alpha + m), old[j], x);
+                  O.out32[sp * O.split_stride + i] = x;
+                } else {
+                  if (O.add != nullptr) {
+                    const int32_t id = __ldg(O.ids + m);
+                    if (id >= 0 && static_cast<uint32_t>(id) < O.n_ids) x += __ldcg(O.add + i);
+                  }
+                  O.out16[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+                }
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[b]);
+      if (!ok) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, 512);
+}
+
+OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t rows, uint32_t K,
+                                  uint32_t max_splits, int sms) {
+  OperandGemmPlan p;
+  p.trans = trans;
+  p.f16 = f16;
+  p.M = M;
+  p.rows = rows;
+  p.K = K;
+  p.sms = static_cast<uint32_t>(sms);
+  const uint64_t blocks = ((trans ? K : rows) + 127) / 128;
+  const uint32_t n_kb = ((trans ? rows : K) + kOgBK - 1) / kOgBK;
+  // the widest token tile that still gives most SMs a tile
+  p.bn = 256;
+  while (p.bn > 32 && (M <= p.bn / 2 || blocks * ((M + p.bn - 1) / p.bn) * 5 < p.sms * 4ull)) p.bn /= 2;
+  const uint64_t tiles = blocks * ((M + p.bn - 1) / p.bn);
+  p.splits = 1;
+  if (trans && tiles * 2 <= p.sms) {
+    // a range is worth its partial sums from about 8 stages on
+    p.splits = static_cast<uint32_t>(std::min<uint64_t>({p.sms / tiles, max_splits, (n_kb + 7) / 8}));
+    if (p.splits < 1) p.splits = 1;
+  }
+  return p;
+}
+
+cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* images, const void* rows16,
+                                const OperandGemmOut& out, uint32_t* status, cudaStream_t stream) {
+  if (plan.M == 0) return cudaSuccess;
+  OperandGemmDev P;
+  std::memset(&P, 0, sizeof(P));
+  P.images = images;
+  P.out = out;
+  P.status = status;
+  P.M = plan.M;
+  P.bn = plan.bn;
+  P.m_blocks = (plan.M + plan.bn - 1) / plan.bn;
+  P.splits = plan.splits;
+  P.k_slabs = plan.K / 16;
+  P.out_cols = plan.trans ? plan.K : plan.rows;
+  const uint32_t red = plan.trans ? plan.rows : plan.K;
+  P.n_kb = (red + kOgBK - 1) / kOgBK;
+  P.n_tiles = (P.out_cols + kOgBM - 1) / kOgBM * P.m_blocks * P.splits;
+  P.b_box_rows = std::min(plan.M, plan.bn);
+  P.stage_bytes = kOgABytes + plan.bn * kOgBK * 2;
+  P.stages = std::min(kOgMaxStages, kOgSmemTiles / P.stage_bytes);
+  const uint32_t tail = plan.M - (P.m_blocks - 1) * plan.bn;
+  // bit 15: A is MN-major
+  P.idesc = idesc_f16(plan.f16 ? 0u : 1u, 128, plan.bn) | (plan.trans ? 1u << 15 : 0u);
+  P.idesc_tail = idesc_f16(plan.f16 ? 0u : 1u, 128, (tail + 15) / 16 * 16) | (plan.trans ? 1u << 15 : 0u);
+  cudaError_t e = encode_tmap(&P.tmap_b, CU_TENSOR_MAP_DATA_TYPE_UINT16, rows16, red, plan.M,
+                              static_cast<uint64_t>(red) * 2, kOgBK, P.b_box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  auto kern = plan.trans ? operand_gemm_kernel<true> : operand_gemm_kernel<false>;
+  static std::atomic<uint64_t> attr_set{0};
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(attr_set.load() & (1ull << dev))) {
+    e = cudaFuncSetAttribute(operand_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(operand_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set.fetch_or(1ull << dev);
+  }
+  const uint32_t grid = std::min(P.n_tiles, plan.sms);
+  return launch_pdl(kern, dim3(grid), dim3(kOgThreads), kOgSmem, stream, P);
+}
+
+// ---- rows of bf16 as scaled f16 ----------------------------------------------
+// One CTA a row: the largest finite magnitude first, then the conversion (the
+// row comes from L2 the second time).  f16 under a power of two of the row's
+// own keeps 11 bits of every value down to 2^-29 of the row's largest, and
+// what is smaller is off by at most 2^-40 of it: more than a rounding to bf16
+// would keep of v * s.  Infinities and NaN pass through.
+constexpr uint32_t kPrepThreads = 256;
+__device__ __forceinline__ float prep_scale(uint32_t kind, const void* scales, uint32_t c) {
+  if (kind == 1) return bf16_to_f32(__ldg(static_cast<const uint16_t*>(scales) + c));
+  if (kind == 2) return __ldg(static_cast<const float*>(scales) + c);
+  return 1.0f;
+}
+__global__ void __launch_bounds__(kPrepThreads) row_prep_kernel(const uint16_t* __restrict__ in, uint32_t C,
+                                                                uint32_t kind, const void* scales, bool f16,
+                                                                uint16_t* __restrict__ out,
+                                                                float* __restrict__ factor) {
+  __shared__ float part[kPrepThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint64_t row = static_cast<uint64_t>(blockIdx.x) * C;
+  auto values = [&](uint32_t c, float (&v)[8]) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(in + row + c));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    }
+    if (kind == 1 || kind == 2) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= prep_scale(kind, scales, c + k);
+    }
+  };
+  float top = 0.0f;
+  for (uint32_t c = threadIdx.x * 8; c < C; c += kPrepThreads * 8) {
+    float v[8];
+    values(c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = fabsf(v[k]);
+      if (a <= 3.402823466e38f) top = fmaxf(top, a);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+  __syncthreads();
+#pragma unroll
+  for (uint32_t k = 0; k < kPrepThreads / 32; ++k) top = fmaxf(top, part[k]);
+  // 2^e with top * 2^e in [2^14, 2^15); both powers stay normal numbers
+  const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+  const int e = top == 0.0f || !f16 ? 0 : min(126, max(-113, 14 - ex));
+  const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  if (threadIdx.x == 0) factor[blockIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  for (uint32_t c = threadIdx.x * 8; c < C; c += kPrepThreads * 8) {
+    float v[8];
+    values(c, v);
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (f16) {
+        const __half2 h = __floats2half2_rn(v[2 * k] * up, v[2 * k + 1] * up);
+        o[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+        o[k] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(out + row + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+cudaError_t launch_row_prep(const uint16_t* in, uint32_t M, uint32_t C, uint32_t scale_kind,
+                            const void* scales, bool f16, uint16_t* out, float* factor, cudaStream_t stream) {
+  if (M == 0) return cudaSuccess;
+  return launch_pdl(row_prep_kernel, dim3(M), dim3(kPrepThreads), 0, stream, in, C, scale_kind, scales, f16,
+                    out, factor);
+}
+
+// ---- the sum over the splits of a transposed product --------------------------
+__global__ void __launch_bounds__(256) sum_splits_kernel(const float* __restrict__ part, uint32_t splits,
+                                                         uint64_t stride, uint32_t K4, uint64_t n4,
+                                                         const float* beta, const float* add,
+                                                         const int32_t* ids, uint32_t n_ids,
+                                                         uint16_t* __restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < n4;
+       i += static_cast<uint64_t>(gridDim.x) * 256) {
+    const uint32_t m = static_cast<uint32_t>(i / K4);
+    float4 a = __ldcg(reinterpret_cast<const float4*>(part) + i);
+    for (uint32_t s = 1; s < splits; ++s) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part + s * stride) + i);
+      a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+    }
+    if (beta != nullptr) {
+      const float f = __ldcg(beta + m);
+      a.x *= f; a.y *= f; a.z *= f; a.w *= f;
+    }
+    if (add != nullptr) {
+      const int32_t id = __ldg(ids + m);
+      if (id >= 0 && static_cast<uint32_t>(id) < n_ids) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(add) + i);
+        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+      }
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
+    *reinterpret_cast<uint2*>(out + 4 * i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+cudaError_t launch_sum_splits(const float* part, uint32_t splits, uint64_t split_stride, uint32_t M,
+                              uint32_t K, const float* beta, const float* add, const int32_t* ids,
+                              uint32_t n_ids, uint16_t* out, cudaStream_t stream) {
+  const uint64_t n4 = static_cast<uint64_t>(M) * K / 4;
+  if (n4 == 0) return cudaSuccess;
+  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>((n4 + 255) / 256, 2048));
+  return launch_pdl(sum_splits_kernel, dim3(grid), dim3(256), 0, stream, part, splits, split_stride, K / 4, n4,
+                    beta, add, ids, n_ids, out);
+}
+
+cudaError_t set_live_wait_budget_operand_gemm(long long cycles) {
+  return cudaMemcpyToSymbol(g_live_wait_budget, &cycles, sizeof(cycles));
+}
+
+}  // namespace ansdev

@@ -49,6 +49,7 @@ constexpr uint32_t kStatusCorrupt = 0x1u;
 constexpr uint32_t kStatusTimeout = 0x2u;
 constexpr uint32_t kStatusBadOffsets = 0x4u;
 constexpr uint32_t kStatusSmemAlign = 0x8u;
+constexpr uint32_t kStatusBadIndex = 0x10u;
 
 // The fused kernels lay out W slabs and X stages at 1024-byte multiples of
 // the dynamic shared-memory base and describe them to the tensor cores (and

@@ -13,9 +13,9 @@
 // (or of W^T) by up to 256 tokens, fp32 accumulators in two TMEM sets so that
 // the stores of a tile overlap the MMAs of the next.
 //
-// A stage holds 64 steps of the sum: 16 KB of W by bulk copies (forward: four
-// consecutive images, one copy; transposed: half of each of eight images) and
-// a 64 x bn box of the tokens by TMA under the 128-byte swizzle.  Four K = 16
+// A stage holds 64 steps of the sum: 16 KB of W by one copy (forward: four
+// consecutive images; transposed: one box of half of each of eight images)
+// and a 64 x bn box of the tokens by TMA under the 128-byte swizzle.  Four K = 16
 // MMAs and one commit a stage.
 // Warps: 0 loads, 1 MMA issue (and TMEM owner), 2-5 epilogue.
 #include <cuda.h>
@@ -43,6 +43,7 @@ constexpr uint32_t kOgSmem = kOgSmemTiles + 1024;
 struct OperandGemmDev {
   const uint8_t* images;
   CUtensorMap tmap_b;  // tokens: 64 x b_box_rows boxes, 128-byte swizzle
+  CUtensorMap tmap_a;  // transposed: images as rows of 512 eight-byte words, boxes of 256 x 8
   OperandGemmOut out;
   uint32_t* status;
   uint32_t M, bn, m_blocks, n_tiles, splits;
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
     tmem_relinquish();
   } else if (warp == 0 && lane == 0) {
     prefetch_tmap(&P.tmap_b);
+    if (kTrans) prefetch_tmap(&P.tmap_a);
   }
   tc_fence_before();
   __syncthreads();
@@ -113,9 +115,6 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
       for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x) {
         uint32_t ab, mb, sp, kb0, kb1;
         tile_of(t, ab, mb, sp, kb0, kb1);
-        // transposed: images of this tile's k that exist (the last block may
-        // hold fewer than 8; its missing rows of D are never stored)
-        const uint32_t n_img = min(8u, P.k_slabs - min(P.k_slabs, 8 * ab));
         for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
           if (it >= n_st && !wait_live(&empty[s], ph, abort, P.status, 20)) {
             live = false;
@@ -124,10 +123,12 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
           const uint32_t bar = smem_u32(&full[s]);
           const uint32_t a_s = smem_s + s * P.stage_bytes, b_s = a_s + kOgABytes;
           if (kTrans) {
-            mbar_arrive_expect_tx_s(bar, n_img * 2048u + P.b_box_rows * kOgBK * 2);
-            const uint8_t* src = P.images + (static_cast<uint64_t>(kb >> 1) * P.k_slabs + 8 * ab) * kSlabBytes +
-                                 (kb & 1u) * 2048u;
-            for (uint32_t j = 0; j < n_img; ++j) bulk_g2s_s(a_s + j * 2048u, src + j * kSlabBytes, 2048u, bar);
+            // half of each of eight images in one box.  Where the last block
+            // of k holds fewer, the box runs into the next row block's (or, at
+            // the end, is filled with zeros): rows of D that are never stored.
+            mbar_arrive_expect_tx_s(bar, kOgABytes + P.b_box_rows * kOgBK * 2);
+            tma_load_2d_s(a_s, &P.tmap_a, static_cast<int32_t>((kb & 1u) * 256u),
+                          static_cast<int32_t>((kb >> 1) * P.k_slabs + 8 * ab), bar);
           } else {
             const uint32_t cnt = min(4u, P.k_slabs - 4 * kb);
             mbar_arrive_expect_tx_s(bar, cnt * kSlabBytes + P.b_box_rows * kOgBK * 2);
@@ -194,66 +195,88 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
     __syncwarp();
   } else {
     // ======================= epilogue (warps 2-5) =======================
+    // 32 tokens at a time.  What is read of global memory for them (the old
+    // values or the addend, 32 independent loads; the tokens' factors, one a
+    // lane) is asked for before the previous 32 are stored, and for a tile's
+    // first 32 before its sums are ready.
     const uint32_t quad = warp & 3u;
     const OperandGemmOut& O = P.out;
+    const bool rmw = kTrans && O.out32 != nullptr && O.alpha != nullptr;
+    const bool adds = kTrans && O.out32 == nullptr && O.add != nullptr;
     uint32_t acc = 0;
     for (uint32_t t = blockIdx.x; t < P.n_tiles; t += gridDim.x, ++acc) {
       uint32_t ab, mb, sp, kb0, kb1;
       tile_of(t, ab, mb, sp, kb0, kb1);
       const uint32_t b = acc & 1u;
-      const bool ok = wait_live(&acc_full[b], (acc >> 1) & 1u, abort, P.status, 23, 64);
-      tc_fence_after();
       const uint32_t c = ab * kOgBM + 32 * quad + lane;  // this thread's column of the output
+      const bool c_in = c < P.out_cols;
       const uint32_t m0 = mb * P.bn;
       const uint32_t cols = min(P.bn, P.M - m0);
+      const uint64_t tile_at = static_cast<uint64_t>(m0) * O.ld + c;
+      float* out32 = O.out32 + (kTrans ? sp * O.split_stride : 0ull);
       float scale = 1.0f;
-      if (!kTrans && c < P.out_cols) {
+      if (!kTrans && c_in) {
         if (O.scale_kind == 1) scale = bf16_to_f32(__ldg(static_cast<const uint16_t*>(O.scales) + c));
         else if (O.scale_kind == 2) scale = __ldg(static_cast<const float*>(O.scales) + c);
       }
-      if (ok) {
-        for (uint32_t c0 = 0; c0 < cols; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(tmem_base + ((32 * quad) << 16) + b * 256 + c0, v);
-          const uint64_t at = static_cast<uint64_t>(m0 + c0) * O.ld + c;
-          float old[32];
-          if (kTrans && O.out32 != nullptr && O.alpha != nullptr) {
+      float old[32], my_alpha = 1.0f, my_beta = 1.0f;
+      uint32_t has = 0;  // tokens that take the addend
+      auto ask = [&](uint32_t c0) {
+        const uint32_t m = m0 + c0 + lane;
+        const bool m_in = c0 + lane < cols;
+        if (rmw) my_alpha = m_in ? __ldcg(O.alpha + m) : 0.0f;
+        if (O.beta != nullptr) my_beta = m_in ? __ldcg(O.beta + m) : 0.0f;
+        if (adds) {
+          const int32_t id = m_in ? __ldg(O.ids + m) : -1;
+          has = __ballot_sync(0xFFFFFFFFu, id >= 0 && static_cast<uint32_t>(id) < O.n_ids);
+        }
+        if (rmw || adds) {
+          const float* src = (rmw ? out32 : O.add) + tile_at + static_cast<uint64_t>(c0) * O.ld;
+          const uint32_t want = c_in ? (rmw ? (cols - c0 < 32 ? (1u << (cols - c0)) - 1u : 0xFFFFFFFFu) : has) : 0u;
 #pragma unroll
-            for (uint32_t j = 0; j < 32; ++j)
-              old[j] = (c0 + j < cols && c < P.out_cols)
-                           ? __ldcg(O.out32 + sp * O.split_stride + at + static_cast<uint64_t>(j) * O.ld) : 0.0f;
+          for (uint32_t j = 0; j < 32; ++j)
+            old[j] = (want >> j) & 1u ? __ldcg(src + static_cast<uint64_t>(j) * O.ld) : 0.0f;
+        }
+      };
+      if (kTrans) ask(0);
+      const bool ok = wait_live(&acc_full[b], (acc >> 1) & 1u, abort, P.status, 23, 64);
+      tc_fence_after();
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      for (uint32_t c0 = 0; c0 < cols; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem_base + ((32 * quad) << 16) + b * 256 + c0, v);
+        tmem_ld_wait();
+        float x[32];
+#pragma unroll
+        for (uint32_t j = 0; j < 32; ++j) {
+          x[j] = __uint_as_float(v[j]);
+          if (!kTrans) {
+            x[j] *= scale;
+          } else {
+            if (O.beta != nullptr) x[j] *= __shfl_sync(0xFFFFFFFFu, my_beta, j);
+            if (rmw) x[j] = fmaf(__shfl_sync(0xFFFFFFFFu, my_alpha, j), old[j], x[j]);
+            else if (adds) x[j] += old[j];
           }
-          tmem_ld_wait();
-          if (c < P.out_cols) {
+        }
+        if (c0 + 32 >= cols) {
+          // every column of this tile has been read: the MMAs may go on
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
+        } else if (kTrans) {
+          ask(c0 + 32);
+        }
+        const uint64_t at = tile_at + static_cast<uint64_t>(c0) * O.ld;
+        if (c_in) {
 #pragma unroll
-            for (uint32_t j = 0; j < 32; ++j) {
-              if (c0 + j >= cols) break;
-              const uint32_t m = m0 + c0 + j;
-              const uint64_t i = at + static_cast<uint64_t>(j) * O.ld;
-              float x = __uint_as_float(v[j]);
-              if (!kTrans) {
-                O.out32[i] = x * scale;
-              } else {
-                if (O.beta != nullptr) x *= __ldcg(O.beta + m);
-                if (O.out32 != nullptr) {
-                  if (O.alpha != nullptr) x = fmaf(__ldcg(O.alpha + m), old[j], x);
-                  O.out32[sp * O.split_stride + i] = x;
-                } else {
-                  if (O.add != nullptr) {
-                    const int32_t id = __ldg(O.ids + m);
-                    if (id >= 0 && static_cast<uint32_t>(id) < O.n_ids) x += __ldcg(O.add + i);
-                  }
-                  O.out16[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-                }
-              }
-            }
+          for (uint32_t j = 0; j < 32; ++j) {
+            if (c0 + j >= cols) break;
+            const uint64_t i = at + static_cast<uint64_t>(j) * O.ld;
+            if (!kTrans || O.out32 != nullptr) out32[i] = x[j];
+            else O.out16[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[b]);
-      if (!ok) break;
     }
   }
   tc_fence_before();
@@ -273,16 +296,21 @@ OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t row
   p.sms = static_cast<uint32_t>(sms);
   const uint64_t blocks = ((trans ? K : rows) + 127) / 128;
   const uint32_t n_kb = ((trans ? rows : K) + kOgBK - 1) / kOgBK;
-  // the widest token tile that still gives most SMs a tile
+  // W is read once per token tile, so the tile is as wide as the tokens go
   p.bn = 256;
-  while (p.bn > 32 && (M <= p.bn / 2 || blocks * ((M + p.bn - 1) / p.bn) * 5 < p.sms * 4ull)) p.bn /= 2;
-  const uint64_t tiles = blocks * ((M + p.bn - 1) / p.bn);
+  while (p.bn > 32 && M <= p.bn / 2) p.bn /= 2;
   p.splits = 1;
-  if (trans && tiles * 2 <= p.sms) {
-    // a range is worth its partial sums from about 8 stages on
-    p.splits = static_cast<uint32_t>(std::min<uint64_t>({p.sms / tiles, max_splits, (n_kb + 7) / 8}));
-    if (p.splits < 1) p.splits = 1;
+  if (trans) {
+    // few tiles: the sum over n is cut rather than the token tile, a range
+    // being worth its partial sums from about 8 stages on
+    const uint64_t tiles = blocks * ((M + p.bn - 1) / p.bn);
+    if (tiles * 2 <= p.sms) {
+      p.splits = static_cast<uint32_t>(std::min<uint64_t>({p.sms / tiles, max_splits, (n_kb + 7) / 8}));
+      if (p.splits < 1) p.splits = 1;
+    }
   }
+  // still few: narrower token tiles
+  while (p.bn > 32 && blocks * ((M + p.bn - 1) / p.bn) * p.splits * 5 < p.sms * 4ull && M > p.bn / 2) p.bn /= 2;
   return p;
 }
 
@@ -313,6 +341,12 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
   cudaError_t e = encode_tmap(&P.tmap_b, CU_TENSOR_MAP_DATA_TYPE_UINT16, rows16, red, plan.M,
                               static_cast<uint64_t>(red) * 2, kOgBK, P.b_box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
+  if (plan.trans) {
+    const uint64_t images_n = static_cast<uint64_t>(plan.rows / 128) * P.k_slabs;
+    e = encode_tmap(&P.tmap_a, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, images, kSlabBytes / 8, images_n, kSlabBytes, 256, 8,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e != cudaSuccess) return e;
+  }
   auto kern = plan.trans ? operand_gemm_kernel<true> : operand_gemm_kernel<false>;
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
@@ -336,11 +370,6 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
 // what is smaller is off by at most 2^-40 of it: more than a rounding to bf16
 // would keep of v * s.  Infinities and NaN pass through.
 constexpr uint32_t kPrepThreads = 256;
-__device__ __forceinline__ float prep_scale(uint32_t kind, const void* scales, uint32_t c) {
-  if (kind == 1) return bf16_to_f32(__ldg(static_cast<const uint16_t*>(scales) + c));
-  if (kind == 2) return __ldg(static_cast<const float*>(scales) + c);
-  return 1.0f;
-}
 __global__ void __launch_bounds__(kPrepThreads) row_prep_kernel(const uint16_t* __restrict__ in, uint32_t C,
                                                                 uint32_t kind, const void* scales, bool f16,
                                                                 uint16_t* __restrict__ out,
@@ -357,9 +386,19 @@ __global__ void __launch_bounds__(kPrepThreads) row_prep_kernel(const uint16_t* 
       v[2 * k] = __uint_as_float(w[k] << 16);
       v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
     }
-    if (kind == 1 || kind == 2) {
+    if (kind == 1) {
+      const uint4 s = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(scales) + c));
+      const uint32_t u[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= prep_scale(kind, scales, c + k);
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] *= __uint_as_float(u[k] << 16);
+        v[2 * k + 1] *= __uint_as_float(u[k] & 0xFFFF0000u);
+      }
+    } else if (kind == 2) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(scales) + c);
+      const float4 s = __ldg(p), r = __ldg(p + 1);
+      v[0] *= s.x; v[1] *= s.y; v[2] *= s.z; v[3] *= s.w;
+      v[4] *= r.x; v[5] *= r.y; v[6] *= r.z; v[7] *= r.w;
     }
   };
   float top = 0.0f;

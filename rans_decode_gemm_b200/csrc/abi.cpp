@@ -961,10 +961,15 @@ ans_status ans_gemm_lora(const uint16_t* d_X, uint32_t M, const ans_tiles* W, an
   // has to be zero before the first call
   const size_t base = up1024(plan.ws_bytes);
   if (ws_bytes < base + p.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
+  uint8_t* lora_ws = static_cast<uint8_t*>(d_ws) + base;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  // the adapters' first product before the base product, whose prologue (slot
+  // table, TMEM) then overlaps it
+  cudaError_t e = ansdev::launch_lora_shrink(p, A, d_X, d_ids, lora_ws, d_status, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "ans_gemm_lora");
   st = launch_planned(plan, d_X, L, true, nullptr, scale_kind, d_scales, group_k, d_Y, d_ws, d_status, stream);
   if (st != ANS_OK) return st;
-  cudaError_t e = ansdev::launch_lora_forward(p, A, d_X, d_ids, d_Y, static_cast<uint8_t*>(d_ws) + base, d_status,
-                                              reinterpret_cast<cudaStream_t>(stream));
+  e = ansdev::launch_lora_expand(p, A, d_ids, d_Y, lora_ws, cs);
   return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gemm_lora");
 }
 

@@ -3,23 +3,23 @@
 // and their gradients dh = s_a dy B_a, dx = dh A_a, dA_a = sum dh^T x,
 // dB_a = s_a sum dy^T h, a the adapter of each token.
 //
-// Tokens are grouped by adapter first (a stable counting sort), so that every
-// product has one adapter's weights as an operand.  All of them are bound by
-// memory: at rank r a token's x of K values meets r dot products, and a tile of
-// y of 64 columns takes r steps of a sum.  So the matrix instructions here are
-// the warp-wide m16n8k16 ones, whose operands come straight from registers:
-// there is no tile to stage, and the order of a sum's steps, and of output
-// columns inside a warp's block, is chosen so that every lane's share of an
-// operand is one contiguous vector load (each kernel says how).
+// Tokens are grouped by adapter first (a stable counting sort into positions,
+// each adapter's starting on a multiple of 16), so that every product has one
+// adapter's weights as an operand.  All of them are bound by memory: at rank r
+// a token's x of K values meets r dot products, and a tile of y of 64 columns
+// takes r steps of a sum.  A tile of r columns is too narrow to feed tcgen05, and
+// its tokens lie anywhere, so these are the warp-wide m16n8k16 instructions on
+// tiles that cp.async gathers, several stages ahead.
 //
 // h and dh are kept in 32 bits and enter the second product as the sum of two
-// bf16 values (16 bits of them; off by 2^-17 at most), so that the product is as
-// exact as the fp32 outputs it is added to.
+// bf16 values (16 bits of them; off by 2^-17 at most), so that the product is
+// nearly as exact as the fp32 outputs it is added to.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "launch.h"
 #include "lora.h"
@@ -29,7 +29,7 @@ namespace ansdev {
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -47,9 +47,40 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t& hi, uint16_t& lo) 
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ uint2 ldg8(const uint16_t* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
 
+// 16 bytes from global to shared memory, zeros where !in (src is then not read).
+__device__ __forceinline__ void cp16(uint32_t dst_s, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_s), "l"(src), "r"(in ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm2(uint32_t& a, uint32_t& b, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm2_t(uint32_t& a, uint32_t& b, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+               : "=r"(a), "=r"(b) : "r"(addr) : "memory");
+}
+
+// Rows of a staged tile are an odd number of 16-byte chunks apart, so that the 8
+// rows a matrix load touches lie in different banks.
+constexpr uint32_t kChunkRow = 9 * 16;  // 64 values and one chunk
+__host__ __device__ constexpr uint32_t odd_row(uint32_t cols) { return ((cols / 8) | 1u) * 16u; }
+constexpr uint32_t kNoToken = 0xFFFFFFFFu;
+
 // ---- grouping -----------------------------------------------------------------
 // One CTA; warp w takes a contiguous range of tokens, so the order inside an
-// adapter is the tokens' own.
+// adapter is the tokens' own.  Positions up to the adapter's next multiple of 16
+// hold no token.
 __global__ void __launch_bounds__(1024) lora_group_kernel(const int32_t* __restrict__ ids, uint32_t M, uint32_t n,
                                                           uint32_t tm, LoraGroups G, uint32_t* status) {
   __shared__ uint32_t cnt[32][kLoraMaxAdapters];
@@ -88,19 +119,20 @@ __global__ void __launch_bounds__(1024) lora_group_kernel(const int32_t* __restr
   if (threadIdx.x < n) {
     uint32_t at = 0, tile = 0;
     for (uint32_t a = 0; a < threadIdx.x; ++a) {
-      at += total[a];
+      at += (total[a] + 15) / 16 * 16;
       tile += (total[a] + tm - 1) / tm;
     }
-    const uint32_t mine = total[threadIdx.x];
+    const uint32_t mine = total[threadIdx.x], padded = (mine + 15) / 16 * 16;
     start[threadIdx.x] = at;
     G.off[threadIdx.x] = at;
     for (uint32_t i = 0; i < mine; i += tm, ++tile) {
       G.tile_adapter[tile] = threadIdx.x;
       G.tile_start[tile] = at + i;
-      G.tile_count[tile] = min(tm, mine - i);
+      G.tile_count[tile] = min(tm, padded - i);
     }
+    for (uint32_t i = mine; i < padded; ++i) G.perm[at + i] = kNoToken;
     if (threadIdx.x == n - 1) {
-      G.off[n] = at + mine;
+      G.off[n] = at + padded;
       *G.n_tiles = tile;
     }
   }
@@ -118,163 +150,221 @@ __global__ void __launch_bounds__(1024) lora_group_kernel(const int32_t* __restr
   }
 }
 
+// Few tokens: a tile is found without the grouping kernel.  Token m leads a tile
+// when a multiple of 16 tokens of its adapter precede it; the tile is m and the
+// next 15 of them.  One warp counts and collects them 32 tokens at a time (the
+// others wait); false where m leads none.  `bad` is set for an index past the
+// adapters.
+struct FewTile {
+  uint32_t adapter, count;
+};
+__device__ __forceinline__ bool few_tile(const int32_t* __restrict__ ids, uint32_t M, uint32_t n, uint32_t m,
+                                         uint32_t (&tok)[16], uint32_t& found_s, FewTile& tile, bool& bad) {
+  const int32_t id = __ldg(ids + m);
+  bad = id >= static_cast<int32_t>(n);
+  if (id < 0 || bad) return false;
+  if (threadIdx.x < 32) {
+    const uint32_t lane = threadIdx.x;
+    uint32_t before = 0, found = 0;
+    for (uint32_t b = 0; b < M && found < 16; b += 32) {
+      const bool mine = b + lane < M && __ldg(ids + b + lane) == id;
+      const uint32_t same = __ballot_sync(0xFFFFFFFFu, mine);
+      const uint32_t from = m <= b ? 0xFFFFFFFFu : m >= b + 32 ? 0u : 0xFFFFFFFFu << (m - b);  // tokens from m on
+      before += __popc(same & ~from);
+      const uint32_t at = found + __popc(same & from & lanemask_lt());
+      if (mine && (from >> lane) & 1u && at < 16) tok[at] = b + lane;
+      found += __popc(same & from);
+    }
+    if (lane == 0) found_s = before % 16 == 0 ? min(16u, found) : 0u;
+  }
+  __syncthreads();
+  tile.adapter = static_cast<uint32_t>(id);
+  tile.count = found_s;
+  return tile.count != 0;
+}
+
 // ---- shrink: a token's C values against rank rows or columns -------------------
 // part[split][p][j] = sum over the split's range of c of in[perm[p]][c] * w,
-// w = A[j][c] (kCols false) or B[c][j] (kCols true).  A CTA takes one tile of
-// tokens (16 or 64) and one range; its 8 warps share the token groups of 16 and
-// interleave the range's steps of 32, and are summed in warp order.
-constexpr uint32_t kShrinkThreads = 256;
+// w = A[j][c] (kCols false) or B[c][j] (kCols true).  A CTA takes one tile of 16
+// or 64 positions and one range; a stage is 64 values of c for all of them and
+// their weights.  With 64 positions each of the 4 warps has 16 of them; with 16,
+// each has a quarter of the stage's sum, and the warps are added in order.
+constexpr uint32_t kShrinkThreads = 128, kShrinkStages = 4;
 
 struct ShrinkDev {
   LoraGroups G;
   const uint16_t* in;       // M x C
   const uint16_t* weights;  // adapter a at a * C * rank
-  float* part;              // split x M x rank
-  uint32_t C, rank, M, groups;  // groups: token groups of 16 in a tile (1 or 4)
+  float* part;              // split x positions x rank
+  uint64_t part_stride;     // positions x rank
+  uint32_t C, rank, groups; // groups: 16-position groups of a tile (1 or 4)
   uint32_t len;
+  // few tokens: tile m is the one that token m leads, and rows of part are tokens
+  const int32_t* ids;
+  uint32_t* status;
+  uint32_t M, n;
 };
 
-// Both operands are contiguous along the sum, so lane (g, t) takes values
-// 8t .. 8t + 7 of every 32 from its rows; the same 8 serve two instructions, and
-// both operands agree on which step of the sum each value is.
-template <int NJ>
-__device__ __forceinline__ void shrink_rows(const ShrinkDev& P, const uint16_t* x0, const uint16_t* x1,
-                                            const uint16_t* w, uint32_t c_begin, uint32_t c_end, uint32_t step,
-                                            uint32_t g, uint32_t t, float* red) {
-  float acc[NJ][4] = {};
+__host__ __device__ constexpr uint32_t shrink_w_bytes(bool cols, uint32_t rank) {
+  return cols ? 64 * odd_row(rank) : rank * kChunkRow;
+}
+
+template <bool kCols, bool kFew, int NJ>
+__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __grid_constant__ ShrinkDev P) {
+  extern __shared__ __align__(128) uint8_t stages_smem[];
+  __shared__ uint32_t tok[16], found;
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t tile = blockIdx.x;
+  uint32_t a, start = 0, count;
+  if constexpr (kFew) {
+    FewTile ft;
+    bool bad;
+    const bool leads = few_tile(P.ids, P.M, P.n, tile, tok, found, ft, bad);
+    if (bad && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(P.status, kStatusBadIndex);
+    if (!leads) return;
+    a = ft.adapter;
+    count = ft.count;
+  } else {
+    if (tile >= __ldcg(P.G.n_tiles)) return;
+    a = __ldcg(P.G.tile_adapter + tile);
+    start = __ldcg(P.G.tile_start + tile);
+    count = __ldcg(P.G.tile_count + tile);
+  }
+  const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const uint32_t c_begin = blockIdx.y * P.len, c_end = min(P.C, c_begin + P.len);
+  const uint32_t x_bytes = 16 * P.groups * kChunkRow, stage = x_bytes + shrink_w_bytes(kCols, P.rank);
+  const uint32_t base = smem_u32(stages_smem);
   const uint32_t nj = P.rank / 8;
-  for (uint32_t c0 = c_begin; c0 < c_end; c0 += step) {
-    const uint32_t c = c0 + 8 * t;
-    const bool in = c < c_end;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 a = in && x0 ? ldg16(x0 + c) : zero, b = in && x1 ? ldg16(x1 + c) : zero;
+  const uint16_t* w = P.weights + static_cast<uint64_t>(a) * P.C * P.rank;
+  // this thread's rows of x: tid / 8 of each group, chunk tid % 8
+  const uint16_t* x[4];
+  bool x_in[4];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      if (j < nj) {
-        const uint4 v = in ? ldg16(w + static_cast<uint64_t>(8 * j + g) * P.C + c) : zero;
-        mma_bf16(acc[j], a.x, b.x, a.y, b.y, v.x, v.y);
-        mma_bf16(acc[j], a.z, b.z, a.w, b.w, v.z, v.w);
+  for (uint32_t i = 0; i < 4; ++i) {
+    const uint32_t row = tid / 8 + 16 * i;
+    uint32_t m = kNoToken;
+    if (i < P.groups && row < count) m = kFew ? tok[row] : __ldcg(P.G.perm + start + row);
+    x_in[i] = m != kNoToken;
+    x[i] = P.in + (x_in[i] ? static_cast<uint64_t>(m) * P.C : 0ull);
+  }
+  auto load = [&](uint32_t slot, uint32_t c0) {
+    const uint32_t xs = base + slot * stage, wsm = xs + x_bytes;
+    const uint32_t c = c0 + 8 * (tid % 8);
+    const bool in = c < c_end;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+      if (i < P.groups)
+        cp16(xs + (tid / 8 + 16 * i) * kChunkRow + (tid % 8) * 16, x[i] + (in ? c : 0u), in && x_in[i]);
+    if constexpr (!kCols) {
+      for (uint32_t j = tid / 8; j < P.rank; j += 16)
+        cp16(wsm + j * kChunkRow + (tid % 8) * 16, w + (in ? static_cast<uint64_t>(j) * P.C + c : 0ull), in);
+    } else {
+      const uint32_t pitch = odd_row(P.rank);
+      for (uint32_t i = tid; i < 64 * nj; i += kShrinkThreads) {
+        const uint32_t row = i / nj, q = i - row * nj;
+        const bool r_in = c0 + row < c_end;
+        cp16(wsm + row * pitch + q * 16, w + (r_in ? static_cast<uint64_t>(c0 + row) * P.rank + 8 * q : 0ull), r_in);
+      }
+    }
+  };
+  const uint32_t n_steps = c_end > c_begin ? (c_end - c_begin + 63) / 64 : 0u;
+#pragma unroll
+  for (uint32_t i = 0; i + 1 < kShrinkStages; ++i) {
+    if (i < n_steps) load(i, c_begin + 64 * i);
+    cp_commit();
+  }
+  float acc[NJ][4] = {};
+  const uint32_t row0 = P.groups == 4 ? 16 * warp : 0u;
+  const uint32_t ks0 = P.groups == 4 ? 0u : warp, ks1 = P.groups == 4 ? 4u : warp + 1;
+  for (uint32_t it = 0; it < n_steps; ++it) {
+    cp_wait<kShrinkStages - 2>();
+    __syncthreads();
+    if (it + kShrinkStages - 1 < n_steps) load((it + kShrinkStages - 1) % kShrinkStages, c_begin + 64 * (it + kShrinkStages - 1));
+    cp_commit();
+    const uint32_t xs = base + (it % kShrinkStages) * stage, wsm = xs + x_bytes;
+    if (row0 >= count) continue;  // this warp's group is empty
+    for (uint32_t ks = ks0; ks < ks1; ++ks) {
+      uint32_t f[4];
+      ldsm4(f, xs + (row0 + (lane & 15u)) * kChunkRow + (2 * ks + (lane >> 4)) * 16);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        if (j < nj) {
+          uint32_t b0, b1;
+          if constexpr (!kCols) ldsm2(b0, b1, wsm + (8 * j + (lane & 7u)) * kChunkRow + (2 * ks + ((lane >> 3) & 1u)) * 16);
+          else ldsm2_t(b0, b1, wsm + (16 * ks + (lane & 15u)) * odd_row(P.rank) + j * 16);
+          mma_bf16(acc[j], f[0], f[1], f[2], f[3], b0, b1);
+        }
       }
     }
   }
+  float* out = P.part + blockIdx.y * P.part_stride + static_cast<uint64_t>(start) * P.rank;
+  if (P.groups == 4) {
+    if (row0 >= count) return;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if (j < nj) {
+        float* r = out + static_cast<uint64_t>(row0 + g) * P.rank + 8 * j + 2 * t;
+        *reinterpret_cast<float2*>(r) = make_float2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<float2*>(r + 8 * P.rank) = make_float2(acc[j][2], acc[j][3]);
+      }
+    }
+    return;
+  }
+  cp_wait<0>();
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(stages_smem);  // 4 warps x 16 x rank
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     if (j < nj) {
-      float* r = red + g * P.rank + 8 * j + 2 * t;
+      float* r = red + (16 * warp + g) * P.rank + 8 * j + 2 * t;
       r[0] = acc[j][0];
       r[1] = acc[j][1];
       r[8 * P.rank] = acc[j][2];
       r[8 * P.rank + 1] = acc[j][3];
     }
   }
-}
-
-// W consecutive bf16 of a row, as W / 2 (at least one) registers.
-template <int W>
-struct RowVec { uint32_t v[W / 2]; };
-template <>
-struct RowVec<1> { uint32_t v[1]; };
-template <int W>
-__device__ __forceinline__ RowVec<W> load_row(const uint16_t* p) {
-  RowVec<W> r;
-  if constexpr (W == 1) {
-    r.v[0] = __ldg(p);
-  } else if constexpr (W == 2) {
-    r.v[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  } else if constexpr (W == 4) {
-    const uint2 q = ldg8(p);
-    r.v[0] = q.x; r.v[1] = q.y;
-  } else {
-    const uint4 q = ldg16(p);
-    r.v[0] = q.x; r.v[1] = q.y; r.v[2] = q.z; r.v[3] = q.w;
-  }
-  return r;
-}
-// Element j of two rows as one register (row a low).
-template <int W>
-__device__ __forceinline__ uint32_t pair_of(const RowVec<W>& a, const RowVec<W>& b, int j) {
-  return __byte_perm(a.v[j / 2], b.v[j / 2], (j & 1) ? 0x7632u : 0x5410u);
-}
-
-// The weights' rows run along the rank, so lane (g, t) takes W consecutive
-// columns g W .. of each of the 8 rows 8t .. 8t + 7 of every 32, and pairs of rows
-// are put together in registers: column j of instruction i is g W + i.
-// One block of 8 W columns from `col` on.  (N and the ranges are multiples of
-// 32.)
-template <int W>
-__device__ __forceinline__ void shrink_cols(const ShrinkDev& P, const uint16_t* x0, const uint16_t* x1,
-                                            const uint16_t* w, uint32_t col, uint32_t c_begin, uint32_t c_end,
-                                            uint32_t step, uint32_t g, uint32_t t, float* red) {
-  float acc[W][4] = {};
-  for (uint32_t c0 = c_begin; c0 < c_end; c0 += step) {
-    const uint32_t c = c0 + 8 * t;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const uint4 a = x0 ? ldg16(x0 + c) : zero, b = x1 ? ldg16(x1 + c) : zero;
-    RowVec<W> r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = load_row<W>(w + static_cast<uint64_t>(c + i) * P.rank + col + g * W);
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      mma_bf16(acc[j], a.x, b.x, a.y, b.y, pair_of<W>(r[0], r[1], j), pair_of<W>(r[2], r[3], j));
-      mma_bf16(acc[j], a.z, b.z, a.w, b.w, pair_of<W>(r[4], r[5], j), pair_of<W>(r[6], r[7], j));
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float* q = red + g * P.rank + col + 2 * t * W + j;
-    q[0] = acc[j][0];
-    q[W] = acc[j][1];
-    q[8 * P.rank] = acc[j][2];
-    q[8 * P.rank + W] = acc[j][3];
-  }
-}
-
-template <bool kCols, int NJ>
-__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __grid_constant__ ShrinkDev P) {
-  extern __shared__ float red[];  // 8 warps x 16 tokens x rank
-  griddep_wait();
-  griddep_launch_dependents();
-  const uint32_t tile = blockIdx.x;
-  if (tile >= __ldcg(P.G.n_tiles)) return;
-  const uint32_t a = __ldcg(P.G.tile_adapter + tile), start = __ldcg(P.G.tile_start + tile),
-                 count = __ldcg(P.G.tile_count + tile);
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const uint32_t grp = warp % P.groups, kw = warp / P.groups, n_kw = 8 / P.groups;
-  const uint32_t c_begin = blockIdx.y * P.len, c_end = min(P.C, c_begin + P.len);
-  const uint32_t r0 = grp * 16 + g, r1 = r0 + 8;
-  const uint16_t* x0 = r0 < count ? P.in + static_cast<uint64_t>(__ldcg(P.G.perm + start + r0)) * P.C : nullptr;
-  const uint16_t* x1 = r1 < count ? P.in + static_cast<uint64_t>(__ldcg(P.G.perm + start + r1)) * P.C : nullptr;
-  const uint16_t* w = P.weights + static_cast<uint64_t>(a) * P.C * P.rank;
-  float* mine = red + warp * 16 * P.rank;
-  const uint32_t first = c_begin + kw * 32, step = n_kw * 32;
-  if constexpr (kCols) {
-    // the rank in blocks of 64, 32, 16 and 8 columns
-    for (uint32_t col = 0; col < P.rank;) {
-      const uint32_t rest = P.rank - col;
-      if (rest >= 64) { shrink_cols<8>(P, x0, x1, w, col, first, c_end, step, g, t, mine); col += 64; }
-      else if (rest >= 32) { shrink_cols<4>(P, x0, x1, w, col, first, c_end, step, g, t, mine); col += 32; }
-      else if (rest >= 16) { shrink_cols<2>(P, x0, x1, w, col, first, c_end, step, g, t, mine); col += 16; }
-      else { shrink_cols<1>(P, x0, x1, w, col, first, c_end, step, g, t, mine); col += 8; }
-    }
-  } else {
-    shrink_rows<NJ>(P, x0, x1, w, first, c_end, step, g, t, mine);
-  }
   __syncthreads();
   const uint32_t per = 16 * P.rank;
-  for (uint32_t i = threadIdx.x; i < P.groups * per; i += kShrinkThreads) {
-    const uint32_t row = i / P.rank;
-    if (row >= count) break;
-    const uint32_t gi = i / per, at = i - gi * per;
-    float s = 0.0f;
-    for (uint32_t q = 0; q < n_kw; ++q) s += red[(q * P.groups + gi) * per + at];
-    P.part[(static_cast<uint64_t>(blockIdx.y) * P.M + start + row) * P.rank + (i - row * P.rank)] = s;
+  for (uint32_t i = tid; i < count * P.rank; i += kShrinkThreads) {
+    const float v = ((red[i] + red[per + i]) + red[2 * per + i]) + red[3 * per + i];
+    if constexpr (kFew) out[static_cast<uint64_t>(tok[i / P.rank]) * P.rank + i % P.rank] = v;
+    else out[i] = v;
   }
 }
 
-// h[p][j] = s_a * sum over the splits, in order.
-__global__ void __launch_bounds__(256) lora_sum_kernel(LoraGroups G, const float* __restrict__ part, uint32_t splits,
-                                                       uint32_t M, uint32_t rank, const float* scale,
-                                                       float* __restrict__ h) {
+// Four neighbouring sums over the splits, in order, 8 loads in flight.
+__device__ __forceinline__ float4 sum_parts(const float* p, uint32_t splits, uint64_t stride) {
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (uint32_t q0 = 0; q0 < splits; q0 += 8) {
+    float4 u[8];
+#pragma unroll
+    for (uint32_t q = 0; q < 8; ++q)
+      u[q] = q0 + q < splits ? __ldcg(reinterpret_cast<const float4*>(p + (q0 + q) * stride))
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (uint32_t q = 0; q < 8; ++q) {
+      v.x += u[q].x; v.y += u[q].y; v.z += u[q].z; v.w += u[q].w;
+    }
+  }
+  return v;
+}
+// Four values times s as their two bf16 parts (hi and lo 8-byte aligned).
+__device__ __forceinline__ void split4(const float4& v, float s, uint16_t* hi, uint16_t* lo) {
+  uint16_t h[4], l[4];
+  split_bf16(v.x * s, h[0], l[0]);
+  split_bf16(v.y * s, h[1], l[1]);
+  split_bf16(v.z * s, h[2], l[2]);
+  split_bf16(v.w * s, h[3], l[3]);
+  *reinterpret_cast<uint2*>(hi) = make_uint2(h[0] | (uint32_t(h[1]) << 16), h[2] | (uint32_t(h[3]) << 16));
+  *reinterpret_cast<uint2*>(lo) = make_uint2(l[0] | (uint32_t(l[1]) << 16), l[2] | (uint32_t(l[3]) << 16));
+}
+
+// The splits' sums, in order, times s_a, as two bf16 parts: hp[part][p][j], rows
+// of r16 values (zeros from the rank on).
+__global__ void __launch_bounds__(256) lora_join_kernel(LoraGroups G, const float* __restrict__ part, uint32_t splits,
+                                                        uint64_t part_stride, uint32_t rank, const float* scale,
+                                                        uint16_t* __restrict__ hp, uint64_t hp_stride) {
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t tile = blockIdx.x;
@@ -282,60 +372,138 @@ __global__ void __launch_bounds__(256) lora_sum_kernel(LoraGroups G, const float
   const uint32_t a = __ldcg(G.tile_adapter + tile), start = __ldcg(G.tile_start + tile),
                  count = __ldcg(G.tile_count + tile);
   const float s = scale != nullptr ? __ldg(scale + a) : 1.0f;
-  const uint64_t base = static_cast<uint64_t>(start) * rank;
-  for (uint32_t i = threadIdx.x; i < count * rank; i += 256) {
-    float v = 0.0f;
-    for (uint32_t q = 0; q < splits; ++q) v += __ldcg(part + static_cast<uint64_t>(q) * M * rank + base + i);
-    h[base + i] = v * s;
+  const uint32_t r16 = (rank + 15) / 16 * 16;
+  const uint32_t per = r16 / 4;
+  for (uint32_t i = blockIdx.y * 256 + threadIdx.x; i < count * per; i += 256 * gridDim.y) {
+    const uint32_t row = i / per, j = 4 * (i - row * per);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (j < rank) v = sum_parts(part + static_cast<uint64_t>(start + row) * rank + j, splits, part_stride);
+    const uint64_t at = static_cast<uint64_t>(start + row) * r16 + j;
+    split4(v, s, hp + at, hp + hp_stride + at);
   }
+}
+
+// 8 consecutive bf16 of a row; element j of two rows as one register (row a low).
+struct Row8 { uint32_t v[4]; };
+__device__ __forceinline__ Row8 load_row8(const uint16_t* p, bool in) {
+  const uint4 q = in ? ldg16(p) : make_uint4(0, 0, 0, 0);
+  return Row8{{q.x, q.y, q.z, q.w}};
+}
+__device__ __forceinline__ uint32_t pair_of(const Row8& a, const Row8& b, int j) {
+  return __byte_perm(a.v[j / 2], b.v[j / 2], (j & 1) ? 0x7632u : 0x5410u);
 }
 
 // ---- expand: rank values of a token against C outputs --------------------------
 // kCols false: out[m][c] += sum_j h[p][j] * B[c][j];  kCols true: out[m][c] =
-// sum_j h[p][j] * A[j][c].  A warp takes 64 columns of a tile's tokens; lane
-// (g, t) holds columns g 8 + i of instruction i, so that the sums it ends with
-// are columns 16 t .. 16 t + 15 of its rows: four 16-byte accesses a row.
+// sum_j h[p][j] * A[j][c].  A warp takes 64 columns of a tile's tokens.  Column
+// g 8 + i of the 64 is column g of instruction i, so that what lane (g, t) ends
+// with is columns 16 t .. 16 t + 15 of its rows: four 16-byte accesses a row.
+// Along the sum lane t has steps 4 t .. 4 t + 3 of every 16, in both operands.
+// Up to rank 64 the warp's weights stay in registers for all of the tile's
+// tokens (kSteps blocks of 16 ranks); above, they are read again for every 16
+// tokens (kSteps 0).
 struct ExpandDev {
   LoraGroups G;
-  const float* h;           // splits x M x rank
-  const float* scale;       // per adapter, or null: 1
+  const float* part;        // few tokens: sums of the shrink (splits x M x rank)
+  const uint16_t* hp;       // else: their two bf16 parts, joined and scaled
+  uint64_t part_stride, hp_stride;
+  const float* scale;       // of the sums: per adapter, or null: 1
   const uint16_t* weights;  // adapter a at a * C * rank
   float* out;               // M x C
-  uint32_t C, rank, M, splits, tm;
+  uint32_t C, rank, splits, tm;
+  const int32_t* ids;       // few tokens (see ShrinkDev)
+  uint32_t M, n;
 };
 
 template <bool kCols>
-__global__ void __launch_bounds__(256) lora_expand_kernel(const __grid_constant__ ExpandDev P) {
+__device__ __forceinline__ void expand_weights(const ExpandDev& P, const uint16_t* w, uint32_t c0, uint32_t k, uint32_t g,
+                                               uint32_t t, uint32_t (&b)[8][2]) {
+  const uint32_t j = k + 4 * t;  // this lane's steps of the sum
+  if constexpr (!kCols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint2 v = j < P.rank ? ldg8(w + static_cast<uint64_t>(c0 + g * 8 + i) * P.rank + j) : make_uint2(0, 0);
+      b[i][0] = v.x;
+      b[i][1] = v.y;
+    }
+  } else {
+    const bool in = j < P.rank && c0 + g * 8 < P.C;  // (the rank is a multiple of 8)
+    const uint16_t* p = w + (in ? static_cast<uint64_t>(j) * P.C + c0 + g * 8 : 0ull);
+    const Row8 v0 = load_row8(p, in), v1 = load_row8(p + P.C, in), v2 = load_row8(p + 2ull * P.C, in),
+               v3 = load_row8(p + 3ull * P.C, in);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      b[i][0] = pair_of(v0, v1, i);
+      b[i][1] = pair_of(v2, v3, i);
+    }
+  }
+}
+
+template <bool kCols, bool kFew, int kSteps>
+__global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant__ ExpandDev P) {
   extern __shared__ __align__(16) uint16_t hs[];  // hi then lo: tm x pitch
-  griddep_wait();
-  griddep_launch_dependents();
+  __shared__ uint32_t tok[16], found;
   const uint32_t tile = blockIdx.x;
-  if (tile >= __ldcg(P.G.n_tiles)) return;
-  const uint32_t a = __ldcg(P.G.tile_adapter + tile), start = __ldcg(P.G.tile_start + tile),
-                 count = __ldcg(P.G.tile_count + tile);
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const uint32_t r16 = (P.rank + 15) / 16 * 16, pitch = r16 + 8;
   uint16_t* lo_s = hs + P.tm * pitch;
-  const float s = P.scale != nullptr ? __ldg(P.scale + a) : 1.0f;
-  const uint32_t rows = (count + 15) / 16 * 16;
-  for (uint32_t i = threadIdx.x; i < rows * r16; i += blockDim.x) {
-    const uint32_t row = i / r16, j = i - row * r16;
-    float v = 0.0f;
-    if (row < count && j < P.rank)
-      for (uint32_t q = 0; q < P.splits; ++q)
-        v += __ldcg(P.h + (static_cast<uint64_t>(q) * P.M + start + row) * P.rank + j);
-    split_bf16(v * s, hs[row * pitch + j], lo_s[row * pitch + j]);
+  const uint32_t c0 = (blockIdx.y * (blockDim.x / 32) + warp) * 64;
+  uint32_t b[kSteps > 0 ? kSteps : 1][8][2];
+  uint32_t a, start = 0, count;
+  griddep_wait();
+  griddep_launch_dependents();
+  if constexpr (kFew) {
+    FewTile ft;
+    bool bad;
+    if (!few_tile(P.ids, P.M, P.n, tile, tok, found, ft, bad)) return;
+    a = ft.adapter;
+    count = 16;
+  } else {
+    if (tile >= __ldcg(P.G.n_tiles)) return;
+    a = __ldcg(P.G.tile_adapter + tile);
+    start = __ldcg(P.G.tile_start + tile);
+    count = __ldcg(P.G.tile_count + tile);
+  }
+  const uint16_t* w = P.weights + static_cast<uint64_t>(a) * P.C * P.rank;
+  if (c0 < P.C) {
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) expand_weights<kCols>(P, w, c0, 16 * q, g, t, b[q]);
+  }
+  if constexpr (!kFew) {
+    const uint32_t per = r16 / 8;
+    for (uint32_t i = threadIdx.x; i < 2 * count * per; i += blockDim.x) {
+      const uint32_t part = i >= count * per ? 1u : 0u, k = i - part * count * per;
+      const uint32_t row = k / per, q = k - row * per;
+      *reinterpret_cast<uint4*>((part ? lo_s : hs) + row * pitch + 8 * q) = __ldcg(reinterpret_cast<const uint4*>(
+          P.hp + part * P.hp_stride + static_cast<uint64_t>(start + row) * r16 + 8 * q));
+    }
+  } else {
+    const float s = P.scale != nullptr ? __ldg(P.scale + a) : 1.0f;
+    const uint32_t per = r16 / 4;
+    for (uint32_t i = threadIdx.x; i < 16 * per; i += blockDim.x) {
+      const uint32_t row = i / per, j = 4 * (i - row * per);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (j < P.rank && row < found)
+        v = sum_parts(P.part + static_cast<uint64_t>(tok[row]) * P.rank + j, P.splits, P.part_stride);
+      split4(v, s, hs + row * pitch + j, lo_s + row * pitch + j);
+    }
   }
   __syncthreads();
-  const uint32_t c0 = (blockIdx.y * (blockDim.x / 32) + warp) * 64;
   if (c0 >= P.C) return;
-  const uint16_t* w = P.weights + static_cast<uint64_t>(a) * P.C * P.rank;
   const uint32_t cl = c0 + 16 * t;  // this lane's output columns
   const bool col_in = cl < P.C;
-  for (uint32_t r = 0; r < rows; r += 16) {
-    const bool v0 = r + g < count && col_in, v1 = r + g + 8 < count && col_in;
-    float* y0 = v0 ? P.out + static_cast<uint64_t>(__ldcg(P.G.perm + start + r + g)) * P.C + cl : nullptr;
-    float* y1 = v1 ? P.out + static_cast<uint64_t>(__ldcg(P.G.perm + start + r + g + 8)) * P.C + cl : nullptr;
+  for (uint32_t r = 0; r < count; r += 16) {
+    uint32_t m0, m1;
+    if constexpr (kFew) {
+      m0 = g < found ? tok[g] : kNoToken;
+      m1 = g + 8 < found ? tok[g + 8] : kNoToken;
+    } else {
+      m0 = __ldcg(P.G.perm + start + r + g);
+      m1 = __ldcg(P.G.perm + start + r + g + 8);
+    }
+    const bool v0 = m0 != kNoToken && col_in, v1 = m1 != kNoToken && col_in;
+    float* y0 = P.out + (v0 ? static_cast<uint64_t>(m0) * P.C + cl : 0ull);
+    float* y1 = P.out + (v1 ? static_cast<uint64_t>(m1) * P.C + cl : 0ull);
     float4 o0[4], o1[4];
     if constexpr (!kCols) {
 #pragma unroll
@@ -346,31 +514,24 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(const __grid_constant_
     }
     float acc[8][4] = {};
     const uint32_t h0 = (r + g) * pitch + 4 * t, h1 = h0 + 8 * pitch;
-    for (uint32_t k = 0; k < r16; k += 16) {
+    auto step = [&](uint32_t k, const uint32_t (&bk)[8][2]) {
       const uint2 a0 = *reinterpret_cast<const uint2*>(hs + h0 + k), a1 = *reinterpret_cast<const uint2*>(hs + h1 + k);
       const uint2 l0 = *reinterpret_cast<const uint2*>(lo_s + h0 + k),
                   l1 = *reinterpret_cast<const uint2*>(lo_s + h1 + k);
-      const uint32_t j = k + 4 * t;  // this lane's steps of the sum
-      if constexpr (!kCols) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint2 b = j < P.rank ? ldg8(w + static_cast<uint64_t>(c0 + g * 8 + i) * P.rank + j) : make_uint2(0, 0);
-          mma_bf16(acc[i], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-          mma_bf16(acc[i], l0.x, l1.x, l0.y, l1.y, b.x, b.y);
-        }
-      } else {
-        RowVec<8> v[4];
+      for (int i = 0; i < 8; ++i) {
+        mma_bf16(acc[i], a0.x, a1.x, a0.y, a1.y, bk[i][0], bk[i][1]);
+        mma_bf16(acc[i], l0.x, l1.x, l0.y, l1.y, bk[i][0], bk[i][1]);
+      }
+    };
+    if constexpr (kSteps > 0) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          v[q] = RowVec<8>{};
-          if (j + q < P.rank && c0 + g * 8 < P.C) v[q] = load_row<8>(w + static_cast<uint64_t>(j + q) * P.C + c0 + g * 8);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t b0 = pair_of<8>(v[0], v[1], i), b1 = pair_of<8>(v[2], v[3], i);
-          mma_bf16(acc[i], a0.x, a1.x, a0.y, a1.y, b0, b1);
-          mma_bf16(acc[i], l0.x, l1.x, l0.y, l1.y, b0, b1);
-        }
+      for (int q = 0; q < kSteps; ++q)
+        if (16u * q < r16) step(16 * q, b[q]);
+    } else {
+      for (uint32_t k = 0; k < r16; k += 16) {
+        expand_weights<kCols>(P, w, c0, k, g, t, b[0]);
+        step(k, b[0]);
       }
     }
     // columns 16 t + i (c0 of instruction i) and 16 t + 8 + i (c1)
@@ -391,108 +552,111 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(const __grid_constant_
 
 // ---- outer: the sum over an adapter's tokens of z^T t ---------------------------
 // out[c][j] = sum_p z[perm[p]][c] * h[p][j] for one adapter, in dB's layout (C x
-// rank) or dA's (rank x C, kRankMajor).  A CTA takes 64 columns c; its 8 warps
-// share the blocks of 32 ranks and split the tokens, 16 a step.  Lane (g, t)
-// loads columns 8 g .. 8 g + 7 of tokens 4 t .. 4 t + 3 (16 bytes each) and
-// puts pairs of tokens together in registers; h comes from shared memory,
-// transposed, as hi + lo.
-constexpr uint32_t kOuterThreads = 256, kOuterTokens = 128;
-constexpr uint32_t kOuterPitch = kOuterTokens + 8;
+// rank) or dA's (rank x C, kRankMajor).  A CTA takes 64 columns c, 16 a warp, and
+// all ranks; a stage is 64 positions of z and of h's two parts, both read by
+// transposing matrix loads.
+constexpr uint32_t kOuterThreads = 128, kOuterStages = 3;
 
 struct OuterDev {
   LoraGroups G;
-  const uint16_t* z;  // M x C
-  const float* h;     // M x rank
+  const uint16_t* z;   // M x C
+  const uint16_t* hp;  // 2 x positions x r16
+  uint64_t hp_stride;
   float* out;
-  uint32_t C, rank, jblocks;  // blocks of 32 ranks, rounded up to a power of two
+  uint32_t C, rank;
 };
+__host__ __device__ constexpr uint32_t outer_stage_bytes(uint32_t r16) { return 64 * kChunkRow + 2 * 64 * odd_row(r16); }
 
-template <bool kRankMajor>
+template <bool kRankMajor, int NJ>
 __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const __grid_constant__ OuterDev P) {
-  extern __shared__ __align__(16) uint8_t outer_smem[];
-  uint16_t* hi_s = reinterpret_cast<uint16_t*>(outer_smem);  // rank x pitch
-  uint16_t* lo_s = hi_s + P.rank * kOuterPitch;
-  float* red = reinterpret_cast<float*>(outer_smem);         // 8 warps x 64 x 32, after the last step
+  extern __shared__ __align__(128) uint8_t stages_smem[];
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t a = blockIdx.y, c0 = blockIdx.x * 64;
   const uint32_t p_begin = __ldcg(P.G.off + a), p_end = __ldcg(P.G.off + a + 1);
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const uint32_t jb = warp % P.jblocks, tw = warp / P.jblocks, n_tw = 8 / P.jblocks;
-  const uint32_t nj = min(4u, P.rank > 32 * jb ? (P.rank - 32 * jb) / 8 : 0u);
-  const bool col_in = c0 + 8 * g < P.C;
-  float acc[4][4][4] = {};  // pairs of columns, rank blocks of 8
-  for (uint32_t p0 = p_begin; p0 < p_end; p0 += kOuterTokens) {
-    const uint32_t n_tok = min(kOuterTokens, p_end - p0);
-    const uint32_t n16 = (n_tok + 15) / 16 * 16;
-    __syncthreads();
-    for (uint32_t i = threadIdx.x; i < n16 * P.rank; i += kOuterThreads) {
-      const uint32_t p = i / P.rank, j = i - p * P.rank;
-      const float v = p < n_tok ? __ldcg(P.h + static_cast<uint64_t>(p0 + p) * P.rank + j) : 0.0f;
-      split_bf16(v, hi_s[j * kOuterPitch + p], lo_s[j * kOuterPitch + p]);
+  const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const uint32_t r16 = (P.rank + 15) / 16 * 16, nj = P.rank / 8;
+  const uint32_t h_row = odd_row(r16), h_bytes = 64 * h_row, stage = outer_stage_bytes(r16);
+  const uint32_t base = smem_u32(stages_smem);
+  const bool col_in = c0 + 8 * (tid % 8) < P.C;
+  auto load = [&](uint32_t slot, uint32_t p0) {
+    const uint32_t zs = base + slot * stage, hsm = zs + 64 * kChunkRow;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t row = tid / 8 + 16 * i;
+      const uint32_t m = p0 + row < p_end ? __ldcg(P.G.perm + p0 + row) : kNoToken;
+      const bool in = m != kNoToken && col_in;
+      cp16(zs + row * kChunkRow + (tid % 8) * 16, P.z + (in ? static_cast<uint64_t>(m) * P.C + c0 + 8 * (tid % 8) : 0ull),
+           in);
     }
+    const uint32_t per = r16 / 8;
+    for (uint32_t i = tid; i < 128 * per; i += kOuterThreads) {
+      const uint32_t row = i / per, q = i - row * per, p = p0 + (row & 63u);
+      const bool in = p < p_end;
+      cp16(hsm + (row >> 6) * h_bytes + (row & 63u) * h_row + q * 16,
+           P.hp + (in ? (row >> 6) * P.hp_stride + static_cast<uint64_t>(p) * r16 + 8 * q : 0ull), in);
+    }
+  };
+  const uint32_t n_steps = (p_end - p_begin + 63) / 64;
+#pragma unroll
+  for (uint32_t i = 0; i + 1 < kOuterStages; ++i) {
+    if (i < n_steps) load(i, p_begin + 64 * i);
+    cp_commit();
+  }
+  float acc[NJ][4] = {};
+  for (uint32_t it = 0; it < n_steps; ++it) {
+    cp_wait<kOuterStages - 2>();
     __syncthreads();
-    for (uint32_t s = 16 * tw; s < n16; s += 16 * n_tw) {
-      RowVec<8> z[4];
+    if (it + kOuterStages - 1 < n_steps) load((it + kOuterStages - 1) % kOuterStages, p_begin + 64 * (it + kOuterStages - 1));
+    cp_commit();
+    const uint32_t zs = base + (it % kOuterStages) * stage, hsm = zs + 64 * kChunkRow;
+    const uint32_t n16 = min(4u, (p_end - p_begin - 64 * it) / 16);
+    for (uint32_t ks = 0; ks < n16; ++ks) {
+      uint32_t f[4];
+      ldsm4_t(f, zs + (16 * ks + (lane & 7u) + ((lane >> 4) << 3)) * kChunkRow + (2 * warp + ((lane >> 3) & 1u)) * 16);
+      const uint32_t hr = hsm + (16 * ks + (lane & 15u)) * h_row;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        z[q] = RowVec<8>{};
-        const uint32_t p = s + 4 * t + q;
-        if (p < n_tok && col_in)
-          z[q] = load_row<8>(P.z + static_cast<uint64_t>(__ldcg(P.G.perm + p0 + p)) * P.C + c0 + 8 * g);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         if (j < nj) {
-          const uint32_t at = (32 * jb + 8 * j + g) * kOuterPitch + s + 4 * t;
-          const uint2 bh = *reinterpret_cast<const uint2*>(hi_s + at), bl = *reinterpret_cast<const uint2*>(lo_s + at);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t a0 = pair_of<8>(z[0], z[1], 2 * u), a1 = pair_of<8>(z[0], z[1], 2 * u + 1);
-            const uint32_t a2 = pair_of<8>(z[2], z[3], 2 * u), a3 = pair_of<8>(z[2], z[3], 2 * u + 1);
-            mma_bf16(acc[u][j], a0, a1, a2, a3, bh.x, bh.y);
-            mma_bf16(acc[u][j], a0, a1, a2, a3, bl.x, bl.y);
-          }
+          uint32_t b0, b1, l0, l1;
+          ldsm2_t(b0, b1, hr + j * 16);
+          ldsm2_t(l0, l1, hr + h_bytes + j * 16);
+          mma_bf16(acc[j], f[0], f[1], f[2], f[3], b0, b1);
+          mma_bf16(acc[j], f[0], f[1], f[2], f[3], l0, l1);
         }
       }
     }
   }
-  __syncthreads();
-  // column 8 g + 2 u (rows g of instruction u) and 8 g + 2 u + 1 (rows g + 8)
-  float* mine = red + warp * 64 * 32;
+  const uint32_t c = c0 + 16 * warp + g;
+  if (c0 + 16 * warp >= P.C) return;  // (C is a multiple of 16)
+  float* out = P.out + static_cast<uint64_t>(a) * P.C * P.rank;
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float* r = mine + (8 * g + 2 * u) * 32 + 8 * j + 2 * t;
-      r[0] = acc[u][j][0];
-      r[1] = acc[u][j][1];
-      r[32] = acc[u][j][2];
-      r[33] = acc[u][j][3];
+  for (int j = 0; j < NJ; ++j) {
+    if (j < nj) {
+      const uint32_t r = 8 * j + 2 * t;
+      if constexpr (kRankMajor) {
+        out[static_cast<uint64_t>(r) * P.C + c] = acc[j][0];
+        out[static_cast<uint64_t>(r + 1) * P.C + c] = acc[j][1];
+        out[static_cast<uint64_t>(r) * P.C + c + 8] = acc[j][2];
+        out[static_cast<uint64_t>(r + 1) * P.C + c + 8] = acc[j][3];
+      } else {
+        *reinterpret_cast<float2*>(out + static_cast<uint64_t>(c) * P.rank + r) = make_float2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<float2*>(out + static_cast<uint64_t>(c + 8) * P.rank + r) = make_float2(acc[j][2], acc[j][3]);
+      }
     }
-  __syncthreads();
-  const uint32_t cols = min(64u, P.C - c0);
-  for (uint32_t i = threadIdx.x; i < cols * P.rank; i += kOuterThreads) {
-    const uint32_t c = kRankMajor ? i % cols : i / P.rank;
-    const uint32_t j = kRankMajor ? i / cols : i - c * P.rank;
-    float v = 0.0f;
-    for (uint32_t q = 0; q < n_tw; ++q) v += red[((q * P.jblocks + j / 32) * 64 + c) * 32 + j % 32];
-    const uint64_t base = static_cast<uint64_t>(a) * P.C * P.rank;
-    if (kRankMajor) P.out[base + static_cast<uint64_t>(j) * P.C + c0 + c] = v;
-    else P.out[base + static_cast<uint64_t>(c0 + c) * P.rank + j] = v;
   }
 }
 
 // ---- host ----------------------------------------------------------------------
 static size_t aligned(size_t n) { return (n + 255) / 256 * 256; }
 
-static LoraGroups groups_at(uint8_t* p, uint32_t M, uint32_t n, uint32_t max_tiles) {
+static LoraGroups groups_at(uint8_t* p, uint32_t positions, uint32_t n, uint32_t max_tiles) {
   LoraGroups G;
   uint32_t* w = reinterpret_cast<uint32_t*>(p);
   G.n_tiles = w;
   G.off = w + 1;
   G.perm = G.off + n + 1;
-  G.tile_adapter = G.perm + M;
+  G.tile_adapter = G.perm + positions;
   G.tile_start = G.tile_adapter + max_tiles;
   G.tile_count = G.tile_start + max_tiles;
   return G;
@@ -502,17 +666,23 @@ static LoraGroups groups_at(uint8_t* p, uint32_t M, uint32_t n, uint32_t max_til
 static void split_range(uint32_t C, uint32_t tiles, uint32_t most, int sms, uint32_t* splits, uint32_t* len) {
   uint32_t want = std::max(1u, 2u * static_cast<uint32_t>(sms) / std::max(1u, tiles));
   want = std::min({want, most, std::max(1u, C / 256)});
-  *len = ((C + want - 1) / want + 255) / 256 * 256;
+  *len = ((C + want - 1) / want + 63) / 64 * 64;
   *splits = (C + *len - 1) / *len;
 }
 
+// Up to this many tokens a tile holds 16 (few tokens share an adapter), and in
+// the forward pass tiles are found and the splits added where they are used,
+// which saves two launches.
+constexpr uint32_t kLoraFewTokens = 256;
+
 void make_lora_plan(uint32_t M, const LoraDev& L, bool grad, int sms, LoraPlan* p) {
   p->M = M;
-  // tiles of 16 tokens where few share an adapter, of 64 where a tile's weights
-  // are read for more of them
-  p->tm = M <= 256 ? 16 : 64;
-  p->max_tiles = static_cast<uint32_t>(
-      std::min<uint64_t>(M, static_cast<uint64_t>(M) / p->tm + std::min(L.n, M)));
+  p->sms = sms;
+  p->tm = M <= kLoraFewTokens ? 16 : 64;
+  const uint32_t used = std::min(L.n, M);  // adapters that can have tokens
+  p->few = !grad && M <= kLoraFewTokens;
+  p->max_tiles = p->few ? M : static_cast<uint32_t>(std::min<uint64_t>(M, static_cast<uint64_t>(M) / p->tm + used));
+  p->positions = p->few ? M : static_cast<uint32_t>((static_cast<uint64_t>(M) + 15ull * used + 15) / 16 * 16);
   const uint32_t likely = (M + p->tm - 1) / p->tm;
   split_range(L.K, likely, 16, sms, &p->splits_k, &p->len_k);
   split_range(L.N, likely, 16, sms, &p->splits_n, &p->len_n);
@@ -522,11 +692,12 @@ void make_lora_plan(uint32_t M, const LoraDev& L, bool grad, int sms, LoraPlan* 
     at += aligned(n);
     return o;
   };
-  const size_t row = static_cast<size_t>(M) * L.rank * 4;
-  p->off_groups = take((2ull + L.n + M + 3ull * p->max_tiles) * 4);
-  p->off_part = take(row * (grad ? std::max(p->splits_k, p->splits_n) : p->splits_k));
-  p->off_h = take(grad ? row : 0);
-  p->off_dh = take(grad ? row : 0);
+  const size_t r16 = (L.rank + 15) / 16 * 16;
+  const size_t sums = static_cast<size_t>(p->positions) * L.rank * 4, parts = static_cast<size_t>(p->positions) * r16 * 4;
+  p->off_groups = take((2ull + L.n + p->positions + 3ull * p->max_tiles) * 4);
+  p->off_part = take(sums * (grad ? std::max(p->splits_k, p->splits_n) : p->splits_k));
+  p->off_h = take(p->few ? 0 : parts);
+  p->off_dh = take(grad ? parts : 0);
   p->bytes = at;
 }
 
@@ -542,113 +713,142 @@ static cudaError_t allow_smem(K kern, uint32_t bytes, std::atomic<uint64_t>& don
   return e;
 }
 
-template <bool kCols, int NJ>
-static cudaError_t shrink_variant(const ShrinkDev& P, dim3 grid, cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(lora_shrink_kernel<kCols, NJ>, 8 * 16 * kLoraMaxRank * 4, done);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(lora_shrink_kernel<kCols, NJ>, grid, dim3(kShrinkThreads), 8 * 16 * P.rank * 4, stream, P);
+// Instances by the rank's 8-column blocks, rounded up to 2, 4, 8 or 16.
+template <typename F>
+static cudaError_t by_rank(uint32_t rank, F f) {
+  if (rank <= 16) return f(std::integral_constant<int, 2>{});
+  if (rank <= 32) return f(std::integral_constant<int, 4>{});
+  if (rank <= 64) return f(std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 16>{});
 }
 
-static cudaError_t shrink(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, bool cols, const uint16_t* in,
-                          float* part, cudaStream_t stream) {
+template <bool kCols, bool kFew>
+static cudaError_t shrink(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const uint16_t* in,
+                          const int32_t* ids, float* part, uint32_t* status, cudaStream_t stream) {
   ShrinkDev P;
+  P.ids = ids;
+  P.status = status;
+  P.M = p.M;
+  P.n = L.n;
   P.G = G;
   P.in = in;
-  P.weights = cols ? L.B : L.A;
+  P.weights = kCols ? L.B : L.A;
   P.part = part;
-  P.C = cols ? L.N : L.K;
+  P.part_stride = static_cast<uint64_t>(p.positions) * L.rank;
+  P.C = kCols ? L.N : L.K;
   P.rank = L.rank;
-  P.M = p.M;
   P.groups = p.tm / 16;
-  P.len = cols ? p.len_n : p.len_k;
-  const dim3 grid(p.max_tiles, cols ? p.splits_n : p.splits_k);
-  if (cols) return shrink_variant<true, 8>(P, grid, stream);
-  if (L.rank <= 16) return shrink_variant<false, 2>(P, grid, stream);
-  if (L.rank <= 32) return shrink_variant<false, 4>(P, grid, stream);
-  if (L.rank <= 64) return shrink_variant<false, 8>(P, grid, stream);
-  return shrink_variant<false, 16>(P, grid, stream);
+  P.len = kCols ? p.len_n : p.len_k;
+  const dim3 grid(p.max_tiles, kCols ? p.splits_n : p.splits_k);
+  const uint32_t smem = kShrinkStages * (16 * P.groups * kChunkRow + shrink_w_bytes(kCols, L.rank));
+  return by_rank(L.rank, [&](auto nj) {
+    constexpr int NJ = decltype(nj)::value;
+    constexpr uint32_t kMost = kShrinkStages * (64 * kChunkRow + shrink_w_bytes(kCols, 8 * NJ));
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(lora_shrink_kernel<kCols, kFew, NJ>, kMost, done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(lora_shrink_kernel<kCols, kFew, NJ>, grid, dim3(kShrinkThreads), smem, stream, P);
+  });
 }
 
-template <bool kCols>
-static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const float* h, uint32_t splits,
-                          const float* scale, float* out, int sms, cudaStream_t stream) {
+static cudaError_t join(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const float* part, uint32_t splits,
+                        uint16_t* hp, cudaStream_t stream) {
+  const uint32_t r16 = (L.rank + 15) / 16 * 16;
+  return launch_pdl(lora_join_kernel, dim3(p.max_tiles, std::max(1u, p.tm * r16 / 1024)), dim3(256), 0, stream, G, part,
+                    splits, static_cast<uint64_t>(p.positions) * L.rank, L.rank, L.scale, hp,
+                    static_cast<uint64_t>(p.positions) * r16);
+}
+
+template <bool kCols, bool kFew>
+static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const int32_t* ids, const float* part,
+                          const uint16_t* hp, float* out, cudaStream_t stream) {
+  const uint32_t r16 = (L.rank + 15) / 16 * 16;
   ExpandDev P;
   P.G = G;
-  P.h = h;
-  P.scale = scale;
+  P.part = part;
+  P.hp = hp;
+  P.part_stride = static_cast<uint64_t>(p.positions) * L.rank;
+  P.hp_stride = static_cast<uint64_t>(p.positions) * r16;
+  P.scale = L.scale;
   P.weights = kCols ? L.A : L.B;
   P.out = out;
   P.C = kCols ? L.K : L.N;
   P.rank = L.rank;
-  P.M = p.M;
-  P.splits = splits;
+  P.splits = p.splits_k;
   P.tm = p.tm;
-  // as many warps a CTA as still leave every SM a CTA
+  P.ids = ids;
+  P.M = p.M;
+  P.n = L.n;
+  // as many warps a CTA as still leave every SM two CTAs
   const uint32_t blocks = (P.C + 63) / 64, likely = (p.M + p.tm - 1) / p.tm;
-  uint32_t warps = 8;
-  while (warps > 1 && (blocks + warps - 1) / warps * likely < static_cast<uint32_t>(sms)) warps /= 2;
-  const uint32_t smem = 2 * p.tm * ((L.rank + 15) / 16 * 16 + 8) * 2;  // 34 KB at most
-  return launch_pdl(lora_expand_kernel<kCols>, dim3(p.max_tiles, (blocks + warps - 1) / warps), dim3(32 * warps), smem,
-                    stream, P);
+  uint32_t warps = 4;
+  while (warps > 1 && (blocks + warps - 1) / warps * likely < 2u * static_cast<uint32_t>(p.sms)) warps /= 2;
+  const uint32_t smem = 2 * p.tm * (r16 + 8) * 2;  // 34 KB at most
+  const dim3 grid(p.max_tiles, (blocks + warps - 1) / warps), block(32 * warps);
+  if (L.rank <= 16) return launch_pdl(lora_expand_kernel<kCols, kFew, 1>, grid, block, smem, stream, P);
+  if (L.rank <= 32) return launch_pdl(lora_expand_kernel<kCols, kFew, 2>, grid, block, smem, stream, P);
+  if (L.rank <= 64) return launch_pdl(lora_expand_kernel<kCols, kFew, 4>, grid, block, smem, stream, P);
+  return launch_pdl(lora_expand_kernel<kCols, kFew, 0>, grid, block, smem, stream, P);
 }
 
 template <bool kRankMajor>
-static cudaError_t outer(const LoraDev& L, const LoraGroups& G, const uint16_t* z, const float* h, float* out,
-                         cudaStream_t stream) {
-  constexpr uint32_t kMost = 2 * kLoraMaxRank * kOuterPitch * 2;  // above the 64 KB of the sums
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(lora_outer_kernel<kRankMajor>, kMost, done);
-  if (e != cudaSuccess) return e;
+static cudaError_t outer(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const uint16_t* z, const uint16_t* hp,
+                         float* out, cudaStream_t stream) {
+  const uint32_t r16 = (L.rank + 15) / 16 * 16;
   OuterDev P;
   P.G = G;
   P.z = z;
-  P.h = h;
+  P.hp = hp;
+  P.hp_stride = static_cast<uint64_t>(p.positions) * r16;
   P.out = out;
   P.C = kRankMajor ? L.K : L.N;
   P.rank = L.rank;
-  P.jblocks = L.rank <= 32 ? 1 : L.rank <= 64 ? 2 : 4;
-  const uint32_t smem = std::max(2 * L.rank * kOuterPitch * 2, 8u * 64 * 32 * 4);
-  return launch_pdl(lora_outer_kernel<kRankMajor>, dim3((P.C + 63) / 64, L.n), dim3(kOuterThreads), smem, stream, P);
+  return by_rank(L.rank, [&](auto nj) {
+    constexpr int NJ = decltype(nj)::value;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(lora_outer_kernel<kRankMajor, NJ>, kOuterStages * outer_stage_bytes(8 * NJ), done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(lora_outer_kernel<kRankMajor, NJ>, dim3((P.C + 63) / 64, L.n), dim3(kOuterThreads),
+                      kOuterStages * outer_stage_bytes(r16), stream, P);
+  });
 }
 
-static int current_sms() {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
-cudaError_t launch_lora_forward(const LoraPlan& p, const LoraDev& L, const uint16_t* X, const int32_t* ids, float* Y,
-                                void* ws, uint32_t* status, cudaStream_t stream) {
+cudaError_t launch_lora_shrink(const LoraPlan& p, const LoraDev& L, const uint16_t* X, const int32_t* ids, void* ws,
+                               uint32_t* status, cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const LoraGroups G = groups_at(w + p.off_groups, p.M, L.n, p.max_tiles);
+  const LoraGroups G = groups_at(w + p.off_groups, p.positions, L.n, p.max_tiles);
   float* part = reinterpret_cast<float*>(w + p.off_part);
+  if (p.few) return shrink<false, true>(p, L, G, X, ids, part, status, stream);
   cudaError_t e = launch_pdl(lora_group_kernel, dim3(1), dim3(1024), 0, stream, ids, p.M, L.n, p.tm, G, status);
-  if (e == cudaSuccess) e = shrink(p, L, G, false, X, part, stream);
-  if (e == cudaSuccess) e = expand<false>(p, L, G, part, p.splits_k, L.scale, Y, current_sms(), stream);
+  if (e == cudaSuccess) e = shrink<false, false>(p, L, G, X, ids, part, status, stream);
+  if (e == cudaSuccess) e = join(p, L, G, part, p.splits_k, reinterpret_cast<uint16_t*>(w + p.off_h), stream);
   return e;
+}
+
+cudaError_t launch_lora_expand(const LoraPlan& p, const LoraDev& L, const int32_t* ids, float* Y, void* ws,
+                               cudaStream_t stream) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const LoraGroups G = groups_at(w + p.off_groups, p.positions, L.n, p.max_tiles);
+  if (p.few) return expand<false, true>(p, L, G, ids, reinterpret_cast<float*>(w + p.off_part), nullptr, Y, stream);
+  return expand<false, false>(p, L, G, ids, nullptr, reinterpret_cast<uint16_t*>(w + p.off_h), Y, stream);
 }
 
 cudaError_t launch_lora_grad(const LoraPlan& p, const LoraDev& L, const uint16_t* X, const uint16_t* dY,
                              const int32_t* ids, float* dA, float* dB, float* delta, void* ws, uint32_t* status,
                              cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const LoraGroups G = groups_at(w + p.off_groups, p.M, L.n, p.max_tiles);
+  const LoraGroups G = groups_at(w + p.off_groups, p.positions, L.n, p.max_tiles);
   float* part = reinterpret_cast<float*>(w + p.off_part);
-  float* h = reinterpret_cast<float*>(w + p.off_h);
-  float* dh = reinterpret_cast<float*>(w + p.off_dh);
+  uint16_t* h = reinterpret_cast<uint16_t*>(w + p.off_h);
+  uint16_t* dh = reinterpret_cast<uint16_t*>(w + p.off_dh);
   cudaError_t e = launch_pdl(lora_group_kernel, dim3(1), dim3(1024), 0, stream, ids, p.M, L.n, p.tm, G, status);
-  auto sum = [&](uint32_t splits, float* to) {
-    return launch_pdl(lora_sum_kernel, dim3(p.max_tiles), dim3(256), 0, stream, G, part, splits, p.M, L.rank, L.scale,
-                      to);
-  };
-  if (e == cudaSuccess) e = shrink(p, L, G, false, X, part, stream);
-  if (e == cudaSuccess) e = sum(p.splits_k, h);
-  if (e == cudaSuccess) e = shrink(p, L, G, true, dY, part, stream);
-  if (e == cudaSuccess) e = sum(p.splits_n, dh);
-  if (e == cudaSuccess) e = outer<false>(L, G, dY, h, dB, stream);
-  if (e == cudaSuccess) e = outer<true>(L, G, X, dh, dA, stream);
-  if (e == cudaSuccess && delta != nullptr) e = expand<true>(p, L, G, dh, 1, nullptr, delta, current_sms(), stream);
+  if (e == cudaSuccess) e = shrink<false, false>(p, L, G, X, ids, part, status, stream);
+  if (e == cudaSuccess) e = join(p, L, G, part, p.splits_k, h, stream);
+  if (e == cudaSuccess) e = shrink<true, false>(p, L, G, dY, ids, part, status, stream);
+  if (e == cudaSuccess) e = join(p, L, G, part, p.splits_n, dh, stream);
+  if (e == cudaSuccess) e = outer<false>(p, L, G, dY, h, dB, stream);
+  if (e == cudaSuccess) e = outer<true>(p, L, G, X, dh, dA, stream);
+  if (e == cudaSuccess && delta != nullptr) e = expand<true, false>(p, L, G, ids, nullptr, dh, delta, stream);
   return e;
 }
 

@@ -891,6 +891,7 @@ cudaError_t launch_grad_x(const GradPlan& p, const ansdev::LayerDev& L, const ui
   e = ansdev::launch_operand_decode(L, 0, L.N, kind, d_scales, group_k, images, d_status, sms, stream);
   if (e != cudaSuccess) return e;
   ansdev::OperandGemmOut out;
+  std::memset(&out, 0, sizeof(out));
   out.ld = L.K;
   if (p.gemm.splits == 1) {
     out.out16 = d_dX;
@@ -898,11 +899,11 @@ cudaError_t launch_grad_x(const GradPlan& p, const ansdev::LayerDev& L, const ui
     out.add = delta;
     out.ids = ids;
     out.n_ids = n_ids;
-    return ansdev::launch_operand_gemm(p.gemm, images, rows, out, d_status, stream);
+    return ansdev::launch_operand_gemm(p.gemm, images, rows, &out, nullptr, d_status, stream);
   }
   out.out32 = reinterpret_cast<float*>(ws + p.off_parts);
   out.split_stride = static_cast<uint64_t>(M) * L.K;
-  e = ansdev::launch_operand_gemm(p.gemm, images, rows, out, d_status, stream);
+  e = ansdev::launch_operand_gemm(p.gemm, images, rows, &out, nullptr, d_status, stream);
   if (e != cudaSuccess) return e;
   return ansdev::launch_sum_splits(out.out32, p.gemm.splits, out.split_stride, M, L.K, factor, delta, ids, n_ids, d_dX,
                                    stream);

@@ -662,6 +662,12 @@ static LoraGroups groups_at(uint8_t* p, uint32_t positions, uint32_t n, uint32_t
   return G;
 }
 
+// Tiles to expect: of few tokens, every one may name its own adapter.
+static uint32_t likely_tiles(uint32_t M, uint32_t tm, uint32_t n) {
+  const uint32_t full = (M + tm - 1) / tm;
+  return M <= 64 ? std::max(full, std::min(M, n)) : full;
+}
+
 // Ranges of a sum over C: enough CTAs for the SMs, at least 256 values each.
 static void split_range(uint32_t C, uint32_t tiles, uint32_t most, int sms, uint32_t* splits, uint32_t* len) {
   uint32_t want = std::max(1u, 2u * static_cast<uint32_t>(sms) / std::max(1u, tiles));
@@ -683,7 +689,8 @@ void make_lora_plan(uint32_t M, const LoraDev& L, bool grad, int sms, LoraPlan* 
   p->few = !grad && M <= kLoraFewTokens;
   p->max_tiles = p->few ? M : static_cast<uint32_t>(std::min<uint64_t>(M, static_cast<uint64_t>(M) / p->tm + used));
   p->positions = p->few ? M : static_cast<uint32_t>((static_cast<uint64_t>(M) + 15ull * used + 15) / 16 * 16);
-  const uint32_t likely = (M + p->tm - 1) / p->tm;
+  p->likely = likely_tiles(M, p->tm, L.n);
+  const uint32_t likely = p->likely;
   split_range(L.K, likely, 16, sms, &p->splits_k, &p->len_k);
   split_range(L.N, likely, 16, sms, &p->splits_n, &p->len_n);
   size_t at = 0;
@@ -780,9 +787,9 @@ static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups&
   P.M = p.M;
   P.n = L.n;
   // as many warps a CTA as still leave every SM two CTAs
-  const uint32_t blocks = (P.C + 63) / 64, likely = (p.M + p.tm - 1) / p.tm;
+  const uint32_t blocks = (P.C + 63) / 64;
   uint32_t warps = 4;
-  while (warps > 1 && (blocks + warps - 1) / warps * likely < 2u * static_cast<uint32_t>(p.sms)) warps /= 2;
+  while (warps > 1 && (blocks + warps - 1) / warps * p.likely < 2u * static_cast<uint32_t>(p.sms)) warps /= 2;
   const uint32_t smem = 2 * p.tm * (r16 + 8) * 2;  // 34 KB at most
   const dim3 grid(p.max_tiles, (blocks + warps - 1) / warps), block(32 * warps);
   if (L.rank <= 16) return launch_pdl(lora_expand_kernel<kCols, kFew, 1>, grid, block, smem, stream, P);

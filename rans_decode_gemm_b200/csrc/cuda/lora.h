@@ -32,7 +32,7 @@ struct LoraGroups {
 };
 
 struct LoraPlan {
-  uint32_t M, tm, max_tiles, positions;
+  uint32_t M, tm, max_tiles, positions, likely;
   uint32_t few;   // forward pass of few tokens: tiles found where they are used
   int sms;
   uint32_t splits_k, len_k;  // ranges of a sum over K, and their length

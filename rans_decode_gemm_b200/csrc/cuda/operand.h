@@ -36,10 +36,10 @@ cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t row
 cudaError_t launch_row_prep(const uint16_t* in, uint32_t M, uint32_t C, uint32_t scale_kind,
                             const void* scales, bool f16, uint16_t* out, float* factor, cudaStream_t stream);
 
-// One GEMM on operand images of `rows` W rows and K columns, X and G 16-bit
-// row-major, fp32 sums:
-//   forward:     out[m][n] = s_n * sum_k X[m][k] W[n][k]        (n < rows)
-//   transposed:  out[m][k] = sum_n G[m][n] W[n][k]              (k < K)
+// A GEMM on operand images of `rows` W rows and K columns, 16-bit row-major
+// operands, fp32 sums:
+//   transposed:  out[m][k] = sum_n G[m][n] W[n][k]        (k < K)
+//   logits:      z[m][n] = f[m] s_n sum_k X[m][k] W[n][k]  (n < rows)
 // The transposed sum may be cut into `splits` ranges of n.
 struct OperandGemmPlan {
   uint32_t trans, f16;
@@ -52,27 +52,51 @@ struct OperandGemmPlan {
 OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t rows, uint32_t K,
                                   uint32_t max_splits, int sms);
 
-// What happens to the sums (v[m][c], c = n or k).
+// What happens to the transposed sums v[m][k].
 struct OperandGemmOut {
-  // forward: out32[m * ld + n] = v * s_n.
-  // transposed with out16: out16[m * ld + k] = bf16(beta[m] * v + add[m * ld + k]),
-  //   the addend taken for rows with 0 <= ids[m] < n_ids only (add may be null).
-  // transposed with out32: out32[split][m * ld + k] = alpha[m] * (its old value) +
-  //   beta[m] * v; alpha null: the old value is not read.  beta null: 1.
-  float* out32 = nullptr;
-  uint16_t* out16 = nullptr;
-  uint64_t split_stride = 0;  // elements between the splits' out32
-  uint32_t ld = 0;
-  const float* alpha = nullptr;
-  const float* beta = nullptr;
-  const float* add = nullptr;
-  const int32_t* ids = nullptr;
-  uint32_t n_ids = 0;
-  uint32_t scale_kind = 0;
-  const void* scales = nullptr;
+  // out16: out16[m * ld + k] = bf16(beta[m] * v + add[m * ld + k]), the addend
+  //   taken for rows with 0 <= ids[m] < n_ids only (add may be null).
+  // out32: out32[split][m * ld + k] = alpha[m] * (its old value) + beta[m] * v;
+  //   alpha null: the old value is not read.  beta null: 1.
+  float* out32;
+  uint16_t* out16;
+  uint64_t split_stride;  // elements between the splits' out32
+  uint32_t ld;
+  const float* alpha;
+  const float* beta;
+  const float* add;
+  const int32_t* ids;
+  uint32_t n_ids;
 };
+
+// What happens to the logits: they are folded into softmax sums, 32 rows of W
+// (a block) at a time.  With r a reference in units of log 2 (a whole number),
+//   e[m][n] = 2^(z[m][n] log2(e) - r),  sum[block][m] = sum of the block's e,
+//   probs[m * rows + n] = e * s_n * lift (16-bit; null: not stored),
+// except that rows n0 + n >= vocab count for nothing, and the token's target has
+// its logit stored in zt[m] and e taken as 0.  r is ref_in[m], unless the
+// block's largest logit lies more than kXentSlack above it: then r is that
+// logit, rounded up.  ref[block][m] says which was used.
+constexpr float kXentSlack = 5.75f;    // e^4: what probabilities may exceed 1 by
+constexpr float kXentNone = -1.0e30f;  // the reference before any logit
+struct XentEpilogue {
+  const float* factor;     // f[m], or null: 1
+  uint32_t scale_kind;     // s_n: bf16 (1), fp32 (2) at scales[n], else 1
+  const void* scales;
+  const float* lift;       // one value
+  const float* ref_in;
+  const int32_t* targets;
+  float* zt;
+  float *ref, *sum;        // [rows / 32][stride]
+  uint32_t stride;
+  uint16_t* probs;
+  uint32_t n0, vocab;
+};
+
+// Exactly one of out (transposed) and xent (logits) is given.
 cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* images, const void* rows16,
-                                const OperandGemmOut& out, uint32_t* status, cudaStream_t stream);
+                                const OperandGemmOut* out, const XentEpilogue* xent, uint32_t* status,
+                                cudaStream_t stream);
 
 // out[m][k] = bf16(beta[m] * sum over splits of part[split][m][k] + add[m][k])
 // (the addend as in OperandGemmOut).

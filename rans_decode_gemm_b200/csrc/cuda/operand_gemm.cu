@@ -1,7 +1,7 @@
 // operand_gemm.cu -- tcgen05 GEMMs on operand images (operand.h), either way
 // round, and the row kernels beside them.
 //
-//   forward      D[n][m] = sum_k W[n][k] X[m][k]    (the logits of a vocabulary piece)
+//   logits       D[n][m] = sum_k W[n][k] X[m][k]
 //   transposed   D[k][m] = sum_n W[n][k] G[m][n]    (a gradient that leaves the layer)
 //
 // One layout of W serves both.  An image is 128 rows of 32 bytes under the
@@ -11,13 +11,23 @@
 // so the transposed product needs neither a second copy of W nor a
 // transposing load.  Tokens are the MMA's N dimension in both: 128 rows of W
 // (or of W^T) by up to 256 tokens, fp32 accumulators in two TMEM sets so that
-// the stores of a tile overlap the MMAs of the next.
+// the epilogue of a tile overlaps the MMAs of the next.
 //
-// A stage holds 64 steps of the sum: 16 KB of W by one copy (forward: four
+// A stage holds 64 steps of the sum: 16 KB of W by one copy (logits: four
 // consecutive images; transposed: one box of half of each of eight images)
 // and a 64 x bn box of the tokens by TMA under the 128-byte swizzle.  Four K = 16
-// MMAs and one commit a stage.
-// Warps: 0 loads, 1 MMA issue (and TMEM owner), 2-5 epilogue.
+// MMAs and one commit a stage.  (Eight 2 KB copies instead of the box held the
+// transposed product at 158 ns an MMA against 115.)
+//
+// The logits never reach memory: the epilogue turns them into exponentials
+// under a reference that is known before the tile (the row's reference after
+// the earlier pieces), and only a block of 32 logits that rises far above it
+// takes a reference of its own.  A warp holds 32 rows n by 32 tokens at a time, one n
+// a lane; maxima and sums over n for the 32 tokens take 31 exchanges each
+// (halving the tokens and the lanes together) and end with token j in lane j.
+// Warps: 0 loads, 1 MMA issue (and TMEM owner), 2-9 epilogue: two for each
+// quarter of TMEM's lanes, on alternating 32 tokens.  (With one each, the
+// epilogue of the logits took longer than the MMAs of a K = 2048 tile.)
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -35,7 +45,8 @@ namespace ansdev {
 
 constexpr uint32_t kOgBM = 128, kOgBK = 64;
 constexpr uint32_t kOgABytes = kOgBM * kOgBK * 2;  // 16 KB
-constexpr uint32_t kOgThreads = 6 * 32;
+constexpr uint32_t kOgEpiWarps = 8;
+constexpr uint32_t kOgThreads = (2 + kOgEpiWarps) * 32;
 constexpr uint32_t kOgMaxStages = 8;
 constexpr uint32_t kOgSmemTiles = 200 * 1024;  // stages
 constexpr uint32_t kOgSmem = kOgSmemTiles + 1024;
@@ -45,6 +56,8 @@ struct OperandGemmDev {
   CUtensorMap tmap_b;  // tokens: 64 x b_box_rows boxes, 128-byte swizzle
   CUtensorMap tmap_a;  // transposed: images as rows of 512 eight-byte words, boxes of 256 x 8
   OperandGemmOut out;
+  XentEpilogue xent;
+  uint32_t f16;
   uint32_t* status;
   uint32_t M, bn, m_blocks, n_tiles, splits;
   uint32_t k_slabs;      // images per 128-row block (K / 16)
@@ -53,6 +66,91 @@ struct OperandGemmDev {
   uint32_t b_box_rows, stages, stage_bytes;
   uint32_t idesc, idesc_tail;
 };
+
+// Over the warp's lanes for each of 32 values at once: lane j ends with value
+// j's result.
+template <typename Op>
+__device__ __forceinline__ float across_lanes(float (&x)[32], uint32_t lane, Op op) {
+#pragma unroll
+  for (uint32_t w = 16; w > 0; w >>= 1) {
+    const bool up = (lane & w) != 0;
+#pragma unroll
+    for (uint32_t i = 0; i < w; ++i) {
+      const float give = up ? x[i] : x[i + w], keep = up ? x[i + w] : x[i];
+      x[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, w));
+    }
+  }
+  return x[0];
+}
+
+// 32 logits of 32 tokens (v[j]: this lane's row n against token m + j), folded
+// as XentEpilogue says.  c: this lane's row in the piece; m: first token; token
+// m + lane's reference, target and factor come in tok.
+struct XentToken {
+  float ref, factor;
+  int32_t target;
+};
+__device__ __forceinline__ XentToken xent_token(const XentEpilogue& E, uint32_t m, bool in) {
+  XentToken t;
+  t.ref = in ? __ldcg(E.ref_in + m) : 0.0f;
+  t.target = in ? __ldg(E.targets + m) : -1;
+  t.factor = E.factor != nullptr && in ? __ldcg(E.factor + m) : 1.0f;
+  return t;
+}
+__device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, uint32_t rows, const uint32_t (&v)[32],
+                                          float scale, float lift, uint32_t c, uint32_t m, uint32_t n_tok,
+                                          uint32_t lane, const XentToken& tok) {
+  constexpr float kLog2E = 1.4426950408889634f;
+  const bool m_in = lane < n_tok;
+  const float ref_in = tok.ref, factor = tok.factor;
+  const int32_t target = tok.target;
+  const bool n_in = E.n0 + c < E.vocab;
+  float z[32], x[32];
+#pragma unroll
+  for (uint32_t j = 0; j < 32; ++j) {
+    z[j] = __uint_as_float(v[j]) * scale;
+    if (E.factor != nullptr) z[j] *= __shfl_sync(0xFFFFFFFFu, factor, j);
+    if (!n_in) z[j] = -INFINITY;
+    x[j] = z[j];
+  }
+  const float top = across_lanes(x, lane, [](float a, float b) { return fmaxf(a, b); }) * kLog2E;
+  float ref = ref_in;
+  if (top > ref_in + kXentSlack && top <= 3.0e38f) ref = ceilf(top);
+  // targets among this warp's rows (one that is past the vocabulary is none)
+  const uint32_t first = E.n0 + c - lane;
+  const bool hit = target >= 0 && static_cast<uint32_t>(target) < E.vocab && static_cast<uint32_t>(target) - first < 32u;
+  const uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit);
+  const float ps = scale * lift;
+#pragma unroll
+  for (uint32_t j = 0; j < 32; ++j) {
+    const float r = __shfl_sync(0xFFFFFFFFu, ref, j);
+    // (the approximate instruction: 2^-22, the same in every use)
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x[j]) : "f"(fmaf(z[j], kLog2E, -r)));
+    if ((hits >> j) & 1u) {
+      const uint32_t t = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, target, j)) - first;
+      if (lane == t) {
+        E.zt[m + j] = z[j];
+        x[j] = 0.0f;
+      }
+    }
+  }
+  if (E.probs != nullptr) {
+    uint16_t* p = E.probs + static_cast<uint64_t>(m) * rows + c;
+#pragma unroll
+    for (uint32_t j = 0; j < 32; ++j) {
+      if (j >= n_tok) break;
+      const float q = x[j] * ps;
+      p[static_cast<uint64_t>(j) * rows] =
+          f16 ? __half_as_ushort(__float2half_rn(q)) : __bfloat16_as_ushort(__float2bfloat16_rn(q));
+    }
+  }
+  const float sum = across_lanes(x, lane, [](float a, float b) { return a + b; });
+  if (m_in) {
+    const uint64_t at = static_cast<uint64_t>(c / 32) * E.stride + m + lane;
+    E.sum[at] = sum;
+    E.ref[at] = ref;
+  }
+}
 
 template <bool kTrans>
 __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __grid_constant__ OperandGemmDev P) {
@@ -75,7 +173,7 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
     }
     for (uint32_t i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);  // one arrival per epilogue warp
+      mbar_init(&acc_empty[i], kOgEpiWarps);  // one arrival per epilogue warp
     }
     mbar_init(&mma_done, 1);
     fence_mbar_init();
@@ -150,7 +248,7 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
   } else if (warp == 1) {
     // ======================= MMA issue =======================
     if (lane == 0) {
-      // forward A: K-major, 8-row groups 256 B apart (SBO), image j of a stage
+      // logits A: K-major, 8-row groups 256 B apart (SBO), image j of a stage
       // is its K = 16 slice j.  Transposed A: MN-major, atoms of 16 k 2 KB
       // apart (LBO), 8-row groups of n 256 B apart (SBO); the K = 16 slice j
       // starts 16 rows (512 B) further.  B: 128-byte swizzle, 8-row groups
@@ -194,86 +292,96 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
     }
     __syncwarp();
   } else {
-    // ======================= epilogue (warps 2-5) =======================
-    // 32 tokens at a time.  What is read of global memory for them (the old
-    // values or the addend, 32 independent loads; the tokens' factors, one a
-    // lane) is asked for before the previous 32 are stored, and for a tile's
-    // first 32 before its sums are ready.
-    const uint32_t quad = warp & 3u;
+    // ======================= epilogue (warps 2-9) =======================
+    // 32 tokens at a time.  Transposed: what is read of global memory for them
+    // (the old values or the addend, 32 independent loads; the tokens' factors,
+    // one a lane) is asked for before the previous 32 are stored, and for a
+    // tile's first 32 before its sums are ready.  Logits: likewise the tokens'
+    // references, targets and factors.
+    const uint32_t quad = warp & 3u, turn = 32u * ((warp - 2) >> 2);
     const OperandGemmOut& O = P.out;
     const bool rmw = kTrans && O.out32 != nullptr && O.alpha != nullptr;
     const bool adds = kTrans && O.out32 == nullptr && O.add != nullptr;
+    const float lift = kTrans ? 1.0f : __ldcg(P.xent.lift);
     uint32_t acc = 0;
     for (uint32_t t = blockIdx.x; t < P.n_tiles; t += gridDim.x, ++acc) {
       uint32_t ab, mb, sp, kb0, kb1;
       tile_of(t, ab, mb, sp, kb0, kb1);
       const uint32_t b = acc & 1u;
-      const uint32_t c = ab * kOgBM + 32 * quad + lane;  // this thread's column of the output
+      const uint32_t c = ab * kOgBM + 32 * quad + lane;  // this thread's row of D
       const bool c_in = c < P.out_cols;
       const uint32_t m0 = mb * P.bn;
       const uint32_t cols = min(P.bn, P.M - m0);
       const uint64_t tile_at = static_cast<uint64_t>(m0) * O.ld + c;
-      float* out32 = O.out32 + (kTrans ? sp * O.split_stride : 0ull);
+      float* out32 = O.out32 + sp * O.split_stride;
       float scale = 1.0f;
-      if (!kTrans && c_in) {
-        if (O.scale_kind == 1) scale = bf16_to_f32(__ldg(static_cast<const uint16_t*>(O.scales) + c));
-        else if (O.scale_kind == 2) scale = __ldg(static_cast<const float*>(O.scales) + c);
+      if (!kTrans) {
+        if (P.xent.scale_kind == 1) scale = bf16_to_f32(__ldg(static_cast<const uint16_t*>(P.xent.scales) + c));
+        else if (P.xent.scale_kind == 2) scale = __ldg(static_cast<const float*>(P.xent.scales) + c);
       }
       float old[32], my_alpha = 1.0f, my_beta = 1.0f;
-      uint32_t has = 0;  // tokens that take the addend
+      XentToken tok;
       auto ask = [&](uint32_t c0) {
         const uint32_t m = m0 + c0 + lane;
         const bool m_in = c0 + lane < cols;
+        if constexpr (!kTrans) {
+          tok = xent_token(P.xent, m, m_in);
+          return;
+        }
         if (rmw) my_alpha = m_in ? __ldcg(O.alpha + m) : 0.0f;
         if (O.beta != nullptr) my_beta = m_in ? __ldcg(O.beta + m) : 0.0f;
-        if (adds) {
-          const int32_t id = m_in ? __ldg(O.ids + m) : -1;
-          has = __ballot_sync(0xFFFFFFFFu, id >= 0 && static_cast<uint32_t>(id) < O.n_ids);
-        }
         if (rmw || adds) {
+          uint32_t want = cols - c0 < 32 ? (1u << (cols - c0)) - 1u : 0xFFFFFFFFu;
+          if (adds) {
+            // tokens that take the addend
+            const int32_t id = m_in ? __ldg(O.ids + m) : -1;
+            want = __ballot_sync(0xFFFFFFFFu, id >= 0 && static_cast<uint32_t>(id) < O.n_ids);
+          }
+          if (!c_in) want = 0;
           const float* src = (rmw ? out32 : O.add) + tile_at + static_cast<uint64_t>(c0) * O.ld;
-          const uint32_t want = c_in ? (rmw ? (cols - c0 < 32 ? (1u << (cols - c0)) - 1u : 0xFFFFFFFFu) : has) : 0u;
 #pragma unroll
           for (uint32_t j = 0; j < 32; ++j)
             old[j] = (want >> j) & 1u ? __ldcg(src + static_cast<uint64_t>(j) * O.ld) : 0.0f;
         }
       };
-      if (kTrans) ask(0);
+      if (turn < cols) ask(turn);
       const bool ok = wait_live(&acc_full[b], (acc >> 1) & 1u, abort, P.status, 23, 64);
       tc_fence_after();
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      for (uint32_t c0 = 0; c0 < cols; c0 += 32) {
+      if (turn >= cols && lane == 0) mbar_arrive(&acc_empty[b]);
+      for (uint32_t c0 = turn; c0 < cols; c0 += 64) {
         uint32_t v[32];
         tmem_ld32(tmem_base + ((32 * quad) << 16) + b * 256 + c0, v);
         tmem_ld_wait();
-        float x[32];
+        if (c0 + 64 >= cols) {
+          // this warp has read its last of the tile's sums
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
+        }
+        if constexpr (!kTrans) {
+          const XentToken now = tok;
+          if (c0 + 64 < cols) ask(c0 + 64);
+          xent_fold(P.xent, P.f16, P.out_cols, v, scale, lift, c, m0 + c0, min(32u, cols - c0), lane, now);
+        } else {
+          float x[32];
 #pragma unroll
-        for (uint32_t j = 0; j < 32; ++j) {
-          x[j] = __uint_as_float(v[j]);
-          if (!kTrans) {
-            x[j] *= scale;
-          } else {
+          for (uint32_t j = 0; j < 32; ++j) {
+            x[j] = __uint_as_float(v[j]);
             if (O.beta != nullptr) x[j] *= __shfl_sync(0xFFFFFFFFu, my_beta, j);
             if (rmw) x[j] = fmaf(__shfl_sync(0xFFFFFFFFu, my_alpha, j), old[j], x[j]);
             else if (adds) x[j] += old[j];
           }
-        }
-        if (c0 + 32 >= cols) {
-          // every column of this tile has been read: the MMAs may go on
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[b]);
-        } else if (kTrans) {
-          ask(c0 + 32);
-        }
-        const uint64_t at = tile_at + static_cast<uint64_t>(c0) * O.ld;
-        if (c_in) {
+          if (c0 + 64 < cols) ask(c0 + 64);
+          const uint64_t at = tile_at + static_cast<uint64_t>(c0) * O.ld;
+          if (c_in) {
 #pragma unroll
-          for (uint32_t j = 0; j < 32; ++j) {
-            if (c0 + j >= cols) break;
-            const uint64_t i = at + static_cast<uint64_t>(j) * O.ld;
-            if (!kTrans || O.out32 != nullptr) out32[i] = x[j];
-            else O.out16[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
+            for (uint32_t j = 0; j < 32; ++j) {
+              if (c0 + j >= cols) break;
+              const uint64_t i = at + static_cast<uint64_t>(j) * O.ld;
+              if (O.out32 != nullptr) out32[i] = x[j];
+              else O.out16[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
+            }
           }
         }
       }
@@ -315,12 +423,15 @@ OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t row
 }
 
 cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* images, const void* rows16,
-                                const OperandGemmOut& out, uint32_t* status, cudaStream_t stream) {
+                                const OperandGemmOut* out, const XentEpilogue* xent, uint32_t* status,
+                                cudaStream_t stream) {
   if (plan.M == 0) return cudaSuccess;
   OperandGemmDev P;
   std::memset(&P, 0, sizeof(P));
   P.images = images;
-  P.out = out;
+  if (out) P.out = *out;
+  if (xent) P.xent = *xent;
+  P.f16 = plan.f16;
   P.status = status;
   P.M = plan.M;
   P.bn = plan.bn;

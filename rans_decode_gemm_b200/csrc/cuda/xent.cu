@@ -5,13 +5,17 @@
 //   dx = g (sum_n p_n w_n - w_t),  p_n = exp(z_n - lse).
 //
 // One pass over the vocabulary serves loss and gradient.  Per piece: its
-// weights are decoded once into operand images, one GEMM gives the piece's
-// logits, a row kernel folds them into the running reference r (the largest
-// logit so far) and sum l and turns them into exp(z - r), and a transposed GEMM
-// on the same images adds exp(z - r) W to the row's running sum of the
-// gradient, rescaled by exp(r_old - r_new) as it is stored.  Two products of
-// 2 M V K operations in all, against three for a pass that has the sums first.
-// Logits exist for one piece and one chunk of tokens.
+// weights are decoded once into operand images; one GEMM computes the logits
+// and folds them, in its epilogue, into blocks of exponentials and their sums
+// (operand.h); a row kernel joins the blocks into the running reference and
+// sum; and a transposed GEMM on the same images adds the exponentials times W
+// to the row's running sum of the gradient, rescaled as it is stored where the
+// reference moved.  Two products of 2 M V K operations in all, against three for
+// a pass that has the sums first.
+//
+// The reference is a whole number r in units of log 2 that lies at most
+// kXentSlack below the largest logit so far, so that moving it rescales by
+// powers of two, exactly, and after the first piece it hardly moves.
 //
 // The target's own term stays out of the running sums.  With l the others'
 // sum and e_t the target's, dx = g / (l + e_t) (sum_{n != t} e_n w_n - l w_t):
@@ -32,161 +36,189 @@
 namespace ansdev {
 
 constexpr uint32_t kXentThreads = 256;
-constexpr uint32_t kXentPieceMax = 8192;  // logits of a row in registers: 32 a thread
-constexpr uint32_t kXentPer = kXentPieceMax / kXentThreads / 4;  // float4s a thread
+constexpr float kLn2 = 0.69314718055994531f, kLog2E = 1.4426950408889634f;
 
 // Running state of M rows: reference r, sum l of the others, target logit,
-// and this piece's factors of the gradient's sum.
+// and this piece's factors of the gradient's sum.  lift: one value.
 struct XentState {
-  float *ref, *sum, *zt, *alpha, *beta;
+  float *ref, *sum, *zt, *alpha, *beta, *lift;
 };
 
-struct XentStep {
-  const float* logits;    // chunk x rows
-  const float* factor;    // power of two of each row's f16 form, or null
-  const int32_t* targets;
-  const void* scales;     // row scales of the layer (scale_kind 1, 2), for P
-  const uint8_t* images;
-  uint16_t* probs;        // chunk x rows, or null (no gradient)
-  uint16_t* target_rows;  // M x K: the target's weights in operand form
-  uint32_t* status;
-  XentState st;
-  uint32_t m0;            // first token of the chunk
-  uint32_t n0, rows;      // the piece
-  uint32_t vocab, K, scale_kind, f16, first;
-};
-
-// Sum and maximum over the CTA, in a fixed order.
-__device__ __forceinline__ float2 block_sum_max(float s, float t, float2* part) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, d));
-  }
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = make_float2(s, t);
-  __syncthreads();
-  float2 r = part[0];
-#pragma unroll
-  for (uint32_t k = 1; k < kXentThreads / 32; ++k) {
-    r.x += part[k].x;
-    r.y = fmaxf(r.y, part[k].y);
-  }
-  return r;
+// 2^e for a whole e; 0 below the normal range.
+__device__ __forceinline__ float pow2(float e) {
+  return e < -126.0f ? 0.0f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(fminf(e, 127.0f)) + 127) << 23);
 }
 
-// One CTA a row of the chunk: the row's logits of this piece stay in
-// registers between the maximum, the sum and the probabilities.
-__global__ void __launch_bounds__(kXentThreads) xent_step_kernel(const __grid_constant__ XentStep P) {
-  __shared__ float2 part[kXentThreads / 32];
+// Clears the state, checks the targets and sets lift: f16 probabilities carry
+// the row scale of W, so they are stored under a power of two that puts the
+// largest scale in [2^8, 2^9): a probability of e^4 (kXentSlack) stays below the
+// largest f16, and 11 bits are kept down to 2^-22 of the reference's.
+__global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t M, const int32_t* __restrict__ targets,
+                                                          uint32_t vocab, uint32_t N, uint32_t f16, uint32_t kind,
+                                                          const void* scales, uint32_t* status) {
+  __shared__ float part[32];
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t m = P.m0 + blockIdx.x;
-  const int32_t target = __ldg(P.targets + m);
-  const bool valid = target >= 0 && static_cast<uint32_t>(target) < P.vocab;
-  if (P.first && threadIdx.x == 0 && target >= 0 && !valid) atomicOr(P.status, kStatusBadIndex);
-  const float up = P.factor != nullptr ? __ldcg(P.factor + m) : 1.0f;
-  const float* row = P.logits + static_cast<uint64_t>(blockIdx.x) * P.rows;
-  const uint32_t lim = P.vocab > P.n0 ? min(P.rows, P.vocab - P.n0) : 0u;  // columns that count
-  // -inf past the vocabulary
-  float z[kXentPer][4];
-  float top = -INFINITY;
-#pragma unroll
-  for (uint32_t i = 0; i < kXentPer; ++i) {
-    const uint32_t c = 4 * (threadIdx.x + i * kXentThreads);
-    float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (c < P.rows) q = __ldcg(reinterpret_cast<const float4*>(row + c));
-    const float w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) {
-      z[i][k] = c + k < lim ? w[k] * up : -INFINITY;
-      top = fmaxf(top, z[i][k]);
+  bool bad = false;
+  for (uint32_t m = blockIdx.x * 1024 + threadIdx.x; m < M; m += gridDim.x * 1024) {
+    st.ref[m] = kXentNone;
+    st.sum[m] = 0.0f;
+    const int32_t t = __ldg(targets + m);
+    bad = bad || (t >= 0 && static_cast<uint32_t>(t) >= vocab);
+  }
+  if (bad) atomicOr(status, kStatusBadIndex);
+  if (blockIdx.x != 0) return;
+  float top = 0.0f;
+  if (f16 && (kind == 1 || kind == 2)) {
+    // (N is a multiple of 128)
+    for (uint32_t n = 4 * threadIdx.x; n < N; n += 4096) {
+      float4 v;
+      if (kind == 1) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(scales) + n));
+        v = make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u), __uint_as_float(q.y << 16),
+                        __uint_as_float(q.y & 0xFFFF0000u));
+      } else {
+        v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(scales) + n));
+      }
+      for (const float s : {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)})
+        if (s <= 3.402823466e38f) top = fmaxf(top, s);
     }
   }
-  top = block_sum_max(0.0f, top, part).y;
-  // An infinite reference is replaced by 0, so that +inf gives an infinite sum
-  // and a row of -inf a sum of 0.  NaN stays NaN through the sum.
-  const float ref_old = P.first ? -INFINITY : __ldcg(P.st.ref + m);
-  const float ref = fmaxf(ref_old, top);
-  const float base = isinf(ref) ? 0.0f : ref;
-  // nothing but -inf so far: sums of 0 (or NaN, which 0 keeps)
-  const float keep = ref_old == -INFINITY ? 0.0f : __expf((isinf(ref_old) ? 0.0f : ref_old) - base);
-  const bool here = valid && static_cast<uint32_t>(target) >= P.n0 && static_cast<uint32_t>(target) < P.n0 + P.rows;
-  const uint32_t tc = here ? static_cast<uint32_t>(target) - P.n0 : 0xFFFFFFFFu;
-  float s = 0.0f, big = 0.0f;
 #pragma unroll
-  for (uint32_t i = 0; i < kXentPer; ++i) {
-    const uint32_t c = 4 * (threadIdx.x + i * kXentThreads);
-    float sc[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-    if (P.probs != nullptr && c < P.rows) {
-      if (P.scale_kind == 1) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(P.scales) + P.n0 + c));
-        sc[0] = __uint_as_float(q.x << 16);
-        sc[1] = __uint_as_float(q.x & 0xFFFF0000u);
-        sc[2] = __uint_as_float(q.y << 16);
-        sc[3] = __uint_as_float(q.y & 0xFFFF0000u);
-      } else if (P.scale_kind == 2) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(P.scales) + P.n0 + c));
-        sc[0] = q.x; sc[1] = q.y; sc[2] = q.z; sc[3] = q.w;
-      }
-    }
-#pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) {
-      float e = c + k < lim ? __expf(z[i][k] - base) : 0.0f;
-      if (c + k == tc) {
-        P.st.zt[m] = z[i][k];
-        e = 0.0f;
-      }
-      s += e;
-      z[i][k] = e * sc[k];
-      big = fmaxf(big, fabsf(z[i][k]));
-    }
-  }
-  const float2 r = block_sum_max(s, big, part);
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+  __syncthreads();
   if (threadIdx.x == 0) {
+    for (int k = 1; k < 32; ++k) top = fmaxf(top, part[k]);
+    const int ex = top == 0.0f ? 0 : static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    *st.lift = f16 ? pow2(static_cast<float>(min(126, max(-118, 8 - ex)))) : 1.0f;
+  }
+}
+
+struct XentJoin {
+  XentState st;
+  const float *ref, *sum;  // blocks: [n_blocks][stride], tokens m0 .. m0 + m - 1 from column 0
+  uint32_t stride, n_blocks, m0, m, rows, f16;
+  uint32_t* moved;         // per 32 tokens: blocks under another reference than the piece's
+  uint16_t* probs;         // m x rows, or null
+  // the targets' rows of W
+  const int32_t* targets;
+  const uint8_t* images;
+  uint16_t* target_rows;   // M x K in operand form
+  uint32_t n0, vocab, K;
+};
+
+// 32 tokens a CTA, one a lane; the warps share the blocks and are joined in
+// order.  The largest of a token's block references is the piece's.
+constexpr uint32_t kJoinWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const __grid_constant__ XentJoin P) {
+  __shared__ float part[kJoinWarps][33];
+  __shared__ uint32_t any;
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, col = blockIdx.x * 32 + lane;
+  const bool in = col < P.m;
+  const uint32_t m = P.m0 + col;
+  if (threadIdx.x == 0) any = 0;
+  const float ref_old = in ? __ldcg(P.st.ref + m) : kXentNone;
+  float ref = ref_old;
+  if (in)
+#pragma unroll 8
+    for (uint32_t b = warp; b < P.n_blocks; b += kJoinWarps)
+      ref = fmaxf(ref, __ldcg(P.ref + static_cast<uint64_t>(b) * P.stride + col));
+  part[warp][lane] = ref;
+  __syncthreads();
+#pragma unroll
+  for (uint32_t k = 0; k < kJoinWarps; ++k) ref = fmaxf(ref, part[k][lane]);
+  __syncthreads();
+  float s = 0.0f;
+  bool other = false;
+  if (in)
+#pragma unroll 8
+    for (uint32_t b = warp; b < P.n_blocks; b += kJoinWarps) {
+      const float r = __ldcg(P.ref + static_cast<uint64_t>(b) * P.stride + col);
+      const float v = __ldcg(P.sum + static_cast<uint64_t>(b) * P.stride + col);
+      s += v == 0.0f ? 0.0f : v * pow2(r - ref);
+      other = other || (r != ref && v != 0.0f);
+    }
+  part[warp][lane] = s;
+  if (__any_sync(0xFFFFFFFFu, other) && lane == 0) any = 1;
+  __syncthreads();
+  if (warp == 0 && in) {
+    s = 0.0f;
+#pragma unroll
+    for (uint32_t k = 0; k < kJoinWarps; ++k) s += part[k][lane];
+    const float keep = ref_old == kXentNone ? 0.0f : pow2(ref_old - ref);
+    const float l = __ldcg(P.st.sum + m);
     P.st.ref[m] = ref;
-    P.st.sum[m] = P.first ? r.x : fmaf(__ldcg(P.st.sum + m), keep, r.x);
+    P.st.sum[m] = fmaf(l, keep, s);  // (NaN stays NaN)
+    if (P.probs != nullptr) {
+      P.st.alpha[m] = keep;
+      P.st.beta[m] = 1.0f / __ldcg(P.st.lift);  // a power of two
+      if (lane == 0) P.moved[blockIdx.x] = any;
+    }
   }
   if (P.probs == nullptr) return;
-  // f16: under a power of two that puts the row's largest value in
-  // [2^14, 2^15), undone by beta.  11 bits of every value down to 2^-29 of it.
-  int e2 = 0;
-  if (P.f16 && r.y > 0.0f && r.y <= 3.402823466e38f)
-    e2 = min(126, max(-113, 14 - (static_cast<int>(__float_as_uint(r.y) >> 23) - 127)));
-  const float lift = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
-  if (threadIdx.x == 0) {
-    P.st.alpha[m] = keep;
-    P.st.beta[m] = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-  }
-  uint16_t* out = P.probs + static_cast<uint64_t>(blockIdx.x) * P.rows;
-#pragma unroll
-  for (uint32_t i = 0; i < kXentPer; ++i) {
-    const uint32_t c = 4 * (threadIdx.x + i * kXentThreads);
-    if (c >= P.rows) continue;
-    uint32_t lo, hi;
-    if (!valid) {
-      lo = hi = 0;
-    } else if (P.f16) {
-      const __half2 a = __floats2half2_rn(z[i][0] * lift, z[i][1] * lift);
-      const __half2 b = __floats2half2_rn(z[i][2] * lift, z[i][3] * lift);
-      lo = *reinterpret_cast<const uint32_t*>(&a);
-      hi = *reinterpret_cast<const uint32_t*>(&b);
-    } else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(z[i][0], z[i][1]);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(z[i][2], z[i][3]);
-      lo = *reinterpret_cast<const uint32_t*>(&a);
-      hi = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    *reinterpret_cast<uint2*>(out + c) = make_uint2(lo, hi);
-  }
-  if (here) {
-    // the target's row of W, while its piece is here
-    const uint32_t k_slabs = P.K / 16, rr = tc & 127u;
+  // the targets' rows of W, while their piece is here
+  for (uint32_t k = warp; k < 32; k += kJoinWarps) {
+    const uint32_t row = blockIdx.x * 32 + k;
+    if (row >= P.m) break;
+    const int32_t target = __ldg(P.targets + P.m0 + row);
+    if (target < 0 || static_cast<uint32_t>(target) >= P.vocab || static_cast<uint32_t>(target) - P.n0 >= P.rows) continue;
+    const uint32_t tc = static_cast<uint32_t>(target) - P.n0, k_slabs = P.K / 16, rr = tc & 127u;
     const uint8_t* src = P.images + static_cast<uint64_t>(tc >> 7) * k_slabs * kSlabBytes + rr * 32u;
-    for (uint32_t q = threadIdx.x; q < P.K / 8; q += kXentThreads) {
-      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src + static_cast<uint64_t>(q >> 1) * kSlabBytes +
-                                                           (((q & 1u) ^ ((rr >> 2) & 1u)) << 4)));
-      *reinterpret_cast<uint4*>(P.target_rows + static_cast<uint64_t>(m) * P.K + 8 * q) = v;
+    uint16_t* dst = P.target_rows + static_cast<uint64_t>(P.m0 + row) * P.K;
+#pragma unroll 4
+    for (uint32_t q = lane; q < P.K / 8; q += 32)
+      *reinterpret_cast<uint4*>(dst + 8 * q) = __ldcg(reinterpret_cast<const uint4*>(
+          src + static_cast<uint64_t>(q >> 1) * kSlabBytes + (((q & 1u) ^ ((rr >> 2) & 1u)) << 4)));
+  }
+}
+
+// Probabilities of blocks under another reference than their token's: in the
+// first piece nearly all of them, later hardly any.  A CTA takes 32 tokens and 32
+// blocks, a warp 4 of the tokens; 4 lanes a block, 16 bytes a lane.
+__global__ void __launch_bounds__(256) xent_rescale_kernel(const __grid_constant__ XentJoin P) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (__ldcg(P.moved + blockIdx.x) == 0) return;
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, b = 32 * blockIdx.y + lane;
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k) {
+    const uint32_t col = blockIdx.x * 32 + 4 * warp + k;
+    if (col >= P.m) return;
+    const float ref = __ldcg(P.st.ref + P.m0 + col);
+    const float r = b < P.n_blocks ? __ldcg(P.ref + static_cast<uint64_t>(b) * P.stride + col) : ref;
+    const float f = pow2(r - ref);
+    uint4* row = reinterpret_cast<uint4*>(P.probs + static_cast<uint64_t>(col) * P.rows + 1024 * blockIdx.y);
+    uint4 w[4];
+    float g[4];
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+      g[q] = __shfl_sync(0xFFFFFFFFu, f, 8 * q + lane / 4);
+      if (g[q] != 1.0f) w[q] = __ldcg(row + 32 * q + lane);
+    }
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+      if (g[q] == 1.0f) continue;
+      uint32_t* u = reinterpret_cast<uint32_t*>(&w[q]);
+      if (P.f16) {
+        // (a factor below f16's range leaves nothing of f16 values)
+        const __half2 h = __float2half2_rn(g[q]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(u + i), h);
+          u[i] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+      } else {
+        const __nv_bfloat162 h = __float2bfloat162_rn(g[q]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(u + i), h);
+          u[i] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+      }
+      row[32 * q + lane] = w[q];
     }
   }
 }
@@ -210,18 +242,19 @@ __global__ void __launch_bounds__(kXentThreads) xent_finish_kernel(const __grid_
   const uint32_t m = blockIdx.x;
   const int32_t target = __ldg(P.targets + m);
   const bool valid = target >= 0 && static_cast<uint32_t>(target) < P.vocab;
-  const float ref = __ldcg(P.st.ref + m), l = __ldcg(P.st.sum + m);
-  const float base = isinf(ref) ? 0.0f : ref;
+  // (a row without a finite logit has no reference: its sum, 0 or NaN, stands for itself)
+  const float ref_raw = __ldcg(P.st.ref + m), ref = ref_raw == kXentNone ? 0.0f : ref_raw;
+  const float l = __ldcg(P.st.sum + m);
   const float zt = valid ? __ldcg(P.st.zt + m) : -INFINITY;
-  const float et = valid ? expf(zt - base) : 0.0f;
+  const float dt = fmaf(zt, kLog2E, -ref);  // the target's distance from the reference, units of log 2
+  const float et = valid ? exp2f(dt) : 0.0f;
   const float total = l + et;
   if (threadIdx.x == 0) {
-    P.lse[m] = base + logf(total);
+    const float lse = fmaf(ref, kLn2, logf(total));
+    P.lse[m] = lse;
     float loss = 0.0f;
     // near the reference: log(1 + l / e_t), exact where the loss is small
-    if (valid)
-      loss = isinf(ref) ? P.lse[m] - zt
-                        : zt > base - 20.0f ? log1pf(l * expf(base - zt)) : (base - zt) + logf(total);
+    if (valid) loss = isinf(lse) ? lse - zt : dt > -30.0f ? log1pf(l * exp2f(-dt)) : fmaf(-dt, kLn2, logf(total));
     P.loss[m] = loss;
   }
   if (P.dX == nullptr) return;
@@ -262,6 +295,11 @@ __global__ void __launch_bounds__(kXentThreads) xent_finish_kernel(const __grid_
 
 static size_t aligned(size_t n) { return (n + 1023) / 1024 * 1024; }
 
+// W rows of a piece, most: its images (2 K bytes a row) and a chunk's
+// probabilities are what has to stay in L2.  With few tokens a piece is a row of
+// tiles, and is made as long as there are SMs.
+constexpr uint32_t kXentPieceRows = 8192;
+
 void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms, XentPlan* p) {
   p->M = M;
   p->N = L.N;
@@ -269,17 +307,16 @@ void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms, XentPlan*
   p->grad = grad;
   p->f16 = operand_is_f16(L.dtype);
   p->sms = sms;
-  // pieces of equal size, at most what a row kernel holds in registers
-  const uint32_t blocks = L.N / L.tile_n, most = kXentPieceMax / L.tile_n;
+  const uint32_t few = static_cast<uint32_t>(sms) / ((M + 255) / 256) * 128;
+  const uint32_t blocks = L.N / L.tile_n, most = std::max(kXentPieceRows, few) / L.tile_n;
   const uint32_t pieces = (blocks + most - 1) / most;
   p->piece = (blocks + pieces - 1) / pieces * L.tile_n;
-  // a chunk's logits and probabilities within 96 MB, so that they stay in L2
-  const uint32_t fit = std::max(256u, static_cast<uint32_t>((96ull << 20) / (6ull * p->piece)) / 256 * 256);
+  // chunks of equal size, at most 4096 tokens with probabilities to store
+  const uint32_t fit = grad ? 4096u : 16384u;
   const uint32_t chunks = (M + fit - 1) / fit;
   p->chunk = chunks <= 1 ? M : std::min(M, ((M + chunks - 1) / chunks + 255) / 256 * 256);
   // one plan for every chunk and piece: partial sums only where one chunk
-  // holds all tokens
-  // (the last piece's sum has to have that many ranges too)
+  // holds all tokens (the last piece's sum has to have that many ranges too)
   const uint32_t last = L.N - (L.N - 1) / p->piece * p->piece;
   p->splits = grad && chunks <= 1 ? plan_operand_gemm(true, p->f16, M, last, L.K, 8, sms).splits : 1;
   size_t at = 0;
@@ -290,11 +327,12 @@ void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms, XentPlan*
   };
   const size_t MK = static_cast<size_t>(M) * L.K;
   p->off_images = take(operand_bytes(p->piece, L.K));
-  p->off_logits = take(static_cast<size_t>(p->chunk) * p->piece * 4);
   p->off_probs = take(grad ? static_cast<size_t>(p->chunk) * p->piece * 2 : 0);
+  p->off_blocks = take(static_cast<size_t>(p->chunk) * (p->piece / 32) * 8);
+  p->off_moved = take((static_cast<size_t>(p->chunk) + 31) / 32 * 4);
   p->off_x16 = take(p->f16 ? MK * 2 : 0);
   p->off_factor = take(p->f16 ? static_cast<size_t>(M) * 4 : 0);
-  p->off_state = take(static_cast<size_t>(M) * 4 * 5);
+  p->off_state = take((static_cast<size_t>(M) * 5 + 1) * 4);
   p->off_acc = take(grad ? MK * 4 * p->splits : 0);
   p->off_target = take(grad ? MK * 2 : 0);
   p->bytes = at;
@@ -303,15 +341,19 @@ void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms, XentPlan*
 cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a, void* ws, cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint8_t* images = w + p.off_images;
-  float* logits = reinterpret_cast<float*>(w + p.off_logits);
   uint16_t* probs = p.grad ? reinterpret_cast<uint16_t*>(w + p.off_probs) : nullptr;
+  float* block_ref = reinterpret_cast<float*>(w + p.off_blocks);
+  float* block_sum = block_ref + static_cast<size_t>(p.chunk) * (p.piece / 32);
   float* acc = reinterpret_cast<float*>(w + p.off_acc);
   uint16_t* target_rows = reinterpret_cast<uint16_t*>(w + p.off_target);
   float* state = reinterpret_cast<float*>(w + p.off_state);
-  XentState st{state, state + p.M, state + 2ull * p.M, state + 3ull * p.M, state + 4ull * p.M};
+  const XentState st{state, state + p.M, state + 2ull * p.M, state + 3ull * p.M, state + 4ull * p.M,
+                     state + 5ull * p.M};
+  cudaError_t e = launch_pdl(xent_begin_kernel, dim3(std::min(64u, (p.M + 1023) / 1024)), dim3(1024), 0, stream, st, p.M,
+                             a.targets, a.vocab, p.N, p.f16, a.scale_kind, a.scales, a.status);
+  if (e != cudaSuccess) return e;
   const uint16_t* x = a.X;
   const float* factor = nullptr;
-  cudaError_t e;
   if (p.f16) {
     uint16_t* x16 = reinterpret_cast<uint16_t*>(w + p.off_x16);
     float* f = reinterpret_cast<float*>(w + p.off_factor);
@@ -327,45 +369,57 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
     if (e != cudaSuccess) return e;
     for (uint32_t m0 = 0; m0 < p.M; m0 += p.chunk) {
       const uint32_t m = std::min(p.chunk, p.M - m0);
-      OperandGemmOut fwd;
-      fwd.out32 = logits;
-      fwd.ld = rows;
-      fwd.scale_kind = a.scale_kind;
-      fwd.scales = a.scale_kind == 1 ? static_cast<const void*>(static_cast<const uint16_t*>(a.scales) + n0)
-                   : a.scale_kind == 2 ? static_cast<const void*>(static_cast<const float*>(a.scales) + n0) : nullptr;
+      XentEpilogue f;
+      f.factor = factor ? factor + m0 : nullptr;
+      f.scale_kind = a.scale_kind;
+      f.scales = a.scale_kind == 1 ? static_cast<const void*>(static_cast<const uint16_t*>(a.scales) + n0)
+                 : a.scale_kind == 2 ? static_cast<const void*>(static_cast<const float*>(a.scales) + n0) : nullptr;
+      f.lift = st.lift;
+      f.ref_in = st.ref + m0;
+      f.targets = a.targets + m0;
+      f.zt = st.zt + m0;
+      f.ref = block_ref;
+      f.sum = block_sum;
+      f.stride = p.chunk;
+      f.probs = probs;
+      f.n0 = n0;
+      f.vocab = a.vocab;
       e = launch_operand_gemm(plan_operand_gemm(false, p.f16, m, rows, p.K, 1, p.sms), images,
-                              x + static_cast<uint64_t>(m0) * p.K, fwd, a.status, stream);
+                              x + static_cast<uint64_t>(m0) * p.K, nullptr, &f, a.status, stream);
       if (e != cudaSuccess) return e;
-      XentStep s;
-      s.logits = logits;
-      s.factor = factor;
-      s.targets = a.targets;
-      s.scales = a.scales;
-      s.images = images;
-      s.probs = probs;
-      s.target_rows = target_rows;
-      s.status = a.status;
-      s.st = st;
-      s.m0 = m0;
-      s.n0 = n0;
-      s.rows = rows;
-      s.vocab = a.vocab;
-      s.K = p.K;
-      s.scale_kind = a.scale_kind;
-      s.f16 = p.f16;
-      s.first = n0 == 0;
-      e = launch_pdl(xent_step_kernel, dim3(m), dim3(kXentThreads), 0, stream, s);
+      XentJoin j;
+      j.st = st;
+      j.ref = block_ref;
+      j.sum = block_sum;
+      j.stride = p.chunk;
+      j.n_blocks = rows / 32;
+      j.m0 = m0;
+      j.m = m;
+      j.rows = rows;
+      j.f16 = p.f16;
+      j.moved = reinterpret_cast<uint32_t*>(w + p.off_moved);
+      j.probs = probs;
+      j.targets = a.targets;
+      j.images = images;
+      j.target_rows = target_rows;
+      j.n0 = n0;
+      j.vocab = a.vocab;
+      j.K = p.K;
+      const uint32_t groups = (m + 31) / 32;
+      e = launch_pdl(xent_join_kernel, dim3(groups), dim3(32 * kJoinWarps), 0, stream, j);
       if (e != cudaSuccess) return e;
       if (!p.grad) continue;
+      e = launch_pdl(xent_rescale_kernel, dim3(groups, (j.n_blocks + 31) / 32), dim3(256), 0, stream, j);
+      if (e != cudaSuccess) return e;
       OperandGemmPlan tp = plan_operand_gemm(true, p.f16, m, rows, p.K, 1, p.sms);
       tp.splits = p.splits;
-      OperandGemmOut back;
+      OperandGemmOut back = {};
       back.out32 = acc + static_cast<uint64_t>(m0) * p.K;
       back.split_stride = MK;
       back.ld = p.K;
       back.alpha = n0 == 0 ? nullptr : st.alpha + m0;
       back.beta = st.beta + m0;
-      e = launch_operand_gemm(tp, images, probs, back, a.status, stream);
+      e = launch_operand_gemm(tp, images, probs, &back, nullptr, a.status, stream);
       if (e != cudaSuccess) return e;
     }
   }

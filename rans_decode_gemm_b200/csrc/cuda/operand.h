@@ -71,12 +71,12 @@ struct OperandGemmOut {
 
 // What happens to the logits: they are folded into softmax sums, 32 rows of W
 // (a block) at a time.  With r a reference in units of log 2 (a whole number),
-//   e[m][n] = 2^(z[m][n] log2(e) - r),  sum[block][m] = sum of the block's e,
+//   e[m][n] = 2^(z[m][n] log2(e) - r),  blocks[block][m] = (r, sum of the block's e),
 //   probs[m * rows + n] = e * s_n * lift (16-bit; null: not stored),
 // except that rows n0 + n >= vocab count for nothing, and the token's target has
 // its logit stored in zt[m] and e taken as 0.  r is ref_in[m], unless the
 // block's largest logit lies more than kXentSlack above it: then r is that
-// logit, rounded up.  ref[block][m] says which was used.
+// logit, rounded up.
 constexpr float kXentSlack = 5.75f;    // e^4: what probabilities may exceed 1 by
 constexpr float kXentNone = -1.0e30f;  // the reference before any logit
 struct XentEpilogue {
@@ -87,7 +87,7 @@ struct XentEpilogue {
   const float* ref_in;
   const int32_t* targets;
   float* zt;
-  float *ref, *sum;        // [rows / 32][stride]
+  float2* blocks;          // [rows / 32][stride]
   uint32_t stride;
   uint16_t* probs;
   uint32_t n0, vocab;

@@ -145,11 +145,7 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
     }
   }
   const float sum = across_lanes(x, lane, [](float a, float b) { return a + b; });
-  if (m_in) {
-    const uint64_t at = static_cast<uint64_t>(c / 32) * E.stride + m + lane;
-    E.sum[at] = sum;
-    E.ref[at] = ref;
-  }
+  if (m_in) E.blocks[static_cast<uint64_t>(c / 32) * E.stride + m + lane] = make_float2(ref, sum);
 }
 
 template <bool kTrans>

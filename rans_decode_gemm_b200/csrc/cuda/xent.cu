@@ -97,9 +97,9 @@ __global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t
 
 struct XentJoin {
   XentState st;
-  const float *ref, *sum;  // blocks: [n_blocks][stride], tokens m0 .. m0 + m - 1 from column 0
+  const float2* blocks;    // (reference, sum): [n_blocks][stride], tokens m0 .. m0 + m - 1 from column 0
   uint32_t stride, n_blocks, m0, m, rows, f16;
-  uint32_t* moved;         // per 32 tokens: blocks under another reference than the piece's
+  uint32_t* moved;         // per 32 tokens, one bit each: has blocks under another reference
   uint16_t* probs;         // m x rows, or null
   // the targets' rows of W
   const int32_t* targets;
@@ -108,54 +108,69 @@ struct XentJoin {
   uint32_t n0, vocab, K;
 };
 
-// 32 tokens a CTA, one a lane; the warps share the blocks and are joined in
-// order.  The largest of a token's block references is the piece's.
-constexpr uint32_t kJoinWarps = 16;
+// 32 tokens a CTA, one a lane; the warps share the blocks, 8 loads in flight
+// each, and are joined in order.  The largest of a token's block references is
+// the piece's.
+constexpr uint32_t kJoinWarps = 16, kJoinBatch = 8;
 __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const __grid_constant__ XentJoin P) {
-  __shared__ float part[kJoinWarps][33];
-  __shared__ uint32_t any;
+  __shared__ float part_ref[kJoinWarps][33], part_low[kJoinWarps][33], part_sum[kJoinWarps][33];
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, col = blockIdx.x * 32 + lane;
   const bool in = col < P.m;
   const uint32_t m = P.m0 + col;
-  if (threadIdx.x == 0) any = 0;
-  const float ref_old = in ? __ldcg(P.st.ref + m) : kXentNone;
-  float ref = ref_old;
-  if (in)
-#pragma unroll 8
-    for (uint32_t b = warp; b < P.n_blocks; b += kJoinWarps)
-      ref = fmaxf(ref, __ldcg(P.ref + static_cast<uint64_t>(b) * P.stride + col));
-  part[warp][lane] = ref;
-  __syncthreads();
+  // (ref, s): sums under the largest reference so far; low: the smallest that a
+  // sum other than 0 came under
+  float ref = kXentNone, low = INFINITY, s = 0.0f;
+  for (uint32_t b0 = warp; b0 < P.n_blocks; b0 += kJoinBatch * kJoinWarps) {
+    float2 u[kJoinBatch];
 #pragma unroll
-  for (uint32_t k = 0; k < kJoinWarps; ++k) ref = fmaxf(ref, part[k][lane]);
-  __syncthreads();
-  float s = 0.0f;
-  bool other = false;
-  if (in)
-#pragma unroll 8
-    for (uint32_t b = warp; b < P.n_blocks; b += kJoinWarps) {
-      const float r = __ldcg(P.ref + static_cast<uint64_t>(b) * P.stride + col);
-      const float v = __ldcg(P.sum + static_cast<uint64_t>(b) * P.stride + col);
-      s += v == 0.0f ? 0.0f : v * pow2(r - ref);
-      other = other || (r != ref && v != 0.0f);
+    for (uint32_t k = 0; k < kJoinBatch; ++k) {
+      const uint32_t b = b0 + k * kJoinWarps;
+      u[k] = in && b < P.n_blocks ? __ldcg(P.blocks + static_cast<uint64_t>(b) * P.stride + col)
+                                  : make_float2(kXentNone, 0.0f);
     }
-  part[warp][lane] = s;
-  if (__any_sync(0xFFFFFFFFu, other) && lane == 0) any = 1;
+    float top = ref;
+#pragma unroll
+    for (uint32_t k = 0; k < kJoinBatch; ++k) top = fmaxf(top, u[k].x);
+    s = s == 0.0f ? 0.0f : s * pow2(ref - top);
+    ref = top;
+#pragma unroll
+    for (uint32_t k = 0; k < kJoinBatch; ++k) {
+      if (u[k].y == 0.0f) continue;
+      s += u[k].y * pow2(u[k].x - ref);
+      low = fminf(low, u[k].x);
+    }
+  }
+  part_ref[warp][lane] = ref;
+  part_low[warp][lane] = low;
+  part_sum[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && in) {
+  if (warp == 0) {
+    const float ref_old = in ? __ldcg(P.st.ref + m) : kXentNone;
+    const float l = in ? __ldcg(P.st.sum + m) : 0.0f;
+    ref = ref_old;
+#pragma unroll
+    for (uint32_t k = 0; k < kJoinWarps; ++k) {
+      ref = fmaxf(ref, part_ref[k][lane]);
+      low = fminf(low, part_low[k][lane]);
+    }
     s = 0.0f;
 #pragma unroll
-    for (uint32_t k = 0; k < kJoinWarps; ++k) s += part[k][lane];
-    const float keep = ref_old == kXentNone ? 0.0f : pow2(ref_old - ref);
-    const float l = __ldcg(P.st.sum + m);
-    P.st.ref[m] = ref;
-    P.st.sum[m] = fmaf(l, keep, s);  // (NaN stays NaN)
-    if (P.probs != nullptr) {
-      P.st.alpha[m] = keep;
-      P.st.beta[m] = 1.0f / __ldcg(P.st.lift);  // a power of two
-      if (lane == 0) P.moved[blockIdx.x] = any;
+    for (uint32_t k = 0; k < kJoinWarps; ++k) {
+      const float v = part_sum[k][lane];
+      s += v == 0.0f ? 0.0f : v * pow2(part_ref[k][lane] - ref);
+    }
+    const uint32_t moved = __ballot_sync(0xFFFFFFFFu, in && low < ref);
+    if (in) {
+      const float keep = ref_old == kXentNone ? 0.0f : pow2(ref_old - ref);
+      P.st.ref[m] = ref;
+      P.st.sum[m] = fmaf(l, keep, s);  // (NaN stays NaN)
+      if (P.probs != nullptr) {
+        P.st.alpha[m] = keep;
+        P.st.beta[m] = 1.0f / __ldcg(P.st.lift);  // a power of two
+        if (lane == 0) P.moved[blockIdx.x] = moved;
+      }
     }
   }
   if (P.probs == nullptr) return;
@@ -181,14 +196,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const __grid
 __global__ void __launch_bounds__(256) xent_rescale_kernel(const __grid_constant__ XentJoin P) {
   griddep_wait();
   griddep_launch_dependents();
-  if (__ldcg(P.moved + blockIdx.x) == 0) return;
+  const uint32_t moved = __ldcg(P.moved + blockIdx.x);
+  if (moved == 0) return;
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, b = 32 * blockIdx.y + lane;
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k) {
     const uint32_t col = blockIdx.x * 32 + 4 * warp + k;
-    if (col >= P.m) return;
+    if (((moved >> (4 * warp + k)) & 1u) == 0) continue;
     const float ref = __ldcg(P.st.ref + P.m0 + col);
-    const float r = b < P.n_blocks ? __ldcg(P.ref + static_cast<uint64_t>(b) * P.stride + col) : ref;
+    const float r = b < P.n_blocks ? __ldcg(P.blocks + static_cast<uint64_t>(b) * P.stride + col).x : ref;
     const float f = pow2(r - ref);
     uint4* row = reinterpret_cast<uint4*>(P.probs + static_cast<uint64_t>(col) * P.rows + 1024 * blockIdx.y);
     uint4 w[4];
@@ -295,30 +311,65 @@ __global__ void __launch_bounds__(kXentThreads) xent_finish_kernel(const __grid_
 
 static size_t aligned(size_t n) { return (n + 1023) / 1024 * 1024; }
 
-// W rows of a piece, most: its images (2 K bytes a row) and a chunk's
-// probabilities are what has to stay in L2.  With few tokens a piece is a row of
-// tiles, and is made as long as there are SMs.
-constexpr uint32_t kXentPieceRows = 8192;
+// W rows of a piece, most, in blocks of 128: its images (2 K bytes a row) and a
+// chunk's probabilities are what has to stay in L2.  With few tokens a piece is
+// a row of tiles, and may be as long as there are SMs.
+constexpr uint32_t kXentMostBlocks = 80, kXentLeastBlocks = 24;
 
-void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms, XentPlan* p) {
+static uint32_t waves(uint64_t tiles, uint32_t sms) { return static_cast<uint32_t>((tiles + sms - 1) / sms); }
+
+void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms_in, XentPlan* p) {
+  const uint32_t sms = static_cast<uint32_t>(sms_in);
   p->M = M;
   p->N = L.N;
   p->K = L.K;
   p->grad = grad;
   p->f16 = operand_is_f16(L.dtype);
-  p->sms = sms;
-  const uint32_t few = static_cast<uint32_t>(sms) / ((M + 255) / 256) * 128;
-  const uint32_t blocks = L.N / L.tile_n, most = std::max(kXentPieceRows, few) / L.tile_n;
-  const uint32_t pieces = (blocks + most - 1) / most;
-  p->piece = (blocks + pieces - 1) / pieces * L.tile_n;
+  p->sms = sms_in;
   // chunks of equal size, at most 4096 tokens with probabilities to store
   const uint32_t fit = grad ? 4096u : 16384u;
   const uint32_t chunks = (M + fit - 1) / fit;
   p->chunk = chunks <= 1 ? M : std::min(M, ((M + chunks - 1) / chunks + 255) / 256 * 256);
-  // one plan for every chunk and piece: partial sums only where one chunk
-  // holds all tokens (the last piece's sum has to have that many ranges too)
-  const uint32_t last = L.N - (L.N - 1) / p->piece * p->piece;
-  p->splits = grad && chunks <= 1 ? plan_operand_gemm(true, p->f16, M, last, L.K, 8, sms).splits : 1;
+  // the piece whose tiles fill whole rounds of the SMs best over the vocabulary;
+  // a piece more costs about a quarter of a round (its join, and the decoder's
+  // and the products' ends)
+  const uint32_t m_blocks = (p->chunk + 255) / 256, blocks = L.N / 128, unit = L.tile_n / 128;
+  const uint32_t most = std::min(blocks, std::max(kXentMostBlocks, sms / m_blocks)) / unit * unit;
+  uint32_t best = most;
+  uint64_t best_cost = ~0ull;
+  for (uint32_t b = most; b >= std::min(most, kXentLeastBlocks); b -= unit) {
+    const uint32_t whole = blocks / b, rest = blocks % b;
+    const uint64_t cost = 4ull * (static_cast<uint64_t>(whole) * waves(static_cast<uint64_t>(b) * m_blocks, sms) +
+                                  waves(static_cast<uint64_t>(rest) * m_blocks, sms)) + whole + (rest != 0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = b;
+    }
+    if (b <= unit) break;
+  }
+  p->piece = best * 128;
+  // The gradient's product has K / 128 x m_blocks tiles whatever the piece.  Its
+  // sum over n is cut where there are too few tiles, or where 2 or 4 ranges fill
+  // the SMs' last round better by more than what their partial sums cost (each
+  // is read and written once a piece, about 8 stages' time a tile).
+  p->splits = 1;
+  if (grad) {
+    const uint32_t last = L.N - (L.N - 1) / p->piece * p->piece;  // the last piece is cut likewise
+    const OperandGemmPlan g = plan_operand_gemm(true, p->f16, p->chunk, last, L.K, 8, sms_in);
+    p->splits = g.splits;
+    if (g.splits == 1) {
+      const uint64_t tiles = static_cast<uint64_t>((L.K + 127) / 128) * ((p->chunk + g.bn - 1) / g.bn);
+      const uint32_t stages = p->piece / 64;
+      uint64_t least = static_cast<uint64_t>(waves(tiles, sms)) * stages;
+      for (uint32_t s = 2; s <= 4 && last / 64 >= s; s *= 2) {
+        const uint64_t t = static_cast<uint64_t>(waves(tiles * s, sms)) * (stages / s + 1) + 8 * s;
+        if (t < least) {
+          least = t;
+          p->splits = s;
+        }
+      }
+    }
+  }
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t o = at;
@@ -342,8 +393,7 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint8_t* images = w + p.off_images;
   uint16_t* probs = p.grad ? reinterpret_cast<uint16_t*>(w + p.off_probs) : nullptr;
-  float* block_ref = reinterpret_cast<float*>(w + p.off_blocks);
-  float* block_sum = block_ref + static_cast<size_t>(p.chunk) * (p.piece / 32);
+  float2* blocks = reinterpret_cast<float2*>(w + p.off_blocks);
   float* acc = reinterpret_cast<float*>(w + p.off_acc);
   uint16_t* target_rows = reinterpret_cast<uint16_t*>(w + p.off_target);
   float* state = reinterpret_cast<float*>(w + p.off_state);
@@ -378,8 +428,7 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       f.ref_in = st.ref + m0;
       f.targets = a.targets + m0;
       f.zt = st.zt + m0;
-      f.ref = block_ref;
-      f.sum = block_sum;
+      f.blocks = blocks;
       f.stride = p.chunk;
       f.probs = probs;
       f.n0 = n0;
@@ -389,8 +438,7 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       if (e != cudaSuccess) return e;
       XentJoin j;
       j.st = st;
-      j.ref = block_ref;
-      j.sum = block_sum;
+      j.blocks = blocks;
       j.stride = p.chunk;
       j.n_blocks = rows / 32;
       j.m0 = m0;

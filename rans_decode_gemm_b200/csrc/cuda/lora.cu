@@ -63,14 +63,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void ldsm2(uint32_t& a, uint32_t& b, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm2_t(uint32_t& a, uint32_t& b, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-               : "=r"(a), "=r"(b) : "r"(addr) : "memory");
-}
-
 // Rows of a staged tile are an odd number of 16-byte chunks apart, so that the 8
 // rows a matrix load touches lie in different banks.
 constexpr uint32_t kChunkRow = 9 * 16;  // 64 values and one chunk
@@ -287,13 +279,17 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
     for (uint32_t ks = ks0; ks < ks1; ++ks) {
       uint32_t f[4];
       ldsm4(f, xs + (row0 + (lane & 15u)) * kChunkRow + (2 * ks + (lane >> 4)) * 16);
+      // two blocks of 8 ranks a load (lanes 16-31 address the second; where there
+      // is none, the first again, unused)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
+      for (int j = 0; j < NJ; j += 2) {
         if (j < nj) {
-          uint32_t b0, b1;
-          if constexpr (!kCols) ldsm2(b0, b1, wsm + (8 * j + (lane & 7u)) * kChunkRow + (2 * ks + ((lane >> 3) & 1u)) * 16);
-          else ldsm2_t(b0, b1, wsm + (16 * ks + (lane & 15u)) * odd_row(P.rank) + j * 16);
-          mma_bf16(acc[j], f[0], f[1], f[2], f[3], b0, b1);
+          const uint32_t jl = j + 1 < nj ? j + (lane >> 4) : j;
+          uint32_t q[4];
+          if constexpr (!kCols) ldsm4(q, wsm + (8 * jl + (lane & 7u)) * kChunkRow + (2 * ks + ((lane >> 3) & 1u)) * 16);
+          else ldsm4_t(q, wsm + (16 * ks + (lane & 15u)) * odd_row(P.rank) + jl * 16);
+          mma_bf16(acc[j], f[0], f[1], f[2], f[3], q[0], q[1]);
+          if (j + 1 < nj) mma_bf16(acc[j + 1], f[0], f[1], f[2], f[3], q[2], q[3]);
         }
       }
     }
@@ -552,10 +548,12 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
 
 // ---- outer: the sum over an adapter's tokens of z^T t ---------------------------
 // out[c][j] = sum_p z[perm[p]][c] * h[p][j] for one adapter, in dB's layout (C x
-// rank) or dA's (rank x C, kRankMajor).  A CTA takes 64 columns c, 16 a warp, and
-// all ranks; a stage is 64 positions of z and of h's two parts, both read by
-// transposing matrix loads.
-constexpr uint32_t kOuterThreads = 128, kOuterStages = 3;
+// rank) or dA's (rank x C, kRankMajor).  A CTA takes 64 columns c and all ranks;
+// a stage is 64 positions of z and of h's two parts, both read by transposing
+// matrix loads.  Warps 0-3 have 16 columns each and the stage's first 32
+// positions, warps 4-7 the same columns and the other 32; the halves are added
+// at the end.  The tokens of a stage are looked up a stage before its loads.
+constexpr uint32_t kOuterThreads = 256, kOuterStages = 3;
 
 struct OuterDev {
   LoraGroups G;
@@ -575,19 +573,28 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const __grid_
   const uint32_t a = blockIdx.y, c0 = blockIdx.x * 64;
   const uint32_t p_begin = __ldcg(P.G.off + a), p_end = __ldcg(P.G.off + a + 1);
   const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
-  const uint32_t r16 = (P.rank + 15) / 16 * 16, nj = P.rank / 8;
+  const uint32_t cw = 16 * (warp & 3u), half = warp >> 2;
+  const uint32_t r16 = (P.rank + 15) / 16 * 16, nj2 = r16 / 16;
   const uint32_t h_row = odd_row(r16), h_bytes = 64 * h_row, stage = outer_stage_bytes(r16);
   const uint32_t base = smem_u32(stages_smem);
   const bool col_in = c0 + 8 * (tid % 8) < P.C;
-  auto load = [&](uint32_t slot, uint32_t p0) {
-    const uint32_t zs = base + slot * stage, hsm = zs + 64 * kChunkRow;
+  const uint32_t n_steps = (p_end - p_begin + 63) / 64;
+  // this thread's two rows of z: positions tid / 8 and tid / 8 + 32 of a stage
+  uint32_t ahead[2];
+  auto look = [&](uint32_t it) {
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-      const uint32_t row = tid / 8 + 16 * i;
-      const uint32_t m = p0 + row < p_end ? __ldcg(P.G.perm + p0 + row) : kNoToken;
-      const bool in = m != kNoToken && col_in;
-      cp16(zs + row * kChunkRow + (tid % 8) * 16, P.z + (in ? static_cast<uint64_t>(m) * P.C + c0 + 8 * (tid % 8) : 0ull),
-           in);
+    for (uint32_t i = 0; i < 2; ++i) {
+      const uint32_t p = p_begin + 64 * it + tid / 8 + 32 * i;
+      ahead[i] = p < p_end ? __ldcg(P.G.perm + p) : kNoToken;
+    }
+  };
+  auto load = [&](uint32_t it) {
+    const uint32_t zs = base + (it % kOuterStages) * stage, hsm = zs + 64 * kChunkRow, p0 = p_begin + 64 * it;
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) {
+      const bool in = ahead[i] != kNoToken && col_in;
+      cp16(zs + (tid / 8 + 32 * i) * kChunkRow + (tid % 8) * 16,
+           P.z + (in ? static_cast<uint64_t>(ahead[i]) * P.C + c0 + 8 * (tid % 8) : 0ull), in);
     }
     const uint32_t per = r16 / 8;
     for (uint32_t i = tid; i < 128 * per; i += kOuterThreads) {
@@ -597,51 +604,75 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const __grid_
            P.hp + (in ? (row >> 6) * P.hp_stride + static_cast<uint64_t>(p) * r16 + 8 * q : 0ull), in);
     }
   };
-  const uint32_t n_steps = (p_end - p_begin + 63) / 64;
+  look(0);
 #pragma unroll
   for (uint32_t i = 0; i + 1 < kOuterStages; ++i) {
-    if (i < n_steps) load(i, p_begin + 64 * i);
+    if (i < n_steps) {
+      load(i);
+      look(i + 1);
+    }
     cp_commit();
   }
   float acc[NJ][4] = {};
   for (uint32_t it = 0; it < n_steps; ++it) {
     cp_wait<kOuterStages - 2>();
     __syncthreads();
-    if (it + kOuterStages - 1 < n_steps) load((it + kOuterStages - 1) % kOuterStages, p_begin + 64 * (it + kOuterStages - 1));
+    if (it + kOuterStages - 1 < n_steps) {
+      load(it + kOuterStages - 1);
+      look(it + kOuterStages);
+    }
     cp_commit();
     const uint32_t zs = base + (it % kOuterStages) * stage, hsm = zs + 64 * kChunkRow;
     const uint32_t n16 = min(4u, (p_end - p_begin - 64 * it) / 16);
-    for (uint32_t ks = 0; ks < n16; ++ks) {
-      uint32_t f[4];
-      ldsm4_t(f, zs + (16 * ks + (lane & 7u) + ((lane >> 4) << 3)) * kChunkRow + (2 * warp + ((lane >> 3) & 1u)) * 16);
-      const uint32_t hr = hsm + (16 * ks + (lane & 15u)) * h_row;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        if (j < nj) {
-          uint32_t b0, b1, l0, l1;
-          ldsm2_t(b0, b1, hr + j * 16);
-          ldsm2_t(l0, l1, hr + h_bytes + j * 16);
-          mma_bf16(acc[j], f[0], f[1], f[2], f[3], b0, b1);
-          mma_bf16(acc[j], f[0], f[1], f[2], f[3], l0, l1);
+    for (uint32_t k = 0; k < 2; ++k) {
+      const uint32_t ks = 2 * half + k;
+      if (ks >= n16) break;
+      uint32_t f[4];
+      ldsm4_t(f, zs + (16 * ks + (lane & 7u) + ((lane >> 4) << 3)) * kChunkRow + (cw / 8 + ((lane >> 3) & 1u)) * 16);
+      // two blocks of 8 ranks a load: lanes 16-31 address the second
+      const uint32_t hr = hsm + (16 * ks + (lane & 15u)) * h_row + (lane >> 4) * 16;
+#pragma unroll
+      for (int j = 0; j < NJ / 2; ++j) {
+        if (j < nj2) {
+          uint32_t hi[4], lo[4];
+          ldsm4_t(hi, hr + j * 32);
+          ldsm4_t(lo, hr + h_bytes + j * 32);
+          mma_bf16(acc[2 * j], f[0], f[1], f[2], f[3], hi[0], hi[1]);
+          mma_bf16(acc[2 * j + 1], f[0], f[1], f[2], f[3], hi[2], hi[3]);
+          mma_bf16(acc[2 * j], f[0], f[1], f[2], f[3], lo[0], lo[1]);
+          mma_bf16(acc[2 * j + 1], f[0], f[1], f[2], f[3], lo[2], lo[3]);
         }
       }
     }
   }
-  const uint32_t c = c0 + 16 * warp + g;
-  if (c0 + 16 * warp >= P.C) return;  // (C is a multiple of 16)
+  cp_wait<0>();
+  __syncthreads();
+  float4* other = reinterpret_cast<float4*>(stages_smem);  // the second half's sums: [rank blocks][4 warps][32 lanes]
+  const uint32_t nj = P.rank / 8;
+  if (half == 1) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (j < nj) other[(j * 4 + (warp & 3u)) * 32 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+  }
+  __syncthreads();
+  if (half == 1 || c0 + cw >= P.C) return;  // (C is a multiple of 16)
+  const uint32_t c = c0 + cw + g;
   float* out = P.out + static_cast<uint64_t>(a) * P.C * P.rank;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     if (j < nj) {
+      const float4 v = other[(j * 4 + warp) * 32 + lane];
+      const float s0 = acc[j][0] + v.x, s1 = acc[j][1] + v.y, s2 = acc[j][2] + v.z, s3 = acc[j][3] + v.w;
       const uint32_t r = 8 * j + 2 * t;
       if constexpr (kRankMajor) {
-        out[static_cast<uint64_t>(r) * P.C + c] = acc[j][0];
-        out[static_cast<uint64_t>(r + 1) * P.C + c] = acc[j][1];
-        out[static_cast<uint64_t>(r) * P.C + c + 8] = acc[j][2];
-        out[static_cast<uint64_t>(r + 1) * P.C + c + 8] = acc[j][3];
+        out[static_cast<uint64_t>(r) * P.C + c] = s0;
+        out[static_cast<uint64_t>(r + 1) * P.C + c] = s1;
+        out[static_cast<uint64_t>(r) * P.C + c + 8] = s2;
+        out[static_cast<uint64_t>(r + 1) * P.C + c + 8] = s3;
       } else {
-        *reinterpret_cast<float2*>(out + static_cast<uint64_t>(c) * P.rank + r) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2*>(out + static_cast<uint64_t>(c + 8) * P.rank + r) = make_float2(acc[j][2], acc[j][3]);
+        *reinterpret_cast<float2*>(out + static_cast<uint64_t>(c) * P.rank + r) = make_float2(s0, s1);
+        *reinterpret_cast<float2*>(out + static_cast<uint64_t>(c + 8) * P.rank + r) = make_float2(s2, s3);
       }
     }
   }
@@ -670,7 +701,7 @@ static uint32_t likely_tiles(uint32_t M, uint32_t tm, uint32_t n) {
 
 // Ranges of a sum over C: enough CTAs for the SMs, at least 256 values each.
 static void split_range(uint32_t C, uint32_t tiles, uint32_t most, int sms, uint32_t* splits, uint32_t* len) {
-  uint32_t want = std::max(1u, 2u * static_cast<uint32_t>(sms) / std::max(1u, tiles));
+  uint32_t want = std::max(1u, 4u * static_cast<uint32_t>(sms) / std::max(1u, tiles));
   want = std::min({want, most, std::max(1u, C / 256)});
   *len = ((C + want - 1) / want + 63) / 64 * 64;
   *splits = (C + *len - 1) / *len;

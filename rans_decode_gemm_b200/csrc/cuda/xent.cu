@@ -173,35 +173,35 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const __grid
       }
     }
   }
-  if (P.probs == nullptr) return;
-  // the targets' rows of W, while their piece is here
-  for (uint32_t k = warp; k < 32; k += kJoinWarps) {
-    const uint32_t row = blockIdx.x * 32 + k;
-    if (row >= P.m) break;
-    const int32_t target = __ldg(P.targets + P.m0 + row);
-    if (target < 0 || static_cast<uint32_t>(target) >= P.vocab || static_cast<uint32_t>(target) - P.n0 >= P.rows) continue;
-    const uint32_t tc = static_cast<uint32_t>(target) - P.n0, k_slabs = P.K / 16, rr = tc & 127u;
-    const uint8_t* src = P.images + static_cast<uint64_t>(tc >> 7) * k_slabs * kSlabBytes + rr * 32u;
-    uint16_t* dst = P.target_rows + static_cast<uint64_t>(P.m0 + row) * P.K;
-#pragma unroll 4
-    for (uint32_t q = lane; q < P.K / 8; q += 32)
-      *reinterpret_cast<uint4*>(dst + 8 * q) = __ldcg(reinterpret_cast<const uint4*>(
-          src + static_cast<uint64_t>(q >> 1) * kSlabBytes + (((q & 1u) ^ ((rr >> 2) & 1u)) << 4)));
-  }
 }
 
-// Probabilities of blocks under another reference than their token's: in the
-// first piece nearly all of them, later hardly any.  A CTA takes 32 tokens and 32
-// blocks, a warp 4 of the tokens; 4 lanes a block, 16 bytes a lane.
-__global__ void __launch_bounds__(256) xent_rescale_kernel(const __grid_constant__ XentJoin P) {
+// What the transposed product and the end need of a piece.  Probabilities of
+// blocks under another reference than their token's are rescaled: in the first
+// piece nearly all of them, later hardly any.  And targets in the piece have
+// their rows of W copied while it is here.  A CTA takes 32 tokens, 32 blocks and a
+// share of the columns, a warp 4 of the tokens; 4 lanes a block, 16 bytes a lane.
+__global__ void __launch_bounds__(256) xent_piece_kernel(const __grid_constant__ XentJoin P) {
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t moved = __ldcg(P.moved + blockIdx.x);
-  if (moved == 0) return;
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, b = 32 * blockIdx.y + lane;
+  const uint32_t row0 = blockIdx.x * 32 + 4 * warp;
+  const int32_t mine = lane < 4 && row0 + lane < P.m ? __ldg(P.targets + P.m0 + row0 + lane) : -1;
+  const bool here = mine >= 0 && static_cast<uint32_t>(mine) < P.vocab && static_cast<uint32_t>(mine) - P.n0 < P.rows;
+  for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, here); todo != 0; todo &= todo - 1) {
+    const uint32_t k = __ffs(todo) - 1;
+    const uint32_t tc = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, mine, k)) - P.n0;
+    const uint32_t k_slabs = P.K / 16, rr = tc & 127u;
+    const uint8_t* src = P.images + static_cast<uint64_t>(tc >> 7) * k_slabs * kSlabBytes + rr * 32u;
+    uint16_t* dst = P.target_rows + static_cast<uint64_t>(P.m0 + row0 + k) * P.K;
+    for (uint32_t q = 32 * blockIdx.y + lane; q < P.K / 8; q += 32 * gridDim.y)
+      *reinterpret_cast<uint4*>(dst + 8 * q) = __ldcg(reinterpret_cast<const uint4*>(
+          src + static_cast<uint64_t>(q >> 1) * kSlabBytes + (((q & 1u) ^ ((rr >> 2) & 1u)) << 4)));
+  }
+  if (moved == 0) return;
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k) {
-    const uint32_t col = blockIdx.x * 32 + 4 * warp + k;
+    const uint32_t col = row0 + k;
     if (((moved >> (4 * warp + k)) & 1u) == 0) continue;
     const float ref = __ldcg(P.st.ref + P.m0 + col);
     const float r = b < P.n_blocks ? __ldcg(P.blocks + static_cast<uint64_t>(b) * P.stride + col).x : ref;
@@ -457,7 +457,7 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       e = launch_pdl(xent_join_kernel, dim3(groups), dim3(32 * kJoinWarps), 0, stream, j);
       if (e != cudaSuccess) return e;
       if (!p.grad) continue;
-      e = launch_pdl(xent_rescale_kernel, dim3(groups, (j.n_blocks + 31) / 32), dim3(256), 0, stream, j);
+      e = launch_pdl(xent_piece_kernel, dim3(groups, (j.n_blocks + 31) / 32), dim3(256), 0, stream, j);
       if (e != cudaSuccess) return e;
       OperandGemmPlan tp = plan_operand_gemm(true, p.f16, m, rows, p.K, 1, p.sms);
       tp.splits = p.splits;

@@ -190,7 +190,7 @@ struct ShrinkDev {
   float* part;              // split x positions x rank
   uint64_t part_stride;     // positions x rank
   uint32_t C, rank, groups; // groups: 16-position groups of a tile (1 or 4)
-  uint32_t len;
+  uint32_t len, splits;
   // few tokens: tile m is the one that token m leads, and rows of part are tokens
   const int32_t* ids;
   uint32_t* status;
@@ -202,11 +202,7 @@ __host__ __device__ constexpr uint32_t shrink_w_bytes(bool cols, uint32_t rank) 
 }
 
 template <bool kCols, bool kFew, int NJ>
-__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __grid_constant__ ShrinkDev P) {
-  extern __shared__ __align__(128) uint8_t stages_smem[];
-  __shared__ uint32_t tok[16], found;
-  griddep_wait();
-  griddep_launch_dependents();
+__device__ __forceinline__ void shrink_cta(const ShrinkDev& P, uint8_t* stages_smem, uint32_t (&tok)[16], uint32_t& found) {
   const uint32_t tile = blockIdx.x;
   uint32_t a, start = 0, count;
   if constexpr (kFew) {
@@ -329,6 +325,22 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __gri
   }
 }
 
+// Both products in one launch (z 0: rows of A, z 1: columns of B; the forward pass
+// has the first alone).
+struct ShrinkBoth {
+  ShrinkDev d[2];
+};
+template <bool kFew, int NJ>
+__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const __grid_constant__ ShrinkBoth P) {
+  extern __shared__ __align__(128) uint8_t stages_smem[];
+  __shared__ uint32_t tok[16], found;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.y >= P.d[blockIdx.z].splits) return;
+  if (blockIdx.z == 0) shrink_cta<false, kFew, NJ>(P.d[0], stages_smem, tok, found);
+  else if constexpr (!kFew) shrink_cta<true, false, NJ>(P.d[1], stages_smem, tok, found);
+}
+
 // Four neighbouring sums over the splits, in order, 8 loads in flight.
 __device__ __forceinline__ float4 sum_parts(const float* p, uint32_t splits, uint64_t stride) {
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -358,9 +370,18 @@ __device__ __forceinline__ void split4(const float4& v, float s, uint16_t* hi, u
 
 // The splits' sums, in order, times s_a, as two bf16 parts: hp[part][p][j], rows
 // of r16 values (zeros from the rank on).
-__global__ void __launch_bounds__(256) lora_join_kernel(LoraGroups G, const float* __restrict__ part, uint32_t splits,
+// z: which of the two products.
+struct JoinDev {
+  const float* part[2];
+  uint32_t splits[2];
+  uint16_t* hp[2];
+};
+__global__ void __launch_bounds__(256) lora_join_kernel(LoraGroups G, const __grid_constant__ JoinDev D,
                                                         uint64_t part_stride, uint32_t rank, const float* scale,
-                                                        uint16_t* __restrict__ hp, uint64_t hp_stride) {
+                                                        uint64_t hp_stride) {
+  const float* __restrict__ part = D.part[blockIdx.z];
+  uint16_t* __restrict__ hp = D.hp[blockIdx.z];
+  const uint32_t splits = D.splits[blockIdx.z];
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t tile = blockIdx.x;
@@ -566,11 +587,8 @@ struct OuterDev {
 __host__ __device__ constexpr uint32_t outer_stage_bytes(uint32_t r16) { return 64 * kChunkRow + 2 * 64 * odd_row(r16); }
 
 template <bool kRankMajor, int NJ>
-__global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const __grid_constant__ OuterDev P) {
-  extern __shared__ __align__(128) uint8_t stages_smem[];
-  griddep_wait();
-  griddep_launch_dependents();
-  const uint32_t a = blockIdx.y, c0 = blockIdx.x * 64;
+__device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_t* stages_smem) {
+  const uint32_t a = blockIdx.y;
   const uint32_t p_begin = __ldcg(P.G.off + a), p_end = __ldcg(P.G.off + a + 1);
   const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const uint32_t cw = 16 * (warp & 3u), half = warp >> 2;
@@ -678,6 +696,20 @@ __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const __grid_
   }
 }
 
+// Both gradients in one launch: dB's blocks of columns first, then dA's.
+struct OuterBoth {
+  OuterDev b, a;
+  uint32_t b_blocks;
+};
+template <int NJ>
+__global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const __grid_constant__ OuterBoth P) {
+  extern __shared__ __align__(128) uint8_t stages_smem[];
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.x < P.b_blocks) outer_cta<false, NJ>(P.b, blockIdx.x * 64, stages_smem);
+  else outer_cta<true, NJ>(P.a, (blockIdx.x - P.b_blocks) * 64, stages_smem);
+}
+
 // ---- host ----------------------------------------------------------------------
 static size_t aligned(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -733,7 +765,7 @@ void make_lora_plan(uint32_t M, const LoraDev& L, bool grad, int sms, LoraPlan* 
   const size_t r16 = (L.rank + 15) / 16 * 16;
   const size_t sums = static_cast<size_t>(p->positions) * L.rank * 4, parts = static_cast<size_t>(p->positions) * r16 * 4;
   p->off_groups = take((2ull + L.n + p->positions + 3ull * p->max_tiles) * 4);
-  p->off_part = take(sums * (grad ? std::max(p->splits_k, p->splits_n) : p->splits_k));
+  p->off_part = take(sums * (grad ? p->splits_k + p->splits_n : p->splits_k));
   p->off_h = take(p->few ? 0 : parts);
   p->off_dh = take(grad ? parts : 0);
   p->bytes = at;
@@ -760,43 +792,52 @@ static cudaError_t by_rank(uint32_t rank, F f) {
   return f(std::integral_constant<int, 16>{});
 }
 
-template <bool kCols, bool kFew>
-static cudaError_t shrink(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const uint16_t* in,
-                          const int32_t* ids, float* part, uint32_t* status, cudaStream_t stream) {
-  ShrinkDev P;
-  P.ids = ids;
-  P.status = status;
-  P.M = p.M;
-  P.n = L.n;
-  P.G = G;
-  P.in = in;
-  P.weights = kCols ? L.B : L.A;
-  P.part = part;
-  P.part_stride = static_cast<uint64_t>(p.positions) * L.rank;
-  P.C = kCols ? L.N : L.K;
-  P.rank = L.rank;
-  P.groups = p.tm / 16;
-  P.len = kCols ? p.len_n : p.len_k;
-  const dim3 grid(p.max_tiles, kCols ? p.splits_n : p.splits_k);
-  const uint32_t smem = kShrinkStages * (16 * P.groups * kChunkRow + shrink_w_bytes(kCols, L.rank));
+// x against A's rows into part_x, and (gradients) dy against B's columns into part_y.
+template <bool kFew>
+static cudaError_t shrink(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const uint16_t* x, float* part_x,
+                          const uint16_t* dy, float* part_y, const int32_t* ids, uint32_t* status, cudaStream_t stream) {
+  ShrinkBoth P;
+  for (uint32_t q = 0; q < 2; ++q) {
+    ShrinkDev& d = P.d[q];
+    d.G = G;
+    d.in = q ? dy : x;
+    d.weights = q ? L.B : L.A;
+    d.part = q ? part_y : part_x;
+    d.part_stride = static_cast<uint64_t>(p.positions) * L.rank;
+    d.C = q ? L.N : L.K;
+    d.rank = L.rank;
+    d.groups = p.tm / 16;
+    d.len = q ? p.len_n : p.len_k;
+    d.splits = q ? p.splits_n : p.splits_k;
+    d.ids = ids;
+    d.status = status;
+    d.M = p.M;
+    d.n = L.n;
+  }
+  const bool both = dy != nullptr;
+  const dim3 grid(p.max_tiles, both ? std::max(p.splits_k, p.splits_n) : p.splits_k, both ? 2 : 1);
+  const uint32_t w_bytes = std::max(shrink_w_bytes(false, L.rank), both ? shrink_w_bytes(true, L.rank) : 0u);
+  const uint32_t smem = kShrinkStages * (16 * (p.tm / 16) * kChunkRow + w_bytes);
   return by_rank(L.rank, [&](auto nj) {
     constexpr int NJ = decltype(nj)::value;
-    constexpr uint32_t kMost = kShrinkStages * (64 * kChunkRow + shrink_w_bytes(kCols, 8 * NJ));
+    constexpr uint32_t kMost = kShrinkStages * (64 * kChunkRow + (shrink_w_bytes(false, 8 * NJ) > shrink_w_bytes(true, 8 * NJ)
+                                                                      ? shrink_w_bytes(false, 8 * NJ)
+                                                                      : shrink_w_bytes(true, 8 * NJ)));
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(lora_shrink_kernel<kCols, kFew, NJ>, kMost, done);
+    cudaError_t e = allow_smem(lora_shrink_kernel<kFew, NJ>, kMost, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(lora_shrink_kernel<kCols, kFew, NJ>, grid, dim3(kShrinkThreads), smem, stream, P);
+    return launch_pdl(lora_shrink_kernel<kFew, NJ>, grid, dim3(kShrinkThreads), smem, stream, P);
   });
 }
 
-static cudaError_t join(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const float* part, uint32_t splits,
-                        uint16_t* hp, cudaStream_t stream) {
+static cudaError_t join(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const JoinDev& D, cudaStream_t stream) {
   const uint32_t r16 = (L.rank + 15) / 16 * 16;
-  return launch_pdl(lora_join_kernel, dim3(p.max_tiles, std::max(1u, p.tm * r16 / 1024)), dim3(256), 0, stream, G, part,
-                    splits, static_cast<uint64_t>(p.positions) * L.rank, L.rank, L.scale, hp,
+  return launch_pdl(lora_join_kernel, dim3(p.max_tiles, std::max(1u, p.tm * r16 / 1024), D.hp[1] ? 2 : 1), dim3(256), 0,
+                    stream, G, D, static_cast<uint64_t>(p.positions) * L.rank, L.rank, L.scale,
                     static_cast<uint64_t>(p.positions) * r16);
 }
 
+// h: the shrink's sums (part) or their joined parts (hp), one of them null.
 template <bool kCols, bool kFew>
 static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const int32_t* ids, const float* part,
                           const uint16_t* hp, float* out, cudaStream_t stream) {
@@ -829,24 +870,20 @@ static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups&
   return launch_pdl(lora_expand_kernel<kCols, kFew, 0>, grid, block, smem, stream, P);
 }
 
-template <bool kRankMajor>
-static cudaError_t outer(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const uint16_t* z, const uint16_t* hp,
-                         float* out, cudaStream_t stream) {
+static cudaError_t outer(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const uint16_t* dY, const uint16_t* h,
+                         float* dB, const uint16_t* X, const uint16_t* dh, float* dA, cudaStream_t stream) {
   const uint32_t r16 = (L.rank + 15) / 16 * 16;
-  OuterDev P;
-  P.G = G;
-  P.z = z;
-  P.hp = hp;
-  P.hp_stride = static_cast<uint64_t>(p.positions) * r16;
-  P.out = out;
-  P.C = kRankMajor ? L.K : L.N;
-  P.rank = L.rank;
+  const uint64_t hp_stride = static_cast<uint64_t>(p.positions) * r16;
+  OuterBoth P;
+  P.b = OuterDev{G, dY, h, hp_stride, dB, L.N, L.rank};
+  P.a = OuterDev{G, X, dh, hp_stride, dA, L.K, L.rank};
+  P.b_blocks = (L.N + 63) / 64;
   return by_rank(L.rank, [&](auto nj) {
     constexpr int NJ = decltype(nj)::value;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(lora_outer_kernel<kRankMajor, NJ>, kOuterStages * outer_stage_bytes(8 * NJ), done);
+    cudaError_t e = allow_smem(lora_outer_kernel<NJ>, kOuterStages * outer_stage_bytes(8 * NJ), done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(lora_outer_kernel<kRankMajor, NJ>, dim3((P.C + 63) / 64, L.n), dim3(kOuterThreads),
+    return launch_pdl(lora_outer_kernel<NJ>, dim3(P.b_blocks + (L.K + 63) / 64, L.n), dim3(kOuterThreads),
                       kOuterStages * outer_stage_bytes(r16), stream, P);
   });
 }
@@ -856,10 +893,11 @@ cudaError_t launch_lora_shrink(const LoraPlan& p, const LoraDev& L, const uint16
   uint8_t* w = static_cast<uint8_t*>(ws);
   const LoraGroups G = groups_at(w + p.off_groups, p.positions, L.n, p.max_tiles);
   float* part = reinterpret_cast<float*>(w + p.off_part);
-  if (p.few) return shrink<false, true>(p, L, G, X, ids, part, status, stream);
+  if (p.few) return shrink<true>(p, L, G, X, part, nullptr, nullptr, ids, status, stream);
   cudaError_t e = launch_pdl(lora_group_kernel, dim3(1), dim3(1024), 0, stream, ids, p.M, L.n, p.tm, G, status);
-  if (e == cudaSuccess) e = shrink<false, false>(p, L, G, X, ids, part, status, stream);
-  if (e == cudaSuccess) e = join(p, L, G, part, p.splits_k, reinterpret_cast<uint16_t*>(w + p.off_h), stream);
+  if (e == cudaSuccess) e = shrink<false>(p, L, G, X, part, nullptr, nullptr, ids, status, stream);
+  if (e == cudaSuccess)
+    e = join(p, L, G, JoinDev{{part, nullptr}, {p.splits_k, 0}, {reinterpret_cast<uint16_t*>(w + p.off_h), nullptr}}, stream);
   return e;
 }
 
@@ -880,12 +918,10 @@ cudaError_t launch_lora_grad(const LoraPlan& p, const LoraDev& L, const uint16_t
   uint16_t* h = reinterpret_cast<uint16_t*>(w + p.off_h);
   uint16_t* dh = reinterpret_cast<uint16_t*>(w + p.off_dh);
   cudaError_t e = launch_pdl(lora_group_kernel, dim3(1), dim3(1024), 0, stream, ids, p.M, L.n, p.tm, G, status);
-  if (e == cudaSuccess) e = shrink<false, false>(p, L, G, X, ids, part, status, stream);
-  if (e == cudaSuccess) e = join(p, L, G, part, p.splits_k, h, stream);
-  if (e == cudaSuccess) e = shrink<true, false>(p, L, G, dY, ids, part, status, stream);
-  if (e == cudaSuccess) e = join(p, L, G, part, p.splits_n, dh, stream);
-  if (e == cudaSuccess) e = outer<false>(p, L, G, dY, h, dB, stream);
-  if (e == cudaSuccess) e = outer<true>(p, L, G, X, dh, dA, stream);
+  float* part_y = part + static_cast<uint64_t>(p.splits_k) * p.positions * L.rank;
+  if (e == cudaSuccess) e = shrink<false>(p, L, G, X, part, dY, part_y, ids, status, stream);
+  if (e == cudaSuccess) e = join(p, L, G, JoinDev{{part, part_y}, {p.splits_k, p.splits_n}, {h, dh}}, stream);
+  if (e == cudaSuccess) e = outer(p, L, G, dY, h, dB, X, dh, dA, stream);
   if (e == cudaSuccess && delta != nullptr) e = expand<true, false>(p, L, G, ids, nullptr, dh, delta, stream);
   return e;
 }

@@ -11,9 +11,12 @@
 // its tokens lie anywhere, so these are the warp-wide m16n8k16 instructions on
 // tiles that cp.async gathers, several stages ahead.
 //
-// h and dh are kept in 32 bits and enter the second product as the sum of two
-// bf16 values (16 bits of them; off by 2^-17 at most), so that the product is
-// nearly as exact as the fp32 outputs it is added to.
+// h and dh are kept in 32 bits and enter the products with fp32 results (y, dA,
+// dB) as the sum of two bf16 values (16 bits of them; off by 2^-17 at most).
+// dx is bf16, and there dh is rounded to bf16 once: the second part would move
+// dx by less than its own rounding does, and costs as many matrix instructions
+// again, which are what bounds that product (a rank of 64 into 4096 x 14336: 84
+// us with both parts).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -416,6 +419,7 @@ __device__ __forceinline__ uint32_t pair_of(const Row8& a, const Row8& b, int j)
 // g 8 + i of the 64 is column g of instruction i, so that what lane (g, t) ends
 // with is columns 16 t .. 16 t + 15 of its rows: four 16-byte accesses a row.
 // Along the sum lane t has steps 4 t .. 4 t + 3 of every 16, in both operands.
+// kCols takes the first part of h alone.
 // Up to rank 64 the warp's weights stay in registers for all of the tile's
 // tokens (kSteps blocks of 16 ranks); above, they are read again for every 16
 // tokens (kSteps 0).
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
   }
   if constexpr (!kFew) {
     const uint32_t per = r16 / 8;
-    for (uint32_t i = threadIdx.x; i < 2 * count * per; i += blockDim.x) {
+    for (uint32_t i = threadIdx.x; i < (kCols ? 1 : 2) * count * per; i += blockDim.x) {
       const uint32_t part = i >= count * per ? 1u : 0u, k = i - part * count * per;
       const uint32_t row = k / per, q = k - row * per;
       *reinterpret_cast<uint4*>((part ? lo_s : hs) + row * pitch + 8 * q) = __ldcg(reinterpret_cast<const uint4*>(
@@ -533,12 +537,13 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
     const uint32_t h0 = (r + g) * pitch + 4 * t, h1 = h0 + 8 * pitch;
     auto step = [&](uint32_t k, const uint32_t (&bk)[8][2]) {
       const uint2 a0 = *reinterpret_cast<const uint2*>(hs + h0 + k), a1 = *reinterpret_cast<const uint2*>(hs + h1 + k);
-      const uint2 l0 = *reinterpret_cast<const uint2*>(lo_s + h0 + k),
-                  l1 = *reinterpret_cast<const uint2*>(lo_s + h1 + k);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        mma_bf16(acc[i], a0.x, a1.x, a0.y, a1.y, bk[i][0], bk[i][1]);
-        mma_bf16(acc[i], l0.x, l1.x, l0.y, l1.y, bk[i][0], bk[i][1]);
+      for (int i = 0; i < 8; ++i) mma_bf16(acc[i], a0.x, a1.x, a0.y, a1.y, bk[i][0], bk[i][1]);
+      if constexpr (!kCols) {
+        const uint2 l0 = *reinterpret_cast<const uint2*>(lo_s + h0 + k),
+                    l1 = *reinterpret_cast<const uint2*>(lo_s + h1 + k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mma_bf16(acc[i], l0.x, l1.x, l0.y, l1.y, bk[i][0], bk[i][1]);
       }
     };
     if constexpr (kSteps > 0) {
@@ -862,7 +867,7 @@ static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups&
   const uint32_t blocks = (P.C + 63) / 64;
   uint32_t warps = 4;
   while (warps > 1 && (blocks + warps - 1) / warps * p.likely < 2u * static_cast<uint32_t>(p.sms)) warps /= 2;
-  const uint32_t smem = 2 * p.tm * (r16 + 8) * 2;  // 34 KB at most
+  const uint32_t smem = (kCols ? 1 : 2) * p.tm * (r16 + 8) * 2;  // 34 KB at most
   const dim3 grid(p.max_tiles, (blocks + warps - 1) / warps), block(32 * warps);
   if (L.rank <= 16) return launch_pdl(lora_expand_kernel<kCols, kFew, 1>, grid, block, smem, stream, P);
   if (L.rank <= 32) return launch_pdl(lora_expand_kernel<kCols, kFew, 2>, grid, block, smem, stream, P);

@@ -83,7 +83,8 @@ def lora_grad_reference(L, A, x, dy, ids):
         g, g_mass = s * (dy64[at] @ b), s * (dy64[at].abs() @ b.abs())
         dx[at] += g @ a
         e_g = sum_eps(L.N) + 2.0 ** -16 + 2.0 ** -23
-        inner = (e_g + sum_eps(A.rank)) * (g_mass @ a.abs())
+        # dH is rounded to bf16 once on its way into dX: half a step, 2^-8 of it
+        inner = (e_g + BF16 + sum_eps(A.rank)) * (g_mass @ a.abs())
         dx_bound[at] += (1 + BF16) * inner + BF16 * (g @ a).abs()
         da[i], db[i] = g.T @ x64[at], dy64[at].T @ h
         n = len(at)

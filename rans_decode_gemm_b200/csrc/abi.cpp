@@ -916,8 +916,9 @@ extern "C" {
 ans_status ans_gemm_lora_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind,
                                    const ans_lora* lora, size_t* bytes) {
   if (!bytes) return ANS_ERR_ARG;
-  size_t base = 0;
-  ans_status st = ans_gemm_workspace(layout, M, scale_kind, &base);
+  ans_status st = check_layout(layout);
+  if (st != ANS_OK) return st;
+  st = check_scale_kind(*layout, scale_kind);
   if (st != ANS_OK) return st;
   ansdev::LoraDev A;
   st = check_lora(lora, *layout, false, &A);
@@ -925,6 +926,9 @@ ans_status ans_gemm_lora_workspace(const ans_layout* layout, uint32_t M, ans_sca
   if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
   *bytes = 0;
   if (M == 0) return ANS_OK;
+  size_t base = 0;
+  st = ans_gemm_workspace(layout, M, scale_kind, &base);
+  if (st != ANS_OK) return st;
   int sms = 0;
   st = device_info(&sms);
   if (st != ANS_OK) return st;

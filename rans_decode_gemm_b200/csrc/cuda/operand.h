@@ -78,7 +78,7 @@ struct OperandGemmOut {
 // block's largest logit lies more than kXentSlack above it: then r is that
 // logit, rounded up.
 constexpr float kXentSlack = 5.75f;    // e^4: what probabilities may exceed 1 by
-constexpr float kXentNone = -1.0e30f;  // the reference before any logit
+constexpr float kXentNone = -3.0e38f;  // the reference before any logit
 struct XentEpilogue {
   const float* factor;     // f[m], or null: 1
   uint32_t scale_kind;     // s_n: bf16 (1), fp32 (2) at scales[n], else 1

@@ -71,6 +71,9 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 constexpr uint32_t kChunkRow = 9 * 16;  // 64 values and one chunk
 __host__ __device__ constexpr uint32_t odd_row(uint32_t cols) { return ((cols / 8) | 1u) * 16u; }
 constexpr uint32_t kNoToken = 0xFFFFFFFFu;
+// Ranks are held in rows of 16, 32, 64 or 128 (zeros from the rank on): a row's
+// length is then a constant of the instance, and so are all offsets inside tiles.
+__host__ __device__ constexpr uint32_t rank_row(uint32_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
 // ---- grouping -----------------------------------------------------------------
 // One CTA; warp w takes a contiguous range of tokens, so the order inside an
@@ -201,7 +204,7 @@ struct ShrinkDev {
 };
 
 __host__ __device__ constexpr uint32_t shrink_w_bytes(bool cols, uint32_t rank) {
-  return cols ? 64 * odd_row(rank) : rank * kChunkRow;
+  return cols ? 64 * odd_row(rank_row(rank)) : rank * kChunkRow;
 }
 
 template <bool kCols, bool kFew, int NJ>
@@ -239,8 +242,8 @@ __device__ __forceinline__ void shrink_cta(const ShrinkDev& P, uint8_t* stages_s
     x_in[i] = m != kNoToken;
     x[i] = P.in + (x_in[i] ? static_cast<uint64_t>(m) * P.C : 0ull);
   }
-  auto load = [&](uint32_t slot, uint32_t c0) {
-    const uint32_t xs = base + slot * stage, wsm = xs + x_bytes;
+  auto load = [&](uint32_t xs, uint32_t c0) {
+    const uint32_t wsm = xs + x_bytes;
     const uint32_t c = c0 + 8 * (tid % 8);
     const bool in = c < c_end;
 #pragma unroll
@@ -248,33 +251,49 @@ __device__ __forceinline__ void shrink_cta(const ShrinkDev& P, uint8_t* stages_s
       if (i < P.groups)
         cp16(xs + (tid / 8 + 16 * i) * kChunkRow + (tid % 8) * 16, x[i] + (in ? c : 0u), in && x_in[i]);
     if constexpr (!kCols) {
-      for (uint32_t j = tid / 8; j < P.rank; j += 16)
-        cp16(wsm + j * kChunkRow + (tid % 8) * 16, w + (in ? static_cast<uint64_t>(j) * P.C + c : 0ull), in);
+      const uint16_t* src = w + (in ? static_cast<uint64_t>(tid / 8) * P.C + c : 0ull);
+#pragma unroll
+      for (uint32_t i = 0; i < (NJ + 1) / 2; ++i) {
+        const uint32_t j = tid / 8 + 16 * i;
+        if (j < P.rank) cp16(wsm + j * kChunkRow + (tid % 8) * 16, src, in);
+        if (in) src += 16ull * P.C;
+      }
     } else {
-      const uint32_t pitch = odd_row(P.rank);
-      for (uint32_t i = tid; i < 64 * nj; i += kShrinkThreads) {
-        const uint32_t row = i / nj, q = i - row * nj;
-        const bool r_in = c0 + row < c_end;
-        cp16(wsm + row * pitch + q * 16, w + (r_in ? static_cast<uint64_t>(c0 + row) * P.rank + 8 * q : 0ull), r_in);
+      // NJ chunks a row (those past the rank are not used)
+      const uint32_t q = tid % NJ;
+      if (q < nj) {
+        const uint16_t* src = w + static_cast<uint64_t>(c0 + tid / NJ) * P.rank + 8 * q;
+#pragma unroll
+        for (uint32_t i = 0; i < 64 * NJ / kShrinkThreads; ++i) {
+          const uint32_t row = tid / NJ + i * (kShrinkThreads / NJ);
+          const bool r_in = c0 + row < c_end;
+          cp16(wsm + row * odd_row(8 * NJ) + q * 16, r_in ? src : w, r_in);
+          src += kShrinkThreads / NJ * P.rank;
+        }
       }
     }
   };
   const uint32_t n_steps = c_end > c_begin ? (c_end - c_begin + 63) / 64 : 0u;
 #pragma unroll
   for (uint32_t i = 0; i + 1 < kShrinkStages; ++i) {
-    if (i < n_steps) load(i, c_begin + 64 * i);
+    if (i < n_steps) load(base + i * stage, c_begin + 64 * i);
     cp_commit();
   }
   float acc[NJ][4] = {};
   const uint32_t row0 = P.groups == 4 ? 16 * warp : 0u;
   const uint32_t ks0 = P.groups == 4 ? 0u : warp, ks1 = P.groups == 4 ? 4u : warp + 1;
+  uint32_t xs_next = base, load_next = base + (kShrinkStages - 1) * stage;
+  const uint32_t ring_end = base + kShrinkStages * stage;
   for (uint32_t it = 0; it < n_steps; ++it) {
     cp_wait<kShrinkStages - 2>();
     __syncthreads();
-    if (it + kShrinkStages - 1 < n_steps) load((it + kShrinkStages - 1) % kShrinkStages, c_begin + 64 * (it + kShrinkStages - 1));
+    if (it + kShrinkStages - 1 < n_steps) load(load_next, c_begin + 64 * (it + kShrinkStages - 1));
     cp_commit();
-    const uint32_t xs = base + (it % kShrinkStages) * stage, wsm = xs + x_bytes;
+    if ((load_next += stage) == ring_end) load_next = base;
+    const uint32_t xs = xs_next, wsm = xs + x_bytes;
+    if ((xs_next += stage) == ring_end) xs_next = base;
     if (row0 >= count) continue;  // this warp's group is empty
+#pragma unroll 4
     for (uint32_t ks = ks0; ks < ks1; ++ks) {
       uint32_t f[4];
       ldsm4(f, xs + (row0 + (lane & 15u)) * kChunkRow + (2 * ks + (lane >> 4)) * 16);
@@ -286,7 +305,7 @@ __device__ __forceinline__ void shrink_cta(const ShrinkDev& P, uint8_t* stages_s
           const uint32_t jl = j + 1 < nj ? j + (lane >> 4) : j;
           uint32_t q[4];
           if constexpr (!kCols) ldsm4(q, wsm + (8 * jl + (lane & 7u)) * kChunkRow + (2 * ks + ((lane >> 3) & 1u)) * 16);
-          else ldsm4_t(q, wsm + (16 * ks + (lane & 15u)) * odd_row(P.rank) + jl * 16);
+          else ldsm4_t(q, wsm + (16 * ks + (lane & 15u)) * odd_row(8 * NJ) + jl * 16);
           mma_bf16(acc[j], f[0], f[1], f[2], f[3], q[0], q[1]);
           if (j + 1 < nj) mma_bf16(acc[j + 1], f[0], f[1], f[2], f[3], q[2], q[3]);
         }
@@ -372,7 +391,7 @@ __device__ __forceinline__ void split4(const float4& v, float s, uint16_t* hi, u
 }
 
 // The splits' sums, in order, times s_a, as two bf16 parts: hp[part][p][j], rows
-// of r16 values (zeros from the rank on).
+// of rank_row values (zeros from the rank on).
 // z: which of the two products.
 struct JoinDev {
   const float* part[2];
@@ -392,32 +411,22 @@ __global__ void __launch_bounds__(256) lora_join_kernel(LoraGroups G, const __gr
   const uint32_t a = __ldcg(G.tile_adapter + tile), start = __ldcg(G.tile_start + tile),
                  count = __ldcg(G.tile_count + tile);
   const float s = scale != nullptr ? __ldg(scale + a) : 1.0f;
-  const uint32_t r16 = (rank + 15) / 16 * 16;
-  const uint32_t per = r16 / 4;
+  const uint32_t rr = rank_row(rank), per = rr / 4;
   for (uint32_t i = blockIdx.y * 256 + threadIdx.x; i < count * per; i += 256 * gridDim.y) {
     const uint32_t row = i / per, j = 4 * (i - row * per);
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (j < rank) v = sum_parts(part + static_cast<uint64_t>(start + row) * rank + j, splits, part_stride);
-    const uint64_t at = static_cast<uint64_t>(start + row) * r16 + j;
+    const uint64_t at = static_cast<uint64_t>(start + row) * rr + j;
     split4(v, s, hp + at, hp + hp_stride + at);
   }
 }
 
-// 8 consecutive bf16 of a row; element j of two rows as one register (row a low).
-struct Row8 { uint32_t v[4]; };
-__device__ __forceinline__ Row8 load_row8(const uint16_t* p, bool in) {
-  const uint4 q = in ? ldg16(p) : make_uint4(0, 0, 0, 0);
-  return Row8{{q.x, q.y, q.z, q.w}};
-}
-__device__ __forceinline__ uint32_t pair_of(const Row8& a, const Row8& b, int j) {
-  return __byte_perm(a.v[j / 2], b.v[j / 2], (j & 1) ? 0x7632u : 0x5410u);
-}
-
 // ---- expand: rank values of a token against C outputs --------------------------
 // kCols false: out[m][c] += sum_j h[p][j] * B[c][j];  kCols true: out[m][c] =
-// sum_j h[p][j] * A[j][c].  A warp takes 64 columns of a tile's tokens.  Column
-// g 8 + i of the 64 is column g of instruction i, so that what lane (g, t) ends
-// with is columns 16 t .. 16 t + 15 of its rows: four 16-byte accesses a row.
+// sum_j h[p][j] * A[j][c].  A warp takes 64 columns of a tile's tokens.  Which of
+// them is column n of instruction i (expand_col) is chosen so that lane (g, t)
+// ends with columns 16 q + 4 t .. + 3 of its rows, q = 0 .. 3: a row's four lanes
+// write 64 neighbouring bytes at a time.
 // Along the sum lane t has steps 4 t .. 4 t + 3 of every 16, in both operands.
 // kCols takes the first part of h alone.
 // Up to rank 64 the warp's weights stay in registers for all of the tile's
@@ -436,6 +445,11 @@ struct ExpandDev {
   uint32_t M, n;
 };
 
+// Column of the warp's 64 that is column n of instruction i.
+__device__ __forceinline__ constexpr uint32_t expand_col(uint32_t n, uint32_t i) {
+  return 32 * (n & 1u) + 16 * (i >> 2) + 4 * (n >> 1) + (i & 3u);
+}
+
 template <bool kCols>
 __device__ __forceinline__ void expand_weights(const ExpandDev& P, const uint16_t* w, uint32_t c0, uint32_t k, uint32_t g,
                                                uint32_t t, uint32_t (&b)[8][2]) {
@@ -443,19 +457,26 @@ __device__ __forceinline__ void expand_weights(const ExpandDev& P, const uint16_
   if constexpr (!kCols) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint2 v = j < P.rank ? ldg8(w + static_cast<uint64_t>(c0 + g * 8 + i) * P.rank + j) : make_uint2(0, 0);
+      const uint2 v = j < P.rank ? ldg8(w + static_cast<uint64_t>(c0 + expand_col(g, i)) * P.rank + j) : make_uint2(0, 0);
       b[i][0] = v.x;
       b[i][1] = v.y;
     }
   } else {
-    const bool in = j < P.rank && c0 + g * 8 < P.C;  // (the rank is a multiple of 8)
-    const uint16_t* p = w + (in ? static_cast<uint64_t>(j) * P.C + c0 + g * 8 : 0ull);
-    const Row8 v0 = load_row8(p, in), v1 = load_row8(p + P.C, in), v2 = load_row8(p + 2ull * P.C, in),
-               v3 = load_row8(p + 3ull * P.C, in);
+    // columns of instructions 0-3 and of 4-7 are four neighbours each
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      b[i][0] = pair_of(v0, v1, i);
-      b[i][1] = pair_of(v2, v3, i);
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t col = c0 + expand_col(g, 4 * h);
+      const bool in = j < P.rank && col < P.C;  // (the rank is a multiple of 8, C of 16)
+      const uint16_t* p = w + (in ? static_cast<uint64_t>(j) * P.C + col : 0ull);
+      uint2 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = in ? ldg8(p + static_cast<uint64_t>(q) * P.C) : make_uint2(0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+        b[4 * h + e][0] = e < 2 ? __byte_perm(v[0].x, v[1].x, sel) : __byte_perm(v[0].y, v[1].y, sel);
+        b[4 * h + e][1] = e < 2 ? __byte_perm(v[2].x, v[3].x, sel) : __byte_perm(v[2].y, v[3].y, sel);
+      }
     }
   }
 }
@@ -466,7 +487,8 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
   __shared__ uint32_t tok[16], found;
   const uint32_t tile = blockIdx.x;
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const uint32_t r16 = (P.rank + 15) / 16 * 16, pitch = r16 + 8;
+  const uint32_t r16 = (P.rank + 15) / 16 * 16;
+  constexpr uint32_t kRow = kSteps > 0 ? 16 * kSteps : kLoraMaxRank, pitch = kRow + 8;
   uint16_t* lo_s = hs + P.tm * pitch;
   const uint32_t c0 = (blockIdx.y * (blockDim.x / 32) + warp) * 64;
   uint32_t b[kSteps > 0 ? kSteps : 1][8][2];
@@ -491,16 +513,16 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
     for (int q = 0; q < kSteps; ++q) expand_weights<kCols>(P, w, c0, 16 * q, g, t, b[q]);
   }
   if constexpr (!kFew) {
-    const uint32_t per = r16 / 8;
+    constexpr uint32_t per = kRow / 8;
     for (uint32_t i = threadIdx.x; i < (kCols ? 1 : 2) * count * per; i += blockDim.x) {
       const uint32_t part = i >= count * per ? 1u : 0u, k = i - part * count * per;
       const uint32_t row = k / per, q = k - row * per;
       *reinterpret_cast<uint4*>((part ? lo_s : hs) + row * pitch + 8 * q) = __ldcg(reinterpret_cast<const uint4*>(
-          P.hp + part * P.hp_stride + static_cast<uint64_t>(start + row) * r16 + 8 * q));
+          P.hp + part * P.hp_stride + static_cast<uint64_t>(start + row) * kRow + 8 * q));
     }
   } else {
     const float s = P.scale != nullptr ? __ldg(P.scale + a) : 1.0f;
-    const uint32_t per = r16 / 4;
+    constexpr uint32_t per = kRow / 4;
     for (uint32_t i = threadIdx.x; i < 16 * per; i += blockDim.x) {
       const uint32_t row = i / per, j = 4 * (i - row * per);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -511,8 +533,7 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
   }
   __syncthreads();
   if (c0 >= P.C) return;
-  const uint32_t cl = c0 + 16 * t;  // this lane's output columns
-  const bool col_in = cl < P.C;
+  const uint32_t cl = c0 + 4 * t;  // this lane's output columns: cl + 16 q .. + 3
   for (uint32_t r = 0; r < count; r += 16) {
     uint32_t m0, m1;
     if constexpr (kFew) {
@@ -522,15 +543,15 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
       m0 = __ldcg(P.G.perm + start + r + g);
       m1 = __ldcg(P.G.perm + start + r + g + 8);
     }
-    const bool v0 = m0 != kNoToken && col_in, v1 = m1 != kNoToken && col_in;
+    const bool v0 = m0 != kNoToken, v1 = m1 != kNoToken;
     float* y0 = P.out + (v0 ? static_cast<uint64_t>(m0) * P.C + cl : 0ull);
     float* y1 = P.out + (v1 ? static_cast<uint64_t>(m1) * P.C + cl : 0ull);
     float4 o0[4], o1[4];
     if constexpr (!kCols) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (v0) o0[q] = *reinterpret_cast<const float4*>(y0 + 4 * q);
-        if (v1) o1[q] = *reinterpret_cast<const float4*>(y1 + 4 * q);
+        if (v0) o0[q] = *reinterpret_cast<const float4*>(y0 + 16 * q);
+        if (v1) o1[q] = *reinterpret_cast<const float4*>(y1 + 16 * q);
       }
     }
     float acc[8][4] = {};
@@ -556,7 +577,7 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
         step(k, b[0]);
       }
     }
-    // columns 16 t + i (c0 of instruction i) and 16 t + 8 + i (c1)
+    // columns 16 q + 4 t + e: instruction 4 (q & 1) + e, its even (q < 2) or odd column
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int i = 4 * (q & 1), k = q >> 1;
@@ -566,8 +587,9 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
         if (v0) { u.x += o0[q].x; u.y += o0[q].y; u.z += o0[q].z; u.w += o0[q].w; }
         if (v1) { v.x += o1[q].x; v.y += o1[q].y; v.z += o1[q].z; v.w += o1[q].w; }
       }
-      if (v0) *reinterpret_cast<float4*>(y0 + 4 * q) = u;
-      if (v1) *reinterpret_cast<float4*>(y1 + 4 * q) = v;
+      const bool in = c0 + 16 * q < P.C;  // (C is a multiple of 16)
+      if (v0 && in) *reinterpret_cast<float4*>(y0 + 16 * q) = u;
+      if (v1 && in) *reinterpret_cast<float4*>(y1 + 16 * q) = v;
     }
   }
 }
@@ -584,12 +606,12 @@ constexpr uint32_t kOuterThreads = 256, kOuterStages = 3;
 struct OuterDev {
   LoraGroups G;
   const uint16_t* z;   // M x C
-  const uint16_t* hp;  // 2 x positions x r16
+  const uint16_t* hp;  // 2 x positions x rank_row
   uint64_t hp_stride;
   float* out;
   uint32_t C, rank;
 };
-__host__ __device__ constexpr uint32_t outer_stage_bytes(uint32_t r16) { return 64 * kChunkRow + 2 * 64 * odd_row(r16); }
+__host__ __device__ constexpr uint32_t outer_stage_bytes(uint32_t row) { return 64 * kChunkRow + 2 * 64 * odd_row(row); }
 
 template <bool kRankMajor, int NJ>
 __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_t* stages_smem) {
@@ -597,8 +619,8 @@ __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_
   const uint32_t p_begin = __ldcg(P.G.off + a), p_end = __ldcg(P.G.off + a + 1);
   const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const uint32_t cw = 16 * (warp & 3u), half = warp >> 2;
-  const uint32_t r16 = (P.rank + 15) / 16 * 16, nj2 = r16 / 16;
-  const uint32_t h_row = odd_row(r16), h_bytes = 64 * h_row, stage = outer_stage_bytes(r16);
+  const uint32_t nj2 = (P.rank + 15) / 16;
+  constexpr uint32_t h_row = odd_row(8 * NJ), h_bytes = 64 * h_row, stage = outer_stage_bytes(8 * NJ);
   const uint32_t base = smem_u32(stages_smem);
   const bool col_in = c0 + 8 * (tid % 8) < P.C;
   const uint32_t n_steps = (p_end - p_begin + 63) / 64;
@@ -611,41 +633,53 @@ __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_
       ahead[i] = p < p_end ? __ldcg(P.G.perm + p) : kNoToken;
     }
   };
-  auto load = [&](uint32_t it) {
-    const uint32_t zs = base + (it % kOuterStages) * stage, hsm = zs + 64 * kChunkRow, p0 = p_begin + 64 * it;
+  // and its chunks of h: NJ a row, of positions tid / NJ and every 256 / NJ further,
+  // of the one part and the other
+  const uint16_t* h_src = P.hp + static_cast<uint64_t>(p_begin + tid / NJ) * (8 * NJ) + 8 * (tid % NJ);
+  auto load = [&](uint32_t zs, uint32_t it) {
+    const uint32_t hsm = zs + 64 * kChunkRow + (tid / NJ) * h_row + (tid % NJ) * 16;
 #pragma unroll
     for (uint32_t i = 0; i < 2; ++i) {
       const bool in = ahead[i] != kNoToken && col_in;
       cp16(zs + (tid / 8 + 32 * i) * kChunkRow + (tid % 8) * 16,
            P.z + (in ? static_cast<uint64_t>(ahead[i]) * P.C + c0 + 8 * (tid % 8) : 0ull), in);
     }
-    const uint32_t per = r16 / 8;
-    for (uint32_t i = tid; i < 128 * per; i += kOuterThreads) {
-      const uint32_t row = i / per, q = i - row * per, p = p0 + (row & 63u);
-      const bool in = p < p_end;
-      cp16(hsm + (row >> 6) * h_bytes + (row & 63u) * h_row + q * 16,
-           P.hp + (in ? (row >> 6) * P.hp_stride + static_cast<uint64_t>(p) * r16 + 8 * q : 0ull), in);
-    }
+    constexpr uint32_t kRows = kOuterThreads / NJ;  // positions in one go
+    const uint32_t left = p_end - p_begin - 64 * it;
+#pragma unroll
+    for (uint32_t part = 0; part < 2; ++part)
+#pragma unroll
+      for (uint32_t i = 0; i < (kRows >= 64 ? 1 : 64 / kRows); ++i) {
+        const uint32_t row = tid / NJ + i * kRows;
+        if (kRows > 64 && row >= 64) break;
+        const bool in = row < left;
+        cp16(hsm + part * h_bytes + i * kRows * h_row,
+             in ? h_src + part * P.hp_stride + static_cast<uint64_t>(64 * it + i * kRows) * (8 * NJ) : P.hp, in);
+      }
   };
   look(0);
 #pragma unroll
   for (uint32_t i = 0; i + 1 < kOuterStages; ++i) {
     if (i < n_steps) {
-      load(i);
+      load(base + i * stage, i);
       look(i + 1);
     }
     cp_commit();
   }
   float acc[NJ][4] = {};
+  uint32_t zs_next = base, load_next = base + (kOuterStages - 1) * stage;
+  const uint32_t ring_end = base + kOuterStages * stage;
   for (uint32_t it = 0; it < n_steps; ++it) {
     cp_wait<kOuterStages - 2>();
     __syncthreads();
     if (it + kOuterStages - 1 < n_steps) {
-      load(it + kOuterStages - 1);
+      load(load_next, it + kOuterStages - 1);
       look(it + kOuterStages);
     }
     cp_commit();
-    const uint32_t zs = base + (it % kOuterStages) * stage, hsm = zs + 64 * kChunkRow;
+    if ((load_next += stage) == ring_end) load_next = base;
+    const uint32_t zs = zs_next, hsm = zs + 64 * kChunkRow;
+    if ((zs_next += stage) == ring_end) zs_next = base;
     const uint32_t n16 = min(4u, (p_end - p_begin - 64 * it) / 16);
 #pragma unroll
     for (uint32_t k = 0; k < 2; ++k) {
@@ -767,8 +801,8 @@ void make_lora_plan(uint32_t M, const LoraDev& L, bool grad, int sms, LoraPlan* 
     at += aligned(n);
     return o;
   };
-  const size_t r16 = (L.rank + 15) / 16 * 16;
-  const size_t sums = static_cast<size_t>(p->positions) * L.rank * 4, parts = static_cast<size_t>(p->positions) * r16 * 4;
+  const size_t sums = static_cast<size_t>(p->positions) * L.rank * 4;
+  const size_t parts = static_cast<size_t>(p->positions) * rank_row(L.rank) * 4;
   p->off_groups = take((2ull + L.n + p->positions + 3ull * p->max_tiles) * 4);
   p->off_part = take(sums * (grad ? p->splits_k + p->splits_n : p->splits_k));
   p->off_h = take(p->few ? 0 : parts);
@@ -836,23 +870,23 @@ static cudaError_t shrink(const LoraPlan& p, const LoraDev& L, const LoraGroups&
 }
 
 static cudaError_t join(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const JoinDev& D, cudaStream_t stream) {
-  const uint32_t r16 = (L.rank + 15) / 16 * 16;
-  return launch_pdl(lora_join_kernel, dim3(p.max_tiles, std::max(1u, p.tm * r16 / 1024), D.hp[1] ? 2 : 1), dim3(256), 0,
+  const uint32_t row = rank_row(L.rank);
+  return launch_pdl(lora_join_kernel, dim3(p.max_tiles, std::max(1u, p.tm * row / 1024), D.hp[1] ? 2 : 1), dim3(256), 0,
                     stream, G, D, static_cast<uint64_t>(p.positions) * L.rank, L.rank, L.scale,
-                    static_cast<uint64_t>(p.positions) * r16);
+                    static_cast<uint64_t>(p.positions) * row);
 }
 
 // h: the shrink's sums (part) or their joined parts (hp), one of them null.
 template <bool kCols, bool kFew>
 static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const int32_t* ids, const float* part,
                           const uint16_t* hp, float* out, cudaStream_t stream) {
-  const uint32_t r16 = (L.rank + 15) / 16 * 16;
+  const uint32_t row = rank_row(L.rank);
   ExpandDev P;
   P.G = G;
   P.part = part;
   P.hp = hp;
   P.part_stride = static_cast<uint64_t>(p.positions) * L.rank;
-  P.hp_stride = static_cast<uint64_t>(p.positions) * r16;
+  P.hp_stride = static_cast<uint64_t>(p.positions) * row;
   P.scale = L.scale;
   P.weights = kCols ? L.A : L.B;
   P.out = out;
@@ -867,7 +901,7 @@ static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups&
   const uint32_t blocks = (P.C + 63) / 64;
   uint32_t warps = 4;
   while (warps > 1 && (blocks + warps - 1) / warps * p.likely < 2u * static_cast<uint32_t>(p.sms)) warps /= 2;
-  const uint32_t smem = (kCols ? 1 : 2) * p.tm * (r16 + 8) * 2;  // 34 KB at most
+  const uint32_t smem = (kCols ? 1 : 2) * p.tm * (row + 8) * 2;  // 34 KB at most
   const dim3 grid(p.max_tiles, (blocks + warps - 1) / warps), block(32 * warps);
   if (L.rank <= 16) return launch_pdl(lora_expand_kernel<kCols, kFew, 1>, grid, block, smem, stream, P);
   if (L.rank <= 32) return launch_pdl(lora_expand_kernel<kCols, kFew, 2>, grid, block, smem, stream, P);
@@ -877,8 +911,7 @@ static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups&
 
 static cudaError_t outer(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const uint16_t* dY, const uint16_t* h,
                          float* dB, const uint16_t* X, const uint16_t* dh, float* dA, cudaStream_t stream) {
-  const uint32_t r16 = (L.rank + 15) / 16 * 16;
-  const uint64_t hp_stride = static_cast<uint64_t>(p.positions) * r16;
+  const uint64_t hp_stride = static_cast<uint64_t>(p.positions) * rank_row(L.rank);
   OuterBoth P;
   P.b = OuterDev{G, dY, h, hp_stride, dB, L.N, L.rank};
   P.a = OuterDev{G, X, dh, hp_stride, dA, L.K, L.rank};
@@ -889,7 +922,7 @@ static cudaError_t outer(const LoraPlan& p, const LoraDev& L, const LoraGroups& 
     cudaError_t e = allow_smem(lora_outer_kernel<NJ>, kOuterStages * outer_stage_bytes(8 * NJ), done);
     if (e != cudaSuccess) return e;
     return launch_pdl(lora_outer_kernel<NJ>, dim3(P.b_blocks + (L.K + 63) / 64, L.n), dim3(kOuterThreads),
-                      kOuterStages * outer_stage_bytes(r16), stream, P);
+                      kOuterStages * outer_stage_bytes(8 * NJ), stream, P);
   });
 }
 

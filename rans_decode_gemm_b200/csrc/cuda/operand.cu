@@ -7,11 +7,13 @@
 // transposed product) decodes them here once and reads the images.
 //
 // One warp streams one contiguous run of tiles (RunPipe) and writes each
-// 128 x 16 slab into one of its two 4 KB slots; the slot leaves by one
-// contiguous 4 KB bulk copy, which the decoding of the next slab overlaps.
-// 16 warps a CTA, one CTA an SM: 2 x 4 KB of slots and a 4 KB ring a warp
-// fill the shared memory, and the decode rate no longer rises beyond that
-// many warps.
+// 128 x 16 slab into its 4 KB slot, which leaves by one contiguous 4 KB bulk copy
+// (a second slot a warp changed nothing: 114.2 against 113.6 us on a bf16
+// 14336 x 4096 layer).  One CTA an SM.  A tile is one warp's, so what counts is
+// how evenly tiles go into warps: a CTA has as many warps, up to 20, as make the
+// tiles come out in whole rounds (that layer's 7,168 tiles: 16 warps an SM, four
+// rounds for 3.03 of work, 114 us; 17 in three rounds, 99 us).  More than 20
+// are no faster (24: 104 us; the decoders' instructions fill the issue slots).
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -25,14 +27,14 @@
 
 namespace ansdev {
 
-constexpr uint32_t kOpWarps = 16;
+constexpr uint32_t kOpWarps = 20;  // at most
 constexpr uint32_t kOpThreads = kOpWarps * 32;
 constexpr uint32_t kOpRawAhead = 3;  // raw-byte groups loaded ahead of their use
-// [slots 16 x 2 x 4 KB][rings 16 x 4,224 B][slot table 16 KB][barriers 16 x 4 x 8 B]
-constexpr uint32_t kOpOffRing = kOpWarps * 2 * kSlabBytes;
-constexpr uint32_t kOpOffLut = kOpOffRing + kOpWarps * kRingStride;
-constexpr uint32_t kOpOffBars = kOpOffLut + kSlots * 4;
-constexpr uint32_t kOpSmem = kOpOffBars + kOpWarps * 4 * 8;
+// [slots 4 KB a warp][rings 4,224 B a warp][slot table 16 KB][barriers 4 x 8 B a warp]
+__host__ __device__ constexpr uint32_t op_off_ring(uint32_t warps) { return warps * kSlabBytes; }
+__host__ __device__ constexpr uint32_t op_off_lut(uint32_t warps) { return op_off_ring(warps) + warps * kRingStride; }
+__host__ __device__ constexpr uint32_t op_off_bars(uint32_t warps) { return op_off_lut(warps) + kSlots * 4; }
+__host__ __device__ constexpr uint32_t op_smem(uint32_t warps) { return op_off_bars(warps) + warps * 4 * 8; }
 
 struct OperandDev {
   LayerDev L;
@@ -88,16 +90,17 @@ __global__ void __launch_bounds__(kOpThreads, 1) operand_decode_kernel(const __g
   constexpr uint32_t kGroups = kPair ? 4 : 8, kOut = kPair ? 8 : 4;
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const LayerDev& L = P.L;
-  uint32_t* lut = reinterpret_cast<uint32_t*>(smem + kOpOffLut);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOpOffBars);
+  const uint32_t cta_warps = blockDim.x / 32;
+  uint32_t* lut = reinterpret_cast<uint32_t*>(smem + op_off_lut(cta_warps));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + op_off_bars(cta_warps));
   const bool single = L.single_symbol != kNoSymbol;
 
   if (threadIdx.x == 0) abort_flag = 0;
-  if (threadIdx.x < kOpWarps * 4) {
-    mbar_init(&bars[threadIdx.x], 1);
+  for (uint32_t i = threadIdx.x; i < cta_warps * 4; i += blockDim.x) {
+    mbar_init(&bars[i], 1);
     fence_mbar_init();
   }
-  if (!single) build_lut(lut, L, warp, kOpWarps, lane);
+  if (!single) build_lut(lut, L, warp, cta_warps, lane);
   __syncthreads();
   // the prologue above read only kernel parameters
   griddep_wait();
@@ -105,16 +108,16 @@ __global__ void __launch_bounds__(kOpThreads, 1) operand_decode_kernel(const __g
 
   volatile uint32_t* abort = &abort_flag;
   // warp-major over the CTAs, so that few tiles spread over all of them
-  const uint32_t n_warps = gridDim.x * kOpWarps, me = warp * gridDim.x + blockIdx.x;
+  const uint32_t n_warps = gridDim.x * cta_warps, me = warp * gridDim.x + blockIdx.x;
   const uint32_t t_begin = P.tile0 + cta_begin(P.n_tiles, n_warps, me);
   const uint32_t t_end = P.tile0 + cta_begin(P.n_tiles, n_warps, me + 1);
   const uint32_t n_kt = L.n_kt, H = L.tile_n / 128, C = L.tile_k / 16, S = L.tile_n * L.tile_k;
   const uint32_t k_slabs = L.K / 16;
   const uint32_t lt = lanemask_lt(), lut_s = smem_u32(lut);
   const uint32_t swz = ((lane >> 2) & 1u) << 4;
-  const uint32_t w_s0 = smem_u32(smem + 2 * warp * kSlabBytes);
+  const uint32_t w_s = smem_u32(smem + warp * kSlabBytes);
   RunPipe pipe;
-  rp_init(pipe, smem + kOpOffRing + warp * kRingStride, bars + 4 * warp);
+  rp_init(pipe, smem + op_off_ring(cta_warps) + warp * kRingStride, bars + 4 * warp);
   TileCursor tc;
   tc.x = tc.pos = tc.cb = tc.bytes = 0;
   tc.xw = 0;
@@ -137,7 +140,6 @@ __global__ void __launch_bounds__(kOpThreads, 1) operand_decode_kernel(const __g
 #pragma unroll
   for (uint32_t k = 0; k < kOpRawAhead; ++k) rq[k] = 0;
   bool rq_ready = false;
-  uint32_t nw = 0;  // slabs written
 
   for (uint32_t t = t_begin; t < t_end; ++t) {
     const uint32_t rb = t / n_kt, kt = t - rb * n_kt;
@@ -181,17 +183,16 @@ __global__ void __launch_bounds__(kOpThreads, 1) operand_decode_kernel(const __g
     // path carries no branch for it
     auto slabs = [&](auto const_sym) {
       constexpr bool kConst = decltype(const_sym)::value;
-      for (uint32_t us = 0; us < H * C; ++us, ++nw) {
+      for (uint32_t us = 0; us < H * C; ++us) {
         const uint32_t h = us % H, s = us / H;
-        const uint32_t w_s = w_s0 + (nw & 1u) * kSlabBytes;
         uint32_t o_prev[kOut];
 #pragma unroll
         for (uint32_t k = 0; k < kOut; ++k) o_prev[k] = 0;
         // the store of a group is deferred into the next group's decode chain
         auto store_prev = [&](uint32_t gg) {
           if (gg == 1) {
-            // the copy that last left this slot (two slabs ago) has read it
-            if (lane == 0) bulk_wait_read<1>();
+            // the previous slab's copy has read the slot
+            if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
           }
           const uint32_t row_s = w_s + (32 * ((gg - 1) & 3) + lane) * 32;
@@ -256,17 +257,18 @@ __global__ void __launch_bounds__(kOpThreads, 1) operand_decode_kernel(const __g
 }
 
 template <uint32_t DT, bool kWide>
-static cudaError_t launch_variant(const OperandDev& P, uint32_t grid, cudaStream_t stream) {
+static cudaError_t launch_variant(const OperandDev& P, uint32_t grid, uint32_t warps, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(attr_set.load() & (1ull << dev))) {
-    e = cudaFuncSetAttribute(operand_decode_kernel<DT, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOpSmem);
+    e = cudaFuncSetAttribute(operand_decode_kernel<DT, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             op_smem(kOpWarps));
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }
-  return launch_pdl(operand_decode_kernel<DT, kWide>, dim3(grid), dim3(kOpThreads), kOpSmem, stream, P);
+  return launch_pdl(operand_decode_kernel<DT, kWide>, dim3(grid), dim3(warps * 32), op_smem(warps), stream, P);
 }
 
 cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t rows, uint32_t scale_kind,
@@ -286,11 +288,14 @@ cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t row
   P.block0 = row0 / 128;
   P.images = images;
   P.status = status;
-  // one CTA an SM; with fewer tiles than that, one tile a CTA
-  const uint32_t grid = P.n_tiles < static_cast<uint32_t>(sms) ? P.n_tiles : static_cast<uint32_t>(sms);
+  // one CTA an SM (with fewer tiles than that, one tile a CTA), and the fewest
+  // warps that need no more rounds of tiles than the most warps would
+  const uint32_t cap = static_cast<uint32_t>(sms), grid = P.n_tiles < cap ? P.n_tiles : cap;
+  const uint32_t rounds = (P.n_tiles + grid * kOpWarps - 1) / (grid * kOpWarps);
+  const uint32_t warps = (P.n_tiles + grid * rounds - 1) / (grid * rounds);
   switch (L.dtype) {
 #define ANS_OPERAND_CASE(DT) \
-  case DT: return L.wide ? launch_variant<DT, true>(P, grid, stream) : launch_variant<DT, false>(P, grid, stream);
+  case DT: return L.wide ? launch_variant<DT, true>(P, grid, warps, stream) : launch_variant<DT, false>(P, grid, warps, stream);
     ANS_OPERAND_CASE(kDtInt4)
     ANS_OPERAND_CASE(kDtBf16Split)
     ANS_OPERAND_CASE(kDtFp8)

@@ -312,9 +312,11 @@ __global__ void __launch_bounds__(kXentThreads) xent_finish_kernel(const __grid_
 static size_t aligned(size_t n) { return (n + 1023) / 1024 * 1024; }
 
 // W rows of a piece, most, in blocks of 128: its images (2 K bytes a row) and a
-// chunk's probabilities are what has to stay in L2.  With few tokens a piece is
-// a row of tiles, and may be as long as there are SMs.
+// chunk's probabilities are what has to stay in L2.  Without probabilities the
+// images may fill 80 MB.  With few tokens a piece is a row of tiles, and may be
+// as long as there are SMs.
 constexpr uint32_t kXentMostBlocks = 80, kXentLeastBlocks = 24;
+constexpr uint32_t kXentImageBytes = 80u << 20;
 
 static uint32_t waves(uint64_t tiles, uint32_t sms) { return static_cast<uint32_t>((tiles + sms - 1) / sms); }
 
@@ -334,7 +336,8 @@ void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms_in, XentPl
   // a piece more costs about a quarter of a round (its join, and the decoder's
   // and the products' ends)
   const uint32_t m_blocks = (p->chunk + 255) / 256, blocks = L.N / 128, unit = L.tile_n / 128;
-  const uint32_t most = std::min(blocks, std::max(kXentMostBlocks, sms / m_blocks)) / unit * unit;
+  const uint32_t fill = grad ? 0u : kXentImageBytes / (256u * L.K);
+  const uint32_t most = std::min(blocks, std::max({kXentMostBlocks, sms / m_blocks, fill})) / unit * unit;
   uint32_t best = most;
   uint64_t best_cost = ~0ull;
   for (uint32_t b = most; b >= std::min(most, kXentLeastBlocks); b -= unit) {

@@ -8,12 +8,15 @@
 //
 // One warp streams one contiguous run of tiles (RunPipe) and writes each
 // 128 x 16 slab into its 4 KB slot, which leaves by one contiguous 4 KB bulk copy
-// (a second slot a warp changed nothing: 114.2 against 113.6 us on a bf16
-// 14336 x 4096 layer).  One CTA an SM.  A tile is one warp's, so what counts is
-// how evenly tiles go into warps: a CTA has as many warps, up to 20, as make the
-// tiles come out in whole rounds (that layer's 7,168 tiles: 16 warps an SM, four
-// rounds for 3.03 of work, 114 us; 17 in three rounds, 99 us).  More than 20
-// are no faster (24: 104 us; the decoders' instructions fill the issue slots).
+// (a second slot a warp changed nothing: 114.2 against 113.6 us for a call on a
+// bf16 14336 x 4096 layer).  One CTA an SM.  What bounds it is how far the
+// decoders' instructions fill the issue slots (57 % with 17 warps) and how evenly
+// tiles go into warps, a tile being one warp's.  A round of tiles takes about
+// 11.8 us and 1.05 us for each warp of the SM (8,192-symbol tiles), so few rounds
+// of many warps are best: a CTA has as many, up to the 25 that shared memory
+// holds, as bring the tiles out in whole rounds.  That layer's 7,168 tiles: 16
+// warps, four rounds for 3.03 of work, 114 us; 17 in three rounds 100 us; 25 in
+// two 90 us.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -27,7 +30,7 @@
 
 namespace ansdev {
 
-constexpr uint32_t kOpWarps = 20;  // at most
+constexpr uint32_t kOpWarps = 25;  // at most
 constexpr uint32_t kOpThreads = kOpWarps * 32;
 constexpr uint32_t kOpRawAhead = 3;  // raw-byte groups loaded ahead of their use
 // [slots 4 KB a warp][rings 4,224 B a warp][slot table 16 KB][barriers 4 x 8 B a warp]
@@ -271,6 +274,10 @@ static cudaError_t launch_variant(const OperandDev& P, uint32_t grid, uint32_t w
   return launch_pdl(operand_decode_kernel<DT, kWide>, dim3(grid), dim3(warps * 32), op_smem(warps), stream, P);
 }
 
+uint32_t operand_decode_rounds(uint32_t tiles, uint32_t ctas) {
+  return (tiles + ctas * kOpWarps - 1) / (ctas * kOpWarps);
+}
+
 cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t rows, uint32_t scale_kind,
                                   const void* scales, uint32_t group_k, uint8_t* images,
                                   uint32_t* status, int sms, cudaStream_t stream) {
@@ -291,7 +298,7 @@ cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t row
   // one CTA an SM (with fewer tiles than that, one tile a CTA), and the fewest
   // warps that need no more rounds of tiles than the most warps would
   const uint32_t cap = static_cast<uint32_t>(sms), grid = P.n_tiles < cap ? P.n_tiles : cap;
-  const uint32_t rounds = (P.n_tiles + grid * kOpWarps - 1) / (grid * kOpWarps);
+  const uint32_t rounds = operand_decode_rounds(P.n_tiles, grid);
   const uint32_t warps = (P.n_tiles + grid * rounds - 1) / (grid * rounds);
   switch (L.dtype) {
 #define ANS_OPERAND_CASE(DT) \

@@ -28,6 +28,9 @@ cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t row
                                   uint32_t scale_kind, const void* scales, uint32_t group_k,
                                   uint8_t* images, uint32_t* status, int sms, cudaStream_t stream);
 
+// Rounds of tiles that decoding them takes on that many SMs.
+uint32_t operand_decode_rounds(uint32_t tiles, uint32_t ctas);
+
 // Rows of a bf16 matrix as f16 under a power of two of their own: out[m][c] =
 // f16(in[m][c] * s[c] * 2^e), factor[m] = 2^-e, with e such that the row's
 // largest finite magnitude lands in [2^14, 2^15).  scale_kind: s[c] as bf16 (1)

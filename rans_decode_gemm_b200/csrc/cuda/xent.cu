@@ -332,18 +332,24 @@ void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms_in, XentPl
   const uint32_t fit = grad ? 4096u : 16384u;
   const uint32_t chunks = (M + fit - 1) / fit;
   p->chunk = chunks <= 1 ? M : std::min(M, ((M + chunks - 1) / chunks + 255) / 256 * 256);
-  // the piece whose tiles fill whole rounds of the SMs best over the vocabulary;
-  // a piece more costs about a quarter of a round (its join, and the decoder's
-  // and the products' ends)
+  // The piece that costs least over the vocabulary: its logits' tiles come in
+  // rounds of the SMs (about 460 ns a stage of 64 columns), its decoding in rounds
+  // of tiles (11.8 us beyond what the work itself takes, for 8,192 symbols), and
+  // its launches and the kernels' ends take some 8 us, with a gradient 35.
   const uint32_t m_blocks = (p->chunk + 255) / 256, blocks = L.N / 128, unit = L.tile_n / 128;
   const uint32_t fill = grad ? 0u : kXentImageBytes / (256u * L.K);
   const uint32_t most = std::min(blocks, std::max({kXentMostBlocks, sms / m_blocks, fill})) / unit * unit;
+  const uint32_t symbols = L.tile_n * L.tile_k / (L.dtype == kDtInt4Pairs || L.dtype == kDtFp4Pairs ? 2u : 1u);
+  const uint64_t round_ns = 11800ull * symbols / 8192, wave_ns = 460ull * ((L.K + 63) / 64);
+  auto cost_of = [&](uint32_t b) {
+    if (b == 0) return uint64_t(0);
+    return wave_ns * waves(static_cast<uint64_t>(b) * m_blocks, sms) +
+           round_ns * operand_decode_rounds(b / unit * L.n_kt, sms) + (grad ? 35000 : 8000);
+  };
   uint32_t best = most;
   uint64_t best_cost = ~0ull;
   for (uint32_t b = most; b >= std::min(most, kXentLeastBlocks); b -= unit) {
-    const uint32_t whole = blocks / b, rest = blocks % b;
-    const uint64_t cost = 4ull * (static_cast<uint64_t>(whole) * waves(static_cast<uint64_t>(b) * m_blocks, sms) +
-                                  waves(static_cast<uint64_t>(rest) * m_blocks, sms)) + whole + (rest != 0);
+    const uint64_t cost = (blocks / b) * cost_of(b) + cost_of(blocks % b);
     if (cost < best_cost) {
       best_cost = cost;
       best = b;

@@ -420,8 +420,10 @@ __global__ void __launch_bounds__(256) lora_join_kernel(LoraGroups G, const __gr
   const uint32_t rr = rank_row(rank), per = rr / 4;
   for (uint32_t i = blockIdx.y * 256 + threadIdx.x; i < count * per; i += 256 * gridDim.y) {
     const uint32_t row = i / per, j = 4 * (i - row * per);
+    // (a position without a token stays 0 even beside an infinite weight)
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (j < rank) v = sum_parts(part + static_cast<uint64_t>(start + row) * rank + j, splits, part_stride);
+    if (j < rank && __ldcg(G.perm + start + row) != kNoToken)
+      v = sum_parts(part + static_cast<uint64_t>(start + row) * rank + j, splits, part_stride);
     const uint64_t at = static_cast<uint64_t>(start + row) * rr + j;
     split4(v, s, hp + at, hp + hp_stride + at);
   }

@@ -243,6 +243,20 @@ __global__ void __launch_bounds__(256) xent_piece_kernel(const __grid_constant__
   }
 }
 
+// Zeros in the images of rows [first, rows): padding behind the vocabulary, whose
+// probabilities are 0, and 0 times an infinity or a NaN is not.
+__global__ void __launch_bounds__(256) xent_blank_kernel(uint8_t* images, uint32_t first, uint32_t rows, uint32_t k_slabs) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint64_t n = static_cast<uint64_t>(rows - first) * k_slabs * 2;
+  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<uint64_t>(gridDim.x) * 256) {
+    const uint64_t slab = (i / 2) % k_slabs;
+    const uint32_t row = first + static_cast<uint32_t>(i / 2 / k_slabs);
+    *reinterpret_cast<uint4*>(images + ((row >> 7) * static_cast<uint64_t>(k_slabs) + slab) * kSlabBytes + (row & 127u) * 32u +
+                              16 * (i & 1)) = make_uint4(0, 0, 0, 0);
+  }
+}
+
 struct XentFinish {
   const int32_t* targets;
   const void* scales;
@@ -426,10 +440,17 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
     factor = f;
   }
   const uint64_t MK = static_cast<uint64_t>(p.M) * p.K;
-  for (uint32_t n0 = 0; n0 < p.N; n0 += p.piece) {
+  for (uint32_t n0 = 0; n0 < a.vocab; n0 += p.piece) {
     const uint32_t rows = std::min(p.piece, p.N - n0);
     e = launch_operand_decode(L, n0, rows, a.scale_kind, a.scales, a.group_k, images, a.status, p.sms, stream);
     if (e != cudaSuccess) return e;
+    if (p.grad && n0 + rows > a.vocab) {
+      const uint32_t first = a.vocab - n0;
+      const uint64_t items = static_cast<uint64_t>(rows - first) * (p.K / 8);
+      e = launch_pdl(xent_blank_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((items + 255) / 256, 1024))), dim3(256), 0,
+                     stream, images, first, rows, p.K / 16);
+      if (e != cudaSuccess) return e;
+    }
     for (uint32_t m0 = 0; m0 < p.M; m0 += p.chunk) {
       const uint32_t m = std::min(p.chunk, p.M - m0);
       XentEpilogue f;

@@ -276,6 +276,32 @@ def test_lora_keeps_infinities_and_nan_to_their_tokens(cuda):
     assert torch.isnan(y[11]).all()
 
 
+def test_a_broken_adapter_reaches_its_own_tokens_alone(cuda):
+    # infinities in one adapter's A and NaN in another's B, as a slot that was never
+    # loaded may hold: the other adapters' tokens and gradients are what they are
+    L = usual(ans.BF16_SPLIT, 256, 128, seed=5)
+    for M in (40, 300):
+        rng = np.random.default_rng(M)
+        A = Adapters(L, 4, 16)
+        A.a[1], A.b[2] = float("inf"), float("nan")
+        A.dev = ans.LoraAdapters(A.a.cuda(), A.b.cuda(), A.s.cuda())
+        A.lora = A.dev.lora
+        x, dy, ids = bf16(rng, M, 128), bf16(rng, M, 256), some_ids(rng, M, 4)
+        good = (ids != 1) & (ids != 2)
+        y, st = run_lora(L, A, x, ids)
+        assert st == 0
+        want, bound = lora_reference(L, A, x, ids)
+        within(y.cpu()[good], want[good], bound[good], "y")
+        dx, da, db, st = run_lora_grad(L, A, x, dy, ids)
+        assert st == 0
+        (wx, bx), (wa, ba), (wb, bb) = lora_grad_reference(L, A, x, dy, ids)
+        within(dx.cpu()[good], wx[good], bx[good], "dx")
+        for i in (0, 3):
+            within(da[i], wa[i], ba[i], "da")
+            within(db[i], wb[i], bb[i], "db")
+        within(da[1], wa[1], ba[1], "da of the adapter whose A is infinite")
+
+
 # ---- ans_gemm_lora_grad ----------------------------------------------------------
 @pytest.mark.parametrize("rank", [8, 16, 24, 40, 72, 104, 128])
 @pytest.mark.parametrize("M", [1, 33, 300])

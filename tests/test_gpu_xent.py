@@ -124,6 +124,18 @@ def test_padding_of_the_vocabulary_counts_for_nothing(cuda):
     check(L, bf16(rng, 30, 64).abs(), some_targets(rng, 30, 300), 300)
 
 
+@pytest.mark.parametrize("code", [0x7F80, 0x7FC0])
+@pytest.mark.parametrize("N,vocab", [(384, 300), (16512, 8200), (16512, 16400)])
+def test_padding_may_hold_infinities_and_nan(cuda, N, vocab, code):
+    L = usual(ans.BF16_SPLIT, N, 64, seed=8)
+    codes = L.codes.copy()
+    codes[vocab:] = code
+    L.layer = ans.CompressedLayer.from_weights(codes.reshape(-1), L.layout)
+    L.tiles = L.layer.tiles
+    rng = np.random.default_rng(2)
+    check(L, bf16(rng, 30, 64), some_targets(rng, 30, vocab), vocab)
+
+
 def test_targets_out_of_range(cuda):
     L = usual(ans.INT8, 256, 64, seed=8)
     rng = np.random.default_rng(2)

@@ -19,6 +19,7 @@
 // two 90 us.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <type_traits>
@@ -299,7 +300,8 @@ cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t row
   // warps that need no more rounds of tiles than the most warps would
   const uint32_t cap = static_cast<uint32_t>(sms), grid = P.n_tiles < cap ? P.n_tiles : cap;
   const uint32_t rounds = operand_decode_rounds(P.n_tiles, grid);
-  const uint32_t warps = (P.n_tiles + grid * rounds - 1) / (grid * rounds);
+  // (8 at least: they build the slot table together, which takes one warp 20 us)
+  const uint32_t warps = std::max(8u, (P.n_tiles + grid * rounds - 1) / (grid * rounds));
   switch (L.dtype) {
 #define ANS_OPERAND_CASE(DT) \
   case DT: return L.wide ? launch_variant<DT, true>(P, grid, warps, stream) : launch_variant<DT, false>(P, grid, warps, stream);

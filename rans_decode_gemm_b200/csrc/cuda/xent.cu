@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(256) xent_piece_kernel(const __grid_constant__
       *reinterpret_cast<uint4*>(dst + 8 * q) = __ldcg(reinterpret_cast<const uint4*>(
           src + static_cast<uint64_t>(q >> 1) * kSlabBytes + (((q & 1u) ^ ((rr >> 2) & 1u)) << 4)));
   }
-  if (moved == 0) return;
+  if (moved == 0 || 32 * blockIdx.y >= P.n_blocks) return;
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k) {
     const uint32_t col = row0 + k;
@@ -375,27 +375,14 @@ void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms_in, XentPl
     if (b <= unit) break;
   }
   p->piece = best * 128;
-  // The gradient's product has K / 128 x m_blocks tiles whatever the piece.  Its
-  // sum over n is cut where there are too few tiles, or where 2 or 4 ranges fill
-  // the SMs' last round better by more than what their partial sums cost (each
-  // is read and written once a piece, about 8 stages' time a tile).
-  p->splits = 1;
+  // one plan of the gradient's product for every piece and chunk (the last piece
+  // is cut into the same ranges)
+  p->splits = p->back_bn = 1;
   if (grad) {
-    const uint32_t last = L.N - (L.N - 1) / p->piece * p->piece;  // the last piece is cut likewise
-    const OperandGemmPlan g = plan_operand_gemm(true, p->f16, p->chunk, last, L.K, 8, sms_in);
+    const uint32_t last = L.N - (L.N - 1) / p->piece * p->piece;
+    const OperandGemmPlan g = plan_operand_gemm(true, p->f16, p->chunk, p->piece, L.K, std::min(8u, last / 64), sms_in);
     p->splits = g.splits;
-    if (g.splits == 1) {
-      const uint64_t tiles = static_cast<uint64_t>((L.K + 127) / 128) * ((p->chunk + g.bn - 1) / g.bn);
-      const uint32_t stages = p->piece / 64;
-      uint64_t least = static_cast<uint64_t>(waves(tiles, sms)) * stages;
-      for (uint32_t s = 2; s <= 4 && last / 64 >= s; s *= 2) {
-        const uint64_t t = static_cast<uint64_t>(waves(tiles * s, sms)) * (stages / s + 1) + 8 * s;
-        if (t < least) {
-          least = t;
-          p->splits = s;
-        }
-      }
-    }
+    p->back_bn = g.bn;
   }
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -491,9 +478,12 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       e = launch_pdl(xent_join_kernel, dim3(groups), dim3(32 * kJoinWarps), 0, stream, j);
       if (e != cudaSuccess) return e;
       if (!p.grad) continue;
-      e = launch_pdl(xent_piece_kernel, dim3(groups, (j.n_blocks + 31) / 32), dim3(256), 0, stream, j);
+      // as many CTAs a group as its blocks take, or as the copies of rows can use
+      const uint32_t copies = std::min((p.K / 8 + 31) / 32, std::max(1u, 4u * static_cast<uint32_t>(p.sms) / groups));
+      e = launch_pdl(xent_piece_kernel, dim3(groups, std::max((j.n_blocks + 31) / 32, copies)), dim3(256), 0, stream, j);
       if (e != cudaSuccess) return e;
       OperandGemmPlan tp = plan_operand_gemm(true, p.f16, m, rows, p.K, 1, p.sms);
+      tp.bn = p.back_bn;
       tp.splits = p.splits;
       OperandGemmOut back = {};
       back.out32 = acc + static_cast<uint64_t>(m0) * p.K;

@@ -121,32 +121,44 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
   const float top = across_lanes(x, lane, [](float a, float b) { return fmaxf(a, b); }) * kLog2E;
   float ref = ref_in;
   if (top > ref_in + kXentSlack && top <= 3.0e38f) ref = ceilf(top);
-  // targets among this warp's rows (one that is past the vocabulary is none)
-  const uint32_t first = E.n0 + c - lane;
-  const bool hit = target >= 0 && static_cast<uint32_t>(target) < E.vocab && static_cast<uint32_t>(target) - first < 32u;
-  const uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit);
-  const float ps = scale * lift;
 #pragma unroll
   for (uint32_t j = 0; j < 32; ++j) {
     const float r = __shfl_sync(0xFFFFFFFFu, ref, j);
     // (the approximate instruction: 2^-22, the same in every use)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x[j]) : "f"(fmaf(z[j], kLog2E, -r)));
-    if ((hits >> j) & 1u) {
-      const uint32_t t = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, target, j)) - first;
-      if (lane == t) {
-        E.zt[m + j] = z[j];
-        x[j] = 0.0f;
+  }
+  // targets among this warp's rows (one that is past the vocabulary is none): few
+  // and far between, so that the loops above and below carry no test for them
+  const uint32_t first = E.n0 + c - lane;
+  const bool hit = target >= 0 && static_cast<uint32_t>(target) < E.vocab && static_cast<uint32_t>(target) - first < 32u;
+  for (uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit); hits != 0; hits &= hits - 1) {
+    const uint32_t k = __ffs(hits) - 1;
+    if (lane == static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, target, k)) - first) {
+#pragma unroll
+      for (uint32_t j = 0; j < 32; ++j) {
+        if (j == k) {
+          E.zt[m + j] = z[j];
+          x[j] = 0.0f;
+        }
       }
     }
+    __syncwarp();
   }
+  const float ps = scale * lift;
   if (E.probs != nullptr) {
     uint16_t* p = E.probs + static_cast<uint64_t>(m) * rows + c;
-#pragma unroll
-    for (uint32_t j = 0; j < 32; ++j) {
-      if (j >= n_tok) break;
+    auto store = [&](uint32_t j) {
       const float q = x[j] * ps;
-      p[static_cast<uint64_t>(j) * rows] =
-          f16 ? __half_as_ushort(__float2half_rn(q)) : __bfloat16_as_ushort(__float2bfloat16_rn(q));
+      *p = f16 ? __half_as_ushort(__float2half_rn(q)) : __bfloat16_as_ushort(__float2bfloat16_rn(q));
+      p += rows;
+    };
+    if (n_tok == 32) {
+#pragma unroll
+      for (uint32_t j = 0; j < 32; ++j) store(j);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < 32; ++j)
+        if (j < n_tok) store(j);
     }
   }
   const float sum = across_lanes(x, lane, [](float a, float b) { return a + b; });

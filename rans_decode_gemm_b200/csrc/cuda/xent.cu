@@ -103,7 +103,7 @@ struct XentJoin {
   XentState st;
   const float2* blocks;    // (reference, sum): [n_blocks][stride], tokens m0 .. m0 + m - 1 from column 0
   uint32_t stride, n_blocks, m0, m, rows, f16;
-  uint32_t* moved;         // per 32 tokens, one bit each: has blocks under another reference
+  uint32_t* moved;         // one bit a token, in order: has blocks under another reference
   uint16_t* probs;         // m x rows, or null
   // the targets' rows of W
   const int32_t* targets;
@@ -112,25 +112,29 @@ struct XentJoin {
   uint32_t n0, vocab, K;
 };
 
-// 32 tokens a CTA, one a lane; the warps share the blocks, 8 loads in flight
-// each, and are joined in order.  The largest of a token's block references is
-// the piece's.
+// kTok tokens a CTA (32, or 8 where there are few), one a lane of each of a warp's
+// 32 / kTok shares; the shares of all warps take the blocks in turn, 8 loads in
+// flight each, and are joined in order.  The largest of a token's block
+// references is the piece's.
 constexpr uint32_t kJoinWarps = 16, kJoinBatch = 8;
+template <uint32_t kTok>
 __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const __grid_constant__ XentJoin P) {
-  __shared__ float part_ref[kJoinWarps][33], part_low[kJoinWarps][33], part_sum[kJoinWarps][33];
+  constexpr uint32_t kShares = kJoinWarps * 32 / kTok;
+  __shared__ float part_ref[kShares][kTok + 1], part_low[kShares][kTok + 1], part_sum[kShares][kTok + 1];
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, col = blockIdx.x * 32 + lane;
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t tok = threadIdx.x % kTok, share = threadIdx.x / kTok, col = blockIdx.x * kTok + tok;
   const bool in = col < P.m;
   const uint32_t m = P.m0 + col;
   // (ref, s): sums under the largest reference so far; low: the smallest that a
   // sum other than 0 came under
   float ref = kXentNone, low = INFINITY, s = 0.0f;
-  for (uint32_t b0 = warp; b0 < P.n_blocks; b0 += kJoinBatch * kJoinWarps) {
+  for (uint32_t b0 = share; b0 < P.n_blocks; b0 += kJoinBatch * kShares) {
     float2 u[kJoinBatch];
 #pragma unroll
     for (uint32_t k = 0; k < kJoinBatch; ++k) {
-      const uint32_t b = b0 + k * kJoinWarps;
+      const uint32_t b = b0 + k * kShares;
       u[k] = in && b < P.n_blocks ? __ldcg(P.blocks + static_cast<uint64_t>(b) * P.stride + col)
                                   : make_float2(kXentNone, 0.0f);
     }
@@ -146,35 +150,39 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const __grid
       low = fminf(low, u[k].x);
     }
   }
-  part_ref[warp][lane] = ref;
-  part_low[warp][lane] = low;
-  part_sum[warp][lane] = s;
+  part_ref[share][tok] = ref;
+  part_low[share][tok] = low;
+  part_sum[share][tok] = s;
   __syncthreads();
   if (warp == 0) {
+    // (with 8 tokens, all four shares of the warp do the same)
     const float ref_old = in ? __ldcg(P.st.ref + m) : kXentNone;
     const float l = in ? __ldcg(P.st.sum + m) : 0.0f;
     ref = ref_old;
-#pragma unroll
-    for (uint32_t k = 0; k < kJoinWarps; ++k) {
-      ref = fmaxf(ref, part_ref[k][lane]);
-      low = fminf(low, part_low[k][lane]);
+#pragma unroll 16
+    for (uint32_t k = 0; k < kShares; ++k) {
+      ref = fmaxf(ref, part_ref[k][tok]);
+      low = fminf(low, part_low[k][tok]);
     }
     s = 0.0f;
-#pragma unroll
-    for (uint32_t k = 0; k < kJoinWarps; ++k) {
-      const float v = part_sum[k][lane];
-      s += v == 0.0f ? 0.0f : v * pow2(part_ref[k][lane] - ref);
+#pragma unroll 16
+    for (uint32_t k = 0; k < kShares; ++k) {
+      const float v = part_sum[k][tok];
+      s += v == 0.0f ? 0.0f : v * pow2(part_ref[k][tok] - ref);
     }
     const uint32_t moved = __ballot_sync(0xFFFFFFFFu, in && low < ref);
-    if (in) {
+    if (in && lane < kTok) {
       const float keep = ref_old == kXentNone ? 0.0f : pow2(ref_old - ref);
       P.st.ref[m] = ref;
       P.st.sum[m] = fmaf(l, keep, s);  // (NaN stays NaN)
       if (P.probs != nullptr) {
         P.st.alpha[m] = keep;
         P.st.beta[m] = 1.0f / __ldcg(P.st.lift);  // a power of two
-        if (lane == 0) P.moved[blockIdx.x] = moved;
       }
+    }
+    if (P.probs != nullptr && lane == 0) {
+      if constexpr (kTok == 32) P.moved[blockIdx.x] = moved;
+      else reinterpret_cast<uint8_t*>(P.moved)[blockIdx.x] = static_cast<uint8_t>(moved);
     }
   }
 }
@@ -206,7 +214,7 @@ __global__ void __launch_bounds__(256) xent_piece_kernel(const __grid_constant__
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k) {
     const uint32_t col = row0 + k;
-    if (((moved >> (4 * warp + k)) & 1u) == 0) continue;
+    if (col >= P.m || ((moved >> (4 * warp + k)) & 1u) == 0) continue;
     const float ref = __ldcg(P.st.ref + P.m0 + col);
     const float r = b < P.n_blocks ? __ldcg(P.blocks + static_cast<uint64_t>(b) * P.stride + col).x : ref;
     const float f = pow2(r - ref);
@@ -475,7 +483,8 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       j.vocab = a.vocab;
       j.K = p.K;
       const uint32_t groups = (m + 31) / 32;
-      e = launch_pdl(xent_join_kernel, dim3(groups), dim3(32 * kJoinWarps), 0, stream, j);
+      e = m <= 128 ? launch_pdl(xent_join_kernel<8>, dim3((m + 7) / 8), dim3(32 * kJoinWarps), 0, stream, j)
+                   : launch_pdl(xent_join_kernel<32>, dim3(groups), dim3(32 * kJoinWarps), 0, stream, j);
       if (e != cudaSuccess) return e;
       if (!p.grad) continue;
       // as many CTAs a group as its blocks take, or as the copies of rows can use

@@ -786,15 +786,18 @@ static void split_range(uint32_t C, uint32_t tiles, uint32_t most, int sms, uint
   *splits = (C + *len - 1) / *len;
 }
 
-// Up to this many tokens a tile holds 16 (few tokens share an adapter), and in
-// the forward pass tiles are found and the splits added where they are used,
-// which saves two launches.
-constexpr uint32_t kLoraFewTokens = 256;
+// Up to this many tokens a tile holds 16 (few tokens share an adapter).
+constexpr uint32_t kLoraSmallTiles = 256;
+// Up to this many, in the forward pass, tiles are found and the splits added
+// where they are used, which saves two launches (a call of 32 tokens 127 us
+// against 131 with them) but repeats the search in every CTA: at 122 tokens 74.6
+// against 74.0 us, at 210 tokens of 22 adapters 147 against 126.
+constexpr uint32_t kLoraFewTokens = 64;
 
 void make_lora_plan(uint32_t M, const LoraDev& L, bool grad, int sms, LoraPlan* p) {
   p->M = M;
   p->sms = sms;
-  p->tm = M <= kLoraFewTokens ? 16 : 64;
+  p->tm = M <= kLoraSmallTiles ? 16 : 64;
   const uint32_t used = std::min(L.n, M);  // adapters that can have tokens
   p->few = !grad && M <= kLoraFewTokens;
   p->max_tiles = p->few ? M : static_cast<uint32_t>(std::min<uint64_t>(M, static_cast<uint64_t>(M) / p->tm + used));

@@ -228,6 +228,20 @@ def test_lora_of_many_and_few_adapters(cuda, M, n, K):
     within(y, *lora_reference(L, A, x, ids), "y")
 
 
+@pytest.mark.parametrize("M", [63, 64, 65, 256])
+def test_lora_where_the_grouping_changes(cuda, M):
+    # one adapter for all, an adapter for each, and every 16th token
+    L = usual(ans.INT8, 256, 192, seed=M)
+    A = Adapters(L, 64, 16)
+    rng = np.random.default_rng(M)
+    x = bf16(rng, M, L.K)
+    for ids in (torch.full((M,), 5), torch.arange(M) % 64, torch.where(torch.arange(M) % 16 == 3, 63, -1)):
+        ids = ids.to(torch.int32)
+        y, st = run_lora(L, A, x, ids)
+        assert st == 0
+        within(y, *lora_reference(L, A, x, ids), "y")
+
+
 def test_lora_tokens_without_an_adapter_are_the_product_itself(cuda):
     L = usual(ans.INT8, 256, 256, seed=9)
     A = Adapters(L, 4, 16)

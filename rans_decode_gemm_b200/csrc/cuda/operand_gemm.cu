@@ -144,7 +144,7 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
     }
     __syncwarp();
   }
-  const float ps = scale * lift;
+  const float ps = n_in ? scale * lift : 0.0f;  // (a padding row's scale may be anything)
   if (E.probs != nullptr) {
     uint16_t* p = E.probs + static_cast<uint64_t>(m) * rows + c;
     auto store = [&](uint32_t j) {

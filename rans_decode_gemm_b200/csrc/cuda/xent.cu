@@ -58,7 +58,7 @@ __device__ __forceinline__ float pow2(float e) {
 // largest scale in [2^8, 2^9): a probability of e^4 (kXentSlack) stays below the
 // largest f16, and 11 bits are kept down to 2^-22 of the reference's.
 __global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t M, const int32_t* __restrict__ targets,
-                                                          uint32_t vocab, uint32_t N, uint32_t f16, uint32_t kind,
+                                                          uint32_t vocab, uint32_t f16, uint32_t kind,
                                                           const void* scales, uint32_t* status) {
   __shared__ float part[32];
   griddep_wait();
@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t
   if (blockIdx.x != 0) return;
   float top = 0.0f;
   if (f16 && (kind == 1 || kind == 2)) {
-    // (N is a multiple of 128)
-    for (uint32_t n = 4 * threadIdx.x; n < N; n += 4096) {
+    // (there are scales up to the next multiple of 128)
+    for (uint32_t n = 4 * threadIdx.x; n < vocab; n += 4096) {
       float4 v;
       if (kind == 1) {
         const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(scales) + n));
@@ -84,8 +84,9 @@ __global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t
       } else {
         v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(scales) + n));
       }
+      uint32_t at = n;
       for (const float s : {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)})
-        if (s <= 3.402823466e38f) top = fmaxf(top, s);
+        if (at++ < vocab && s <= 3.402823466e38f) top = fmaxf(top, s);
     }
   }
 #pragma unroll
@@ -422,7 +423,7 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
   const XentState st{state, state + p.M, state + 2ull * p.M, state + 3ull * p.M, state + 4ull * p.M,
                      state + 5ull * p.M};
   cudaError_t e = launch_pdl(xent_begin_kernel, dim3(std::min(64u, (p.M + 1023) / 1024)), dim3(1024), 0, stream, st, p.M,
-                             a.targets, a.vocab, p.N, p.f16, a.scale_kind, a.scales, a.status);
+                             a.targets, a.vocab, p.f16, a.scale_kind, a.scales, a.status);
   if (e != cudaSuccess) return e;
   const uint16_t* x = a.X;
   const float* factor = nullptr;

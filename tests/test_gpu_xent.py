@@ -136,6 +136,18 @@ def test_padding_may_hold_infinities_and_nan(cuda, N, vocab, code):
     check(L, bf16(rng, 30, 64), some_targets(rng, 30, vocab), vocab)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 1e30, 0.0])
+@pytest.mark.parametrize("N,vocab", [(384, 299), (8320, 8200)])
+@pytest.mark.parametrize("dtype,kind", [(ans.INT8, ans.SCALE_ROW_F32), (ans.FP8_E4M3, ans.SCALE_ROW_BF16),
+                                        (ans.BF16_SPLIT, ans.SCALE_ROW_F32), (ans.INT4, ans.SCALE_GROUP_BF16)])
+def test_padding_may_have_any_scale(cuda, dtype, kind, N, vocab, value):
+    L = Layer(dtype, N, 64, 128, 64, kind, 64 if kind == ans.SCALE_GROUP_BF16 else 0, seed=12)
+    L.scales[vocab:] = value
+    L.w[vocab:] = 0.0
+    rng = np.random.default_rng(2)
+    check(L, bf16(rng, 30, 64, scale=0.1), some_targets(rng, 30, vocab), vocab)
+
+
 def test_targets_out_of_range(cuda):
     L = usual(ans.INT8, 256, 64, seed=8)
     rng = np.random.default_rng(2)

@@ -392,7 +392,8 @@ ans_status ans_gemm_batched(const ans_gemm_job* jobs, uint32_t n_jobs, uint32_t 
  * low-rank adapters of many requests beside a projection, the gradients that
  * train them, and the loss of a compressed vocabulary head.  W is never
  * changed and has no gradient.  The scale kinds are ans_gemm's, dequantised
- * weights w(n, k) as there.
+ * weights w(n, k) as there (group scales in [2^-14, 2^12], as there).
+ * Outputs and workspace overlap neither the inputs nor one another.
  *
  * All of these calls take M up to 2^24 tokens (ANS_ERR_UNSUPPORTED above),
  * write nothing outside the outputs they name and the workspace, and give the

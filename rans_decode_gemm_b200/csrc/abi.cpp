@@ -870,11 +870,11 @@ void make_grad_plan(const ans_layout& ly, uint32_t M, ans_scale_kind kind, const
   p->bytes = at;
 }
 
-// dX = dY W (+ delta, for the tokens of an adapter).
+// dX = dY W (+ delta, for the tokens of an adapter), after launch_operand_decode
+// and what runs beside it.
 cudaError_t launch_grad_x(const GradPlan& p, const ansdev::LayerDev& L, const uint16_t* d_dY, uint32_t M,
-                          ans_scale_kind kind, const void* d_scales, uint32_t group_k, const float* delta,
-                          const int32_t* ids, uint32_t n_ids, uint16_t* d_dX, uint8_t* ws, uint32_t* d_status,
-                          int sms, cudaStream_t stream) {
+                          ans_scale_kind kind, const void* d_scales, const float* delta, const int32_t* ids,
+                          uint32_t n_ids, uint16_t* d_dX, uint8_t* ws, uint32_t* d_status, cudaStream_t stream) {
   const void* rows = d_dY;
   const float* factor = nullptr;
   cudaError_t e;
@@ -888,8 +888,6 @@ cudaError_t launch_grad_x(const GradPlan& p, const ansdev::LayerDev& L, const ui
     factor = f;
   }
   uint8_t* images = ws + p.off_images;
-  e = ansdev::launch_operand_decode(L, 0, L.N, kind, d_scales, group_k, images, d_status, sms, stream);
-  if (e != cudaSuccess) return e;
   ansdev::OperandGemmOut out;
   std::memset(&out, 0, sizeof(out));
   out.ld = L.K;
@@ -1014,8 +1012,12 @@ ans_status ans_gemm_grad(const uint16_t* d_dY, uint32_t M, const ans_tiles* W, a
   GradPlan p;
   make_grad_plan(W->layout, M, scale_kind, nullptr, sms, &p);
   if (ws_bytes < p.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
-  cudaError_t e = launch_grad_x(p, L, d_dY, M, scale_kind, d_scales, group_k, nullptr, nullptr, 0, d_dX,
-                                static_cast<uint8_t*>(d_ws), d_status, sms, reinterpret_cast<cudaStream_t>(stream));
+  uint8_t* ws = static_cast<uint8_t*>(d_ws);
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = ansdev::launch_operand_decode(L, 0, L.N, scale_kind, d_scales, group_k, ws + p.off_images, d_status,
+                                                sms, cs);
+  if (e == cudaSuccess)
+    e = launch_grad_x(p, L, d_dY, M, scale_kind, d_scales, nullptr, nullptr, 0, d_dX, ws, d_status, cs);
   return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gemm_grad");
 }
 
@@ -1073,9 +1075,15 @@ ans_status ans_gemm_lora_grad(const uint16_t* d_X, const uint16_t* d_dY, uint32_
   if (ws_bytes < p.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
   uint8_t* ws = static_cast<uint8_t*>(d_ws);
   float* delta = d_dX ? reinterpret_cast<float*>(ws + p.off_delta) : nullptr;
-  cudaError_t e = ansdev::launch_lora_grad(p.lora, A, d_X, d_dY, d_ids, d_dA, d_dB, delta, ws + p.off_lora, d_status, cs);
+  // decoding leaves the matrix instructions and most of the memory's rate free: the
+  // adapters' outer products, the expansion and the form of dY run beside it
+  cudaError_t e = ansdev::launch_lora_grad_shrink(p.lora, A, d_X, d_dY, d_ids, ws + p.off_lora, d_status, cs);
   if (e == cudaSuccess && d_dX)
-    e = launch_grad_x(p, L, d_dY, M, scale_kind, d_scales, group_k, delta, d_ids, A.n, d_dX, ws, d_status, sms, cs);
+    e = ansdev::launch_operand_decode(L, 0, L.N, scale_kind, d_scales, group_k, ws + p.off_images, d_status, sms, cs);
+  if (e == cudaSuccess)
+    e = ansdev::launch_lora_grad_outer(p.lora, A, d_X, d_dY, d_ids, d_dA, d_dB, delta, ws + p.off_lora, cs);
+  if (e == cudaSuccess && d_dX)
+    e = launch_grad_x(p, L, d_dY, M, scale_kind, d_scales, delta, d_ids, A.n, d_dX, ws, d_status, cs);
   return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gemm_lora_grad");
 }
 

@@ -490,9 +490,7 @@ __device__ __forceinline__ void expand_weights(const ExpandDev& P, const uint16_
 }
 
 template <bool kCols, bool kFew, int kSteps>
-__global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant__ ExpandDev P) {
-  extern __shared__ __align__(16) uint16_t hs[];  // hi then lo: tm x pitch
-  __shared__ uint32_t tok[16], found;
+__device__ __forceinline__ void expand_cta(const ExpandDev& P, uint16_t* hs, uint32_t (&tok)[16], uint32_t& found) {
   const uint32_t tile = blockIdx.x;
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const uint32_t r16 = (P.rank + 15) / 16 * 16;
@@ -501,8 +499,6 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
   const uint32_t c0 = (blockIdx.y * (blockDim.x / 32) + warp) * 64;
   uint32_t b[kSteps > 0 ? kSteps : 1][8][2];
   uint32_t a, start = 0, count;
-  griddep_wait();
-  griddep_launch_dependents();
   if constexpr (kFew) {
     FewTile ft;
     bool bad;
@@ -600,6 +596,16 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
       if (v1 && in) *reinterpret_cast<float4*>(y1 + 16 * q) = v;
     }
   }
+}
+// (kCols, into dx: beside the outer products, which run beside the decoding)
+template <bool kCols, bool kFew, int kSteps>
+__global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant__ ExpandDev P) {
+  extern __shared__ __align__(16) uint16_t hs[];  // hi then lo: tm x pitch
+  __shared__ uint32_t tok[16], found;
+  if constexpr (!kCols) griddep_wait();
+  griddep_launch_dependents();
+  expand_cta<kCols, kFew, kSteps>(P, hs, tok, found);
+  if constexpr (kCols) griddep_beside_end();
 }
 
 // ---- outer: the sum over an adapter's tokens of z^T t ---------------------------
@@ -747,14 +753,16 @@ __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_
 struct OuterBoth {
   OuterDev b, a;
   uint32_t b_blocks;
+  uint32_t beside;  // runs beside the decoding of the weights
 };
 template <int NJ>
 __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const __grid_constant__ OuterBoth P) {
   extern __shared__ __align__(128) uint8_t stages_smem[];
-  griddep_wait();
+  if (P.beside == 0) griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x < P.b_blocks) outer_cta<false, NJ>(P.b, blockIdx.x * 64, stages_smem);
   else outer_cta<true, NJ>(P.a, (blockIdx.x - P.b_blocks) * 64, stages_smem);
+  if (P.beside != 0) griddep_beside_end();
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -921,12 +929,13 @@ static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups&
 }
 
 static cudaError_t outer(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const uint16_t* dY, const uint16_t* h,
-                         float* dB, const uint16_t* X, const uint16_t* dh, float* dA, cudaStream_t stream) {
+                         float* dB, const uint16_t* X, const uint16_t* dh, float* dA, bool beside, cudaStream_t stream) {
   const uint64_t hp_stride = static_cast<uint64_t>(p.positions) * rank_row(L.rank);
   OuterBoth P;
   P.b = OuterDev{G, dY, h, hp_stride, dB, L.N, L.rank};
   P.a = OuterDev{G, X, dh, hp_stride, dA, L.K, L.rank};
   P.b_blocks = (L.N + 63) / 64;
+  P.beside = beside;
   return by_rank(L.rank, [&](auto nj) {
     constexpr int NJ = decltype(nj)::value;
     static std::atomic<uint64_t> done{0};
@@ -958,9 +967,8 @@ cudaError_t launch_lora_expand(const LoraPlan& p, const LoraDev& L, const int32_
   return expand<false, false>(p, L, G, ids, nullptr, reinterpret_cast<uint16_t*>(w + p.off_h), Y, stream);
 }
 
-cudaError_t launch_lora_grad(const LoraPlan& p, const LoraDev& L, const uint16_t* X, const uint16_t* dY,
-                             const int32_t* ids, float* dA, float* dB, float* delta, void* ws, uint32_t* status,
-                             cudaStream_t stream) {
+cudaError_t launch_lora_grad_shrink(const LoraPlan& p, const LoraDev& L, const uint16_t* X, const uint16_t* dY,
+                                    const int32_t* ids, void* ws, uint32_t* status, cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   const LoraGroups G = groups_at(w + p.off_groups, p.positions, L.n, p.max_tiles);
   float* part = reinterpret_cast<float*>(w + p.off_part);
@@ -970,7 +978,17 @@ cudaError_t launch_lora_grad(const LoraPlan& p, const LoraDev& L, const uint16_t
   float* part_y = part + static_cast<uint64_t>(p.splits_k) * p.positions * L.rank;
   if (e == cudaSuccess) e = shrink<false>(p, L, G, X, part, dY, part_y, ids, status, stream);
   if (e == cudaSuccess) e = join(p, L, G, JoinDev{{part, part_y}, {p.splits_k, p.splits_n}, {h, dh}}, stream);
-  if (e == cudaSuccess) e = outer(p, L, G, dY, h, dB, X, dh, dA, stream);
+  return e;
+}
+
+cudaError_t launch_lora_grad_outer(const LoraPlan& p, const LoraDev& L, const uint16_t* X, const uint16_t* dY,
+                                   const int32_t* ids, float* dA, float* dB, float* delta, void* ws,
+                                   cudaStream_t stream) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const LoraGroups G = groups_at(w + p.off_groups, p.positions, L.n, p.max_tiles);
+  uint16_t* h = reinterpret_cast<uint16_t*>(w + p.off_h);
+  uint16_t* dh = reinterpret_cast<uint16_t*>(w + p.off_dh);
+  cudaError_t e = outer(p, L, G, dY, h, dB, X, dh, dA, delta != nullptr, stream);
   if (e == cudaSuccess && delta != nullptr) e = expand<true, false>(p, L, G, ids, nullptr, dh, delta, stream);
   return e;
 }

@@ -51,8 +51,14 @@ cudaError_t launch_lora_expand(const LoraPlan& plan, const LoraDev& L, const int
 // dH[m][j] = s_a sum_n dY[m][n] B_a[n][j];  dA_a = sum_m dH[m]^T X[m];
 // dB_a = s_a sum_m dY[m]^T (X[m] A_a^T);  delta[m] = dH[m] A_a where delta is
 // given (fp32 M x K, rows of tokens with an adapter only).
-cudaError_t launch_lora_grad(const LoraPlan& plan, const LoraDev& L, const uint16_t* X,
-                             const uint16_t* dY, const int32_t* ids, float* dA, float* dB,
-                             float* delta, void* ws, uint32_t* status, cudaStream_t stream);
+// In two parts: dH and X A_a^T, and what is made of them.  With delta, the second
+// part runs beside one kernel launched between the two, which has to wait for
+// the first as every kernel does, and to leave workspace and operands alone.
+cudaError_t launch_lora_grad_shrink(const LoraPlan& plan, const LoraDev& L, const uint16_t* X,
+                                    const uint16_t* dY, const int32_t* ids, void* ws, uint32_t* status,
+                                    cudaStream_t stream);
+cudaError_t launch_lora_grad_outer(const LoraPlan& plan, const LoraDev& L, const uint16_t* X,
+                                   const uint16_t* dY, const int32_t* ids, float* dA, float* dB,
+                                   float* delta, void* ws, cudaStream_t stream);
 
 }  // namespace ansdev

@@ -498,15 +498,15 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
 // row comes from L2 the second time).  f16 under a power of two of the row's
 // own keeps 11 bits of every value down to 2^-29 of the row's largest, and
 // what is smaller is off by at most 2^-40 of it: more than a rounding to bf16
-// would keep of v * s.  Infinities and NaN pass through.
+// would keep of v * s.  Infinities and NaN pass through.  Runs beside the decoding
+// of the weights.
 constexpr uint32_t kPrepThreads = 256;
 __global__ void __launch_bounds__(kPrepThreads) row_prep_kernel(const uint16_t* __restrict__ in, uint32_t C,
                                                                 uint32_t kind, const void* scales, bool f16,
                                                                 uint16_t* __restrict__ out,
                                                                 float* __restrict__ factor) {
   __shared__ float part[kPrepThreads / 32];
-  griddep_wait();
-  griddep_launch_dependents();
+  griddep_beside();
   const uint64_t row = static_cast<uint64_t>(blockIdx.x) * C;
   auto values = [&](uint32_t c, float (&v)[8]) {
     const uint4 q = __ldg(reinterpret_cast<const uint4*>(in + row + c));
@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kPrepThreads) row_prep_kernel(const uint16_t* 
     }
     *reinterpret_cast<uint4*>(out + row + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
+  griddep_beside_end();
 }
 
 cudaError_t launch_row_prep(const uint16_t* in, uint32_t M, uint32_t C, uint32_t scale_kind,

@@ -32,6 +32,16 @@ __device__ __forceinline__ void griddep_wait() {
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// A kernel that runs beside the one before it in the stream and uses none of its
+// results (nor writes what it reads).  It starts when all CTAs of that kernel have
+// started, and so, as an ordinary kernel waits before it lets the next one start,
+// when the kernels before the nearest ordinary one have finished: what it reads has
+// to come from those.  Its first CTA ends after the kernel beside it, so that
+// whoever waits for this one has waited for both.
+__device__ __forceinline__ void griddep_beside() { griddep_launch_dependents(); }
+__device__ __forceinline__ void griddep_beside_end() {
+  if (threadIdx.x == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) griddep_wait();
+}
 
 // Release/acquire fence at GPU scope (lighter than the sequentially
 // consistent fence of __threadfence); with a relaxed atomic after it (before

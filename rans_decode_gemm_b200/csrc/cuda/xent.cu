@@ -53,7 +53,7 @@ __device__ __forceinline__ float pow2(float e) {
   return e < -126.0f ? 0.0f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(fminf(e, 127.0f)) + 127) << 23);
 }
 
-// Clears the state, checks the targets and sets lift: f16 probabilities carry
+// Beside the first piece's decoding.  Clears the state, checks the targets and sets lift: f16 probabilities carry
 // the row scale of W, so they are stored under a power of two that puts the
 // largest scale in [2^8, 2^9): a probability of e^4 (kXentSlack) stays below the
 // largest f16, and 11 bits are kept down to 2^-22 of the reference's.
@@ -61,8 +61,7 @@ __global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t
                                                           uint32_t vocab, uint32_t f16, uint32_t kind,
                                                           const void* scales, uint32_t* status) {
   __shared__ float part[32];
-  griddep_wait();
-  griddep_launch_dependents();
+  griddep_beside();
   bool bad = false;
   for (uint32_t m = blockIdx.x * 1024 + threadIdx.x; m < M; m += gridDim.x * 1024) {
     st.ref[m] = kXentNone;
@@ -71,7 +70,7 @@ __global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t
     bad = bad || (t >= 0 && static_cast<uint32_t>(t) >= vocab);
   }
   if (bad) atomicOr(status, kStatusBadIndex);
-  if (blockIdx.x != 0) return;
+  if (blockIdx.x != 0) return;  // (the first CTA is the one that ends last)
   float top = 0.0f;
   if (f16 && (kind == 1 || kind == 2)) {
     // (there are scales up to the next multiple of 128)
@@ -98,12 +97,14 @@ __global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t
     const int ex = top == 0.0f ? 0 : static_cast<int>(__float_as_uint(top) >> 23) - 127;
     *st.lift = f16 ? pow2(static_cast<float>(min(126, max(-118, 8 - ex)))) : 1.0f;
   }
+  griddep_beside_end();
 }
 
 struct XentJoin {
   XentState st;
   const float2* blocks;    // (reference, sum): [n_blocks][stride], tokens m0 .. m0 + m - 1 from column 0
   uint32_t stride, n_blocks, m0, m, rows, f16;
+  uint32_t beside;         // runs beside the next piece's decoding
   uint32_t* moved;         // one bit a token, in order: has blocks under another reference
   uint16_t* probs;         // m x rows, or null
   // the targets' rows of W
@@ -122,7 +123,7 @@ template <uint32_t kTok>
 __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const __grid_constant__ XentJoin P) {
   constexpr uint32_t kShares = kJoinWarps * 32 / kTok;
   __shared__ float part_ref[kShares][kTok + 1], part_low[kShares][kTok + 1], part_sum[kShares][kTok + 1];
-  griddep_wait();
+  if (P.beside == 0) griddep_wait();
   griddep_launch_dependents();
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t tok = threadIdx.x % kTok, share = threadIdx.x / kTok, col = blockIdx.x * kTok + tok;
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const __grid
       else reinterpret_cast<uint8_t*>(P.moved)[blockIdx.x] = static_cast<uint8_t>(moved);
     }
   }
+  if (P.beside != 0) griddep_beside_end();
 }
 
 // What the transposed product and the end need of a piece.  Probabilities of
@@ -422,19 +424,17 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
   float* state = reinterpret_cast<float*>(w + p.off_state);
   const XentState st{state, state + p.M, state + 2ull * p.M, state + 3ull * p.M, state + 4ull * p.M,
                      state + 5ull * p.M};
-  cudaError_t e = launch_pdl(xent_begin_kernel, dim3(std::min(64u, (p.M + 1023) / 1024)), dim3(1024), 0, stream, st, p.M,
-                             a.targets, a.vocab, p.f16, a.scale_kind, a.scales, a.status);
-  if (e != cudaSuccess) return e;
-  const uint16_t* x = a.X;
-  const float* factor = nullptr;
-  if (p.f16) {
-    uint16_t* x16 = reinterpret_cast<uint16_t*>(w + p.off_x16);
-    float* f = reinterpret_cast<float*>(w + p.off_factor);
-    e = launch_row_prep(a.X, p.M, p.K, 0, nullptr, true, x16, f, stream);
-    if (e != cudaSuccess) return e;
-    x = x16;
-    factor = f;
-  }
+  uint16_t* x16 = reinterpret_cast<uint16_t*>(w + p.off_x16);
+  float* x_factor = reinterpret_cast<float*>(w + p.off_factor);
+  const uint16_t* x = p.f16 ? x16 : a.X;
+  const float* factor = p.f16 ? x_factor : nullptr;
+  auto launch_join = [&](const XentJoin& j) {
+    return j.m <= 128 ? launch_pdl(xent_join_kernel<8>, dim3((j.m + 7) / 8), dim3(32 * kJoinWarps), 0, stream, j)
+                      : launch_pdl(xent_join_kernel<32>, dim3((j.m + 31) / 32), dim3(32 * kJoinWarps), 0, stream, j);
+  };
+  XentJoin j;
+  bool pending = false;  // j is still to be joined
+  cudaError_t e;
   const uint64_t MK = static_cast<uint64_t>(p.M) * p.K;
   for (uint32_t n0 = 0; n0 < a.vocab; n0 += p.piece) {
     const uint32_t rows = std::min(p.piece, p.N - n0);
@@ -446,6 +446,18 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       e = launch_pdl(xent_blank_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((items + 255) / 256, 1024))), dim3(256), 0,
                      stream, images, first, rows, p.K / 16);
       if (e != cudaSuccess) return e;
+    }
+    if (n0 == 0) {
+      e = launch_pdl(xent_begin_kernel, dim3(std::min(64u, (p.M + 1023) / 1024)), dim3(1024), 0, stream, st, p.M, a.targets,
+                     a.vocab, p.f16, a.scale_kind, a.scales, a.status);
+      if (e == cudaSuccess && p.f16) e = launch_row_prep(a.X, p.M, p.K, 0, nullptr, true, x16, x_factor, stream);
+      if (e != cudaSuccess) return e;
+    }
+    if (pending) {
+      j.beside = 1;
+      e = launch_join(j);
+      if (e != cudaSuccess) return e;
+      pending = false;
     }
     for (uint32_t m0 = 0; m0 < p.M; m0 += p.chunk) {
       const uint32_t m = std::min(p.chunk, p.M - m0);
@@ -466,7 +478,6 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       e = launch_operand_gemm(plan_operand_gemm(false, p.f16, m, rows, p.K, 1, p.sms), images,
                               x + static_cast<uint64_t>(m0) * p.K, nullptr, &f, a.status, stream);
       if (e != cudaSuccess) return e;
-      XentJoin j;
       j.st = st;
       j.blocks = blocks;
       j.stride = p.chunk;
@@ -483,9 +494,13 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       j.n0 = n0;
       j.vocab = a.vocab;
       j.K = p.K;
+      j.beside = 0;
       const uint32_t groups = (m + 31) / 32;
-      e = m <= 128 ? launch_pdl(xent_join_kernel<8>, dim3((m + 7) / 8), dim3(32 * kJoinWarps), 0, stream, j)
-                   : launch_pdl(xent_join_kernel<32>, dim3(groups), dim3(32 * kJoinWarps), 0, stream, j);
+      // without a gradient, the last tokens' blocks are joined beside the next
+      // piece's decoding
+      pending = !p.grad && m0 + m == p.M && n0 + p.piece < a.vocab;
+      if (pending) break;
+      e = launch_join(j);
       if (e != cudaSuccess) return e;
       if (!p.grad) continue;
       // as many CTAs a group as its blocks take, or as the copies of rows can use

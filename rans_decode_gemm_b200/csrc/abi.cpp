@@ -842,13 +842,13 @@ struct GradPlan {
   ansdev::OperandGemmPlan gemm;
   ansdev::LoraPlan lora;
   bool prep;  // dY needs a form of its own (f16, or row scales applied)
-  size_t off_images, off_rows, off_factor, off_parts, off_delta, off_lora, bytes;
+  size_t off_images, off_rows, off_factor, off_gemm, off_delta, off_lora, bytes;
 };
 
 void make_grad_plan(const ans_layout& ly, uint32_t M, ans_scale_kind kind, const ansdev::LoraDev* lora, int sms,
                     GradPlan* p) {
   const bool f16 = ansdev::operand_is_f16(ly.dtype);
-  p->gemm = ansdev::plan_operand_gemm(true, f16, M, ly.N, ly.K, 16, sms);
+  p->gemm = ansdev::plan_operand_gemm(true, f16, M, ly.N, ly.K, sms);
   p->prep = f16 || kind == ANS_SCALE_ROW_BF16 || kind == ANS_SCALE_ROW_F32;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -860,7 +860,7 @@ void make_grad_plan(const ans_layout& ly, uint32_t M, ans_scale_kind kind, const
   p->off_images = take(ansdev::operand_bytes(ly.N, ly.K));
   p->off_rows = take(p->prep ? static_cast<size_t>(M) * ly.N * 2 : 0);
   p->off_factor = take(p->prep ? static_cast<size_t>(M) * 4 : 0);
-  p->off_parts = take(p->gemm.splits > 1 ? MK * 4 * p->gemm.splits : 0);
+  p->off_gemm = take(ansdev::operand_gemm_workspace(p->gemm));
   p->off_delta = take(lora ? MK * 4 : 0);
   p->off_lora = at;
   if (lora) {
@@ -891,20 +891,12 @@ cudaError_t launch_grad_x(const GradPlan& p, const ansdev::LayerDev& L, const ui
   ansdev::OperandGemmOut out;
   std::memset(&out, 0, sizeof(out));
   out.ld = L.K;
-  if (p.gemm.splits == 1) {
-    out.out16 = d_dX;
-    out.beta = factor;
-    out.add = delta;
-    out.ids = ids;
-    out.n_ids = n_ids;
-    return ansdev::launch_operand_gemm(p.gemm, images, rows, &out, nullptr, d_status, stream);
-  }
-  out.out32 = reinterpret_cast<float*>(ws + p.off_parts);
-  out.split_stride = static_cast<uint64_t>(M) * L.K;
-  e = ansdev::launch_operand_gemm(p.gemm, images, rows, &out, nullptr, d_status, stream);
-  if (e != cudaSuccess) return e;
-  return ansdev::launch_sum_splits(out.out32, p.gemm.splits, out.split_stride, M, L.K, factor, delta, ids, n_ids, d_dX,
-                                   stream);
+  out.out16 = d_dX;
+  out.beta = factor;
+  out.add = delta;
+  out.ids = ids;
+  out.n_ids = n_ids;
+  return ansdev::launch_operand_gemm(p.gemm, images, rows, &out, nullptr, ws + p.off_gemm, d_status, stream);
 }
 
 }  // namespace

@@ -51,19 +51,18 @@ struct OperandGemmPlan {
   uint32_t splits;   // ranges of the sum (transposed only)
   uint32_t sms;
 };
-// max_splits 1: never cut.
-OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t rows, uint32_t K,
-                                  uint32_t max_splits, int sms);
+OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t rows, uint32_t K, int sms);
+// Workspace of a sum that is cut (256-byte aligned).
+size_t operand_gemm_workspace(const OperandGemmPlan& plan);
 
 // What happens to the transposed sums v[m][k].
 struct OperandGemmOut {
   // out16: out16[m * ld + k] = bf16(beta[m] * v + add[m * ld + k]), the addend
   //   taken for rows with 0 <= ids[m] < n_ids only (add may be null).
-  // out32: out32[split][m * ld + k] = alpha[m] * (its old value) + beta[m] * v;
+  // out32: out32[m * ld + k] = alpha[m] * (its old value) + beta[m] * v;
   //   alpha null: the old value is not read.  beta null: 1.
   float* out32;
   uint16_t* out16;
-  uint64_t split_stride;  // elements between the splits' out32
   uint32_t ld;
   const float* alpha;
   const float* beta;
@@ -98,14 +97,8 @@ struct XentEpilogue {
 
 // Exactly one of out (transposed) and xent (logits) is given.
 cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* images, const void* rows16,
-                                const OperandGemmOut* out, const XentEpilogue* xent, uint32_t* status,
+                                const OperandGemmOut* out, const XentEpilogue* xent, void* ws, uint32_t* status,
                                 cudaStream_t stream);
-
-// out[m][k] = bf16(beta[m] * sum over splits of part[split][m][k] + add[m][k])
-// (the addend as in OperandGemmOut).
-cudaError_t launch_sum_splits(const float* part, uint32_t splits, uint64_t split_stride, uint32_t M,
-                              uint32_t K, const float* beta, const float* add, const int32_t* ids,
-                              uint32_t n_ids, uint16_t* out, cudaStream_t stream);
 
 cudaError_t set_live_wait_budget_operand(long long cycles);
 cudaError_t set_live_wait_budget_operand_gemm(long long cycles);

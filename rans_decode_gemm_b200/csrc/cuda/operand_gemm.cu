@@ -65,6 +65,7 @@ struct OperandGemmDev {
   uint32_t f16;
   uint32_t* status;
   uint32_t M, bn, m_blocks, n_tiles, splits;
+  float* parts;            // where splits > 1: [tile without its split][split][bn][128]
   uint32_t k_slabs;      // images per 128-row block (K / 16)
   uint32_t out_cols;     // rows of D that exist: rows of W, or K (transposed)
   uint32_t n_kb;         // stages of the whole sum
@@ -313,8 +314,10 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
     // references, targets and factors.
     const uint32_t quad = warp & 3u, turn = 32u * ((warp - 2) >> 2);
     const OperandGemmOut& O = P.out;
-    const bool rmw = kTrans && O.out32 != nullptr && O.alpha != nullptr;
-    const bool adds = kTrans && O.out32 == nullptr && O.add != nullptr;
+    // (a part of a sum that is cut goes to memory as it is)
+    const bool cut = kTrans && P.splits > 1;
+    const bool rmw = kTrans && !cut && O.out32 != nullptr && O.alpha != nullptr;
+    const bool adds = kTrans && !cut && O.out32 == nullptr && O.add != nullptr;
     const float lift = kTrans ? 1.0f : __ldcg(P.xent.lift);
     uint32_t acc = 0;
     for (uint32_t t = blockIdx.x; t < P.n_tiles; t += gridDim.x, ++acc) {
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
       const uint32_t m0 = mb * P.bn;
       const uint32_t cols = min(P.bn, P.M - m0);
       const uint64_t tile_at = static_cast<uint64_t>(m0) * O.ld + c;
-      float* out32 = O.out32 + sp * O.split_stride;
+      float* out32 = O.out32;
       float scale = 1.0f;
       if (!kTrans) {
         if (P.xent.scale_kind == 1) scale = bf16_to_f32(__ldg(static_cast<const uint16_t*>(P.xent.scales) + c));
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
           return;
         }
         if (rmw) my_alpha = m_in ? __ldcg(O.alpha + m) : 0.0f;
-        if (O.beta != nullptr) my_beta = m_in ? __ldcg(O.beta + m) : 0.0f;
+        if (!cut && O.beta != nullptr) my_beta = m_in ? __ldcg(O.beta + m) : 0.0f;
         if (rmw || adds) {
           uint32_t want = cols - c0 < 32 ? (1u << (cols - c0)) - 1u : 0xFFFFFFFFu;
           if (adds) {
@@ -376,6 +379,12 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
           const XentToken now = tok;
           if (c0 + 64 < cols) ask(c0 + 64);
           xent_fold(P.xent, P.f16, P.out_cols, v, scale, lift, c, m0 + c0, min(32u, cols - c0), lane, now);
+        } else if (cut) {
+          const uint64_t at = static_cast<uint64_t>(ab * P.m_blocks + mb) * P.splits + sp;
+          float* part = P.parts + (at * P.bn + c0) * kOgBM + 32 * quad + lane;
+#pragma unroll
+          for (uint32_t j = 0; j < 32; ++j)
+            if (c0 + j < cols) __stcg(part + j * kOgBM, __uint_as_float(v[j]));
         } else {
           float x[32];
 #pragma unroll
@@ -406,8 +415,60 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
   if (warp == 1) tmem_dealloc(tmem_base, 512);
 }
 
-OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t rows, uint32_t K,
-                                  uint32_t max_splits, int sms) {
+// The parts of sums that are cut, added in order and stored: a warp a token of a
+// tile, four rows of D a lane.  (Parts in planes of M x K, added by a kernel over the
+// whole of them, held a bf16 4096 x 4096 gradient of 200 tokens at 45.6 us against 42.7;
+// added by the CTA with a tile's last part, behind flags, at 51.3.)
+struct JoinParts {
+  OperandGemmOut out;
+  const float* parts;
+  uint32_t M, bn, m_blocks, splits, out_cols;
+};
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ JoinParts P) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t tile = blockIdx.x, ab = tile / P.m_blocks, j = blockIdx.y * 8 + threadIdx.x / 32;
+  const uint32_t m = (tile - ab * P.m_blocks) * P.bn + j, c = 4 * (threadIdx.x % 32), k = ab * kOgBM + c;
+  if (m >= P.M || j >= P.bn || k >= P.out_cols) return;  // (out_cols is a multiple of 16)
+  const OperandGemmOut& O = P.out;
+  const float* part = P.parts + (static_cast<uint64_t>(tile) * P.splits * P.bn + j) * kOgBM + c;
+  const uint64_t at = static_cast<uint64_t>(m) * O.ld + k, step = static_cast<uint64_t>(P.bn) * kOgBM;
+  float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float alpha = 0.0f;
+  bool adds = false;
+  if (O.out32 != nullptr && O.alpha != nullptr) {
+    alpha = __ldcg(O.alpha + m);
+    old = __ldcg(reinterpret_cast<const float4*>(O.out32 + at));
+    adds = true;
+  } else if (O.out32 == nullptr && O.add != nullptr) {
+    const int32_t id = __ldg(O.ids + m);
+    adds = id >= 0 && static_cast<uint32_t>(id) < O.n_ids;
+    alpha = 1.0f;
+    if (adds) old = __ldcg(reinterpret_cast<const float4*>(O.add + at));
+  }
+  float4 v = __ldcg(reinterpret_cast<const float4*>(part));
+#pragma unroll 4
+  for (uint32_t s = 1; s < P.splits; ++s) {
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(part + s * step));
+    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+  }
+  if (O.beta != nullptr) {
+    const float f = __ldcg(O.beta + m);
+    v.x *= f; v.y *= f; v.z *= f; v.w *= f;
+  }
+  if (adds) {
+    v.x = fmaf(alpha, old.x, v.x); v.y = fmaf(alpha, old.y, v.y); v.z = fmaf(alpha, old.z, v.z); v.w = fmaf(alpha, old.w, v.w);
+  }
+  if (O.out32 != nullptr) {
+    *reinterpret_cast<float4*>(O.out32 + at) = v;
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(O.out16 + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t rows, uint32_t K, int sms) {
   OperandGemmPlan p;
   p.trans = trans;
   p.f16 = f16;
@@ -421,12 +482,13 @@ OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t row
   // its tokens (one round of 32 stages measured 19.3, 19.4, 22.2 and 28.7 us at
   // 32, 64, 128 and 256 tokens, some 9 of it the launch and its ends).  A narrow
   // tile hardly runs faster, so it only serves to fill the SMs.  A sum over n may
-  // be cut instead: its partial sums are written and read at about 4 TB/s.
+  // be cut instead (8 stages a part at least): its parts are written and read at
+  // about 4 TB/s by a second kernel.
   uint64_t least = ~0ull;
   for (uint32_t bn = 256; bn >= 32; bn /= 2) {
     if (bn > 32 && M <= bn / 2) continue;
     const uint64_t tiles = blocks * ((M + bn - 1) / bn);
-    const uint32_t most = trans ? std::min(max_splits, (n_kb + 7) / 8) : 1u;
+    const uint32_t most = trans ? std::min(16u, std::max(1u, n_kb / 8)) : 1u;
     for (uint32_t s = 1; s <= most; ++s) {
       const uint64_t rounds = (tiles * s + p.sms - 1) / p.sms;
       uint64_t cost = rounds * ((n_kb + s - 1) / s) * (300 + bn * 13 / 20);
@@ -441,8 +503,14 @@ OperandGemmPlan plan_operand_gemm(bool trans, bool f16, uint32_t M, uint32_t row
   return p;
 }
 
+size_t operand_gemm_workspace(const OperandGemmPlan& p) {
+  if (p.splits <= 1) return 0;
+  const size_t tiles = static_cast<size_t>((p.K + kOgBM - 1) / kOgBM) * ((p.M + p.bn - 1) / p.bn);
+  return tiles * p.splits * p.bn * kOgBM * 4;
+}
+
 cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* images, const void* rows16,
-                                const OperandGemmOut* out, const XentEpilogue* xent, uint32_t* status,
+                                const OperandGemmOut* out, const XentEpilogue* xent, void* ws, uint32_t* status,
                                 cudaStream_t stream) {
   if (plan.M == 0) return cudaSuccess;
   OperandGemmDev P;
@@ -456,6 +524,7 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
   P.bn = plan.bn;
   P.m_blocks = (plan.M + plan.bn - 1) / plan.bn;
   P.splits = plan.splits;
+  P.parts = static_cast<float*>(ws);
   P.k_slabs = plan.K / 16;
   P.out_cols = plan.trans ? plan.K : plan.rows;
   const uint32_t red = plan.trans ? plan.rows : plan.K;
@@ -490,7 +559,11 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }
   const uint32_t grid = std::min(P.n_tiles, plan.sms);
-  return launch_pdl(kern, dim3(grid), dim3(kOgThreads), kOgSmem, stream, P);
+  e = launch_pdl(kern, dim3(grid), dim3(kOgThreads), kOgSmem, stream, P);
+  if (e != cudaSuccess || plan.splits == 1) return e;
+  // a CTA 8 tokens of a tile
+  const JoinParts J{P.out, P.parts, plan.M, plan.bn, P.m_blocks, plan.splits, P.out_cols};
+  return launch_pdl(join_parts_kernel, dim3(P.n_tiles / plan.splits, (P.b_box_rows + 7) / 8), dim3(256), 0, stream, J);
 }
 
 // ---- rows of bf16 as scaled f16 ----------------------------------------------
@@ -576,49 +649,6 @@ cudaError_t launch_row_prep(const uint16_t* in, uint32_t M, uint32_t C, uint32_t
   if (M == 0) return cudaSuccess;
   return launch_pdl(row_prep_kernel, dim3(M), dim3(kPrepThreads), 0, stream, in, C, scale_kind, scales, f16,
                     out, factor);
-}
-
-// ---- the sum over the splits of a transposed product --------------------------
-__global__ void __launch_bounds__(256) sum_splits_kernel(const float* __restrict__ part, uint32_t splits,
-                                                         uint64_t stride, uint32_t K4, uint64_t n4,
-                                                         const float* beta, const float* add,
-                                                         const int32_t* ids, uint32_t n_ids,
-                                                         uint16_t* __restrict__ out) {
-  griddep_wait();
-  griddep_launch_dependents();
-  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < n4;
-       i += static_cast<uint64_t>(gridDim.x) * 256) {
-    const uint32_t m = static_cast<uint32_t>(i / K4);
-    float4 a = __ldcg(reinterpret_cast<const float4*>(part) + i);
-    for (uint32_t s = 1; s < splits; ++s) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(part + s * stride) + i);
-      a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-    }
-    if (beta != nullptr) {
-      const float f = __ldcg(beta + m);
-      a.x *= f; a.y *= f; a.z *= f; a.w *= f;
-    }
-    if (add != nullptr) {
-      const int32_t id = __ldg(ids + m);
-      if (id >= 0 && static_cast<uint32_t>(id) < n_ids) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(add) + i);
-        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-      }
-    }
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
-    *reinterpret_cast<uint2*>(out + 4 * i) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  }
-}
-
-cudaError_t launch_sum_splits(const float* part, uint32_t splits, uint64_t split_stride, uint32_t M,
-                              uint32_t K, const float* beta, const float* add, const int32_t* ids,
-                              uint32_t n_ids, uint16_t* out, cudaStream_t stream) {
-  const uint64_t n4 = static_cast<uint64_t>(M) * K / 4;
-  if (n4 == 0) return cudaSuccess;
-  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>((n4 + 255) / 256, 2048));
-  return launch_pdl(sum_splits_kernel, dim3(grid), dim3(256), 0, stream, part, splits, split_stride, K / 4, n4,
-                    beta, add, ids, n_ids, out);
 }
 
 cudaError_t set_live_wait_budget_operand_gemm(long long cycles) {

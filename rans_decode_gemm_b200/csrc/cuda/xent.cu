@@ -272,13 +272,12 @@ struct XentFinish {
   const int32_t* targets;
   const void* scales;
   XentState st;
-  const float* acc;        // splits x M x K
-  uint64_t split_stride;
+  const float* acc;        // M x K
   const uint16_t* target_rows;
   const float* weight;
   float *loss, *lse;
   uint16_t* dX;
-  uint32_t vocab, K, scale_kind, f16, splits;
+  uint32_t vocab, K, scale_kind, f16;
 };
 
 __global__ void __launch_bounds__(kXentThreads) xent_finish_kernel(const __grid_constant__ XentFinish P) {
@@ -312,11 +311,7 @@ __global__ void __launch_bounds__(kXentThreads) xent_finish_kernel(const __grid_
     const uint64_t at = static_cast<uint64_t>(m) * P.K + k;
     uint32_t lo = 0, hi = 0;
     if (valid) {
-      float4 a = __ldcg(reinterpret_cast<const float4*>(P.acc + at));
-      for (uint32_t q = 1; q < P.splits; ++q) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(P.acc + q * P.split_stride + at));
-        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-      }
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(P.acc + at));
       const uint2 w = __ldcg(reinterpret_cast<const uint2*>(P.target_rows + at));
       float t[4];
       if (P.f16) {
@@ -386,15 +381,12 @@ void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms_in, XentPl
     if (b <= unit) break;
   }
   p->piece = best * 128;
-  // one plan of the gradient's product for every piece and chunk (the last piece
-  // is cut into the same ranges)
-  p->splits = p->back_bn = 1;
-  if (grad) {
-    const uint32_t last = L.N - (L.N - 1) / p->piece * p->piece;
-    const OperandGemmPlan g = plan_operand_gemm(true, p->f16, p->chunk, p->piece, L.K, std::min(8u, last / 64), sms_in);
-    p->splits = g.splits;
-    p->back_bn = g.bn;
-  }
+  // the gradient's product, for the usual and the last of pieces and chunks
+  size_t gemm = 0;
+  if (grad)
+    for (const uint32_t rows : {p->piece, L.N - (L.N - 1) / p->piece * p->piece})
+      for (const uint32_t m : {p->chunk, M - (M - 1) / p->chunk * p->chunk})
+        gemm = std::max(gemm, operand_gemm_workspace(plan_operand_gemm(true, p->f16, m, rows, L.K, sms_in)));
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t o = at;
@@ -409,8 +401,9 @@ void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms_in, XentPl
   p->off_x16 = take(p->f16 ? MK * 2 : 0);
   p->off_factor = take(p->f16 ? static_cast<size_t>(M) * 4 : 0);
   p->off_state = take((static_cast<size_t>(M) * 5 + 1) * 4);
-  p->off_acc = take(grad ? MK * 4 * p->splits : 0);
+  p->off_acc = take(grad ? MK * 4 : 0);
   p->off_target = take(grad ? MK * 2 : 0);
+  p->off_gemm = take(gemm);
   p->bytes = at;
 }
 
@@ -435,7 +428,6 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
   XentJoin j;
   bool pending = false;  // j is still to be joined
   cudaError_t e;
-  const uint64_t MK = static_cast<uint64_t>(p.M) * p.K;
   for (uint32_t n0 = 0; n0 < a.vocab; n0 += p.piece) {
     const uint32_t rows = std::min(p.piece, p.N - n0);
     e = launch_operand_decode(L, n0, rows, a.scale_kind, a.scales, a.group_k, images, a.status, p.sms, stream);
@@ -475,8 +467,8 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       f.probs = probs;
       f.n0 = n0;
       f.vocab = a.vocab;
-      e = launch_operand_gemm(plan_operand_gemm(false, p.f16, m, rows, p.K, 1, p.sms), images,
-                              x + static_cast<uint64_t>(m0) * p.K, nullptr, &f, a.status, stream);
+      e = launch_operand_gemm(plan_operand_gemm(false, p.f16, m, rows, p.K, p.sms), images,
+                              x + static_cast<uint64_t>(m0) * p.K, nullptr, &f, w + p.off_gemm, a.status, stream);
       if (e != cudaSuccess) return e;
       j.st = st;
       j.blocks = blocks;
@@ -507,16 +499,13 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       const uint32_t copies = std::min((p.K / 8 + 31) / 32, std::max(1u, 4u * static_cast<uint32_t>(p.sms) / groups));
       e = launch_pdl(xent_piece_kernel, dim3(groups, std::max((j.n_blocks + 31) / 32, copies)), dim3(256), 0, stream, j);
       if (e != cudaSuccess) return e;
-      OperandGemmPlan tp = plan_operand_gemm(true, p.f16, m, rows, p.K, 1, p.sms);
-      tp.bn = p.back_bn;
-      tp.splits = p.splits;
       OperandGemmOut back = {};
       back.out32 = acc + static_cast<uint64_t>(m0) * p.K;
-      back.split_stride = MK;
       back.ld = p.K;
       back.alpha = n0 == 0 ? nullptr : st.alpha + m0;
       back.beta = st.beta + m0;
-      e = launch_operand_gemm(tp, images, probs, &back, nullptr, a.status, stream);
+      e = launch_operand_gemm(plan_operand_gemm(true, p.f16, m, rows, p.K, p.sms), images, probs, &back, nullptr,
+                              w + p.off_gemm, a.status, stream);
       if (e != cudaSuccess) return e;
     }
   }
@@ -525,7 +514,6 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
   f.scales = a.scales;
   f.st = st;
   f.acc = acc;
-  f.split_stride = MK;
   f.target_rows = target_rows;
   f.weight = a.weight;
   f.loss = a.loss;
@@ -535,7 +523,6 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
   f.K = p.K;
   f.scale_kind = a.scale_kind;
   f.f16 = p.f16;
-  f.splits = p.splits;
   return launch_pdl(xent_finish_kernel, dim3(p.M), dim3(kXentThreads), 0, stream, f);
 }
 

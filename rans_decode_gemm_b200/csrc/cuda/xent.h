@@ -15,11 +15,9 @@ struct XentPlan {
   uint32_t grad, f16;
   uint32_t piece;    // W rows of one piece of the vocabulary (the last may hold fewer)
   uint32_t chunk;    // tokens whose probabilities of one piece exist at a time
-  uint32_t splits;   // partial sums of the gradient
-  uint32_t back_bn;  // token tile of its product
   int sms;
   // workspace, byte offsets
-  size_t off_images, off_probs, off_blocks, off_moved, off_x16, off_factor, off_state, off_acc, off_target, bytes;
+  size_t off_images, off_probs, off_blocks, off_moved, off_x16, off_factor, off_state, off_acc, off_target, off_gemm, bytes;
 };
 
 struct XentArgs {

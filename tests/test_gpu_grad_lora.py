@@ -130,6 +130,21 @@ def test_grad_of_odd_sizes(cuda, dtype, N, K, M):
     within(run_grad(L, dy), *grad_reference(L, dy), "dx")
 
 
+# sums that are cut into 16, 8 and 9 parts (these of uneven lengths), with ragged tiles; and
+# more tiles than a round of the SMs, one to three rounds
+@pytest.mark.parametrize("N,K,M", [(10240, 128, 40), (4096, 400, 300), (14336, 1040, 300), (1024, 4112, 1290),
+                                   (2048, 4096, 1280), (640, 16384, 600)])
+@pytest.mark.parametrize("dtype", [ans.BF16_SPLIT, ans.FP8_E4M3])
+def test_grad_where_sums_are_cut(cuda, dtype, N, K, M):
+    L = usual(dtype, N, K, seed=N + K)
+    dy = bf16(np.random.default_rng(M), M, N)
+    ws = workspace(ans.ans_gemm_grad_workspace(L.layout, M, L.kind))
+    first = run_grad(L, dy, ws)
+    within(first, *grad_reference(L, dy), "dx")
+    ws.fill_(0xFF)                                # every part is written before it is read
+    assert torch.equal(run_grad(L, dy, ws), first)
+
+
 @pytest.mark.parametrize("state_bits", [32, 64])
 @pytest.mark.parametrize("dtype,kind,group", [
     (ans.BF16_SPLIT, ans.SCALE_ROW_F32, 0), (ans.BF16_SPLIT, ans.SCALE_ROW_BF16, 0), (ans.INT4, ans.SCALE_NONE, 0),

@@ -610,12 +610,14 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
 
 // ---- outer: the sum over an adapter's tokens of z^T t ---------------------------
 // out[c][j] = sum_p z[perm[p]][c] * h[p][j] for one adapter, in dB's layout (C x
-// rank) or dA's (rank x C, kRankMajor).  A CTA takes 64 columns c and all ranks;
+// rank) or dA's (rank x C, kRankMajor).  A CTA takes 64 columns c and up to 64 ranks
+// (kHalf: half of those in rows of 128.  All 128 left room for one CTA an SM: 181
+// us for 3,332 tokens of 12 adapters at rank 104, 6400 x 11008; halves, 167);
 // a stage is 64 positions of z and of h's two parts, both read by transposing
 // matrix loads.  Warps 0-3 have 16 columns each and the stage's first 32
 // positions, warps 4-7 the same columns and the other 32; the halves are added
 // at the end.  The tokens of a stage are looked up a stage before its loads.
-constexpr uint32_t kOuterThreads = 256, kOuterStages = 3;
+constexpr uint32_t kOuterThreads = 256, kOuterStages = 2;
 
 struct OuterDev {
   LoraGroups G;
@@ -627,13 +629,15 @@ struct OuterDev {
 };
 __host__ __device__ constexpr uint32_t outer_stage_bytes(uint32_t row) { return 64 * kChunkRow + 2 * 64 * odd_row(row); }
 
-template <bool kRankMajor, int NJ>
+template <bool kRankMajor, int NJ, bool kHalf>
 __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_t* stages_smem) {
+  constexpr uint32_t kRow = kHalf ? 128 : 8 * NJ;  // of hp
+  const uint32_t r0 = kHalf ? 64 * blockIdx.z : 0u, ranks = kHalf ? min(64u, P.rank - r0) : P.rank;
   const uint32_t a = blockIdx.y;
   const uint32_t p_begin = __ldcg(P.G.off + a), p_end = __ldcg(P.G.off + a + 1);
   const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const uint32_t cw = 16 * (warp & 3u), half = warp >> 2;
-  const uint32_t nj2 = (P.rank + 15) / 16;
+  const uint32_t nj2 = (ranks + 15) / 16;
   constexpr uint32_t h_row = odd_row(8 * NJ), h_bytes = 64 * h_row, stage = outer_stage_bytes(8 * NJ);
   const uint32_t base = smem_u32(stages_smem);
   const bool col_in = c0 + 8 * (tid % 8) < P.C;
@@ -649,7 +653,7 @@ __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_
   };
   // and its chunks of h: NJ a row, of positions tid / NJ and every 256 / NJ further,
   // of the one part and the other
-  const uint16_t* h_src = P.hp + static_cast<uint64_t>(p_begin + tid / NJ) * (8 * NJ) + 8 * (tid % NJ);
+  const uint16_t* h_src = P.hp + static_cast<uint64_t>(p_begin + tid / NJ) * kRow + r0 + 8 * (tid % NJ);
   auto load = [&](uint32_t zs, uint32_t it) {
     const uint32_t hsm = zs + 64 * kChunkRow + (tid / NJ) * h_row + (tid % NJ) * 16;
 #pragma unroll
@@ -668,7 +672,7 @@ __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_
         if (kRows > 64 && row >= 64) break;
         const bool in = row < left;
         cp16(hsm + part * h_bytes + i * kRows * h_row,
-             in ? h_src + part * P.hp_stride + static_cast<uint64_t>(64 * it + i * kRows) * (8 * NJ) : P.hp, in);
+             in ? h_src + part * P.hp_stride + static_cast<uint64_t>(64 * it + i * kRows) * kRow : P.hp, in);
       }
   };
   look(0);
@@ -720,7 +724,7 @@ __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_
   cp_wait<0>();
   __syncthreads();
   float4* other = reinterpret_cast<float4*>(stages_smem);  // the second half's sums: [rank blocks][4 warps][32 lanes]
-  const uint32_t nj = P.rank / 8;
+  const uint32_t nj = ranks / 8;
   if (half == 1) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
@@ -735,7 +739,7 @@ __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_
     if (j < nj) {
       const float4 v = other[(j * 4 + warp) * 32 + lane];
       const float s0 = acc[j][0] + v.x, s1 = acc[j][1] + v.y, s2 = acc[j][2] + v.z, s3 = acc[j][3] + v.w;
-      const uint32_t r = 8 * j + 2 * t;
+      const uint32_t r = r0 + 8 * j + 2 * t;
       if constexpr (kRankMajor) {
         out[static_cast<uint64_t>(r) * P.C + c] = s0;
         out[static_cast<uint64_t>(r + 1) * P.C + c] = s1;
@@ -755,13 +759,13 @@ struct OuterBoth {
   uint32_t b_blocks;
   uint32_t beside;  // runs beside the decoding of the weights
 };
-template <int NJ>
+template <int NJ, bool kHalf>
 __global__ void __launch_bounds__(kOuterThreads) lora_outer_kernel(const __grid_constant__ OuterBoth P) {
   extern __shared__ __align__(128) uint8_t stages_smem[];
   if (P.beside == 0) griddep_wait();
   griddep_launch_dependents();
-  if (blockIdx.x < P.b_blocks) outer_cta<false, NJ>(P.b, blockIdx.x * 64, stages_smem);
-  else outer_cta<true, NJ>(P.a, (blockIdx.x - P.b_blocks) * 64, stages_smem);
+  if (blockIdx.x < P.b_blocks) outer_cta<false, NJ, kHalf>(P.b, blockIdx.x * 64, stages_smem);
+  else outer_cta<true, NJ, kHalf>(P.a, (blockIdx.x - P.b_blocks) * 64, stages_smem);
   if (P.beside != 0) griddep_beside_end();
 }
 
@@ -925,7 +929,7 @@ static cudaError_t expand(const LoraPlan& p, const LoraDev& L, const LoraGroups&
   if (L.rank <= 16) return launch_pdl(lora_expand_kernel<kCols, kFew, 1>, grid, block, smem, stream, P);
   if (L.rank <= 32) return launch_pdl(lora_expand_kernel<kCols, kFew, 2>, grid, block, smem, stream, P);
   if (L.rank <= 64) return launch_pdl(lora_expand_kernel<kCols, kFew, 4>, grid, block, smem, stream, P);
-  return launch_pdl(lora_expand_kernel<kCols, kFew, 0>, grid, block, smem, stream, P);
+  return launch_pdl(lora_expand_kernel<kCols, kFew, 8>, grid, block, smem, stream, P);
 }
 
 static cudaError_t outer(const LoraPlan& p, const LoraDev& L, const LoraGroups& G, const uint16_t* dY, const uint16_t* h,
@@ -937,12 +941,13 @@ static cudaError_t outer(const LoraPlan& p, const LoraDev& L, const LoraGroups& 
   P.b_blocks = (L.N + 63) / 64;
   P.beside = beside;
   return by_rank(L.rank, [&](auto nj) {
-    constexpr int NJ = decltype(nj)::value;
+    constexpr bool kHalf = decltype(nj)::value == 16;
+    constexpr int NJ = kHalf ? 8 : decltype(nj)::value;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(lora_outer_kernel<NJ>, kOuterStages * outer_stage_bytes(8 * NJ), done);
+    cudaError_t e = allow_smem(lora_outer_kernel<NJ, kHalf>, kOuterStages * outer_stage_bytes(8 * NJ), done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(lora_outer_kernel<NJ>, dim3(P.b_blocks + (L.K + 63) / 64, L.n), dim3(kOuterThreads),
-                      kOuterStages * outer_stage_bytes(8 * NJ), stream, P);
+    return launch_pdl(lora_outer_kernel<NJ, kHalf>, dim3(P.b_blocks + (L.K + 63) / 64, L.n, kHalf ? 2 : 1),
+                      dim3(kOuterThreads), kOuterStages * outer_stage_bytes(8 * NJ), stream, P);
   });
 }
 

@@ -193,7 +193,7 @@ __device__ __forceinline__ bool few_tile(const int32_t* __restrict__ ids, uint32
 // or 64 positions and one range; a stage is 64 values of c for all of them and
 // their weights.  With 64 positions each of the 4 warps has 16 of them; with 16,
 // each has a quarter of the stage's sum, and the warps are added in order.
-constexpr uint32_t kShrinkThreads = 128, kShrinkStages = 4;
+constexpr uint32_t kShrinkThreads = 128, kShrinkStages = 3;
 
 struct ShrinkDev {
   LoraGroups G;

@@ -18,11 +18,12 @@
 // again, which are what bounds that product (a rank of 64 into 4096 x 14336: 84
 // us with both parts).
 //
-// Measured at rank 64, 4096 tokens of 2 adapters, 4096 x 14336: both shrinks 62 us
-// (150 MB of x and dy; 2.4 TB/s), both outer products 70 us (19 GFLOP in two
-// parts, 60 % of the 520 TFLOP/s these instructions reach), the expansion into dx
-// 52 us (235 MB written; 4.5 TB/s); one token at rank 16, 4096 x 4096: 7 us beside
-// a base product of 35.
+// Measured at rank 64, 4096 tokens of 2 adapters, 4096 x 14336, each alone: both
+// shrinks 49 us (150 MB of x and dy; 3 TB/s), both outer products 96 us (19 GFLOP in
+// two parts, 40 % of the 520 TFLOP/s these instructions reach; see kOuterStages),
+// the expansion into dx 52 us (235 MB written; 4.5 TB/s); one token at rank 16,
+// 4096 x 4096: 7 us beside a base product of 35.  The outer products and the
+// expansion are launched beside the decoding of the weights (griddep_beside).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -193,6 +194,7 @@ __device__ __forceinline__ bool few_tile(const int32_t* __restrict__ ids, uint32
 // or 64 positions and one range; a stage is 64 values of c for all of them and
 // their weights.  With 64 positions each of the 4 warps has 16 of them; with 16,
 // each has a quarter of the stage's sum, and the warps are added in order.
+// Three stages: 626.5 us for the same call against 638 with four (fewer CTAs an SM).
 constexpr uint32_t kShrinkThreads = 128, kShrinkStages = 3;
 
 struct ShrinkDev {
@@ -617,6 +619,9 @@ __global__ void __launch_bounds__(128) lora_expand_kernel(const __grid_constant_
 // matrix loads.  Warps 0-3 have 16 columns each and the stage's first 32
 // positions, warps 4-7 the same columns and the other 32; the halves are added
 // at the end.  The tokens of a stage are looked up a stage before its loads.
+// Two stages leave room for three CTAs an SM at rank 64.  With three stages the
+// outer products of the call above took 70 us alone, but beside the decoding the
+// call was slower: 639 against 628.5 us; with 500 tokens at rank 16, 78 against 74.
 constexpr uint32_t kOuterThreads = 256, kOuterStages = 2;
 
 struct OuterDev {

@@ -29,7 +29,9 @@
 // 115 ns an MMA, 70 % of the tensor pipe's cycles, 1.25-1.33 PFLOP/s on 2048 x 9472
 // x 4096 either way (117 and 125 us); with 3 stages 135 and 161 us.  A pair of
 // CTAs on one tile (32 KB a stage and SM) measured the same, and L2 prefetches
-// of the boxes 10-25 % more.
+// of the boxes 10-25 % more.  A last round of tiles dealt out evenly to all SMs
+// (the CTA with a tile's end adding the others' parts), 1.73 rounds in place of 2,
+// gained 1 %: the SMs that run share the chip's power.
 // Warps: 0 loads, 1 MMA issue (and TMEM owner), 2-9 epilogue: two for each
 // quarter of TMEM's lanes, on alternating 32 tokens.  (With one each, the
 // epilogue of the logits took longer than the MMAs of a K = 2048 tile.)

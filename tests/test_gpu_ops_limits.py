@@ -145,3 +145,80 @@ def test_layers_of_the_measured_sizes(cuda, dtype, N, K, M):
     assert st == 0
     for got, w in zip((loss, lse, dx), reference(L, x[rows], t[rows], N - 5)):
         within(got[rows.cuda()], *w)
+
+
+@pytest.mark.parametrize("dtype,M", [(ans.INT8, 16500), (ans.INT8, 70), (ans.BF16_SPLIT, 300)])
+def test_loss_alone_over_pieces_and_chunks(cuda, dtype, M):
+    # more than one piece of the vocabulary; the first size also has two chunks of tokens.  A piece's
+    # last blocks are joined while the next piece is decoded
+    N, K, vocab = 24832, 2064, 24820
+    L = usual(dtype, N, K, seed=3)
+    rng = np.random.default_rng(M)
+    x, t = bf16(rng, M, K, scale=0.02), some_targets(rng, M, vocab)
+    rows = torch.unique(torch.tensor([0, 1, M // 2, min(M - 1, 8447), min(M - 1, 8448), M - 2, M - 1]))
+    ws = workspace(ans.ans_xent_workspace(L.layout, M, L.kind, False))
+    loss, lse, _, st = run(L, x, t, vocab, grad=False, ws=ws)
+    assert st == 0
+    want = reference(L, x[rows], t[rows], vocab)
+    within(loss[rows.cuda()], *want[0], "loss")
+    within(lse[rows.cuda()], *want[1], "lse")
+    for _ in range(3):
+        again = run(L, x, t, vocab, grad=False, ws=ws)
+        assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("dtype,M", [(ans.INT8, 600), (ans.BF16_SPLIT, 200), (ans.INT4_PAIRS, 2100)])
+def test_calls_one_behind_another_share_a_workspace(cuda, dtype, M, graph):
+    # kernels run beside the one before them: calls on other inputs, one behind another without a
+    # pause and in one workspace an operator, give what each gives by itself
+    L = usual(dtype, 4096, 2048, seed=4)
+    A = Adapters(L, 3, 64)
+    rng = np.random.default_rng(M)
+    sets = [(bf16(rng, M, L.K, scale=0.1).cuda(), bf16(rng, M, L.N, scale=0.1).cuda(), some_ids(rng, M, 3).cuda(),
+             some_targets(rng, M, 4000).cuda()) for _ in range(3)]
+    g_ws, b_ws, x_ws, l_ws = (workspace(n) for n in (
+        ans.ans_gemm_grad_workspace(L.layout, M, L.kind), ans.ans_gemm_lora_grad_workspace(L.layout, M, L.kind, A.lora),
+        ans.ans_xent_workspace(L.layout, M, L.kind, True), ans.ans_xent_workspace(L.layout, M, L.kind, False)))
+    st = status()
+
+    def new():
+        dx = [torch.zeros(M, L.K, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+        return (*dx, torch.zeros(A.a.shape, device="cuda"), torch.zeros(A.b.shape, device="cuda"),
+                *(torch.zeros(M, device="cuda") for _ in range(4)))
+
+    def calls(s, o):
+        x, dy, ids, t = s
+        stream = torch.cuda.current_stream()
+        yield lambda: ans.ans_gemm_grad(dy, M, *L.args, o[0], g_ws, g_ws.numel(), st, stream)
+        yield lambda: ans.ans_gemm_lora_grad(x, dy, M, *L.args, A.lora, ids, o[1], o[3], o[4], b_ws, b_ws.numel(), st, stream)
+        yield lambda: ans.ans_xent(x, M, *L.args, 4000, t, o[5], o[6], None, o[2], x_ws, x_ws.numel(), st, stream)
+        yield lambda: ans.ans_xent(x, M, *L.args, 4000, t, o[7], o[8], None, None, l_ws, l_ws.numel(), st, stream)
+
+    want, got = [new() for _ in sets], [new() for _ in sets]
+    for s, o in zip(sets, want):
+        for call in calls(s, o):
+            call()
+            torch.cuda.synchronize()
+
+    def all_of_them():
+        for each in zip(*(list(calls(s, o)) for s, o in zip(sets, got))):   # the same operator behind itself
+            for call in each:
+                call()
+        for s, o in zip(sets, got):                                         # and behind the others
+            for call in calls(s, o):
+                call()
+
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            all_of_them()
+        for _ in range(3):
+            g.replay()
+    else:
+        all_of_them()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for a, b in zip(want, got):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)

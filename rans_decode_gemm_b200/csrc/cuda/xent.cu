@@ -234,12 +234,13 @@ __global__ void __launch_bounds__(256) xent_piece_kernel(const __grid_constant__
       if (g[q] == 1.0f) continue;
       uint32_t* u = reinterpret_cast<uint32_t*>(&w[q]);
       if (P.f16) {
-        // (a factor below f16's range leaves nothing of f16 values)
-        const __half2 h = __float2half2_rn(g[q]);
+        // (in fp32: a factor of 2^-25 is none of f16's values, but a stored value is up to
+        // 2^14, and its product with the factor may be one)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(u + i), h);
-          u[i] = *reinterpret_cast<const uint32_t*>(&x);
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(u + i));
+          const __half2 h = __floats2half2_rn(x.x * g[q], x.y * g[q]);
+          u[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
       } else {
         const __nv_bfloat162 h = __float2bfloat162_rn(g[q]);

@@ -408,8 +408,11 @@ ans_status ans_gemm_batched(const ans_gemm_job* jobs, uint32_t n_jobs, uint32_t 
  * scales) round that value once: to f16 under a power of two of its row for the
  * formats whose values are exact in f16 (all but bf16), to bf16 beside bf16
  * weights and beside the (bf16) adapters in dX.  bf16 weights without scales
- * take d_dY as it is.  Probabilities carry W's row scales there and keep their
- * 11 bits of f16 for rows whose scale is within 2^22 of the largest. */
+ * take d_dY as it is.  A probability is stored times its row's scale, against the
+ * token's largest but for its target's and the largest scale: in f16 with 11 bits
+ * where the product is within 2^21 of theirs, and off by at most 2^-32 of theirs
+ * where it is not (by twice that where a block of the vocabulary is moved to a
+ * larger reference); in bf16 with 8 bits throughout. */
 
 /* A set of low-rank adapters of one projection (W is N x K): adapter a adds
  * s_a (x A_a^T) B_a^T to y.  All have one rank (a multiple of 8 up to 128; an

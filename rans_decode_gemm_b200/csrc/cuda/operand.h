@@ -75,10 +75,11 @@ struct OperandGemmOut {
 // (a block) at a time.  With r a reference in units of log 2 (a whole number),
 //   e[m][n] = 2^(z[m][n] log2(e) - r),  blocks[block][m] = (r, sum of the block's e),
 //   probs[m * rows + n] = e * s_n * lift (16-bit; null: not stored),
-// except that rows n0 + n >= vocab count for nothing, and the token's target has
-// its logit stored in zt[m] and e taken as 0.  r is ref_in[m], unless the
-// block's largest logit lies more than kXentSlack above it: then r is that
-// logit, rounded up.
+// except that rows n0 + n >= vocab count for nothing, and neither does the token's
+// target, whose logit is stored in zt[m]: it has no part in r either, or the others
+// of a token that is all but certain would be stored far below 1.  r is ref_in[m],
+// unless the block's largest logit lies more than kXentSlack above it: then r is
+// that logit, rounded up.
 constexpr float kXentSlack = 5.75f;    // e^4: what probabilities may exceed 1 by
 constexpr float kXentNone = -3.0e38f;  // the reference before any logit
 struct XentEpilogue {

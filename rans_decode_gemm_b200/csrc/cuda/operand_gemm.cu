@@ -119,16 +119,6 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
     z[j] = __uint_as_float(v[j]) * scale;
     if (E.factor != nullptr) z[j] *= __shfl_sync(0xFFFFFFFFu, factor, j);
     if (!n_in) z[j] = -INFINITY;
-    x[j] = z[j];
-  }
-  const float top = across_lanes(x, lane, [](float a, float b) { return fmaxf(a, b); }) * kLog2E;
-  float ref = ref_in;
-  if (top > ref_in + kXentSlack && top <= 3.0e38f) ref = ceilf(top);
-#pragma unroll
-  for (uint32_t j = 0; j < 32; ++j) {
-    const float r = __shfl_sync(0xFFFFFFFFu, ref, j);
-    // (the approximate instruction: 2^-22, the same in every use)
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x[j]) : "f"(fmaf(z[j], kLog2E, -r)));
   }
   // targets among this warp's rows (one that is past the vocabulary is none): few
   // and far between, so that the loops above and below carry no test for them
@@ -141,11 +131,22 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
       for (uint32_t j = 0; j < 32; ++j) {
         if (j == k) {
           E.zt[m + j] = z[j];
-          x[j] = 0.0f;
+          z[j] = -INFINITY;
         }
       }
     }
     __syncwarp();
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < 32; ++j) x[j] = z[j];
+  const float top = across_lanes(x, lane, [](float a, float b) { return fmaxf(a, b); }) * kLog2E;
+  float ref = ref_in;
+  if (top > ref_in + kXentSlack && top <= 3.0e38f) ref = ceilf(top);
+#pragma unroll
+  for (uint32_t j = 0; j < 32; ++j) {
+    const float r = __shfl_sync(0xFFFFFFFFu, ref, j);
+    // (the approximate instruction: 2^-22, the same in every use)
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x[j]) : "f"(fmaf(z[j], kLog2E, -r)));
   }
   const float ps = n_in ? scale * lift : 0.0f;  // (a padding row's scale may be anything)
   if (E.probs != nullptr) {

@@ -1,4 +1,5 @@
-"""ans_xent where probabilities are small: what they leave in dX.
+"""ans_xent for tokens that are all but certain of their target: heads whose rows
+share a mean, one row beside the target, and targets far above or alone.
 
 The bounds here scale with 1 - p_t.  A probability's rounding counts against the
 others' sum alone: half a step of the format (2^-11 of it in f16, 2^-8 in bf16),
@@ -12,7 +13,7 @@ import torch
 
 from rans_decode_gemm_b200 import ans
 
-from _ops_util import BF16, status, sum_eps, usual, within, workspace
+from _ops_util import BF16, E2M1, bf16, status, sum_eps, usual, within, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -60,6 +61,18 @@ def run(L, x, targets, vocab, weight=None, grad=True):
     return loss, lse, dx
 
 
+def check(L, x, targets, vocab, weight=None):
+    loss, lse, dx = run(L, x, targets, vocab, weight)
+    a, b, c, rest = reference(L, x, targets, vocab, weight)
+    within(loss, *a, "loss")
+    within(lse, *b, "lse")
+    within(dx, *c, "dx")
+    loss, lse, _ = run(L, x, targets, vocab, grad=False)
+    within(loss, *a, "loss alone")
+    within(lse, *b, "lse alone")
+    return rest
+
+
 def put(L, codes, values):
     """Other codes (as stored) and their values in the layer L."""
     L.codes = np.ascontiguousarray(codes)
@@ -70,6 +83,128 @@ def put(L, codes, values):
     elif L.kind == ans.SCALE_GROUP_BF16:
         values = values * np.repeat(L.scales.cpu().double().numpy(), L.group_k, axis=1)
     L.w = torch.from_numpy(np.ascontiguousarray(values))
+
+
+def with_a_mean(L, seed):
+    """Rows with a mean of their own size in every column, as a trained head's have."""
+    rng = np.random.default_rng(seed)
+    v = rng.standard_normal((L.N, L.K)).astype(np.float32) + rng.standard_normal((1, L.K)).astype(np.float32)
+    if L.dtype == ans.INT8:
+        q = np.clip(np.rint(30 * v), -127, 127).astype(np.int8)
+        put(L, q.view(np.uint8), q.astype(np.float64))
+    elif L.dtype == ans.FP8_E4M3:
+        t = torch.from_numpy(20 * v).to(torch.float8_e4m3fn)
+        put(L, t.view(torch.uint8).numpy(), t.double().numpy())
+    elif L.dtype == ans.BF16_SPLIT:
+        t = torch.from_numpy(0.05 * v).bfloat16()
+        put(L, t.view(torch.int16).numpy().view(np.uint16), t.double().numpy())
+    elif L.dtype == ans.INT4_PAIRS:
+        q = np.clip(np.rint(2 * v), -8, 7).astype(np.int64)
+        nib = (q & 15).astype(np.uint8)
+        put(L, nib[:, 0::2] | (nib[:, 1::2] << 4), q.astype(np.float64))
+    else:
+        nib = np.abs(np.abs(2 * v)[..., None] - E2M1[:8]).argmin(-1).astype(np.uint8)
+        nib = np.where((v < 0) & (nib > 0), nib | 8, nib).astype(np.uint8)
+        put(L, nib[:, 0::2] | (nib[:, 1::2] << 4), E2M1[nib])
+
+
+def leaning(L, targets, vocab, wanted):
+    """Hidden states along their target's row less the mean row, as long as they
+    have to be for each 1 - p_t wanted."""
+    w = L.w[:vocab]
+    out = []
+    for t, rest in zip(targets, wanted):
+        d = w[t] - w.mean(0)
+        z = w @ d
+        low, high = 0.0, 400.0 / float(d @ d)
+        for _ in range(60):
+            b = 0.5 * (low + high)
+            e = b * z
+            e[t] = -torch.inf
+            gap = float(b * z[t] - torch.logsumexp(e, 0))
+            low, high = (b, high) if gap < np.log((1 - rest) / rest) else (low, b)
+        out.append(low * d)
+    return torch.stack(out).float().bfloat16()
+
+
+REST = [0.3, 1e-2, 1e-3, 1e-4, 1e-5, 1e-6, 1e-7]
+
+
+@pytest.mark.parametrize("place", ["first", "last"])
+@pytest.mark.parametrize("dtype", FORMATS)
+def test_a_head_whose_rows_share_a_mean(cuda, dtype, place):
+    N, vocab = 32000, 31990
+    L = usual(dtype, N, 256, seed=1)
+    with_a_mean(L, 2)
+    start = 40 if place == "first" else vocab - 700
+    targets = torch.arange(start, start + 97 * len(REST), 97, dtype=torch.int32)
+    x = leaning(L, targets.tolist(), vocab, REST)
+    rest = check(L, x, targets, vocab)
+    assert rest.min() < 1e-6 and rest.max() > 0.1
+
+
+@pytest.mark.parametrize("dtype", [ans.INT8, ans.FP8_E4M3, ans.FP4_E2M1])
+def test_one_row_of_a_larger_scale(cuda, dtype):
+    N = vocab = 32000
+    L = usual(dtype, N, 128, seed=3)
+    L.scales[777] = 8 * L.scales.max()
+    with_a_mean(L, 4)
+    targets = torch.arange(5, 5 + 4001 * len(REST), 4001, dtype=torch.int32)
+    check(L, leaning(L, targets.tolist(), vocab, REST), targets, vocab)
+
+
+def beside(L, pairs, gaps):
+    """Hidden states under which row t of each pair stands first and row r the given
+    number of nats below it (60 in all; the other rows are far lower)."""
+    out = []
+    for (t, r), gap in zip(pairs, gaps):
+        rows = L.w[[t, r]]
+        out.append(torch.linalg.lstsq(rows, torch.tensor([60.0, 60.0 - gap]).double()[:, None], driver="gelsd").solution[:, 0])
+    return torch.stack(out).float().bfloat16()
+
+
+# the runner-up in the target's block of 32, in another block, in another row block
+@pytest.mark.parametrize("t,r", [(3, 30), (30, 3), (3, 40), (40, 3), (100, 255), (255, 0)])
+@pytest.mark.parametrize("dtype", FORMATS)
+def test_one_row_beside_the_target(cuda, dtype, t, r):
+    L = usual(dtype, 256, 256, seed=5)
+    gaps = [6.0, 10.0, 14.0, 16.0, 18.0, 20.0, 22.0]
+    x = beside(L, [(t, r)] * len(gaps), gaps)
+    check(L, x, torch.full((len(gaps),), t, dtype=torch.int32), 256)
+
+
+# and in an earlier and a later piece of the vocabulary
+@pytest.mark.parametrize("t,r", [(5, 24000), (24000, 5), (18900, 18990), (24600, 24570)])
+@pytest.mark.parametrize("dtype", FORMATS)
+def test_one_row_in_another_piece(cuda, dtype, t, r):
+    L = usual(dtype, 24832, 256, seed=6)
+    gaps = [14.0, 16.0, 18.0, 20.0, 22.0]
+    x = beside(L, [(t, r)] * len(gaps), gaps)
+    check(L, x, torch.full((len(gaps),), t, dtype=torch.int32), 24800, torch.tensor([1.0, -3.0, 1e5, 1e8, 0.5]))
+
+
+@pytest.mark.parametrize("dtype", [ans.INT8, ans.BF16_SPLIT])
+def test_targets_beyond_the_range_of_exponentials(cuda, dtype):
+    # the target 100 to 5,000 nats above or below all others (its loss or its
+    # probability is then nothing at all), and a vocabulary of the target alone
+    L = usual(dtype, 256, 64, seed=7)
+    rng = np.random.default_rng(8)
+    d = L.w[9] / (L.w[9] @ L.w[9])
+    x = (d[None, :] * torch.tensor([200., 2000., 10000., -200., -2000., -10000.])[:, None]).float().bfloat16()
+    t = torch.full((6,), 9, dtype=torch.int32)
+    a, b, c, rest = reference(L, x, t, 256)
+    loss, lse, dx = run(L, x, t, 256)
+    assert rest[0] < 1e-15 and rest[5] == 1
+    # a loss below fp32's normal numbers may be flushed to 0, and so may what is left of dX
+    within(loss, a[0], a[1] + 2.0 ** -126, "loss")
+    within(lse, *b, "lse")
+    within(dx, c[0], c[1] + 2.0 ** -120, "dx")
+    x = bf16(rng, 5, 64, scale=300.0)
+    t = torch.tensor([0, 0, -1, 0, 0], dtype=torch.int32)
+    loss, lse, dx = run(L, x, t, 1)
+    z = x.double() @ L.w[0]
+    within(lse, z, sum_eps(64) * (x.double().abs() @ L.w[0].abs()) + 2.0 ** -22 * z.abs(), "lse of one row")
+    assert not loss.any() and not dx.any()
 
 
 @pytest.mark.parametrize("N,vocab", [(256, 256), (24832, 24800)])

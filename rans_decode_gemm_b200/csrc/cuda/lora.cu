@@ -54,6 +54,16 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t& hi, uint16_t& lo) 
   lo = isfinite(v) ? __bfloat16_as_ushort(__float2bfloat16_rn(r)) : uint16_t(0);
 }
 
+// Two bf16 values: is one of them infinite or NaN, and the two with 0 in such a place.
+// An infinite factor meets the first part of a split value alone: times a second part
+// of 0, or of the other sign, it would leave NaN where the product is an infinity.
+__device__ __forceinline__ bool not_finite2(uint32_t v) {
+  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+  return v & (((v & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((v & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u));
+}
+
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ uint2 ldg8(const uint16_t* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
 
@@ -518,6 +528,16 @@ __device__ __forceinline__ void expand_cta(const ExpandDev& P, uint16_t* hs, uin
 #pragma unroll
     for (int q = 0; q < kSteps; ++q) expand_weights<kCols>(P, w, c0, 16 * q, g, t, b[q]);
   }
+  bool odd = false;  // the warp has weights that are not finite
+  if constexpr (!kCols) {
+    if (c0 < P.C) {
+#pragma unroll
+      for (int q = 0; q < kSteps; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) odd = odd || not_finite2(b[q][i][0]) || not_finite2(b[q][i][1]);
+    }
+    odd = __any_sync(0xFFFFFFFFu, odd);
+  }
   if constexpr (!kFew) {
     constexpr uint32_t per = kRow / 8;
     for (uint32_t i = threadIdx.x; i < (kCols ? 1 : 2) * count * per; i += blockDim.x) {
@@ -540,64 +560,86 @@ __device__ __forceinline__ void expand_cta(const ExpandDev& P, uint16_t* hs, uin
   __syncthreads();
   if (c0 >= P.C) return;
   const uint32_t cl = c0 + 4 * t;  // this lane's output columns: cl + 16 q .. + 3
-  for (uint32_t r = 0; r < count; r += 16) {
-    uint32_t m0, m1;
-    if constexpr (kFew) {
-      m0 = g < found ? tok[g] : kNoToken;
-      m1 = g + 8 < found ? tok[g + 8] : kNoToken;
-    } else {
-      m0 = __ldcg(P.G.perm + start + r + g);
-      m1 = __ldcg(P.G.perm + start + r + g + 8);
-    }
-    const bool v0 = m0 != kNoToken, v1 = m1 != kNoToken;
-    float* y0 = P.out + (v0 ? static_cast<uint64_t>(m0) * P.C + cl : 0ull);
-    float* y1 = P.out + (v1 ? static_cast<uint64_t>(m1) * P.C + cl : 0ull);
-    float4 o0[4], o1[4];
-    if constexpr (!kCols) {
+  auto tokens = [&](auto apart) {  // apart: infinite and NaN weights are kept from h's second part
+    constexpr bool kApart = decltype(apart)::value;
+    for (uint32_t r = 0; r < count; r += 16) {
+      uint32_t m0, m1;
+      if constexpr (kFew) {
+        m0 = g < found ? tok[g] : kNoToken;
+        m1 = g + 8 < found ? tok[g + 8] : kNoToken;
+      } else {
+        m0 = __ldcg(P.G.perm + start + r + g);
+        m1 = __ldcg(P.G.perm + start + r + g + 8);
+      }
+      const bool v0 = m0 != kNoToken, v1 = m1 != kNoToken;
+      float* y0 = P.out + (v0 ? static_cast<uint64_t>(m0) * P.C + cl : 0ull);
+      float* y1 = P.out + (v1 ? static_cast<uint64_t>(m1) * P.C + cl : 0ull);
+      [[maybe_unused]] float4 o0[4], o1[4];
+      if constexpr (!kCols) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (v0) o0[q] = *reinterpret_cast<const float4*>(y0 + 16 * q);
+          if (v1) o1[q] = *reinterpret_cast<const float4*>(y1 + 16 * q);
+        }
+      }
+      float acc[8][4] = {};
+      const uint32_t h0 = (r + g) * pitch + 4 * t, h1 = h0 + 8 * pitch;
+      auto step = [&](const uint16_t* part, uint32_t k, const uint32_t (&bk)[8][2]) {
+        const uint2 a0 = *reinterpret_cast<const uint2*>(part + h0 + k), a1 = *reinterpret_cast<const uint2*>(part + h1 + k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mma_bf16(acc[i], a0.x, a1.x, a0.y, a1.y, bk[i][0], bk[i][1]);
+      };
+      if constexpr (kApart) {
+        // (read again, so that no more of them are held than below)
+        uint32_t bk[8][2];
+#pragma unroll 1
+        for (uint32_t k = 0; k < r16; k += 16) {
+          expand_weights<kCols>(P, w, c0, k, g, t, bk);
+          step(hs, k, bk);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            bk[i][0] = finite2(bk[i][0]);
+            bk[i][1] = finite2(bk[i][1]);
+          }
+          step(lo_s, k, bk);
+        }
+      } else if constexpr (kSteps > 0) {
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q) {
+          if (16u * q >= r16) continue;
+          step(hs, 16 * q, b[q]);
+          if constexpr (!kCols) step(lo_s, 16 * q, b[q]);
+        }
+      } else {
+        for (uint32_t k = 0; k < r16; k += 16) {
+          expand_weights<kCols>(P, w, c0, k, g, t, b[0]);
+          step(hs, k, b[0]);
+          if constexpr (!kCols) step(lo_s, k, b[0]);
+        }
+      }
+      // columns 16 q + 4 t + e: instruction 4 (q & 1) + e, its even (q < 2) or odd column
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (v0) o0[q] = *reinterpret_cast<const float4*>(y0 + 16 * q);
-        if (v1) o1[q] = *reinterpret_cast<const float4*>(y1 + 16 * q);
+        const int i = 4 * (q & 1), k = q >> 1;
+        float4 u = make_float4(acc[i][k], acc[i + 1][k], acc[i + 2][k], acc[i + 3][k]);
+        float4 v = make_float4(acc[i][k + 2], acc[i + 1][k + 2], acc[i + 2][k + 2], acc[i + 3][k + 2]);
+        if constexpr (!kCols) {
+          if (v0) { u.x += o0[q].x; u.y += o0[q].y; u.z += o0[q].z; u.w += o0[q].w; }
+          if (v1) { v.x += o1[q].x; v.y += o1[q].y; v.z += o1[q].z; v.w += o1[q].w; }
+        }
+        const bool in = c0 + 16 * q < P.C;  // (C is a multiple of 16)
+        if (v0 && in) *reinterpret_cast<float4*>(y0 + 16 * q) = u;
+        if (v1 && in) *reinterpret_cast<float4*>(y1 + 16 * q) = v;
       }
     }
-    float acc[8][4] = {};
-    const uint32_t h0 = (r + g) * pitch + 4 * t, h1 = h0 + 8 * pitch;
-    auto step = [&](uint32_t k, const uint32_t (&bk)[8][2]) {
-      const uint2 a0 = *reinterpret_cast<const uint2*>(hs + h0 + k), a1 = *reinterpret_cast<const uint2*>(hs + h1 + k);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mma_bf16(acc[i], a0.x, a1.x, a0.y, a1.y, bk[i][0], bk[i][1]);
-      if constexpr (!kCols) {
-        const uint2 l0 = *reinterpret_cast<const uint2*>(lo_s + h0 + k),
-                    l1 = *reinterpret_cast<const uint2*>(lo_s + h1 + k);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mma_bf16(acc[i], l0.x, l1.x, l0.y, l1.y, bk[i][0], bk[i][1]);
-      }
-    };
-    if constexpr (kSteps > 0) {
-#pragma unroll
-      for (int q = 0; q < kSteps; ++q)
-        if (16u * q < r16) step(16 * q, b[q]);
-    } else {
-      for (uint32_t k = 0; k < r16; k += 16) {
-        expand_weights<kCols>(P, w, c0, k, g, t, b[0]);
-        step(k, b[0]);
-      }
-    }
-    // columns 16 q + 4 t + e: instruction 4 (q & 1) + e, its even (q < 2) or odd column
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = 4 * (q & 1), k = q >> 1;
-      float4 u = make_float4(acc[i][k], acc[i + 1][k], acc[i + 2][k], acc[i + 3][k]);
-      float4 v = make_float4(acc[i][k + 2], acc[i + 1][k + 2], acc[i + 2][k + 2], acc[i + 3][k + 2]);
-      if constexpr (!kCols) {
-        if (v0) { u.x += o0[q].x; u.y += o0[q].y; u.z += o0[q].z; u.w += o0[q].w; }
-        if (v1) { v.x += o1[q].x; v.y += o1[q].y; v.z += o1[q].z; v.w += o1[q].w; }
-      }
-      const bool in = c0 + 16 * q < P.C;  // (C is a multiple of 16)
-      if (v0 && in) *reinterpret_cast<float4*>(y0 + 16 * q) = u;
-      if (v1 && in) *reinterpret_cast<float4*>(y1 + 16 * q) = v;
+  };
+  if constexpr (!kCols) {
+    if (odd) {
+      tokens(std::true_type{});
+      return;
     }
   }
+  tokens(std::false_type{});
 }
 // (kCols, into dx: beside the outer products, which run beside the decoding)
 template <bool kCols, bool kFew, int kSteps>
@@ -680,54 +722,71 @@ __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_
              in ? h_src + part * P.hp_stride + static_cast<uint64_t>(64 * it + i * kRows) * kRow : P.hp, in);
       }
   };
-  look(0);
+  float acc[NJ][4];
+  auto sums = [&](auto apart) {  // apart: z's infinities and NaN are kept from h's second part
+    constexpr bool kApart = decltype(apart)::value;
 #pragma unroll
-  for (uint32_t i = 0; i + 1 < kOuterStages; ++i) {
-    if (i < n_steps) {
-      load(base + i * stage, i);
-      look(i + 1);
+    for (int j = 0; j < NJ; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    look(0);
+#pragma unroll
+    for (uint32_t i = 0; i + 1 < kOuterStages; ++i) {
+      if (i < n_steps) {
+        load(base + i * stage, i);
+        look(i + 1);
+      }
+      cp_commit();
     }
-    cp_commit();
-  }
-  float acc[NJ][4] = {};
-  uint32_t zs_next = base, load_next = base + (kOuterStages - 1) * stage;
-  const uint32_t ring_end = base + kOuterStages * stage;
-  for (uint32_t it = 0; it < n_steps; ++it) {
-    cp_wait<kOuterStages - 2>();
-    __syncthreads();
-    if (it + kOuterStages - 1 < n_steps) {
-      load(load_next, it + kOuterStages - 1);
-      look(it + kOuterStages);
-    }
-    cp_commit();
-    if ((load_next += stage) == ring_end) load_next = base;
-    const uint32_t zs = zs_next, hsm = zs + 64 * kChunkRow;
-    if ((zs_next += stage) == ring_end) zs_next = base;
-    const uint32_t n16 = min(4u, (p_end - p_begin - 64 * it) / 16);
+    uint32_t zs_next = base, load_next = base + (kOuterStages - 1) * stage;
+    const uint32_t ring_end = base + kOuterStages * stage;
+    for (uint32_t it = 0; it < n_steps; ++it) {
+      cp_wait<kOuterStages - 2>();
+      __syncthreads();
+      if (it + kOuterStages - 1 < n_steps) {
+        load(load_next, it + kOuterStages - 1);
+        look(it + kOuterStages);
+      }
+      cp_commit();
+      if ((load_next += stage) == ring_end) load_next = base;
+      const uint32_t zs = zs_next, hsm = zs + 64 * kChunkRow;
+      if ((zs_next += stage) == ring_end) zs_next = base;
+      const uint32_t n16 = min(4u, (p_end - p_begin - 64 * it) / 16);
 #pragma unroll
-    for (uint32_t k = 0; k < 2; ++k) {
-      const uint32_t ks = 2 * half + k;
-      if (ks >= n16) break;
-      uint32_t f[4];
-      ldsm4_t(f, zs + (16 * ks + (lane & 7u) + ((lane >> 4) << 3)) * kChunkRow + (cw / 8 + ((lane >> 3) & 1u)) * 16);
-      // two blocks of 8 ranks a load: lanes 16-31 address the second
-      const uint32_t hr = hsm + (16 * ks + (lane & 15u)) * h_row + (lane >> 4) * 16;
+      for (uint32_t k = 0; k < 2; ++k) {
+        const uint32_t ks = 2 * half + k;
+        if (ks >= n16) break;
+        uint32_t f[4];
+        ldsm4_t(f, zs + (16 * ks + (lane & 7u) + ((lane >> 4) << 3)) * kChunkRow + (cw / 8 + ((lane >> 3) & 1u)) * 16);
+        uint32_t fl[4];
 #pragma unroll
-      for (int j = 0; j < NJ / 2; ++j) {
-        if (j < nj2) {
-          uint32_t hi[4], lo[4];
-          ldsm4_t(hi, hr + j * 32);
-          ldsm4_t(lo, hr + h_bytes + j * 32);
-          mma_bf16(acc[2 * j], f[0], f[1], f[2], f[3], hi[0], hi[1]);
-          mma_bf16(acc[2 * j + 1], f[0], f[1], f[2], f[3], hi[2], hi[3]);
-          mma_bf16(acc[2 * j], f[0], f[1], f[2], f[3], lo[0], lo[1]);
-          mma_bf16(acc[2 * j + 1], f[0], f[1], f[2], f[3], lo[2], lo[3]);
+        for (int i = 0; i < 4; ++i) fl[i] = kApart ? finite2(f[i]) : f[i];
+        // two blocks of 8 ranks a load: lanes 16-31 address the second
+        const uint32_t hr = hsm + (16 * ks + (lane & 15u)) * h_row + (lane >> 4) * 16;
+#pragma unroll
+        for (int j = 0; j < NJ / 2; ++j) {
+          if (j < nj2) {
+            uint32_t hi[4], lo[4];
+            ldsm4_t(hi, hr + j * 32);
+            ldsm4_t(lo, hr + h_bytes + j * 32);
+            mma_bf16(acc[2 * j], f[0], f[1], f[2], f[3], hi[0], hi[1]);
+            mma_bf16(acc[2 * j + 1], f[0], f[1], f[2], f[3], hi[2], hi[3]);
+            mma_bf16(acc[2 * j], fl[0], fl[1], fl[2], fl[3], lo[0], lo[1]);
+            mma_bf16(acc[2 * j + 1], fl[0], fl[1], fl[2], fl[3], lo[2], lo[3]);
+          }
         }
       }
     }
+    cp_wait<0>();
+  };
+  // z is not looked at first; where a sum is not finite, they are formed again
+  sums(std::false_type{});
+  bool odd = false;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    odd = odd || !isfinite(acc[j][0]) || !isfinite(acc[j][1]) || !isfinite(acc[j][2]) || !isfinite(acc[j][3]);
+  if (__syncthreads_or(odd)) {
+    sums(std::true_type{});
+    __syncthreads();
   }
-  cp_wait<0>();
-  __syncthreads();
   float4* other = reinterpret_cast<float4*>(stages_smem);  // the second half's sums: [rank blocks][4 warps][32 lanes]
   const uint32_t nj = ranks / 8;
   if (half == 1) {

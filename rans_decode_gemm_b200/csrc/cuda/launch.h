@@ -1,7 +1,9 @@
 // launch.h -- host-side kernel launch with programmatic dependent launch:
-// the kernel may start (and run its prologue, which touches no global memory)
-// while the previous kernel in the stream is finishing; the kernel's
-// griddep_wait() orders every global-memory access after that kernel.
+// the kernel may start while the previous kernel in the stream is still running.
+// An ordinary kernel runs only a prologue that touches no global memory, and its
+// griddep_wait() orders every global-memory access after that kernel.  A kernel
+// that uses none of that kernel's results runs beside it (griddep_beside() in
+// ptx.cuh says what it may read and write, and how the next kernel waits for both).
 #pragma once
 #include <cuda_runtime.h>
 

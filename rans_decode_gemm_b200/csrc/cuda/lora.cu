@@ -449,9 +449,8 @@ __global__ void __launch_bounds__(256) lora_join_kernel(LoraGroups G, const __gr
 // write 64 neighbouring bytes at a time.
 // Along the sum lane t has steps 4 t .. 4 t + 3 of every 16, in both operands.
 // kCols takes the first part of h alone.
-// Up to rank 64 the warp's weights stay in registers for all of the tile's
-// tokens (kSteps blocks of 16 ranks); above, they are read again for every 16
-// tokens (kSteps 0).
+// The warp's weights stay in registers for all of the tile's tokens: kSteps (1, 2, 4
+// or 8) blocks of 16 ranks.
 struct ExpandDev {
   LoraGroups G;
   const float* part;        // few tokens: sums of the shrink (splits x M x rank)
@@ -506,10 +505,10 @@ __device__ __forceinline__ void expand_cta(const ExpandDev& P, uint16_t* hs, uin
   const uint32_t tile = blockIdx.x;
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const uint32_t r16 = (P.rank + 15) / 16 * 16;
-  constexpr uint32_t kRow = kSteps > 0 ? 16 * kSteps : kLoraMaxRank, pitch = kRow + 8;
+  constexpr uint32_t kRow = 16 * kSteps, pitch = kRow + 8;
   uint16_t* lo_s = hs + P.tm * pitch;
   const uint32_t c0 = (blockIdx.y * (blockDim.x / 32) + warp) * 64;
-  uint32_t b[kSteps > 0 ? kSteps : 1][8][2];
+  uint32_t b[kSteps][8][2];
   uint32_t a, start = 0, count;
   if constexpr (kFew) {
     FewTile ft;
@@ -603,18 +602,12 @@ __device__ __forceinline__ void expand_cta(const ExpandDev& P, uint16_t* hs, uin
           }
           step(lo_s, k, bk);
         }
-      } else if constexpr (kSteps > 0) {
+      } else {
 #pragma unroll
         for (int q = 0; q < kSteps; ++q) {
           if (16u * q >= r16) continue;
           step(hs, 16 * q, b[q]);
           if constexpr (!kCols) step(lo_s, 16 * q, b[q]);
-        }
-      } else {
-        for (uint32_t k = 0; k < r16; k += 16) {
-          expand_weights<kCols>(P, w, c0, k, g, t, b[0]);
-          step(hs, k, b[0]);
-          if constexpr (!kCols) step(lo_s, k, b[0]);
         }
       }
       // columns 16 q + 4 t + e: instruction 4 (q & 1) + e, its even (q < 2) or odd column

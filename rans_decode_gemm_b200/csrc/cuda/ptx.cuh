@@ -23,7 +23,7 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
 // Programmatic dependent launch.  griddep_wait: block until the grid that
 // precedes this one in the stream has completed and its memory operations are
 // visible (a no-op when the launch did not opt in); every global-memory access
-// of a kernel comes after it.  griddep_launch_dependents: allow the next grid
+// of a kernel comes after it, but in kernels that run beside another (below).  griddep_launch_dependents: allow the next grid
 // in the stream to start launching (its own griddep_wait still waits for this
 // grid to finish).
 __device__ __forceinline__ void griddep_wait() {

@@ -349,7 +349,21 @@ def ans_gemm_batched(jobs, M: int, scale_kind: int, group_k: int, d_ws, ws_bytes
            "ans_gemm_batched")
 
 
+def _check_lora(where: str, lora: AnsLora, layout: AnsLayout, d_X=None):
+    """The struct names no N, K or device: what LoraAdapters knows of them is checked here, before the
+    call (a struct that a caller fills in is the caller's to get right).  d_X: of a call, not a query."""
+    held = getattr(lora, "tensors", None)
+    if held is None:
+        return
+    A, B, _ = held
+    if (B.shape[1], A.shape[2]) != (layout.N, layout.K):
+        raise AnsError(2, where, f"adapters of a {B.shape[1]} x {A.shape[2]} projection, a layer of {layout.N} x {layout.K}")
+    if d_X is not None and (not A.is_cuda or d_X.device != A.device):
+        raise AnsError(1, where, f"adapters on {A.device}, activations on {d_X.device}")
+
+
 def ans_gemm_lora_workspace(layout: AnsLayout, M: int, scale_kind: int, lora: AnsLora) -> int:
+    _check_lora("ans_gemm_lora_workspace", lora, layout)
     out = C.c_size_t(0)
     _check(load().ans_gemm_lora_workspace(C.byref(layout), M, scale_kind, C.byref(lora), C.byref(out)),
            "ans_gemm_lora_workspace")
@@ -359,6 +373,7 @@ def ans_gemm_lora_workspace(layout: AnsLayout, M: int, scale_kind: int, lora: An
 def ans_gemm_lora(d_X, M: int, tiles: AnsTiles, scale_kind: int, d_scales, group_k: int, lora: AnsLora,
                   d_ids, d_Y, d_ws, ws_bytes: int, d_status, stream=None):
     """ans_gemm with the adapter of each token beside it (d_ids: int32, negative = none)."""
+    _check_lora("ans_gemm_lora", lora, tiles.layout, d_X)
     _check(load().ans_gemm_lora(_ptr(d_X), M, C.byref(tiles), scale_kind, _ptr(d_scales), group_k,
                                 C.byref(lora), _ptr(d_ids), _ptr(d_Y), _ptr(d_ws), ws_bytes,
                                 _ptr(d_status), _stream(stream)),
@@ -381,6 +396,7 @@ def ans_gemm_grad(d_dY, M: int, tiles: AnsTiles, scale_kind: int, d_scales, grou
 
 
 def ans_gemm_lora_grad_workspace(layout: AnsLayout, M: int, scale_kind: int, lora: AnsLora) -> int:
+    _check_lora("ans_gemm_lora_grad_workspace", lora, layout)
     out = C.c_size_t(0)
     _check(load().ans_gemm_lora_grad_workspace(C.byref(layout), M, scale_kind, C.byref(lora),
                                                C.byref(out)),
@@ -391,6 +407,7 @@ def ans_gemm_lora_grad_workspace(layout: AnsLayout, M: int, scale_kind: int, lor
 def ans_gemm_lora_grad(d_X, d_dY, M: int, tiles: AnsTiles, scale_kind: int, d_scales, group_k: int,
                        lora: AnsLora, d_ids, d_dX, d_dA, d_dB, d_ws, ws_bytes: int, d_status, stream=None):
     """Gradients of ans_gemm_lora: dX (bf16, or None) and the adapters' dA and dB (fp32)."""
+    _check_lora("ans_gemm_lora_grad", lora, tiles.layout, d_X)
     _check(load().ans_gemm_lora_grad(_ptr(d_X), _ptr(d_dY), M, C.byref(tiles), scale_kind,
                                      _ptr(d_scales), group_k, C.byref(lora), _ptr(d_ids), _ptr(d_dX),
                                      _ptr(d_dA), _ptr(d_dB), _ptr(d_ws), ws_bytes, _ptr(d_status),
@@ -565,17 +582,22 @@ class CompressedLayer:
 
 class LoraAdapters:
     """A projection's adapters on the device: A bf16 [n, rank, K], B bf16 [n, N, rank], scale fp32 [n]
-    or None.  Holds the tensors, and the ans_lora struct pointing at them in `lora`."""
+    or None.  `lora` is the ans_lora struct of them for the calls; it holds the tensors as well, and
+    the calls refuse it for a layer of another N or K."""
 
     def __init__(self, A, B, scale=None):
         import torch
-        n, rank, _ = A.shape
-        if B.shape[0] != n or B.shape[2] != rank or (scale is not None and tuple(scale.shape) != (n,)):
+        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2] or \
+                (scale is not None and tuple(scale.shape) != (A.shape[0],)):
             raise AnsError(2, "LoraAdapters", "A, B and scale disagree about the adapters or the rank")
         if (A.dtype, B.dtype) != (torch.bfloat16, torch.bfloat16) or \
                 (scale is not None and scale.dtype != torch.float32):
             raise AnsError(1, "LoraAdapters", "A and B are bf16, scale is fp32")
         if not (A.is_contiguous() and B.is_contiguous() and (scale is None or scale.is_contiguous())):
             raise AnsError(1, "LoraAdapters", "A, B and scale are contiguous")
+        if A.device != B.device or (scale is not None and scale.device != A.device):
+            raise AnsError(1, "LoraAdapters", "A, B and scale are on one device")
         self.A, self.B, self.scale = A, B, scale
-        self.lora = AnsLora(n, rank, A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr())
+        self.lora = AnsLora(A.shape[0], A.shape[1], A.data_ptr(), B.data_ptr(),
+                            None if scale is None else scale.data_ptr())
+        self.lora.tensors = A, B, scale

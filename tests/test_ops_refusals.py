@@ -141,3 +141,41 @@ def test_adapter_tensors(ans_lib):
                 (a, b.expand(2, 128, 8).transpose(0, 0).flip(0)[:, ::2], s)):
         with pytest.raises(ans.AnsError):
             ans.LoraAdapters(*bad)
+
+
+def test_adapters_of_another_projection_or_device(ans_lib):
+    # the struct carries neither N nor K: a set made for another layer would be read past its end
+    def of(N, K, device="cpu"):
+        return ans.LoraAdapters(torch.zeros(2, 8, K, dtype=torch.bfloat16, device=device),
+                                torch.zeros(2, N, 8, dtype=torch.bfloat16, device=device)).lora
+    W, x = layer(), torch.zeros(8, 128, dtype=torch.bfloat16)
+    calls = [
+        lambda lora: ans.ans_gemm_lora(x, 8, W, 0, None, 0, lora, x, x, x, 1 << 40, x),
+        lambda lora: ans.ans_gemm_lora_grad(x, x, 8, W, 0, None, 0, lora, x, x, x, x, x, 1 << 40, x),
+        lambda lora: ans.ans_gemm_lora_workspace(W.layout, 8, 0, lora),
+        lambda lora: ans.ans_gemm_lora_grad_workspace(W.layout, 8, 0, lora)]
+    for fn in calls:
+        for N, K in ((256, 64), (256, 256), (128, 128), (384, 128), (128, 256)):
+            with pytest.raises(ans.AnsError) as e:
+                fn(of(N, K))
+            assert e.value.status == SHAPE
+    for fn in calls[:2]:
+        for device in ("cpu", "meta"):
+            with pytest.raises(ans.AnsError) as e:
+                fn(of(256, 128, device))
+            assert e.value.status == ARG
+    with pytest.raises(ans.AnsError):
+        ans.LoraAdapters(torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(2, 128, 8, dtype=torch.bfloat16, device="meta"))
+    with pytest.raises(ans.AnsError):
+        ans.LoraAdapters(torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(2, 128, 8, dtype=torch.bfloat16))
+
+
+def test_the_struct_holds_the_adapters(ans_lib):
+    import gc
+    import weakref
+    a, b = torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(2, 128, 8, dtype=torch.bfloat16)
+    held = weakref.ref(a)
+    lora = ans.LoraAdapters(a, b).lora
+    del a, b
+    gc.collect()
+    assert held() is not None and lora.d_A == held().data_ptr()

@@ -54,15 +54,11 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t& hi, uint16_t& lo) 
   lo = isfinite(v) ? __bfloat16_as_ushort(__float2bfloat16_rn(r)) : uint16_t(0);
 }
 
-// Two bf16 values: is one of them infinite or NaN, and the two with 0 in such a place.
-// An infinite factor meets the first part of a split value alone: times a second part
-// of 0, or of the other sign, it would leave NaN where the product is an infinity.
-__device__ __forceinline__ bool not_finite2(uint32_t v) {
-  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
-}
-__device__ __forceinline__ uint32_t finite2(uint32_t v) {
-  return v & (((v & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((v & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u));
-}
+// Is one of two bf16 values infinite or NaN (an exponent of all ones carries into the
+// bit above)?  An infinite factor meets the first part of a split value alone: times a
+// second part of 0, or of the other sign, it would leave NaN where the product is an
+// infinity.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t v) { return ((v & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ uint2 ldg8(const uint16_t* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
@@ -500,6 +496,26 @@ __device__ __forceinline__ void expand_weights(const ExpandDev& P, const uint16_
   }
 }
 
+// What expand_cta does for the warp's columns c0 .. + 63 into y, with infinite and NaN
+// weights kept from h's second part.  Out of line, and one output at a time: rare.
+__device__ __noinline__ void expand_apart(const ExpandDev& P, const uint16_t* w, const uint16_t* hi, const uint16_t* lo,
+                                          uint32_t pitch, const uint32_t* tok, uint32_t count, uint32_t c0) {
+  auto value = [](uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); };
+  for (uint32_t r = 0; r < count; ++r) {
+    const uint32_t m = tok[r];
+    if (m == kNoToken) continue;
+    for (uint32_t c = c0 + threadIdx.x % 32; c < c0 + 64; c += 32) {
+      float sum = 0.0f;
+      for (uint32_t j = 0; j < P.rank; ++j) {
+        const float b = value(__ldg(w + static_cast<uint64_t>(c) * P.rank + j));
+        sum = fmaf(value(hi[r * pitch + j]), b, sum);
+        if (isfinite(b)) sum = fmaf(value(lo[r * pitch + j]), b, sum);
+      }
+      P.out[static_cast<uint64_t>(m) * P.C + c] += sum;
+    }
+  }
+}
+
 template <bool kCols, bool kFew, int kSteps>
 __device__ __forceinline__ void expand_cta(const ExpandDev& P, uint16_t* hs, uint32_t (&tok)[16], uint32_t& found) {
   const uint32_t tile = blockIdx.x;
@@ -523,19 +539,10 @@ __device__ __forceinline__ void expand_cta(const ExpandDev& P, uint16_t* hs, uin
     count = __ldcg(P.G.tile_count + tile);
   }
   const uint16_t* w = P.weights + static_cast<uint64_t>(a) * P.C * P.rank;
+  bool apart = false;  // the warp has weights that are not finite
   if (c0 < P.C) {
 #pragma unroll
     for (int q = 0; q < kSteps; ++q) expand_weights<kCols>(P, w, c0, 16 * q, g, t, b[q]);
-  }
-  bool odd = false;  // the warp has weights that are not finite
-  if constexpr (!kCols) {
-    if (c0 < P.C) {
-#pragma unroll
-      for (int q = 0; q < kSteps; ++q)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) odd = odd || not_finite2(b[q][i][0]) || not_finite2(b[q][i][1]);
-    }
-    odd = __any_sync(0xFFFFFFFFu, odd);
   }
   if constexpr (!kFew) {
     constexpr uint32_t per = kRow / 8;
@@ -556,83 +563,71 @@ __device__ __forceinline__ void expand_cta(const ExpandDev& P, uint16_t* hs, uin
       split4(v, s, hs + row * pitch + j, lo_s + row * pitch + j);
     }
   }
+  if constexpr (!kCols) {
+    uint32_t odd = 0;
+    if (c0 < P.C) {
+#pragma unroll
+      for (int q = 0; q < kSteps; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) odd |= not_finite2(b[q][i][0]) | not_finite2(b[q][i][1]);
+    }
+    apart = __any_sync(0xFFFFFFFFu, odd != 0);
+  }
   __syncthreads();
   if (c0 >= P.C) return;
+  if (apart) {
+    expand_apart(P, w, hs, lo_s, pitch, kFew ? tok : P.G.perm + start, kFew ? found : count, c0);
+    return;
+  }
   const uint32_t cl = c0 + 4 * t;  // this lane's output columns: cl + 16 q .. + 3
-  auto tokens = [&](auto apart) {  // apart: infinite and NaN weights are kept from h's second part
-    constexpr bool kApart = decltype(apart)::value;
-    for (uint32_t r = 0; r < count; r += 16) {
-      uint32_t m0, m1;
-      if constexpr (kFew) {
-        m0 = g < found ? tok[g] : kNoToken;
-        m1 = g + 8 < found ? tok[g + 8] : kNoToken;
-      } else {
-        m0 = __ldcg(P.G.perm + start + r + g);
-        m1 = __ldcg(P.G.perm + start + r + g + 8);
-      }
-      const bool v0 = m0 != kNoToken, v1 = m1 != kNoToken;
-      float* y0 = P.out + (v0 ? static_cast<uint64_t>(m0) * P.C + cl : 0ull);
-      float* y1 = P.out + (v1 ? static_cast<uint64_t>(m1) * P.C + cl : 0ull);
-      [[maybe_unused]] float4 o0[4], o1[4];
-      if constexpr (!kCols) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (v0) o0[q] = *reinterpret_cast<const float4*>(y0 + 16 * q);
-          if (v1) o1[q] = *reinterpret_cast<const float4*>(y1 + 16 * q);
-        }
-      }
-      float acc[8][4] = {};
-      const uint32_t h0 = (r + g) * pitch + 4 * t, h1 = h0 + 8 * pitch;
-      auto step = [&](const uint16_t* part, uint32_t k, const uint32_t (&bk)[8][2]) {
-        const uint2 a0 = *reinterpret_cast<const uint2*>(part + h0 + k), a1 = *reinterpret_cast<const uint2*>(part + h1 + k);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mma_bf16(acc[i], a0.x, a1.x, a0.y, a1.y, bk[i][0], bk[i][1]);
-      };
-      if constexpr (kApart) {
-        // (read again, so that no more of them are held than below)
-        uint32_t bk[8][2];
-#pragma unroll 1
-        for (uint32_t k = 0; k < r16; k += 16) {
-          expand_weights<kCols>(P, w, c0, k, g, t, bk);
-          step(hs, k, bk);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            bk[i][0] = finite2(bk[i][0]);
-            bk[i][1] = finite2(bk[i][1]);
-          }
-          step(lo_s, k, bk);
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < kSteps; ++q) {
-          if (16u * q >= r16) continue;
-          step(hs, 16 * q, b[q]);
-          if constexpr (!kCols) step(lo_s, 16 * q, b[q]);
-        }
-      }
-      // columns 16 q + 4 t + e: instruction 4 (q & 1) + e, its even (q < 2) or odd column
+  for (uint32_t r = 0; r < count; r += 16) {
+    uint32_t m0, m1;
+    if constexpr (kFew) {
+      m0 = g < found ? tok[g] : kNoToken;
+      m1 = g + 8 < found ? tok[g + 8] : kNoToken;
+    } else {
+      m0 = __ldcg(P.G.perm + start + r + g);
+      m1 = __ldcg(P.G.perm + start + r + g + 8);
+    }
+    const bool v0 = m0 != kNoToken, v1 = m1 != kNoToken;
+    float* y0 = P.out + (v0 ? static_cast<uint64_t>(m0) * P.C + cl : 0ull);
+    float* y1 = P.out + (v1 ? static_cast<uint64_t>(m1) * P.C + cl : 0ull);
+    float4 o0[4], o1[4];
+    if constexpr (!kCols) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int i = 4 * (q & 1), k = q >> 1;
-        float4 u = make_float4(acc[i][k], acc[i + 1][k], acc[i + 2][k], acc[i + 3][k]);
-        float4 v = make_float4(acc[i][k + 2], acc[i + 1][k + 2], acc[i + 2][k + 2], acc[i + 3][k + 2]);
-        if constexpr (!kCols) {
-          if (v0) { u.x += o0[q].x; u.y += o0[q].y; u.z += o0[q].z; u.w += o0[q].w; }
-          if (v1) { v.x += o1[q].x; v.y += o1[q].y; v.z += o1[q].z; v.w += o1[q].w; }
-        }
-        const bool in = c0 + 16 * q < P.C;  // (C is a multiple of 16)
-        if (v0 && in) *reinterpret_cast<float4*>(y0 + 16 * q) = u;
-        if (v1 && in) *reinterpret_cast<float4*>(y1 + 16 * q) = v;
+        if (v0) o0[q] = *reinterpret_cast<const float4*>(y0 + 16 * q);
+        if (v1) o1[q] = *reinterpret_cast<const float4*>(y1 + 16 * q);
       }
     }
-  };
-  if constexpr (!kCols) {
-    if (odd) {
-      tokens(std::true_type{});
-      return;
+    float acc[8][4] = {};
+    const uint32_t h0 = (r + g) * pitch + 4 * t, h1 = h0 + 8 * pitch;
+    auto step = [&](const uint16_t* part, uint32_t k, const uint32_t (&bk)[8][2]) {
+      const uint2 a0 = *reinterpret_cast<const uint2*>(part + h0 + k), a1 = *reinterpret_cast<const uint2*>(part + h1 + k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mma_bf16(acc[i], a0.x, a1.x, a0.y, a1.y, bk[i][0], bk[i][1]);
+    };
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      if (16u * q >= r16) continue;
+      step(hs, 16 * q, b[q]);
+      if constexpr (!kCols) step(lo_s, 16 * q, b[q]);
+    }
+    // columns 16 q + 4 t + e: instruction 4 (q & 1) + e, its even (q < 2) or odd column
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = 4 * (q & 1), k = q >> 1;
+      float4 u = make_float4(acc[i][k], acc[i + 1][k], acc[i + 2][k], acc[i + 3][k]);
+      float4 v = make_float4(acc[i][k + 2], acc[i + 1][k + 2], acc[i + 2][k + 2], acc[i + 3][k + 2]);
+      if constexpr (!kCols) {
+        if (v0) { u.x += o0[q].x; u.y += o0[q].y; u.z += o0[q].z; u.w += o0[q].w; }
+        if (v1) { v.x += o1[q].x; v.y += o1[q].y; v.z += o1[q].z; v.w += o1[q].w; }
+      }
+      const bool in = c0 + 16 * q < P.C;  // (C is a multiple of 16)
+      if (v0 && in) *reinterpret_cast<float4*>(y0 + 16 * q) = u;
+      if (v1 && in) *reinterpret_cast<float4*>(y1 + 16 * q) = v;
     }
   }
-  tokens(std::false_type{});
 }
 // (kCols, into dx: beside the outer products, which run beside the decoding)
 template <bool kCols, bool kFew, int kSteps>
@@ -668,6 +663,36 @@ struct OuterDev {
   uint32_t C, rank;
 };
 __host__ __device__ constexpr uint32_t outer_stage_bytes(uint32_t row) { return 64 * kChunkRow + 2 * 64 * odd_row(row); }
+
+// What outer_cta does, with z's infinities and NaN kept from h's second part (row: of
+// hp; the ranks r0 .. + ranks - 1).  Out of line, and four outputs a thread at a time: rare.
+template <bool kRankMajor>
+__device__ __noinline__ void outer_apart(const OuterDev& P, uint32_t c0, uint32_t row, uint32_t r0, uint32_t ranks) {
+  auto value = [](uint32_t v) { return __uint_as_float(v << 16); };
+  const uint32_t a = blockIdx.y, c = c0 + threadIdx.x % 64;
+  const uint32_t p_begin = __ldcg(P.G.off + a), p_end = __ldcg(P.G.off + a + 1);
+  if (c >= P.C) return;
+  float* out = P.out + static_cast<uint64_t>(a) * P.C * P.rank;
+  for (uint32_t j = r0 + 4 * (threadIdx.x / 64); j < r0 + ranks; j += 16) {
+    float sum[4] = {};
+    for (uint32_t p = p_begin; p < p_end; ++p) {
+      const uint32_t m = __ldcg(P.G.perm + p);
+      if (m == kNoToken) continue;
+      const float z = value(__ldg(P.z + static_cast<uint64_t>(m) * P.C + c));
+      const uint16_t* h = P.hp + static_cast<uint64_t>(p) * row + j;
+      for (uint32_t part = 0; part < (isfinite(z) ? 2u : 1u); ++part) {
+        const uint2 v = __ldcg(reinterpret_cast<const uint2*>(h + part * P.hp_stride));
+        sum[0] = fmaf(z, value(v.x & 0xFFFFu), sum[0]);
+        sum[1] = fmaf(z, value(v.x >> 16), sum[1]);
+        sum[2] = fmaf(z, value(v.y & 0xFFFFu), sum[2]);
+        sum[3] = fmaf(z, value(v.y >> 16), sum[3]);
+      }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+      out[kRankMajor ? static_cast<uint64_t>(j + i) * P.C + c : static_cast<uint64_t>(c) * P.rank + j + i] = sum[i];
+  }
+}
 
 template <bool kRankMajor, int NJ, bool kHalf>
 __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_t* stages_smem) {
@@ -715,70 +740,61 @@ __device__ __forceinline__ void outer_cta(const OuterDev& P, uint32_t c0, uint8_
              in ? h_src + part * P.hp_stride + static_cast<uint64_t>(64 * it + i * kRows) * kRow : P.hp, in);
       }
   };
-  float acc[NJ][4];
-  auto sums = [&](auto apart) {  // apart: z's infinities and NaN are kept from h's second part
-    constexpr bool kApart = decltype(apart)::value;
+  float acc[NJ][4] = {};
+  look(0);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-    look(0);
-#pragma unroll
-    for (uint32_t i = 0; i + 1 < kOuterStages; ++i) {
-      if (i < n_steps) {
-        load(base + i * stage, i);
-        look(i + 1);
-      }
-      cp_commit();
+  for (uint32_t i = 0; i + 1 < kOuterStages; ++i) {
+    if (i < n_steps) {
+      load(base + i * stage, i);
+      look(i + 1);
     }
-    uint32_t zs_next = base, load_next = base + (kOuterStages - 1) * stage;
-    const uint32_t ring_end = base + kOuterStages * stage;
-    for (uint32_t it = 0; it < n_steps; ++it) {
-      cp_wait<kOuterStages - 2>();
-      __syncthreads();
-      if (it + kOuterStages - 1 < n_steps) {
-        load(load_next, it + kOuterStages - 1);
-        look(it + kOuterStages);
-      }
-      cp_commit();
-      if ((load_next += stage) == ring_end) load_next = base;
-      const uint32_t zs = zs_next, hsm = zs + 64 * kChunkRow;
-      if ((zs_next += stage) == ring_end) zs_next = base;
-      const uint32_t n16 = min(4u, (p_end - p_begin - 64 * it) / 16);
+    cp_commit();
+  }
+  uint32_t zs_next = base, load_next = base + (kOuterStages - 1) * stage;
+  const uint32_t ring_end = base + kOuterStages * stage;
+  for (uint32_t it = 0; it < n_steps; ++it) {
+    cp_wait<kOuterStages - 2>();
+    __syncthreads();
+    if (it + kOuterStages - 1 < n_steps) {
+      load(load_next, it + kOuterStages - 1);
+      look(it + kOuterStages);
+    }
+    cp_commit();
+    if ((load_next += stage) == ring_end) load_next = base;
+    const uint32_t zs = zs_next, hsm = zs + 64 * kChunkRow;
+    if ((zs_next += stage) == ring_end) zs_next = base;
+    const uint32_t n16 = min(4u, (p_end - p_begin - 64 * it) / 16);
 #pragma unroll
-      for (uint32_t k = 0; k < 2; ++k) {
-        const uint32_t ks = 2 * half + k;
-        if (ks >= n16) break;
-        uint32_t f[4];
-        ldsm4_t(f, zs + (16 * ks + (lane & 7u) + ((lane >> 4) << 3)) * kChunkRow + (cw / 8 + ((lane >> 3) & 1u)) * 16);
-        uint32_t fl[4];
+    for (uint32_t k = 0; k < 2; ++k) {
+      const uint32_t ks = 2 * half + k;
+      if (ks >= n16) break;
+      uint32_t f[4];
+      ldsm4_t(f, zs + (16 * ks + (lane & 7u) + ((lane >> 4) << 3)) * kChunkRow + (cw / 8 + ((lane >> 3) & 1u)) * 16);
+      // two blocks of 8 ranks a load: lanes 16-31 address the second
+      const uint32_t hr = hsm + (16 * ks + (lane & 15u)) * h_row + (lane >> 4) * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fl[i] = kApart ? finite2(f[i]) : f[i];
-        // two blocks of 8 ranks a load: lanes 16-31 address the second
-        const uint32_t hr = hsm + (16 * ks + (lane & 15u)) * h_row + (lane >> 4) * 16;
-#pragma unroll
-        for (int j = 0; j < NJ / 2; ++j) {
-          if (j < nj2) {
-            uint32_t hi[4], lo[4];
-            ldsm4_t(hi, hr + j * 32);
-            ldsm4_t(lo, hr + h_bytes + j * 32);
-            mma_bf16(acc[2 * j], f[0], f[1], f[2], f[3], hi[0], hi[1]);
-            mma_bf16(acc[2 * j + 1], f[0], f[1], f[2], f[3], hi[2], hi[3]);
-            mma_bf16(acc[2 * j], fl[0], fl[1], fl[2], fl[3], lo[0], lo[1]);
-            mma_bf16(acc[2 * j + 1], fl[0], fl[1], fl[2], fl[3], lo[2], lo[3]);
-          }
+      for (int j = 0; j < NJ / 2; ++j) {
+        if (j < nj2) {
+          uint32_t hi[4], lo[4];
+          ldsm4_t(hi, hr + j * 32);
+          ldsm4_t(lo, hr + h_bytes + j * 32);
+          mma_bf16(acc[2 * j], f[0], f[1], f[2], f[3], hi[0], hi[1]);
+          mma_bf16(acc[2 * j + 1], f[0], f[1], f[2], f[3], hi[2], hi[3]);
+          mma_bf16(acc[2 * j], f[0], f[1], f[2], f[3], lo[0], lo[1]);
+          mma_bf16(acc[2 * j + 1], f[0], f[1], f[2], f[3], lo[2], lo[3]);
         }
       }
     }
-    cp_wait<0>();
-  };
-  // z is not looked at first; where a sum is not finite, they are formed again
-  sums(std::false_type{});
+  }
+  cp_wait<0>();
+  // the sums were formed without a look at z: where one is not finite, again
   bool odd = false;
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
     odd = odd || !isfinite(acc[j][0]) || !isfinite(acc[j][1]) || !isfinite(acc[j][2]) || !isfinite(acc[j][3]);
   if (__syncthreads_or(odd)) {
-    sums(std::true_type{});
-    __syncthreads();
+    outer_apart<kRankMajor>(P, c0, kRow, r0, ranks);
+    return;
   }
   float4* other = reinterpret_cast<float4*>(stages_smem);  // the second half's sums: [rank blocks][4 warps][32 lanes]
   const uint32_t nj = ranks / 8;

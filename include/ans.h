@@ -412,7 +412,10 @@ ans_status ans_gemm_batched(const ans_gemm_job* jobs, uint32_t n_jobs, uint32_t 
  * token's largest but for its target's and the largest scale: in f16 with 11 bits
  * where the product is within 2^21 of theirs, and off by at most 2^-32 of theirs
  * where it is not (by twice that where a block of the vocabulary is moved to a
- * larger reference); in bf16 with 8 bits throughout. */
+ * larger reference); in bf16 with 8 bits throughout.  X A_a^T and dH, sums in
+ * fp32, enter Y, dA and dB as two bf16 parts (off by at most 2^-17 of them), and
+ * dH enters dX as one.  Infinities and NaN go where the formulas take them, and
+ * reach no other token's and no other adapter's results. */
 
 /* A set of low-rank adapters of one projection (W is N x K): adapter a adds
  * s_a (x A_a^T) B_a^T to y.  All have one rank (a multiple of 8 up to 128; an
@@ -463,7 +466,8 @@ ans_status ans_gemm_lora_grad_workspace(const ans_layout* layout, uint32_t M,
  *   dA_a = sum over a's tokens of dH[m]^T X[m]              fp32, shaped as A
  *   dB_a = s_a * sum over a's tokens of dY[m]^T (X[m] A_a^T)  fp32, shaped as B
  * Every element of dA and dB is written: zeros for an adapter without tokens
- * (for all of them when M == 0).  Indices as for ans_gemm_lora. */
+ * (for all of them when M == 0).  Indices as for ans_gemm_lora.  The workspace
+ * is the same size with and without d_dX. */
 ans_status ans_gemm_lora_grad(const uint16_t* d_X, const uint16_t* d_dY, uint32_t M,
                               const ans_tiles* W, ans_scale_kind scale_kind, const void* d_scales,
                               uint32_t group_k, const ans_lora* lora, const int32_t* d_ids,
@@ -483,8 +487,9 @@ ans_status ans_xent_workspace(const ans_layout* layout, uint32_t M, ans_scale_ki
  * X bf16 M x K, targets int32, loss and lse fp32 [M], dX bf16 M x K (NULL: loss
  * only), g = d_weight fp32 [M] (NULL: 1; read with d_dX only): the gradient of
  * sum_m g[m] loss[m].  A token with a negative target has loss 0 and a zero dX;
- * its lse is written.  A target of vocab or more sets ANS_STATUS_BAD_INDEX and
- * is taken as negative.  M == 0 is a no-op. */
+ * its lse is written.  A token with a target whose lse is not finite has NaN in dX.
+ * A target of vocab or more sets ANS_STATUS_BAD_INDEX and is taken as negative.
+ * M == 0 is a no-op. */
 ans_status ans_xent(const uint16_t* d_X, uint32_t M, const ans_tiles* W, ans_scale_kind scale_kind,
                     const void* d_scales, uint32_t group_k, uint32_t vocab,
                     const int32_t* d_targets, float* d_loss, float* d_lse, const float* d_weight,

@@ -12,17 +12,22 @@
 // tiles that cp.async gathers, several stages ahead.
 //
 // h and dh are kept in 32 bits and enter the products with fp32 results (y, dA,
-// dB) as the sum of two bf16 values (16 bits of them; off by 2^-17 at most).
+// dB) as the sum of two bf16 values (17 bits with the second one's sign; off by 2^-17
+// at most, 2.2e-6 in the root mean square, which is what dA and dB are off by).  A
+// third part brought 500 tokens' dA from 2.5e-6 to 6e-7 and the outer products from 70
+// us to 97.
 // dx is bf16, and there dh is rounded to bf16 once: the second part would move
 // dx by less than its own rounding does, and costs as many matrix instructions
 // again, which are what bounds that product (a rank of 64 into 4096 x 14336: 84
 // us with both parts).
 //
 // Measured at rank 64, 4096 tokens of 2 adapters, 4096 x 14336, each alone: both
-// shrinks 49 us (150 MB of x and dy; 3 TB/s), both outer products 96 us (19 GFLOP in
+// shrinks 52 us (150 MB of x and dy; 3 TB/s), both outer products 99 us (19 GFLOP in
 // two parts, 40 % of the 520 TFLOP/s these instructions reach; see kOuterStages),
-// the expansion into dx 52 us (235 MB written; 4.5 TB/s); one token at rank 16,
-// 4096 x 4096: 7 us beside a base product of 35.  The outer products and the
+// the expansion into dx 53 us (235 MB written; 4.4 TB/s); one token at rank 16,
+// 4096 x 4096: 7 us beside a base product of 35.  Times of whole calls in this file
+// are from runs of ten; over seconds, under the power cap, large ones take some
+// 10 % longer.  The outer products and the
 // expansion are launched beside the decoding of the weights (griddep_beside).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -572,9 +572,9 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
 // ---- rows of bf16 as scaled f16 ----------------------------------------------
 // One CTA a row: the largest finite magnitude first, then the conversion (the
 // row comes from L2 the second time).  f16 under a power of two of the row's
-// own keeps 11 bits of every value down to 2^-29 of the row's largest, and
-// what is smaller is off by at most 2^-40 of it: more than a rounding to bf16
-// would keep of v * s.  Infinities and NaN pass through.  Runs beside the decoding
+// own (its largest value then lies in [2^14, 2^15)) keeps 11 bits of every value
+// down to 2^-28 of the row's largest, and what is smaller is off by at most 2^-39
+// of it; bf16 would keep 8 bits of every v * s.  Infinities and NaN pass through.  Runs beside the decoding
 // of the weights.
 constexpr uint32_t kPrepThreads = 256;
 __global__ void __launch_bounds__(kPrepThreads) row_prep_kernel(const uint16_t* __restrict__ in, uint32_t C,

@@ -14,8 +14,8 @@
 // a pass that has the sums first.
 //
 // The reference is a whole number r in units of log 2 that lies at most
-// kXentSlack below the largest logit so far (the target's aside), so that moving it rescales by
-// powers of two, exactly, and after the first piece it hardly moves.
+// kXentSlack below the largest logit so far (the target's aside), so that moving
+// it rescales by powers of two, exactly, and after the first piece it hardly moves.
 //
 // The target's own term stays out of the running sums and their reference, so that
 // the others' exponentials keep their bits (f16 has 22 powers of two below the
@@ -25,9 +25,11 @@
 // where p_t is near 1, and so does the loss, log(1 + l / e_t).  Where e_t passes the
 // others' reference, all of it is divided by e_t.
 //
-// Measured on a 32000 x 4096 bf16 head with 2048 tokens: 1.11 ms, of it the two
-// products 0.95 (see operand_gemm.cu), decoding 0.12, joining the blocks 0.03,
-// rescaling and the targets' rows 0.06.
+// Measured on a 32000 x 4096 bf16 head with 2048 tokens: 1.10 ms a call in runs of
+// ten, 1.26 over seconds, under the power cap.  Its kernels one by one, with a cold
+// cache, take 1.19: the two products 0.43 and 0.47 (see operand_gemm.cu), decoding
+// 0.18, joining the blocks 0.035, rescaling and the targets' rows 0.053, the rest
+// 0.02; they read 1.28 GB and write 0.15.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -59,7 +61,8 @@ __device__ __forceinline__ float pow2(float e) {
 // Beside the first piece's decoding.  Clears the state, checks the targets and sets lift: f16 probabilities carry
 // the row scale of W, so they are stored under a power of two that puts the
 // largest scale in [2^8, 2^9): a probability of e^4 (kXentSlack) stays below the
-// largest f16, and 11 bits are kept down to 2^-22 of the reference's.
+// largest f16, and 11 bits are kept where probability times scale is down to 2^-22 of
+// the reference's times the largest scale.
 __global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t M, const int32_t* __restrict__ targets,
                                                           uint32_t vocab, uint32_t f16, uint32_t kind,
                                                           const void* scales, uint32_t* status) {

@@ -501,20 +501,30 @@ __device__ __forceinline__ void expand_weights(const ExpandDev& P, const uint16_
   }
 }
 
+// sum + the eight products of x and y; not those whose y is not finite, where finite_only.
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float sum, bool finite_only) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+    const float b = __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+    if (!finite_only || isfinite(b)) sum = fmaf(a, b, sum);
+  }
+  return sum;
+}
 // What expand_cta does for the warp's columns c0 .. + 63 into y, with infinite and NaN
-// weights kept from h's second part.  Out of line, and one output at a time: rare.
+// weights kept from h's second part.  Out of line, in plain fp32: rare.
 __device__ __noinline__ void expand_apart(const ExpandDev& P, const uint16_t* w, const uint16_t* hi, const uint16_t* lo,
                                           uint32_t pitch, const uint32_t* tok, uint32_t count, uint32_t c0) {
-  auto value = [](uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); };
   for (uint32_t r = 0; r < count; ++r) {
     const uint32_t m = tok[r];
     if (m == kNoToken) continue;
     for (uint32_t c = c0 + threadIdx.x % 32; c < c0 + 64; c += 32) {
       float sum = 0.0f;
-      for (uint32_t j = 0; j < P.rank; ++j) {
-        const float b = value(__ldg(w + static_cast<uint64_t>(c) * P.rank + j));
-        sum = fmaf(value(hi[r * pitch + j]), b, sum);
-        if (isfinite(b)) sum = fmaf(value(lo[r * pitch + j]), b, sum);
+      for (uint32_t j = 0; j < P.rank; j += 8) {
+        const uint4 b = ldg16(w + static_cast<uint64_t>(c) * P.rank + j);
+        sum = dot8(*reinterpret_cast<const uint4*>(hi + r * pitch + j), b, sum, false);
+        sum = dot8(*reinterpret_cast<const uint4*>(lo + r * pitch + j), b, sum, true);
       }
       P.out[static_cast<uint64_t>(m) * P.C + c] += sum;
     }
@@ -670,33 +680,42 @@ struct OuterDev {
 __host__ __device__ constexpr uint32_t outer_stage_bytes(uint32_t row) { return 64 * kChunkRow + 2 * 64 * odd_row(row); }
 
 // What outer_cta does, with z's infinities and NaN kept from h's second part (row: of
-// hp; the ranks r0 .. + ranks - 1).  Out of line, and four outputs a thread at a time: rare.
+// hp; the ranks r0 .. + ranks - 1).  Out of line, in plain fp32, four columns by four
+// ranks a thread: rare.
 template <bool kRankMajor>
 __device__ __noinline__ void outer_apart(const OuterDev& P, uint32_t c0, uint32_t row, uint32_t r0, uint32_t ranks) {
-  auto value = [](uint32_t v) { return __uint_as_float(v << 16); };
-  const uint32_t a = blockIdx.y, c = c0 + threadIdx.x % 64;
+  const uint32_t a = blockIdx.y, c = c0 + 4 * (threadIdx.x % 16), j = 4 * (threadIdx.x / 16);
+  if (c >= P.C || j >= ranks) return;  // (C is a multiple of 16, the ranks of 8)
   const uint32_t p_begin = __ldcg(P.G.off + a), p_end = __ldcg(P.G.off + a + 1);
-  if (c >= P.C) return;
-  float* out = P.out + static_cast<uint64_t>(a) * P.C * P.rank;
-  for (uint32_t j = r0 + 4 * (threadIdx.x / 64); j < r0 + ranks; j += 16) {
-    float sum[4] = {};
-    for (uint32_t p = p_begin; p < p_end; ++p) {
-      const uint32_t m = __ldcg(P.G.perm + p);
-      if (m == kNoToken) continue;
-      const float z = value(__ldg(P.z + static_cast<uint64_t>(m) * P.C + c));
-      const uint16_t* h = P.hp + static_cast<uint64_t>(p) * row + j;
-      for (uint32_t part = 0; part < (isfinite(z) ? 2u : 1u); ++part) {
-        const uint2 v = __ldcg(reinterpret_cast<const uint2*>(h + part * P.hp_stride));
-        sum[0] = fmaf(z, value(v.x & 0xFFFFu), sum[0]);
-        sum[1] = fmaf(z, value(v.x >> 16), sum[1]);
-        sum[2] = fmaf(z, value(v.y & 0xFFFFu), sum[2]);
-        sum[3] = fmaf(z, value(v.y >> 16), sum[3]);
-      }
-    }
+  auto values = [](uint2 v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x << 16);
+    f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(v.y << 16);
+    f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  };
+  float sum[4][4] = {};
+  const uint16_t* h = P.hp + static_cast<uint64_t>(p_begin) * row + r0 + j;
+#pragma unroll 2
+  for (uint32_t p = p_begin; p < p_end; ++p, h += row) {
+    const uint32_t m = __ldcg(P.G.perm + p);
+    const uint2 zv = m == kNoToken ? make_uint2(0, 0) : ldg8(P.z + static_cast<uint64_t>(m) * P.C + c);
+    float z[4], hi[4], lo[4];
+    values(zv, z);
+    values(__ldcg(reinterpret_cast<const uint2*>(h)), hi);
+    values(__ldcg(reinterpret_cast<const uint2*>(h + P.hp_stride)), lo);
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-      out[kRankMajor ? static_cast<uint64_t>(j + i) * P.C + c : static_cast<uint64_t>(c) * P.rank + j + i] = sum[i];
+    for (int i = 0; i < 4; ++i) {
+      const float z2 = isfinite(z[i]) ? z[i] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[i][k] = fmaf(z2, lo[k], fmaf(z[i], hi[k], sum[i][k]));
+    }
   }
+  float* out = P.out + static_cast<uint64_t>(a) * P.C * P.rank;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      out[kRankMajor ? static_cast<uint64_t>(r0 + j + k) * P.C + c + i : static_cast<uint64_t>(c + i) * P.rank + r0 + j + k] = sum[i][k];
 }
 
 template <bool kRankMajor, int NJ, bool kHalf>

@@ -496,6 +496,50 @@ ans_status ans_xent(const uint16_t* d_X, uint32_t M, const ans_tiles* W, ans_sca
                     uint16_t* d_dX, void* d_ws, size_t ws_bytes, uint32_t* d_status,
                     ans_stream_t stream);
 
+/* ---- Drafted tokens --------------------------------------------------------- */
+
+/* Bytes of device workspace of ans_verify. */
+ans_status ans_verify_workspace(uint32_t n_seqs, uint32_t n_drafted, uint32_t vocab, size_t* bytes);
+
+/* Speculative decoding: which of the tokens that a draft model proposed a target
+ * model's logits (ans_gemm's Y of a vocabulary head, say) accept, and the token
+ * that follows them, so that what comes out is distributed as the target's own
+ * samples are.  n_seqs sequences; d_starts[b] (int32, n_seqs + 1 of them) counts
+ * the tokens drafted before sequence b, so that sequence b has drafts d_starts[b]
+ * to d_starts[b + 1] - 1 (none is allowed: plain sampling), n_drafted in all.
+ *   d_target  fp32 logits, row r at r * target_stride: one row a draft and, behind a
+ *             sequence's, one more.  The row of draft d of sequence b is d + b, and
+ *             holds what the target has to say about that token.
+ *   d_draft   the draft model's logits of its tokens, draft d's row at d *
+ *             draft_stride, or NULL: the drafts were looked up, q is 1 at the token.
+ * With p = softmax(z / T) and q = softmax(y / T) over the first `vocab` logits,
+ * T = d_temperature[b] (fp32 [n_seqs], or NULL: 1), x = d_tokens[d]:
+ *   draft d is accepted while all before it are and d_u[d] q(x) < p(x);
+ *   the next token is the first n with sum_{j <= n} w_j > d_v[b] sum_j w_j, where
+ *   w = max(0, p - q) at the draft that was refused (p where those sum to 2^-40 or
+ *   less), or w = p behind the last draft.
+ * u and v are uniform random numbers in [0, 1) (fp32).  T = 0 (or less, or NaN) is
+ * greedy: p is 1 at the first of the largest logits; the draft's logits are not
+ * looked at.  Logits of -infinity have probability 0; T above 1e30 counts as 1e30.
+ * d_accepted[b] (int32 [n_seqs]) is how many drafts were accepted; d_out (int32
+ * [n_drafted + n_seqs], laid out as the rows of d_target) has a sequence's accepted
+ * tokens, its next token, and -1 behind it.
+ * A row with NaN or +infinity, or with nothing above -infinity, has no
+ * distribution: where a sequence meets one (of either model), it stops with -1 in
+ * place of the next token.  Starts that do not rise from 0 to n_drafted, and tokens
+ * outside the vocabulary, set ANS_STATUS_BAD_INDEX; such a token is refused (and
+ * has no part in w), and starts are taken as the nearest that lie within the rows.
+ * All in 64 bits; the same bits for the same inputs.  vocab <= 2^24 and n_drafted +
+ * n_seqs <= 2^20 (ANS_ERR_UNSUPPORTED above); strides (in logits) of vocab or more,
+ * any alignment of 4 bytes; d_ws 256-byte aligned, with any contents.  n_seqs == 0
+ * (with n_drafted == 0) is a no-op. */
+ans_status ans_verify(const float* d_target, uint64_t target_stride, const float* d_draft,
+                      uint64_t draft_stride, uint32_t n_seqs, uint32_t n_drafted, uint32_t vocab,
+                      const int32_t* d_starts, const int32_t* d_tokens, const float* d_u,
+                      const float* d_v, const float* d_temperature, int32_t* d_accepted,
+                      int32_t* d_out, void* d_ws, size_t ws_bytes, uint32_t* d_status,
+                      ans_stream_t stream);
+
 /* ---- Versioned on-disk container of a compressed layer ---------------------
  * "Approaching Shannon Bound", s3.1: the offline stage yields per layer a
  * shared codebook, a tile offset index and the tile stream (and, for the bf16

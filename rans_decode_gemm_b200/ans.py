@@ -33,7 +33,7 @@ EXPORTS = ["ans_status_string", "ans_last_error", "ans_num_tiles", "ans_layout_c
            "ans_gemm_noalloc", "ans_gemm_uncompressed", "ans_gemm_batched_workspace",
            "ans_gemm_batched", "ans_gemm_lora_workspace", "ans_gemm_lora", "ans_gemm_grad_workspace",
            "ans_gemm_grad", "ans_gemm_lora_grad_workspace", "ans_gemm_lora_grad", "ans_xent_workspace",
-           "ans_xent", "ans_container_write", "ans_container_read"]
+           "ans_xent", "ans_verify_workspace", "ans_verify", "ans_container_write", "ans_container_read"]
 MAX_BATCH = 8
 
 
@@ -124,6 +124,8 @@ def load():
             L.ans_gemm_lora_grad.argtypes = [P, P, u32, P, i32, P, u32, P, P, P, P, P, P, sz, P, P]
             L.ans_xent_workspace.argtypes = [P, u32, i32, i32, P]
             L.ans_xent.argtypes = [P, u32, P, i32, P, u32, u32, P, P, P, P, P, P, sz, P, P]
+            L.ans_verify_workspace.argtypes = [u32, u32, u32, P]
+            L.ans_verify.argtypes = [P, u64, P, u64, u32, u32, u32, P, P, P, P, P, P, P, P, sz, P, P]
             L.ans_container_write.argtypes = [P, P, u64, P]
             L.ans_container_read.argtypes = [P, u64, P]
             for name in EXPORTS:
@@ -431,6 +433,24 @@ def ans_xent(d_X, M: int, tiles: AnsTiles, scale_kind: int, d_scales, group_k: i
                            _ptr(d_targets), _ptr(d_loss), _ptr(d_lse), _ptr(d_weight), _ptr(d_dX),
                            _ptr(d_ws), ws_bytes, _ptr(d_status), _stream(stream)),
            "ans_xent")
+
+
+def ans_verify_workspace(n_seqs: int, n_drafted: int, vocab: int) -> int:
+    out = C.c_size_t(0)
+    _check(load().ans_verify_workspace(n_seqs, n_drafted, vocab, C.byref(out)), "ans_verify_workspace")
+    return out.value
+
+
+def ans_verify(d_target, target_stride: int, d_draft, draft_stride: int, n_seqs: int, n_drafted: int, vocab: int,
+               d_starts, d_tokens, d_u, d_v, d_temperature, d_accepted, d_out, d_ws, ws_bytes: int, d_status,
+               stream=None):
+    """Which drafted tokens (d_tokens, int32) the target's logits accept, given uniform random numbers d_u
+    and d_v, and the token that follows them; d_draft: the draft model's logits, or None."""
+    _check(load().ans_verify(_ptr(d_target), target_stride, _ptr(d_draft), draft_stride, n_seqs, n_drafted, vocab,
+                             _ptr(d_starts), _ptr(d_tokens), _ptr(d_u), _ptr(d_v), _ptr(d_temperature),
+                             _ptr(d_accepted), _ptr(d_out), _ptr(d_ws), ws_bytes, _ptr(d_status),
+                             _stream(stream)),
+           "ans_verify")
 
 
 def ans_container_write(layout: AnsLayout, prob_bits: int, freq, stream: np.ndarray,

@@ -10,6 +10,7 @@
 #include "cuda/kernels.h"
 #include "cuda/lora.h"
 #include "cuda/operand.h"
+#include "cuda/verify.h"
 #include "cuda/xent.h"
 #include "host/codec_host.h"
 
@@ -1128,6 +1129,66 @@ ans_status ans_xent(const uint16_t* d_X, uint32_t M, const ans_tiles* W, ans_sca
                            d_weight, d_dX, d_status};
   cudaError_t e = ansdev::launch_xent(plan, L, a, d_ws, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_xent");
+}
+
+}  // extern "C"
+
+// ---- drafted tokens --------------------------------------------------------------
+namespace {
+
+ans_status check_verify_sizes(uint32_t n_seqs, uint32_t n_drafted, uint32_t vocab) {
+  if (vocab == 0) return ANS_ERR_SHAPE;
+  if (n_seqs == 0 && n_drafted != 0) return ANS_ERR_SHAPE;
+  if (vocab > ansdev::kVerifyMaxVocab || n_seqs > ansdev::kVerifyMaxRows || n_drafted > ansdev::kVerifyMaxRows - n_seqs)
+    return ANS_ERR_UNSUPPORTED;
+  return ANS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ans_status ans_verify_workspace(uint32_t n_seqs, uint32_t n_drafted, uint32_t vocab, size_t* bytes) {
+  if (!bytes) return ANS_ERR_ARG;
+  ans_status st = check_verify_sizes(n_seqs, n_drafted, vocab);
+  if (st != ANS_OK) return st;
+  ansdev::VerifyPlan p;
+  ansdev::make_verify_plan(n_seqs, n_drafted, vocab, &p);
+  *bytes = p.bytes;
+  return ANS_OK;
+}
+
+ans_status ans_verify(const float* d_target, uint64_t target_stride, const float* d_draft, uint64_t draft_stride,
+                      uint32_t n_seqs, uint32_t n_drafted, uint32_t vocab, const int32_t* d_starts,
+                      const int32_t* d_tokens, const float* d_u, const float* d_v, const float* d_temperature,
+                      int32_t* d_accepted, int32_t* d_out, void* d_ws, size_t ws_bytes, uint32_t* d_status,
+                      ans_stream_t stream) {
+  ans_status st = check_verify_sizes(n_seqs, n_drafted, vocab);
+  if (st != ANS_OK) return st;
+  if (n_seqs == 0) return ANS_OK;
+  // (a stride past 2^40 would wrap a row's address)
+  const uint64_t most = 1ull << 40;
+  if (target_stride < vocab || target_stride > most) return ANS_ERR_SHAPE;
+  if (d_draft && n_drafted && (draft_stride < vocab || draft_stride > most)) return ANS_ERR_SHAPE;
+  if (!d_target || !d_starts || !d_v || !d_accepted || !d_out || !d_status || (n_drafted && (!d_tokens || !d_u)))
+    return ANS_ERR_ARG;
+  for (const void* p : {static_cast<const void*>(d_target), static_cast<const void*>(d_draft),
+                        static_cast<const void*>(d_starts), static_cast<const void*>(d_tokens),
+                        static_cast<const void*>(d_u), static_cast<const void*>(d_v),
+                        static_cast<const void*>(d_temperature), static_cast<const void*>(d_accepted),
+                        static_cast<const void*>(d_out), static_cast<const void*>(d_status)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return ANS_ERR_ARG;
+  if (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0) return ANS_ERR_ARG;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ansdev::VerifyPlan p;
+  ansdev::make_verify_plan(n_seqs, n_drafted, vocab, &p);
+  if (ws_bytes < p.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
+  const ansdev::VerifyArgs a{d_target, target_stride, n_drafted ? d_draft : nullptr, draft_stride, n_seqs, n_drafted,
+                             vocab, d_starts, d_tokens, d_u, d_v, d_temperature, d_accepted, d_out, d_status};
+  cudaError_t e = ansdev::launch_verify(p, a, d_ws, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_verify");
 }
 
 }  // extern "C"

@@ -1,0 +1,518 @@
+// verify.cu -- which drafted tokens a target's logits accept, and the token that
+// follows them.
+//
+//   p = softmax(z / T) of a target row, q = softmax(y / T) of a draft row;
+//   draft i of a sequence is accepted while u_i q_i(x_i) < p_i(x_i);
+//   the next token is the first n with  sum_{j <= n} w_j > v sum_j w_j,
+//   w = max(0, p - q) of the row that refused, or p of the row behind the last draft.
+//
+// A decision compares numbers that may lie next to one another, so everything is
+// held in 64 bits: a running sum over a vocabulary has a border every 1 / vocab,
+// which sums in 32 bits would move.  2^d is a table of sixteenths times a polynomial
+// of degree 5 on |f| <= 1/32: (log(2) / 32)^6 / 720 = 1.4e-13 of the value.
+//
+// Two kernels.  The first reads every row once and leaves a reference and a sum for
+// each part of it; the second, a cluster of eight CTAs a sequence, joins the parts
+// of the rows that it decides by, and reads the one or two rows that the next token
+// is drawn from once more.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "gemm_common.cuh"
+#include "launch.h"
+#include "rans_core.cuh"
+#include "verify.h"
+
+namespace ansdev {
+
+constexpr uint32_t kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
+constexpr uint32_t kVerifyCluster = 8;
+constexpr uint32_t kVerifyMaxChunks = 64;
+constexpr double kLog2E64 = 1.4426950408889634;
+constexpr double kNoRef = -1.0e300;              // the reference of a part without a finite logit
+constexpr double kNoMass = 1.0 / (1ull << 40);   // p - q is rounding from here down
+
+__constant__ double g_sixteenths[16] = {
+    1.0, 1.0442737824274138, 1.0905077326652577, 1.1387886347566916, 1.189207115002721, 1.241857812073484,
+    1.2968395546510096, 1.3542555469368927, 1.4142135623730951, 1.4768261459394993, 1.5422108254079407,
+    1.6104903319492543, 1.681792830507429, 1.7562521603732995, 1.8340080864093424, 1.9152065613971474};
+
+// 2^d as value * scale (scale a power of two times a sixteenth power of two; 0 for
+// d below -1020 and for -infinity).  d at most 1000.
+__device__ __forceinline__ void exp2_parts(double d, const double* sixteenths, double& value, double& scale) {
+  constexpr double kRound = 422212465065984.0;  // 1.5 * 2^48: adding it rounds to sixteenths
+  const bool none = static_cast<uint32_t>(__double2hiint(d)) > 0xC08FE000u;  // below -1020
+  d = __hiloint2double(none ? 0 : __double2hiint(d), __double2loint(d));     // (a finite polynomial)
+  const double a = d + kRound;
+  const int q = __double2loint(a);
+  const double f = d - (a - kRound);
+  value = fma(f, 0.0013333558146428441, 0.009618129107628477);
+  value = fma(value, f, 0.055504108664821576);
+  value = fma(value, f, 0.2402265069591007);
+  value = fma(value, f, 0.6931471805599453);
+  value = fma(value, f, 1.0);
+  const double s = sixteenths[q & 15];
+  scale = __hiloint2double(none ? 0 : __double2hiint(s) + ((q >> 4) << 20), none ? 0 : __double2loint(s));
+}
+__device__ __forceinline__ double exp2_of(double d, const double* sixteenths) {
+  double value, scale;
+  exp2_parts(d, sixteenths, value, scale);
+  return value * scale;
+}
+// 2^k for a whole k <= 0; 0 below -1020
+__device__ __forceinline__ double pow2_whole(double k) {
+  return k < -1020.0 ? 0.0 : __hiloint2double((static_cast<int>(k) + 1023) << 20, 0);
+}
+
+// A logit's distance from a reference, in units of log 2.  The product is rounded by
+// itself, as the reference was that came of it: equal logits are then at distance 0
+// however large they are, which a fused product would miss by half a step of 2^-53.
+__device__ __forceinline__ double distance(double z, double c, double ref) {
+  return __dsub_rn(__dmul_rn(z, c), ref);
+}
+
+// log2(e) / T; 0 for a greedy sequence.  (T from 1e30 on leaves all finite logits alike already.)
+__device__ __forceinline__ double per_temperature(const float* temperature, uint32_t b) {
+  const float t = temperature == nullptr ? 1.0f : __ldg(temperature + b);
+  return t > 0.0f ? kLog2E64 / static_cast<double>(fminf(t, 1e30f)) : 0.0;
+}
+
+// The last sequence whose first row (its drafts' rows and, for a target, one more
+// for every sequence before) is at most `row`; by whole warps.
+__device__ __forceinline__ uint32_t sequence_of(const int32_t* starts, uint32_t n_seqs, uint32_t row, uint32_t extra,
+                                                uint32_t lane) {
+  uint32_t lo = 0, hi = n_seqs;
+  while (hi - lo > 1) {
+    const uint32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const bool in = lane == 0 || (at < hi && static_cast<int64_t>(__ldg(starts + at)) + extra * at <= row);
+    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, in);
+    const uint32_t k = 31 - __clz(bits);
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+struct VerifyDev {
+  VerifyArgs a;
+  double2* parts;  // [target rows, then draft rows][n_chunks]: (reference, sum), or (value, index) of the largest
+  uint32_t chunk, n_chunks;
+};
+
+// One part of one row.
+__global__ void __launch_bounds__(kVerifyThreads) verify_sums_kernel(const __grid_constant__ VerifyDev P) {
+  __shared__ double sixteenths[16];
+  __shared__ double part_ref[kVerifyWarps], part_sum[kVerifyWarps];
+  const VerifyArgs& A = P.a;
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  if (threadIdx.x < 16) sixteenths[threadIdx.x] = g_sixteenths[threadIdx.x];
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t row = blockIdx.x / P.n_chunks, part = blockIdx.x - row * P.n_chunks;
+  const uint32_t n_target = A.n_drafted + A.n_seqs;
+  const bool is_target = row < n_target;
+  const uint32_t r = is_target ? row : row - n_target;
+  const uint32_t b = sequence_of(A.starts, A.n_seqs, r, is_target ? 1u : 0u, lane);
+  const double c = per_temperature(A.temperature, b);
+  const float* z = is_target ? A.target + static_cast<uint64_t>(r) * A.target_stride
+                             : A.draft + static_cast<uint64_t>(r) * A.draft_stride;
+  const bool greedy = c == 0.0;
+  if (greedy && !is_target) return;  // (all that a greedy sequence asks is the target's largest)
+  __syncthreads();
+  // groups of four logits on 16-byte boundaries: group g holds logits 4 g - off .. + 3
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z) >> 2) & 3u;
+  const uint32_t groups = (A.vocab + off + 3) / 4;
+  const uint32_t g0 = part * (P.chunk / 4), g1 = part + 1 == P.n_chunks ? groups : min(groups, g0 + P.chunk / 4);
+  const float* base = z - off;
+  constexpr uint32_t kDeep = 4;
+  bool bad = false;
+  double ref = kNoRef, sum = 0.0;
+  float best = -INFINITY;
+  uint32_t best_at = 0xFFFFFFFFu;
+  for (uint32_t g = g0 + threadIdx.x; g < g1; g += kDeep * kVerifyThreads) {
+    float x[4 * kDeep];
+#pragma unroll
+    for (uint32_t k = 0; k < kDeep; ++k) {
+      const uint32_t at = g + k * kVerifyThreads;
+      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (at < g1) {
+        const uint32_t n = 4 * at - off;  // (wraps below 0 in the first group)
+        if (n < A.vocab && n + 3 < A.vocab) {
+          q = __ldcs(reinterpret_cast<const float4*>(base + 4ull * at));
+        } else {
+          // (places in 32 bits throughout: the sum has wrapped back before it meets the pointer)
+          const uint32_t n1 = n + 1, n2 = n + 2, n3 = n + 3;
+          if (n < A.vocab) q.x = __ldg(z + n);
+          if (n1 < A.vocab) q.y = __ldg(z + n1);
+          if (n2 < A.vocab) q.z = __ldg(z + n2);
+          if (n3 < A.vocab) q.w = __ldg(z + n3);
+        }
+      }
+      x[4 * k] = q.x;
+      x[4 * k + 1] = q.y;
+      x[4 * k + 2] = q.z;
+      x[4 * k + 3] = q.w;
+    }
+    float top = x[0];
+#pragma unroll
+    for (uint32_t k = 0; k < 4 * kDeep; ++k) {
+      bad = bad || !(x[k] <= 3.402823466e38f);
+      top = fmaxf(top, x[k]);
+    }
+    if (greedy) {
+      if (top > best) {
+        best = top;
+#pragma unroll
+        for (int k = 4 * kDeep - 1; k >= 0; --k)
+          if (x[k] == top) best_at = 4 * (g + (k / 4) * kVerifyThreads) + k % 4 - off;
+      }
+      continue;
+    }
+    // (64 bits reach 2^1000 above a reference, so that it hardly ever moves)
+    const double d = __dmul_rn(top, c);
+    if (d > ref + 500.0 && top >= -3.402823466e38f) {
+      const double next = rint(d);
+      sum *= pow2_whole(fmax(ref - next, -2000.0));
+      ref = next;
+    }
+    const double from = ref == kNoRef ? 0.0 : ref;
+#pragma unroll
+    for (uint32_t k = 0; k < 4 * kDeep; ++k) {
+      double value, scale;
+      exp2_parts(distance(x[k], c, from), sixteenths, value, scale);
+      sum = fma(value, scale, sum);
+    }
+  }
+  double2* out = P.parts + static_cast<uint64_t>(row) * P.n_chunks + part;
+  bad = __syncthreads_or(bad) != 0;
+  if (bad) {
+    if (threadIdx.x == 0) *out = make_double2(kNoRef, __longlong_as_double(0x7FF8000000000000ll));
+    return;
+  }
+  if (greedy) {
+    ref = best;
+    sum = best_at;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const double v = __shfl_xor_sync(0xFFFFFFFFu, ref, d), at = __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      if (v > ref || (v == ref && at < sum)) {
+        ref = v;
+        sum = at;
+      }
+    }
+  } else {
+    double top = ref;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmax(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    sum *= pow2_whole(fmax(ref - top, -2000.0));
+    ref = top;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  }
+  if (lane == 0) {
+    part_ref[warp] = ref;
+    part_sum[warp] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (uint32_t w = 1; w < kVerifyWarps; ++w) {
+    const double r2 = part_ref[w], s2 = part_sum[w];
+    if (greedy) {
+      if (r2 > ref || (r2 == ref && s2 < sum)) {
+        ref = r2;
+        sum = s2;
+      }
+    } else {
+      const double top = fmax(ref, r2);
+      sum = sum * pow2_whole(fmax(ref - top, -2000.0)) + s2 * pow2_whole(fmax(r2 - top, -2000.0));
+      ref = top;
+    }
+  }
+  *out = make_double2(ref, sum);
+}
+
+// A row's parts joined: (reference, sum), or (value, index) of the largest; sum NaN
+// (index -1) where the row has no distribution.  By whole warps.
+__device__ __forceinline__ double2 join_row(const VerifyDev& P, uint64_t row, bool greedy, uint32_t lane) {
+  double ref = greedy ? -INFINITY : kNoRef, sum = greedy ? 4294967295.0 : 0.0;
+  double2 u[kVerifyMaxChunks / 32];
+  bool bad = false;
+#pragma unroll
+  for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k) {
+    const uint32_t at = lane + 32 * k;
+    u[k] = at < P.n_chunks ? __ldcg(P.parts + row * P.n_chunks + at) : make_double2(ref, sum);
+    bad = bad || isnan(u[k].y);
+  }
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if (greedy) {
+#pragma unroll
+    for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k)
+      if (u[k].x > ref || (u[k].x == ref && u[k].y < sum)) {
+        ref = u[k].x;
+        sum = u[k].y;
+      }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const double v = __shfl_xor_sync(0xFFFFFFFFu, ref, d), at = __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      if (v > ref || (v == ref && at < sum)) {
+        ref = v;
+        sum = at;
+      }
+    }
+    if (bad || ref == -INFINITY) sum = -1.0;
+    return make_double2(ref, sum);
+  }
+  double top = kNoRef;
+#pragma unroll
+  for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k) top = fmax(top, u[k].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmax(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+#pragma unroll
+  for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k) sum += u[k].y * pow2_whole(fmax(u[k].x - top, -2000.0));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  if (bad || sum == 0.0) sum = __longlong_as_double(0x7FF8000000000000ll);
+  return make_double2(top, sum);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ double cluster_read(const double* p, uint32_t rank) {
+  uint32_t at;
+  double v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// Of eight sums in order, the first whose running total passes `aim`, or else the
+// last above 0 (8: none is); `before` ends as the total before it.
+template <typename F>
+__device__ __forceinline__ uint32_t first_past(double aim, double& before, F sum_of) {
+  double run = before;
+  uint32_t last = 8;
+  double last_before = before;
+#pragma unroll
+  for (uint32_t k = 0; k < 8; ++k) {
+    const double s = sum_of(k);
+    if (s > 0.0) {
+      last = k;
+      last_before = run;
+      if (run + s > aim) break;
+    }
+    run += s;
+  }
+  before = last_before;
+  return last;
+}
+
+struct VerifyRows {
+  const float *p, *q;    // the last row, and the draft's (null: none)
+  double c, p_ref, p_per, q_ref, q_per;  // value = 2^(z c - ref) * per
+  uint32_t without;      // a token that counts for nothing (a draft without logits), or -1
+};
+__device__ __forceinline__ double verify_weight(const VerifyRows& R, uint32_t n, const double* sixteenths) {
+  double w = exp2_of(distance(__ldg(R.p + n), R.c, R.p_ref), sixteenths) * R.p_per;
+  if (R.q != nullptr) {
+    const double q = exp2_of(distance(__ldg(R.q + n), R.c, R.q_ref), sixteenths) * R.q_per;
+    w = fmax(w - q, 0.0);
+  }
+  return n == R.without ? 0.0 : w;
+}
+
+// A cluster a sequence.  Every CTA decides where the sequence stops; for the next
+// token the vocabulary is cut into 64 runs, one a warp.
+__global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerifyThreads, 2)
+    verify_decide_kernel(const __grid_constant__ VerifyDev P) {
+  __shared__ double sixteenths[16];
+  __shared__ double run_sum[kVerifyWarps], cta_sum[2], piece_sum[kVerifyWarps];
+  __shared__ double2 row_join[2];
+  __shared__ uint32_t first;
+  const VerifyArgs& A = P.a;
+  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const uint32_t b = blockIdx.x / kVerifyCluster, rank = blockIdx.x % kVerifyCluster;
+  if (threadIdx.x < 16) sixteenths[threadIdx.x] = g_sixteenths[threadIdx.x];
+  griddep_wait();
+  griddep_launch_dependents();
+  // (whatever starts hold, rows stay within the logits)
+  const int32_t raw0 = __ldg(A.starts + b), raw1 = __ldg(A.starts + b + 1);
+  const int32_t drafted = static_cast<int32_t>(A.n_drafted);
+  const int32_t s0 = max(0, min(raw0, drafted)), s1 = max(s0, min(raw1, drafted));
+  bool wrong = s0 != raw0 || s1 != raw1 || (b == 0 && raw0 != 0) || (b + 1 == A.n_seqs && raw1 != drafted);
+  const uint32_t count = static_cast<uint32_t>(s1 - s0), t0 = static_cast<uint32_t>(s0) + b;
+  const uint64_t n_target = static_cast<uint64_t>(A.n_drafted) + A.n_seqs;
+  const double c = per_temperature(A.temperature, b);
+  const bool greedy = c == 0.0;
+  if (threadIdx.x == 0) first = count;
+  __syncthreads();
+  // a warp a draft, in turn
+  for (uint32_t i = warp; i < count; i += kVerifyWarps) {
+    if (i > *static_cast<volatile uint32_t*>(&first)) break;
+    const double2 t = join_row(P, t0 + i, greedy, lane);
+    const int32_t x = __ldg(A.tokens + s0 + i);
+    const bool in = x >= 0 && static_cast<uint32_t>(x) < A.vocab;
+    bool keep = false;
+    if (greedy) {
+      keep = in && t.y == static_cast<double>(x);
+    } else {
+      double2 d = make_double2(0.0, 1.0);
+      if (A.draft != nullptr) d = join_row(P, n_target + s0 + i, false, lane);
+      if (in) {
+        const double zx = __ldg(A.target + (t0 + i) * A.target_stride + x);
+        const double px = exp2_of(distance(zx, c, t.x), sixteenths) / t.y;
+        double qx = 1.0;
+        if (A.draft != nullptr) {
+          const double yx = __ldg(A.draft + static_cast<uint64_t>(s0 + i) * A.draft_stride + x);
+          qx = exp2_of(distance(yx, c, d.x), sixteenths) / d.y;
+        }
+        keep = static_cast<double>(__ldg(A.u + s0 + i)) * qx < px;  // (false where a row has no distribution)
+      }
+    }
+    if (!keep && lane == 0) atomicMin(&first, i);
+  }
+  __syncthreads();
+  const uint32_t stop = first;
+  const bool refused = stop < count;
+  const uint32_t row = t0 + stop;
+  if (rank == 0) {
+    if (threadIdx.x == 0) A.accepted[b] = static_cast<int32_t>(stop);
+    for (uint32_t i = threadIdx.x; i <= count; i += kVerifyThreads) {
+      const int32_t x = i < count ? __ldg(A.tokens + s0 + i) : 0;
+      wrong = wrong || x < 0 || static_cast<uint32_t>(x) >= A.vocab;
+      if (i != stop) A.out[t0 + i] = i < stop ? x : -1;
+    }
+    if (wrong) atomicOr(A.status, kStatusBadIndex);
+  }
+  if (greedy) {
+    if (rank == 0 && warp == 0) {
+      const double2 t = join_row(P, row, true, lane);
+      if (lane == 0) A.out[row] = static_cast<int32_t>(t.y);
+    }
+    return;
+  }
+  const bool has_draft = refused && A.draft != nullptr;
+  if (warp == 0) {
+    const double2 t = join_row(P, row, false, lane);
+    if (lane == 0) row_join[0] = t;
+  } else if (warp == 1) {
+    double2 t = make_double2(0.0, 1.0);
+    if (has_draft) t = join_row(P, n_target + s0 + stop, false, lane);
+    if (lane == 0) row_join[1] = t;
+  }
+  __syncthreads();
+  if (isnan(row_join[0].y) || isnan(row_join[1].y)) {
+    if (rank == 0 && threadIdx.x == 0) A.out[row] = -1;
+    return;
+  }
+  VerifyRows R;
+  R.c = c;
+  R.p = A.target + static_cast<uint64_t>(row) * A.target_stride;
+  R.p_ref = row_join[0].x;
+  R.p_per = 1.0 / row_join[0].y;
+  R.q = has_draft ? A.draft + static_cast<uint64_t>(s0 + stop) * A.draft_stride : nullptr;
+  R.q_ref = row_join[1].x;
+  R.q_per = 1.0 / row_join[1].y;
+  R.without = 0xFFFFFFFFu;
+  if (refused && A.draft == nullptr) {
+    const int32_t x = __ldg(A.tokens + s0 + stop);
+    if (x >= 0 && static_cast<uint32_t>(x) < A.vocab) R.without = static_cast<uint32_t>(x);
+  }
+  // runs are whole numbers of 32 logits for each of eight warps
+  const uint32_t run = (A.vocab + 64 * 256 - 1) / (64 * 256) * 256;
+  const double v = __ldg(A.v + b);
+  for (uint32_t turn = 0;; ++turn) {
+    const uint64_t n0 = static_cast<uint64_t>(rank * kVerifyWarps + warp) * run;
+    const uint32_t end = static_cast<uint32_t>(min(static_cast<uint64_t>(A.vocab), n0 + run));
+    double s = 0.0;
+    if (n0 < end) {
+#pragma unroll 4
+      for (uint32_t n = static_cast<uint32_t>(n0) + lane; n < end; n += 32) s += verify_weight(R, n, sixteenths);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    if (lane == 0) run_sum[warp] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      double all = 0.0;
+      for (uint32_t k = 0; k < kVerifyWarps; ++k) all += run_sum[k];
+      cta_sum[turn] = all;
+    }
+    cluster_sync();
+    double all = 0.0;
+#pragma unroll
+    for (uint32_t k = 0; k < kVerifyCluster; ++k) all += cluster_read(&cta_sum[turn], k);
+    if (turn == 0 && refused && all <= kNoMass) {
+      // nothing that p has more of than q: p itself
+      R.q = nullptr;
+      R.without = 0xFFFFFFFFu;
+      continue;
+    }
+    const double aim = v * all;
+    double before = 0.0;
+    const uint32_t at = first_past(aim, before, [&](uint32_t k) { return cluster_read(&cta_sum[turn], k); });
+    cluster_sync();  // (every CTA's sums have been read: it may end)
+    if (at != rank) return;
+    const uint32_t w_at = first_past(aim, before, [&](uint32_t k) { return run_sum[k]; });
+    // that run once more, an eighth a warp
+    const uint32_t piece = run / kVerifyWarps, r0 = (rank * kVerifyWarps + w_at) * run;
+    const uint32_t p0 = r0 + warp * piece, p1 = min(A.vocab, p0 + piece);
+    s = 0.0;
+    for (uint32_t n = p0 + lane; n < p1; n += 32) s += verify_weight(R, n, sixteenths);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    if (lane == 0) piece_sum[warp] = s;
+    __syncthreads();
+    const uint32_t p_at = first_past(aim, before, [&](uint32_t k) { return piece_sum[k]; });
+    if (p_at != warp) return;
+    uint32_t token = 0xFFFFFFFFu;
+    bool done = false;
+    for (uint32_t n32 = p0; n32 < p1 && !done; n32 += 32) {
+      const uint32_t n = n32 + lane;
+      const double w = n < p1 ? verify_weight(R, n, sixteenths) : 0.0;
+      double upto = w;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const double o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= static_cast<uint32_t>(d)) upto += o;
+      }
+      const uint32_t some = __ballot_sync(0xFFFFFFFFu, w > 0.0);
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, w > 0.0 && before + upto > aim);
+      if (past != 0) {
+        token = n32 + __ffs(past) - 1;
+        done = true;
+      } else if (some != 0) {
+        token = n32 + 31 - __clz(some);
+      }
+      before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    if (lane == 0) A.out[row] = static_cast<int32_t>(token);
+    return;
+  }
+}
+
+void make_verify_plan(uint32_t n_seqs, uint32_t n_drafted, uint32_t vocab, VerifyPlan* p) {
+  // parts of 2,048 to 32,768 logits, so that a few rows fill the SMs and many rows
+  // have few ends; 64 of them at most
+  const uint64_t rows = 2ull * n_drafted + n_seqs, all = rows * vocab;
+  uint64_t chunk = (all / (148 * 16) + 1023) / 1024 * 1024;
+  chunk = std::max<uint64_t>(2048, std::min<uint64_t>(chunk, 32768));
+  // (a row that starts off a 16-byte boundary has up to three places more)
+  const uint64_t places = static_cast<uint64_t>(vocab) + 3;
+  chunk = std::max(chunk, ((places + kVerifyMaxChunks - 1) / kVerifyMaxChunks + 1023) / 1024 * 1024);
+  p->chunk = static_cast<uint32_t>(chunk);
+  p->n_chunks = static_cast<uint32_t>((places + chunk - 1) / chunk);
+  p->bytes = static_cast<size_t>(rows) * p->n_chunks * sizeof(double2);
+}
+
+cudaError_t launch_verify(const VerifyPlan& plan, const VerifyArgs& a, void* ws, cudaStream_t stream) {
+  const VerifyDev P{a, static_cast<double2*>(ws), plan.chunk, plan.n_chunks};
+  const uint32_t rows = a.n_drafted + a.n_seqs + (a.draft != nullptr ? a.n_drafted : 0u);
+  const cudaError_t e =
+      launch_pdl(verify_sums_kernel, dim3(rows * plan.n_chunks), dim3(kVerifyThreads), 0, stream, P);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(verify_decide_kernel, dim3(a.n_seqs * kVerifyCluster), dim3(kVerifyThreads), 0, stream, P);
+}
+
+}  // namespace ansdev

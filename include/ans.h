@@ -496,6 +496,49 @@ ans_status ans_xent(const uint16_t* d_X, uint32_t M, const ans_tiles* W, ans_sca
                     uint16_t* d_dX, void* d_ws, size_t ws_bytes, uint32_t* d_status,
                     ans_stream_t stream);
 
+/* ---- The gated feed-forward block ---------------------------------------------
+ * H = act(G) * U with G = X Wg^T and U = X Wu^T: the gate and up projections of a
+ * feed-forward block, the activation and the product of both.  Two compressed
+ * layers of one layout (dtype, N, K, tile and state width; ANS_ERR_SHAPE
+ * otherwise), each with its codebook and its scales, of one kind.  What is said
+ * of the calls above (token counts, workspaces, roundings, overlaps) holds for
+ * these: G, U and the activation are fp32, each result is rounded to bf16 once. */
+typedef enum {
+  ANS_ACT_SILU = 0,      /* g / (1 + e^-g) */
+  ANS_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
+  ANS_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+  ANS_ACT_RELU = 3       /* max(0, g); derivative 0 at 0 */
+} ans_act;
+
+/* Bytes of device workspace of ans_gated (`layout`: of either layer). */
+ans_status ans_gated_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind,
+                               size_t* bytes);
+
+/* H bf16 M x N from X bf16 M x K, row-major, 16-byte aligned.  Up to 32 tokens for
+ * 128-row tiles and 16 for 256-row ones no decoded weight reaches global memory,
+ * and G and U are ans_gemm_batched's (X beyond f16's range, and X of 2^-17 and
+ * less, as there); above, both layers are decoded once into the workspace
+ * (4 N K bytes), and X enters under a power of two of its row.  M == 0 is a no-op. */
+ans_status ans_gated(const uint16_t* d_X, uint32_t M, const ans_tiles* gate, const ans_tiles* up,
+                     ans_scale_kind scale_kind, const void* d_gate_scales,
+                     const void* d_up_scales, uint32_t group_k, ans_act act, uint16_t* d_H,
+                     void* d_ws, size_t ws_bytes, uint32_t* d_status, ans_stream_t stream);
+
+ans_status ans_gated_grad_workspace(const ans_layout* layout, uint32_t M,
+                                    ans_scale_kind scale_kind, size_t* bytes);
+
+/* The gradients of ans_gated from dH (bf16 M x N); G and U are computed again:
+ *   dG = dH * U * act'(G),  dU = dH * act(G)        bf16 M x N
+ *   dX = dG Wg + dU Wu, of dG and dU as returned    bf16 M x K; d_dX NULL: not computed
+ * dG and dU are what ans_gemm_lora_grad takes as d_dY of the two projections
+ * (d_dX NULL there) for the gradients of their adapters.  The workspace is the
+ * same size with and without d_dX.  M == 0 is a no-op. */
+ans_status ans_gated_grad(const uint16_t* d_X, const uint16_t* d_dH, uint32_t M,
+                          const ans_tiles* gate, const ans_tiles* up, ans_scale_kind scale_kind,
+                          const void* d_gate_scales, const void* d_up_scales, uint32_t group_k,
+                          ans_act act, uint16_t* d_dX, uint16_t* d_dG, uint16_t* d_dU, void* d_ws,
+                          size_t ws_bytes, uint32_t* d_status, ans_stream_t stream);
+
 /* ---- Drafted tokens --------------------------------------------------------- */
 
 /* Bytes of device workspace of ans_verify. */

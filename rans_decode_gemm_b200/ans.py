@@ -19,6 +19,7 @@ from . import build as _build
 
 INT4, BF16_SPLIT, FP8_E4M3, INT4_PAIRS, INT8, FP4_E2M1, FP4_PAIRS = 0, 1, 2, 3, 4, 5, 6
 BF16_WHOLE = 7   # bf16 as whole 16-bit symbols: the ans_*16 entry points only
+ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = 0, 1, 2, 3
 SCALE_NONE, SCALE_ROW_BF16, SCALE_ROW_F32, SCALE_GROUP_BF16 = 0, 1, 2, 3
 STATUS_CORRUPT, STATUS_TIMEOUT, STATUS_BAD_OFFSETS, STATUS_SMEM_ALIGN = 0x1, 0x2, 0x4, 0x8
 STATUS_BAD_INDEX = 0x10
@@ -33,7 +34,8 @@ EXPORTS = ["ans_status_string", "ans_last_error", "ans_num_tiles", "ans_layout_c
            "ans_gemm_noalloc", "ans_gemm_uncompressed", "ans_gemm_batched_workspace",
            "ans_gemm_batched", "ans_gemm_lora_workspace", "ans_gemm_lora", "ans_gemm_grad_workspace",
            "ans_gemm_grad", "ans_gemm_lora_grad_workspace", "ans_gemm_lora_grad", "ans_xent_workspace",
-           "ans_xent", "ans_verify_workspace", "ans_verify", "ans_container_write", "ans_container_read"]
+           "ans_xent", "ans_gated_workspace", "ans_gated", "ans_gated_grad_workspace", "ans_gated_grad",
+           "ans_verify_workspace", "ans_verify", "ans_container_write", "ans_container_read"]
 MAX_BATCH = 8
 
 
@@ -124,6 +126,10 @@ def load():
             L.ans_gemm_lora_grad.argtypes = [P, P, u32, P, i32, P, u32, P, P, P, P, P, P, sz, P, P]
             L.ans_xent_workspace.argtypes = [P, u32, i32, i32, P]
             L.ans_xent.argtypes = [P, u32, P, i32, P, u32, u32, P, P, P, P, P, P, sz, P, P]
+            L.ans_gated_workspace.argtypes = [P, u32, i32, P]
+            L.ans_gated.argtypes = [P, u32, P, P, i32, P, P, u32, i32, P, P, sz, P, P]
+            L.ans_gated_grad_workspace.argtypes = [P, u32, i32, P]
+            L.ans_gated_grad.argtypes = [P, P, u32, P, P, i32, P, P, u32, i32, P, P, P, P, sz, P, P]
             L.ans_verify_workspace.argtypes = [u32, u32, u32, P]
             L.ans_verify.argtypes = [P, u64, P, u64, u32, u32, u32, P, P, P, P, P, P, P, P, sz, P, P]
             L.ans_container_write.argtypes = [P, P, u64, P]
@@ -433,6 +439,37 @@ def ans_xent(d_X, M: int, tiles: AnsTiles, scale_kind: int, d_scales, group_k: i
                            _ptr(d_targets), _ptr(d_loss), _ptr(d_lse), _ptr(d_weight), _ptr(d_dX),
                            _ptr(d_ws), ws_bytes, _ptr(d_status), _stream(stream)),
            "ans_xent")
+
+
+def ans_gated_workspace(layout: AnsLayout, M: int, scale_kind: int = SCALE_NONE) -> int:
+    out = C.c_size_t(0)
+    _check(load().ans_gated_workspace(C.byref(layout), M, scale_kind, C.byref(out)), "ans_gated_workspace")
+    return out.value
+
+
+def ans_gated(d_X, M: int, gate: AnsTiles, up: AnsTiles, scale_kind: int, d_gate_scales, d_up_scales, group_k: int,
+              act: int, d_H, d_ws, ws_bytes: int, d_status, stream=None):
+    """H = act(X Wg^T) * (X Wu^T) of two compressed layers (bf16 in, bf16 out)."""
+    _check(load().ans_gated(_ptr(d_X), M, C.byref(gate), C.byref(up), scale_kind, _ptr(d_gate_scales),
+                            _ptr(d_up_scales), group_k, act, _ptr(d_H), _ptr(d_ws), ws_bytes, _ptr(d_status),
+                            _stream(stream)),
+           "ans_gated")
+
+
+def ans_gated_grad_workspace(layout: AnsLayout, M: int, scale_kind: int = SCALE_NONE) -> int:
+    out = C.c_size_t(0)
+    _check(load().ans_gated_grad_workspace(C.byref(layout), M, scale_kind, C.byref(out)),
+           "ans_gated_grad_workspace")
+    return out.value
+
+
+def ans_gated_grad(d_X, d_dH, M: int, gate: AnsTiles, up: AnsTiles, scale_kind: int, d_gate_scales, d_up_scales,
+                   group_k: int, act: int, d_dX, d_dG, d_dU, d_ws, ws_bytes: int, d_status, stream=None):
+    """Gradients of ans_gated: dG and dU of the projections' outputs, and dX (or None), all bf16."""
+    _check(load().ans_gated_grad(_ptr(d_X), _ptr(d_dH), M, C.byref(gate), C.byref(up), scale_kind,
+                                 _ptr(d_gate_scales), _ptr(d_up_scales), group_k, act, _ptr(d_dX), _ptr(d_dG),
+                                 _ptr(d_dU), _ptr(d_ws), ws_bytes, _ptr(d_status), _stream(stream)),
+           "ans_gated_grad")
 
 
 def ans_verify_workspace(n_seqs: int, n_drafted: int, vocab: int) -> int:

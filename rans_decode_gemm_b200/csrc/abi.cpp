@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "../../include/ans.h"
+#include "cuda/gated.h"
 #include "cuda/kernels.h"
 #include "cuda/lora.h"
 #include "cuda/operand.h"
@@ -568,6 +569,7 @@ int ansdev_set_wait_budget(long long cycles) {
   if (e == cudaSuccess) e = ansdev::set_live_wait_budget_decode16(c);
   if (e == cudaSuccess) e = ansdev::set_live_wait_budget_operand(c);
   if (e == cudaSuccess) e = ansdev::set_live_wait_budget_operand_gemm(c);
+  if (e == cudaSuccess) e = ansdev::set_live_wait_budget_gated(c);
   return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ansdev_set_wait_budget");
 }
 
@@ -1129,6 +1131,160 @@ ans_status ans_xent(const uint16_t* d_X, uint32_t M, const ans_tiles* W, ans_sca
                            d_weight, d_dX, d_status};
   cudaError_t e = ansdev::launch_xent(plan, L, a, d_ws, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_xent");
+}
+
+}  // extern "C"
+
+// ---- the gated block -------------------------------------------------------------
+namespace {
+
+// A call through operand images, or, while both layers' products take the small-M
+// schedule on half of the SMs each, ans_gemm_batched's one launch of both and their
+// products joined: no weight reaches global memory.
+struct GatedChoice {
+  bool few;
+  size_t off_y, bytes;
+  ansdev::GatedPlan images;
+  ansdev::GemmPlan share[ANS_MAX_BATCH], full[ANS_MAX_BATCH];
+  size_t ws_off[ANS_MAX_BATCH + 1];
+};
+
+ans_status choose_gated(const ans_tiles* gate, const ans_tiles* up, uint32_t M, ans_scale_kind kind, bool grad, int sms,
+                        GatedChoice* c) {
+  c->few = false;
+  if (!grad) {
+    const ans_gemm_job jobs[2] = {{nullptr, gate, nullptr, nullptr}, {nullptr, up, nullptr, nullptr}};
+    if (batch_plan(jobs, 2, M, kind, sms, c->share, c->full, c->ws_off, &c->few) != ANS_OK) c->few = false;
+  }
+  if (c->few) {
+    c->off_y = up1024(c->ws_off[2]);
+    c->bytes = c->off_y + 2 * up1024(static_cast<size_t>(M) * gate->layout.N * 4);
+    return ANS_OK;
+  }
+  ansdev::LayerDev L;
+  fill_layer_plain(&gate->layout, &L);
+  ansdev::make_gated_plan(L, M, kind, grad, sms, &c->images);
+  c->bytes = c->images.bytes;
+  return ANS_OK;
+}
+
+ans_status gated_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind kind, bool grad, size_t* bytes) {
+  if (!bytes) return ANS_ERR_ARG;
+  ans_status st = check_layout(layout);
+  if (st != ANS_OK) return st;
+  st = check_scale_kind(*layout, kind);
+  if (st != ANS_OK) return st;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (M == 0) return ANS_OK;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ans_tiles t;
+  std::memset(&t, 0, sizeof(t));
+  t.layout = *layout;
+  GatedChoice c;
+  st = choose_gated(&t, &t, M, kind, grad, sms, &c);
+  if (st != ANS_OK) return st;
+  *bytes = c.bytes;
+  return ANS_OK;
+}
+
+// What both calls check of their layers and the activation (no device work).
+ans_status check_gated(const ans_tiles* gate, const ans_tiles* up, ans_scale_kind kind, const void* gate_scales,
+                       const void* up_scales, uint32_t group_k, ans_act act) {
+  ans_status st = check_gemm_tiles(gate, kind, gate_scales, group_k);
+  if (st != ANS_OK) return st;
+  st = check_gemm_tiles(up, kind, up_scales, group_k);
+  if (st != ANS_OK) return st;
+  const ans_layout &a = gate->layout, &b = up->layout;
+  if (a.dtype != b.dtype || a.N != b.N || a.K != b.K || a.tile_n != b.tile_n || a.tile_k != b.tile_k ||
+      (a.state_bits == 64) != (b.state_bits == 64))
+    return ANS_ERR_SHAPE;
+  if (act < ANS_ACT_SILU || act > ANS_ACT_RELU) return ANS_ERR_ARG;
+  return ANS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ans_status ans_gated_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind, size_t* bytes) {
+  return gated_workspace(layout, M, scale_kind, false, bytes);
+}
+
+ans_status ans_gated_grad_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind, size_t* bytes) {
+  return gated_workspace(layout, M, scale_kind, true, bytes);
+}
+
+ans_status ans_gated(const uint16_t* d_X, uint32_t M, const ans_tiles* gate, const ans_tiles* up,
+                     ans_scale_kind scale_kind, const void* d_gate_scales, const void* d_up_scales, uint32_t group_k,
+                     ans_act act, uint16_t* d_H, void* d_ws, size_t ws_bytes, uint32_t* d_status, ans_stream_t stream) {
+  ans_status st = check_gated(gate, up, scale_kind, d_gate_scales, d_up_scales, group_k, act);
+  if (st != ANS_OK) return st;
+  if (M == 0) return ANS_OK;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  if (!d_X || !d_H || !d_status || misaligned16(d_X) || misaligned16(d_H) || misaligned16(d_gate_scales) ||
+      misaligned16(d_up_scales))
+    return ANS_ERR_ARG;
+  if (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0) return ANS_ERR_ARG;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  GatedChoice c;
+  st = choose_gated(gate, up, M, scale_kind, false, sms, &c);
+  if (st != ANS_OK) return st;
+  if (ws_bytes < c.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
+  ansdev::LayerDev Lg, Lu;
+  fill_layer(gate, &Lg);
+  fill_layer(up, &Lu);
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(d_ws);
+  cudaError_t e;
+  if (c.few) {
+    float* Y[2];
+    Y[0] = reinterpret_cast<float*>(ws + c.off_y);
+    Y[1] = reinterpret_cast<float*>(ws + c.off_y + up1024(static_cast<size_t>(M) * Lg.N * 4));
+    const ansdev::LayerDev* Ls[2] = {&Lg, &Lu};
+    const uint16_t* Xs[2] = {d_X, d_X};
+    const void* Ss[2] = {d_gate_scales, d_up_scales};
+    e = ansdev::launch_gemm_batched(c.share, 2, Ls, Xs, Ss, scale_kind, group_k, Y, d_ws, c.ws_off, d_status, cs);
+    if (e == cudaSuccess)
+      e = ansdev::launch_gated_join(Y[0], Y[1], static_cast<uint64_t>(M) * Lg.N, act, d_H, cs);
+  } else {
+    const ansdev::GatedArgs a{d_X, static_cast<uint32_t>(scale_kind), d_gate_scales, d_up_scales, group_k,
+                              static_cast<uint32_t>(act), d_H, nullptr, nullptr, nullptr, nullptr, d_status};
+    e = ansdev::launch_gated(c.images, Lg, Lu, a, d_ws, cs);
+  }
+  return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gated");
+}
+
+ans_status ans_gated_grad(const uint16_t* d_X, const uint16_t* d_dH, uint32_t M, const ans_tiles* gate,
+                          const ans_tiles* up, ans_scale_kind scale_kind, const void* d_gate_scales,
+                          const void* d_up_scales, uint32_t group_k, ans_act act, uint16_t* d_dX, uint16_t* d_dG,
+                          uint16_t* d_dU, void* d_ws, size_t ws_bytes, uint32_t* d_status, ans_stream_t stream) {
+  ans_status st = check_gated(gate, up, scale_kind, d_gate_scales, d_up_scales, group_k, act);
+  if (st != ANS_OK) return st;
+  if (M == 0) return ANS_OK;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  if (!d_X || !d_dH || !d_dG || !d_dU || !d_status || misaligned16(d_X) || misaligned16(d_dH) || misaligned16(d_dX) ||
+      misaligned16(d_dG) || misaligned16(d_dU) || misaligned16(d_gate_scales) || misaligned16(d_up_scales))
+    return ANS_ERR_ARG;
+  if (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0) return ANS_ERR_ARG;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  GatedChoice c;
+  st = choose_gated(gate, up, M, scale_kind, true, sms, &c);
+  if (st != ANS_OK) return st;
+  if (ws_bytes < c.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
+  ansdev::LayerDev Lg, Lu;
+  fill_layer(gate, &Lg);
+  fill_layer(up, &Lu);
+  const ansdev::GatedArgs a{d_X, static_cast<uint32_t>(scale_kind), d_gate_scales, d_up_scales, group_k,
+                            static_cast<uint32_t>(act), nullptr, d_dH, d_dX, d_dG, d_dU, d_status};
+  cudaError_t e = ansdev::launch_gated(c.images, Lg, Lu, a, d_ws, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gated_grad");
 }
 
 }  // extern "C"

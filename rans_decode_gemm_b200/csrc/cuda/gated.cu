@@ -1,0 +1,507 @@
+// gated.cu -- the gated feed-forward block on two compressed layers:
+//
+//   G = X Wg^T,  U = X Wu^T,  H = act(G) * U
+//   dG = dH * U * act'(G),  dU = dH * act(G),  dX = dG Wg + dU Wu
+//
+// Both layers are decoded into operand images (operand.h), gate and up side by
+// side, and one tcgen05 product meets both: 128 tokens are the MMA's M, 128 rows of
+// Wg and the same 128 of Wu its N = 256, so that a token's g_n and u_n end in one
+// TMEM lane, 128 columns apart, and the thread that reads them has all that H_n, or
+// dG_n and dU_n, take.  G and U never reach memory; the gradient computes them
+// again.  dX is one transposed product over both layers' rows (operand_gemm.cu).
+//
+// A stage holds 64 steps of the sum: 16 KB of tokens by TMA (128-byte swizzle) and
+// 32 KB of images by one copy.  An image's rows are K-major under the 32-byte
+// swizzle, so 8 KB of a gate and an up image are one 256-row operand.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "gated.h"
+#include "gemm_common.cuh"
+#include "launch.h"
+#include "rans_core.cuh"
+
+namespace ansdev {
+
+constexpr uint32_t kGaBM = 128, kGaBN = 128, kGaBK = 64;
+constexpr uint32_t kGaABytes = kGaBM * kGaBK * 2;           // 16 KB of tokens
+constexpr uint32_t kGaBBytes = 2 * kGaBN * kGaBK * 2;       // 32 KB of both layers
+constexpr uint32_t kGaStageBytes = kGaABytes + kGaBBytes;
+constexpr uint32_t kGaStages = 4;
+constexpr uint32_t kGaSmem = kGaStages * kGaStageBytes + 1024;
+constexpr uint32_t kGaEpiWarps = 8;
+constexpr uint32_t kGaThreads = (2 + kGaEpiWarps) * 32;
+
+// act(g) and, where asked, its derivative.  Sigmoids for tanh and erfc for 1 + erf:
+// the small values at negative g keep their digits.
+template <bool kSlope>
+__device__ __forceinline__ void activation(uint32_t act, float g, float& value, float& slope) {
+  if (act == kActRelu) {
+    value = g < 0.0f ? 0.0f : g;  // (NaN stays)
+    if (kSlope) slope = g > 0.0f ? 1.0f : 0.0f;
+  } else if (act == kActGelu) {
+    const float p = 0.5f * erfcf(-0.70710678118654752f * g);
+    value = g * p;
+    if (kSlope) slope = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), p);
+  } else {
+    float y = g, dy = 1.0f;  // value = g * sigmoid(y)
+    if (act == kActGeluTanh) {
+      constexpr float kA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+      const float q = 0.044715f * g * g;
+      y = kA * fmaf(g, q, g);
+      if (kSlope) dy = kA * fmaf(3.0f, q, 1.0f);
+    }
+    const float e = __expf(-y);
+    const float p = 1.0f / (1.0f + e);
+    value = g * p;
+    // p' = p (1 - p) y', and 1 - p = e p
+    if (kSlope) slope = e > 1e30f ? 0.0f : fmaf(g * dy, p * (e * p), p);
+  }
+}
+
+struct GatedDev {
+  const uint8_t* images;
+  CUtensorMap tmap_x;       // tokens: 64 x b_rows boxes, 128-byte swizzle
+  const float* factor;      // a token's factor, or null: 1
+  const void *gate_scales, *up_scales;
+  uint32_t scale_kind, act;
+  uint16_t* H;
+  const uint16_t* dH;
+  uint16_t *dG, *dU;
+  uint32_t* status;
+  uint32_t M, N, m_blocks, n_tiles, k_slabs, n_kb, box_rows, idesc;
+};
+
+// Eight row scales from n on.
+__device__ __forceinline__ void row_scales8(uint32_t kind, const void* scales, uint32_t n, float (&s)[8]) {
+  if (kind == 1) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(scales) + n));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s[2 * k] = __uint_as_float(w[k] << 16);
+      s[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(scales) + n);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    s[0] = a.x; s[1] = a.y; s[2] = a.z; s[3] = a.w;
+    s[4] = b.x; s[5] = b.y; s[6] = b.z; s[7] = b.w;
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <bool kGrad>
+__global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_constant__ GatedDev P) {
+  extern __shared__ __align__(1024) uint8_t dsmem_raw[];
+  __shared__ __align__(8) uint64_t full[kGaStages], empty[kGaStages];
+  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t abort_flag;
+
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t smem_s = (smem_u32(dsmem_raw) + 1023u) & ~1023u;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (uint32_t i = 0; i < kGaStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kGaEpiWarps);  // one arrival per epilogue warp
+    }
+    mbar_init(&mma_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  } else if (warp == 0 && lane == 0) {
+    prefetch_tmap(&P.tmap_x);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  volatile uint32_t* abort = &abort_flag;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // tile t: rows 128 ab of both layers, tokens 128 mb; row block major, so that the
+  // CTAs running at one time share the weights through L2
+  if (warp == 0) {
+    // ======================= loads =======================
+    if (lane == 0) {
+      uint32_t it = 0, s = 0, ph = 1;  // the first pass over the ring finds it free
+      bool live = true;
+      for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x) {
+        const uint32_t ab = t / P.m_blocks, mb = t - ab * P.m_blocks;
+        for (uint32_t kb = 0; kb < P.n_kb; ++kb, ++it) {
+          if (it >= kGaStages && !wait_live(&empty[s], ph, abort, P.status, 20)) {
+            live = false;
+            break;
+          }
+          const uint32_t bar = smem_u32(&full[s]);
+          const uint32_t a_s = smem_s + s * kGaStageBytes, b_s = a_s + kGaABytes;
+          const uint32_t bytes = min(4u, P.k_slabs - 4 * kb) * 2 * kSlabBytes;
+          mbar_arrive_expect_tx_s(bar, bytes + P.box_rows * kGaBK * 2);
+          bulk_g2s_s(b_s, P.images + (static_cast<uint64_t>(ab) * P.k_slabs + 4 * kb) * 2 * kSlabBytes, bytes, bar);
+          tma_load_2d_s(a_s, &P.tmap_x, static_cast<int32_t>(kb * kGaBK), static_cast<int32_t>(mb * kGaBM), bar);
+          if (++s == kGaStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // loads still in flight (only after an abort) land before exit
+      const uint32_t first = it > kGaStages ? it - kGaStages : 0;
+      for (uint32_t q = first; q < it; ++q) wait_drain(&full[q % kGaStages], (q / kGaStages) & 1u, P.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ======================= MMA issue =======================
+    if (lane == 0) {
+      // tokens: 128-byte swizzle, 8-row groups 1024 B apart, K = 16 slice j 32 j bytes
+      // into each row.  Weights: 32-byte swizzle, 8-row groups 256 B apart, slice j the
+      // j-th pair of images.
+      const uint64_t da = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+      const uint64_t db = (1ull << 16) | (16ull << 32) | (1ull << 46) | (6ull << 61);
+      uint32_t s = 0, ph = 0, acc = 0;
+      bool live = true;
+      for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x, ++acc) {
+        const uint32_t b = acc & 1u;
+        if (acc >= 2 && !wait_live(&acc_empty[b], ((acc >> 1) + 1) & 1u, abort, P.status, 21)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + b * 256;
+        for (uint32_t kb = 0; kb < P.n_kb; ++kb) {
+          if (!wait_live(&full[s], ph, abort, P.status, 22)) {
+            live = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a16 = (smem_s + s * kGaStageBytes) >> 4, b16 = a16 + (kGaABytes >> 4);
+          const uint32_t cnt = min(4u, P.k_slabs - 4 * kb);
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j)
+            if (j < cnt)
+              umma_f16(d_tmem, da | (a16 + 2 * j), db | (b16 + j * (2 * kSlabBytes >> 4)), P.idesc,
+                       (kb != 0 || j != 0) ? 1u : 0u);
+          umma_commit(&empty[s]);
+          if (++s == kGaStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (live) umma_commit(&acc_full[b]);
+      }
+      umma_commit(&mma_done);
+      wait_drain(&mma_done, 0, P.status);
+    }
+    __syncwarp();
+  } else {
+    // ======================= epilogue (warps 2-9) =======================
+    // a token a lane; two warps for each quarter of TMEM's lanes, 64 of the tile's
+    // rows each, 32 at a time
+    const uint32_t quad = warp & 3u, half = (warp - 2) >> 2;
+    uint32_t acc = 0;
+    for (uint32_t t = blockIdx.x; t < P.n_tiles; t += gridDim.x, ++acc) {
+      const uint32_t ab = t / P.m_blocks, mb = t - ab * P.m_blocks;
+      const uint32_t b = acc & 1u;
+      const uint32_t m = mb * kGaBM + 32 * quad + lane;
+      const bool m_in = m < P.M;
+      const float f = P.factor != nullptr && m_in ? __ldcg(P.factor + m) : 1.0f;
+      const uint64_t row = static_cast<uint64_t>(m) * P.N;
+      const bool ok = wait_live(&acc_full[b], (acc >> 1) & 1u, abort, P.status, 23, 64);
+      tc_fence_after();
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+#pragma unroll
+      for (uint32_t step = 0; step < 2; ++step) {
+        const uint32_t c0 = 64 * half + 32 * step, n0 = ab * kGaBN + c0;
+        uint32_t g[32], u[32];
+        const uint32_t at = tmem_base + ((32 * quad) << 16) + b * 256 + c0;
+        tmem_ld32(at, g);
+        tmem_ld32(at + kGaBN, u);
+        uint4 d[4];
+        if (kGrad) {
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            d[k] = m_in ? __ldg(reinterpret_cast<const uint4*>(P.dH + row + n0) + k) : make_uint4(0, 0, 0, 0);
+        }
+        tmem_ld_wait();
+        if (step == 1) {
+          // this warp has read its last of the tile's sums
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+          float sg[8], su[8];
+          if (P.scale_kind == 1 || P.scale_kind == 2) {
+            row_scales8(P.scale_kind, P.gate_scales, n0 + 8 * k, sg);
+            row_scales8(P.scale_kind, P.up_scales, n0 + 8 * k, su);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sg[i] = su[i] = 1.0f;
+          }
+          uint32_t o[4], o2[4];
+          const uint32_t dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w};
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) {
+            float r[2], r2[2];
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+              const uint32_t j = 8 * k + 2 * i + h;
+              const float gv = __uint_as_float(g[j]) * sg[2 * i + h] * f;
+              const float uv = __uint_as_float(u[j]) * su[2 * i + h] * f;
+              float value, slope;
+              activation<kGrad>(P.act, gv, value, slope);
+              if (kGrad) {
+                const float dh = __uint_as_float(h ? dw[i] & 0xFFFF0000u : dw[i] << 16);
+                r[h] = dh * uv * slope;
+                r2[h] = dh * value;
+              } else {
+                r[h] = value * uv;
+              }
+            }
+            o[i] = bf16x2(r[0], r[1]);
+            if (kGrad) o2[i] = bf16x2(r2[0], r2[1]);
+          }
+          if (m_in) {
+            uint16_t* out = (kGrad ? P.dG : P.H) + row + n0 + 8 * k;
+            *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (kGrad) *reinterpret_cast<uint4*>(P.dU + row + n0 + 8 * k) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, 512);
+}
+
+// ---- products that are there ---------------------------------------------------
+__global__ void __launch_bounds__(256) gated_join_kernel(const float* __restrict__ G, const float* __restrict__ U,
+                                                         uint64_t n8, uint32_t act, uint16_t* __restrict__ H) {
+  griddep_wait();
+  griddep_launch_dependents();
+  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<uint64_t>(gridDim.x) * 256) {
+    uint32_t o[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 2; ++k) {
+      const float4 g = __ldcg(reinterpret_cast<const float4*>(G) + 2 * i + k);
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(U) + 2 * i + k);
+      const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
+      float r[4], slope;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        activation<false>(act, gv[j], r[j], slope);
+        r[j] *= uv[j];
+      }
+      o[2 * k] = bf16x2(r[0], r[1]);
+      o[2 * k + 1] = bf16x2(r[2], r[3]);
+    }
+    reinterpret_cast<uint4*>(H)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+cudaError_t launch_gated_join(const float* G, const float* U, uint64_t n, uint32_t act, uint16_t* H, cudaStream_t stream) {
+  const uint64_t n8 = n / 8;
+  return launch_pdl(gated_join_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((n8 + 255) / 256, 148 * 8))), dim3(256), 0,
+                    stream, G, U, n8, act, H);
+}
+
+// ---- dG and dU as rows of the transposed product --------------------------------
+// As row_prep_kernel (operand_gemm.cu), for two rows under one power of two: both
+// products add into one sum.  A CTA a token.
+struct GatedPrep {
+  const uint16_t *dG, *dU;
+  const void *gate_scales, *up_scales;
+  uint32_t N, scale_kind, f16;
+  uint16_t* rows;   // [2][M][N]
+  uint64_t second;  // elements from the first to the second
+  float* factor;
+};
+__device__ __forceinline__ void prep_values(const GatedPrep& P, uint32_t which, uint64_t row, uint32_t c, float (&v)[8]) {
+  const uint4 q = __ldcg(reinterpret_cast<const uint4*>((which ? P.dU : P.dG) + row + c));
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+  }
+  if (P.scale_kind == 1 || P.scale_kind == 2) {
+    float s[8];
+    row_scales8(P.scale_kind, which ? P.up_scales : P.gate_scales, c, s);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= s[k];
+  }
+}
+constexpr uint32_t kGaPrepThreads = 256;
+__global__ void __launch_bounds__(kGaPrepThreads) gated_prep_kernel(const __grid_constant__ GatedPrep P) {
+  __shared__ float part[kGaPrepThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint64_t row = static_cast<uint64_t>(blockIdx.x) * P.N;
+  float top = 0.0f;
+  if (P.f16) {
+    for (uint32_t c = threadIdx.x * 8; c < 2 * P.N; c += kGaPrepThreads * 8) {
+      float v[8];
+      prep_values(P, c >= P.N, row, c >= P.N ? c - P.N : c, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float a = fabsf(v[k]);
+        if (a <= 3.402823466e38f) top = fmaxf(top, a);
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+  __syncthreads();
+#pragma unroll
+  for (uint32_t k = 0; k < kGaPrepThreads / 32; ++k) top = fmaxf(top, part[k]);
+  // 2^e with top * 2^e in [2^14, 2^15); both powers stay normal numbers
+  const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+  const int e = top == 0.0f ? 0 : min(126, max(-113, 14 - ex));
+  const float scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  if (threadIdx.x == 0) P.factor[blockIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  for (uint32_t c = threadIdx.x * 8; c < 2 * P.N; c += kGaPrepThreads * 8) {
+    const bool which = c >= P.N;
+    const uint32_t cc = which ? c - P.N : c;
+    float v[8];
+    prep_values(P, which, row, cc, v);
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (P.f16) {
+        const __half2 h = __floats2half2_rn(v[2 * k] * scale, v[2 * k + 1] * scale);
+        o[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        o[k] = bf16x2(v[2 * k], v[2 * k + 1]);
+      }
+    }
+    *reinterpret_cast<uint4*>(P.rows + (which ? P.second : 0) + row + cc) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+static size_t aligned(size_t n) { return (n + 1023) / 1024 * 1024; }
+
+void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool grad, int sms, GatedPlan* p) {
+  p->M = M;
+  p->N = L.N;
+  p->K = L.K;
+  p->f16 = operand_is_f16(L.dtype);
+  p->grad = grad;
+  p->sms = sms;
+  p->prep = p->f16 || scale_kind == 1 || scale_kind == 2;
+  p->back = plan_operand_gemm(true, p->f16, M, 2 * L.N, L.K, sms);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += aligned(n);
+    return o;
+  };
+  p->off_images = take(2 * operand_bytes(L.N, L.K));
+  p->off_x16 = take(p->f16 ? static_cast<size_t>(M) * L.K * 2 : 0);
+  p->off_factor = take(p->f16 ? static_cast<size_t>(M) * 4 : 0);
+  p->off_rows = take(grad && p->prep ? static_cast<size_t>(M) * L.N * 4 : 0);
+  p->off_rows_factor = take(grad && p->prep ? static_cast<size_t>(M) * 4 : 0);
+  p->off_gemm = take(grad ? operand_gemm_workspace(p->back) : 0);
+  p->bytes = at;
+}
+
+template <bool kGrad>
+static cudaError_t launch_gated_gemm(const GatedDev& P, int sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(attr_set.load() & (1ull << dev))) {
+    e = cudaFuncSetAttribute(gated_gemm_kernel<kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGaSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set.fetch_or(1ull << dev);
+  }
+  return launch_pdl(gated_gemm_kernel<kGrad>, dim3(std::min(P.n_tiles, static_cast<uint32_t>(sms))), dim3(kGaThreads),
+                    kGaSmem, stream, P);
+}
+
+cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDev& up, const GatedArgs& a, void* ws,
+                         cudaStream_t stream) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint8_t* images = w + p.off_images;
+  uint16_t* x16 = reinterpret_cast<uint16_t*>(w + p.off_x16);
+  float* factor = reinterpret_cast<float*>(w + p.off_factor);
+  cudaError_t e = launch_operand_decode(gate, 0, p.N, a.scale_kind, a.gate_scales, a.group_k, images, a.status, p.sms,
+                                        stream, 2 * kOperandImage);
+  if (e == cudaSuccess)
+    e = launch_operand_decode(up, 0, p.N, a.scale_kind, a.up_scales, a.group_k, images + kOperandImage, a.status, p.sms,
+                              stream, 2 * kOperandImage);
+  if (e == cudaSuccess && p.f16) e = launch_row_prep(a.X, p.M, p.K, 0, nullptr, true, x16, factor, stream);
+  if (e != cudaSuccess) return e;
+  GatedDev P;
+  std::memset(&P, 0, sizeof(P));
+  P.images = images;
+  P.factor = p.f16 ? factor : nullptr;
+  P.gate_scales = a.gate_scales;
+  P.up_scales = a.up_scales;
+  P.scale_kind = a.scale_kind;
+  P.act = a.act;
+  P.H = a.H;
+  P.dH = a.dH;
+  P.dG = a.dG;
+  P.dU = a.dU;
+  P.status = a.status;
+  P.M = p.M;
+  P.N = p.N;
+  P.m_blocks = (p.M + kGaBM - 1) / kGaBM;
+  P.n_tiles = p.N / kGaBN * P.m_blocks;
+  P.k_slabs = p.K / 16;
+  P.n_kb = (p.K + kGaBK - 1) / kGaBK;
+  P.box_rows = std::min(p.M, kGaBM);
+  P.idesc = idesc_f16(p.f16 ? 0u : 1u, 128, 256);
+  e = encode_tmap(&P.tmap_x, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.f16 ? x16 : a.X, p.K, p.M, static_cast<uint64_t>(p.K) * 2,
+                  kGaBK, P.box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  if (!p.grad) return launch_gated_gemm<false>(P, p.sms, stream);
+  e = launch_gated_gemm<true>(P, p.sms, stream);
+  if (e != cudaSuccess || a.dX == nullptr) return e;
+  OperandGemmOut out;
+  std::memset(&out, 0, sizeof(out));
+  out.out16 = a.dX;
+  out.ld = p.K;
+  const uint16_t *rows = a.dG, *rows2 = a.dU;
+  if (p.prep) {
+    uint16_t* r = reinterpret_cast<uint16_t*>(w + p.off_rows);
+    float* f = reinterpret_cast<float*>(w + p.off_rows_factor);
+    const GatedPrep q{a.dG, a.dU, a.gate_scales, a.up_scales, p.N, a.scale_kind, p.f16, r,
+                      static_cast<uint64_t>(p.M) * p.N, f};
+    e = launch_pdl(gated_prep_kernel, dim3(p.M), dim3(kGaPrepThreads), 0, stream, q);
+    if (e != cudaSuccess) return e;
+    rows = r;
+    rows2 = r + q.second;
+    out.beta = f;
+  }
+  const OperandPair pair{images + kOperandImage, rows2, 2 * kOperandImage};
+  return launch_operand_gemm(p.back, images, rows, &out, nullptr, w + p.off_gemm, a.status, stream, &pair);
+}
+
+cudaError_t set_live_wait_budget_gated(long long cycles) {
+  return cudaMemcpyToSymbol(g_live_wait_budget, &cycles, sizeof(cycles));
+}
+
+}  // namespace ansdev

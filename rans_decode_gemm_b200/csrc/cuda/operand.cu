@@ -50,6 +50,7 @@ struct OperandDev {
   uint32_t tile0, n_tiles;       // the range's tiles
   uint32_t block0;               // its first 128-row block
   uint8_t* images;
+  uint32_t step;                 // bytes from an image to the next
   uint32_t* status;
 };
 
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kOpThreads, 1) operand_decode_kernel(const __g
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
-          bulk_s2g_s(P.images + (static_cast<uint64_t>(rb * H + h - P.block0) * k_slabs + kt * C + s) * kSlabBytes,
+          bulk_s2g_s(P.images + (static_cast<uint64_t>(rb * H + h - P.block0) * k_slabs + kt * C + s) * P.step,
                      w_s, kSlabBytes);
       }
     };
@@ -284,7 +285,7 @@ uint32_t operand_decode_rounds(uint32_t tiles, uint32_t ctas) {
 
 cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t rows, uint32_t scale_kind,
                                   const void* scales, uint32_t group_k, uint8_t* images,
-                                  uint32_t* status, int sms, cudaStream_t stream) {
+                                  uint32_t* status, int sms, cudaStream_t stream, uint32_t step) {
   if (rows == 0) return cudaSuccess;
   OperandDev P;
   std::memset(&P, 0, sizeof(P));
@@ -298,6 +299,7 @@ cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t row
   P.n_tiles = rows / L.tile_n * L.n_kt;
   P.block0 = row0 / 128;
   P.images = images;
+  P.step = step;
   P.status = status;
   // one CTA an SM (with fewer tiles than that, one tile a CTA), and the fewest
   // warps that need no more rounds of tiles than the most warps would

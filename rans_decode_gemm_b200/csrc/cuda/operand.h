@@ -23,10 +23,13 @@ namespace ansdev {
 inline bool operand_is_f16(uint32_t dtype) { return dtype != 1; }
 inline size_t operand_bytes(uint64_t rows, uint32_t K) { return static_cast<size_t>(rows) * K * 2; }
 
-// Decodes row blocks [row0, row0 + rows) (multiples of tile_n) into images.
+// Decodes row blocks [row0, row0 + rows) (multiples of tile_n) into images, one
+// every `step` bytes (two layers' images may lie side by side).
+constexpr uint32_t kOperandImage = 4096;
 cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t rows,
                                   uint32_t scale_kind, const void* scales, uint32_t group_k,
-                                  uint8_t* images, uint32_t* status, int sms, cudaStream_t stream);
+                                  uint8_t* images, uint32_t* status, int sms, cudaStream_t stream,
+                                  uint32_t step = kOperandImage);
 
 // Rounds of tiles that decoding them takes on that many SMs.
 uint32_t operand_decode_rounds(uint32_t tiles, uint32_t ctas);
@@ -96,10 +99,19 @@ struct XentEpilogue {
   uint32_t n0, vocab;
 };
 
+// A second layer of the same shape in a transposed product, whose sum runs over
+// both: out[m][k] = sum_n G[m][n] W[n][k] + G2[m][n] W2[n][k].  (The plan is made
+// for twice a layer's rows.)  step: bytes from an image to a layer's next.
+struct OperandPair {
+  const uint8_t* images;
+  const void* rows16;
+  uint32_t step;
+};
+
 // Exactly one of out (transposed) and xent (logits) is given.
 cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* images, const void* rows16,
                                 const OperandGemmOut* out, const XentEpilogue* xent, void* ws, uint32_t* status,
-                                cudaStream_t stream);
+                                cudaStream_t stream, const OperandPair* pair = nullptr);
 
 cudaError_t set_live_wait_budget_operand(long long cycles);
 cudaError_t set_live_wait_budget_operand_gemm(long long cycles);

@@ -62,6 +62,8 @@ struct OperandGemmDev {
   const uint8_t* images;
   CUtensorMap tmap_b;  // tokens: 64 x b_box_rows boxes, 128-byte swizzle
   CUtensorMap tmap_a;  // transposed: images as rows of 512 eight-byte words, boxes of 256 x 8
+  CUtensorMap tmap_b2, tmap_a2;  // transposed: the second layer's, from stage half_kb on
+  uint32_t half_kb;
   OperandGemmOut out;
   XentEpilogue xent;
   uint32_t f16;
@@ -237,20 +239,23 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
           }
           const uint32_t bar = smem_u32(&full[s]);
           const uint32_t a_s = smem_s + s * P.stage_bytes, b_s = a_s + kOgABytes;
+          const bool second = kTrans && kb >= P.half_kb;
+          const uint32_t kl = second ? kb - P.half_kb : kb;
           if (kTrans) {
             // half of each of eight images in one box.  Where the last block
             // of k holds fewer, the box runs into the next row block's (or, at
             // the end, is filled with zeros): rows of D that are never stored.
             mbar_arrive_expect_tx_s(bar, kOgABytes + P.b_box_rows * kOgBK * 2);
-            tma_load_2d_s(a_s, &P.tmap_a, static_cast<int32_t>((kb & 1u) * 256u),
-                          static_cast<int32_t>((kb >> 1) * P.k_slabs + 8 * ab), bar);
+            tma_load_2d_s(a_s, second ? &P.tmap_a2 : &P.tmap_a, static_cast<int32_t>((kl & 1u) * 256u),
+                          static_cast<int32_t>((kl >> 1) * P.k_slabs + 8 * ab), bar);
           } else {
             const uint32_t cnt = min(4u, P.k_slabs - 4 * kb);
             mbar_arrive_expect_tx_s(bar, cnt * kSlabBytes + P.b_box_rows * kOgBK * 2);
             bulk_g2s_s(a_s, P.images + (static_cast<uint64_t>(ab) * P.k_slabs + 4 * kb) * kSlabBytes,
                        cnt * kSlabBytes, bar);
           }
-          tma_load_2d_s(b_s, &P.tmap_b, static_cast<int32_t>(kb * kOgBK), static_cast<int32_t>(mb * P.bn), bar);
+          tma_load_2d_s(b_s, second ? &P.tmap_b2 : &P.tmap_b, static_cast<int32_t>(kl * kOgBK),
+                        static_cast<int32_t>(mb * P.bn), bar);
           if (++s == n_st) {
             s = 0;
             ph ^= 1u;
@@ -514,7 +519,7 @@ size_t operand_gemm_workspace(const OperandGemmPlan& p) {
 
 cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* images, const void* rows16,
                                 const OperandGemmOut* out, const XentEpilogue* xent, void* ws, uint32_t* status,
-                                cudaStream_t stream) {
+                                cudaStream_t stream, const OperandPair* pair) {
   if (plan.M == 0) return cudaSuccess;
   OperandGemmDev P;
   std::memset(&P, 0, sizeof(P));
@@ -540,15 +545,23 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
   // bit 15: A is MN-major
   P.idesc = idesc_f16(plan.f16 ? 0u : 1u, 128, plan.bn) | (plan.trans ? 1u << 15 : 0u);
   P.idesc_tail = idesc_f16(plan.f16 ? 0u : 1u, 128, (tail + 15) / 16 * 16) | (plan.trans ? 1u << 15 : 0u);
-  cudaError_t e = encode_tmap(&P.tmap_b, CU_TENSOR_MAP_DATA_TYPE_UINT16, rows16, red, plan.M,
-                              static_cast<uint64_t>(red) * 2, kOgBK, P.b_box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  // rows of one layer, and the stage that the second's start at
+  const uint32_t rows = pair ? plan.rows / 2 : plan.rows, inner = plan.trans ? rows : plan.K;
+  P.half_kb = pair ? rows / kOgBK : P.n_kb;
+  auto tokens = [&](CUtensorMap* map, const void* base) {
+    return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, base, inner, plan.M, static_cast<uint64_t>(inner) * 2, kOgBK,
+                       P.b_box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  auto weights = [&](CUtensorMap* map, const uint8_t* base) {
+    return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, base, kSlabBytes / 8,
+                       static_cast<uint64_t>(rows / 128) * P.k_slabs, pair ? pair->step : kSlabBytes, 256, 8,
+                       CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  cudaError_t e = tokens(&P.tmap_b, rows16);
+  if (e == cudaSuccess && plan.trans) e = weights(&P.tmap_a, images);
+  if (e == cudaSuccess && pair) e = tokens(&P.tmap_b2, pair->rows16);
+  if (e == cudaSuccess && pair) e = weights(&P.tmap_a2, pair->images);
   if (e != cudaSuccess) return e;
-  if (plan.trans) {
-    const uint64_t images_n = static_cast<uint64_t>(plan.rows / 128) * P.k_slabs;
-    e = encode_tmap(&P.tmap_a, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, images, kSlabBytes / 8, images_n, kSlabBytes, 256, 8,
-                    CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e != cudaSuccess) return e;
-  }
   auto kern = plan.trans ? operand_gemm_kernel<true> : operand_gemm_kernel<false>;
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;

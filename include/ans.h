@@ -539,6 +539,43 @@ ans_status ans_gated_grad(const uint16_t* d_X, const uint16_t* d_dH, uint32_t M,
                           ans_act act, uint16_t* d_dX, uint16_t* d_dG, uint16_t* d_dU, void* d_ws,
                           size_t ws_bytes, uint32_t* d_status, ans_stream_t stream);
 
+/* ---- Distillation ----------------------------------------------------------- */
+
+/* Bytes of device workspace of ans_distill; with_grad: 1 for calls with d_dX (the
+ * whole decoded vocabulary, 2 N K bytes, and 2 N bytes a token for up to 4096 tokens
+ * at a time). */
+ans_status ans_distill_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind,
+                                 uint32_t n_top, int with_grad, size_t* bytes);
+
+/* The loss of a student's compressed vocabulary head W (N x K, of which `vocab` rows
+ * count, as for ans_xent) against a teacher's top logits: the Kullback-Leibler
+ * divergence over what the teacher lists.  Each token lists up to n_top (1 to 256)
+ * rows n_j with the teacher's logits v_j: d_ids int32 and d_logits fp32, both
+ * [M][n_top], in any order; a negative index lists nothing.  With 1 / T =
+ * inverse_temperature (2^-40 to 2^40; ANS_ERR_ARG otherwise):
+ *   z[m][n] = sum_k X[m][k] w(n, k) / T,   lse[m] = log sum_{n < vocab} exp z[m][n],
+ *   log p_n = z[m][n] - lse[m],   log t_j = v_j / T - (the teacher's lse),
+ *   loss[m] = sum_j t_j (log t_j - log p_{n_j})
+ *   dX[m] = g[m] / T sum_n (S p_n - t_n) w(n),   S = sum_j t_j, t_n what is listed of n
+ * The teacher's lse is d_teacher_lse[m] (fp32: of all its logits / T, so that S is the
+ * part of its mass that is listed), or, where that is NULL, the listed logits' own
+ * (S = 1).  A row that is listed more than once has the sum of its shares.
+ * X bf16 M x K; loss and lse fp32 [M]; dX bf16 M x K (NULL: loss only), the gradient
+ * of sum_m g[m] loss[m] with g = d_weight fp32 [M] (NULL: 1; read with d_dX only); it
+ * is not times T^2.  A token that lists nothing has loss 0 and a zero dX; its lse is
+ * written.  An entry whose t_j is 0 (v_j = -infinity) has no part in the loss.  A
+ * token whose lse is not finite has NaN in dX, if it lists anything.  An index of
+ * vocab or more sets ANS_STATUS_BAD_INDEX and lists nothing.  Probabilities and
+ * listed coefficients S p - t (taken in 64 bits) are rounded once, to 16 bits, as
+ * ans_xent's probabilities are; t, S, lse and the loss are summed in 64 bits.
+ * M == 0 is a no-op. */
+ans_status ans_distill(const uint16_t* d_X, uint32_t M, const ans_tiles* W,
+                       ans_scale_kind scale_kind, const void* d_scales, uint32_t group_k,
+                       uint32_t vocab, float inverse_temperature, uint32_t n_top,
+                       const int32_t* d_ids, const float* d_logits, const float* d_teacher_lse,
+                       float* d_loss, float* d_lse, const float* d_weight, uint16_t* d_dX,
+                       void* d_ws, size_t ws_bytes, uint32_t* d_status, ans_stream_t stream);
+
 /* ---- Drafted tokens --------------------------------------------------------- */
 
 /* Bytes of device workspace of ans_verify. */

@@ -35,7 +35,7 @@ EXPORTS = ["ans_status_string", "ans_last_error", "ans_num_tiles", "ans_layout_c
            "ans_gemm_batched", "ans_gemm_lora_workspace", "ans_gemm_lora", "ans_gemm_grad_workspace",
            "ans_gemm_grad", "ans_gemm_lora_grad_workspace", "ans_gemm_lora_grad", "ans_xent_workspace",
            "ans_xent", "ans_gated_workspace", "ans_gated", "ans_gated_grad_workspace", "ans_gated_grad",
-           "ans_verify_workspace", "ans_verify", "ans_container_write", "ans_container_read"]
+           "ans_distill_workspace", "ans_distill", "ans_verify_workspace", "ans_verify", "ans_container_write", "ans_container_read"]
 MAX_BATCH = 8
 
 
@@ -130,6 +130,8 @@ def load():
             L.ans_gated.argtypes = [P, u32, P, P, i32, P, P, u32, i32, P, P, sz, P, P]
             L.ans_gated_grad_workspace.argtypes = [P, u32, i32, P]
             L.ans_gated_grad.argtypes = [P, P, u32, P, P, i32, P, P, u32, i32, P, P, P, P, sz, P, P]
+            L.ans_distill_workspace.argtypes = [P, u32, i32, u32, i32, P]
+            L.ans_distill.argtypes = [P, u32, P, i32, P, u32, u32, C.c_float, u32, P, P, P, P, P, P, P, P, sz, P, P]
             L.ans_verify_workspace.argtypes = [u32, u32, u32, P]
             L.ans_verify.argtypes = [P, u64, P, u64, u32, u32, u32, P, P, P, P, P, P, P, P, sz, P, P]
             L.ans_container_write.argtypes = [P, P, u64, P]
@@ -470,6 +472,26 @@ def ans_gated_grad(d_X, d_dH, M: int, gate: AnsTiles, up: AnsTiles, scale_kind: 
                                  _ptr(d_gate_scales), _ptr(d_up_scales), group_k, act, _ptr(d_dX), _ptr(d_dG),
                                  _ptr(d_dU), _ptr(d_ws), ws_bytes, _ptr(d_status), _stream(stream)),
            "ans_gated_grad")
+
+
+def ans_distill_workspace(layout: AnsLayout, M: int, scale_kind: int, n_top: int, with_grad: bool = False) -> int:
+    out = C.c_size_t(0)
+    _check(load().ans_distill_workspace(C.byref(layout), M, scale_kind, n_top, 1 if with_grad else 0,
+                                        C.byref(out)),
+           "ans_distill_workspace")
+    return out.value
+
+
+def ans_distill(d_X, M: int, tiles: AnsTiles, scale_kind: int, d_scales, group_k: int, vocab: int,
+                inverse_temperature: float, n_top: int, d_ids, d_logits, d_teacher_lse, d_loss, d_lse, d_weight,
+                d_dX, d_ws, ws_bytes: int, d_status, stream=None):
+    """Divergence of a compressed vocabulary head from a teacher's top logits (d_ids int32 and d_logits fp32,
+    [M][n_top]); d_dX (bf16) with the gradient of sum(d_weight * loss), or None for the loss alone."""
+    _check(load().ans_distill(_ptr(d_X), M, C.byref(tiles), scale_kind, _ptr(d_scales), group_k, vocab,
+                              inverse_temperature, n_top, _ptr(d_ids), _ptr(d_logits), _ptr(d_teacher_lse),
+                              _ptr(d_loss), _ptr(d_lse), _ptr(d_weight), _ptr(d_dX), _ptr(d_ws), ws_bytes,
+                              _ptr(d_status), _stream(stream)),
+           "ans_distill")
 
 
 def ans_verify_workspace(n_seqs: int, n_drafted: int, vocab: int) -> int:

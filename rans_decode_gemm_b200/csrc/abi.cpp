@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "../../include/ans.h"
+#include "cuda/distill.h"
 #include "cuda/gated.h"
 #include "cuda/kernels.h"
 #include "cuda/lora.h"
@@ -1285,6 +1286,68 @@ ans_status ans_gated_grad(const uint16_t* d_X, const uint16_t* d_dH, uint32_t M,
                             static_cast<uint32_t>(act), nullptr, d_dH, d_dX, d_dG, d_dU, d_status};
   cudaError_t e = ansdev::launch_gated(c.images, Lg, Lu, a, d_ws, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_gated_grad");
+}
+
+}  // extern "C"
+
+// ---- distillation ----------------------------------------------------------------
+extern "C" {
+
+ans_status ans_distill_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind, uint32_t n_top,
+                                 int with_grad, size_t* bytes) {
+  if (!bytes) return ANS_ERR_ARG;
+  ans_status st = check_layout(layout);
+  if (st != ANS_OK) return st;
+  st = check_scale_kind(*layout, scale_kind);
+  if (st != ANS_OK) return st;
+  if (n_top == 0) return ANS_ERR_SHAPE;
+  if (M > kMaxTokens || n_top > ansdev::kDistillMaxTop) return ANS_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (M == 0) return ANS_OK;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ansdev::LayerDev L;
+  fill_layer_plain(layout, &L);
+  ansdev::DistillPlan p;
+  ansdev::make_distill_plan(L, M, n_top, with_grad != 0, sms, &p);
+  *bytes = p.bytes;
+  return ANS_OK;
+}
+
+ans_status ans_distill(const uint16_t* d_X, uint32_t M, const ans_tiles* W, ans_scale_kind scale_kind,
+                       const void* d_scales, uint32_t group_k, uint32_t vocab, float inverse_temperature,
+                       uint32_t n_top, const int32_t* d_ids, const float* d_logits, const float* d_teacher_lse,
+                       float* d_loss, float* d_lse, const float* d_weight, uint16_t* d_dX, void* d_ws,
+                       size_t ws_bytes, uint32_t* d_status, ans_stream_t stream) {
+  ans_status st = check_gemm_tiles(W, scale_kind, d_scales, group_k);
+  if (st != ANS_OK) return st;
+  if (vocab == 0 || vocab > W->layout.N || n_top == 0) return ANS_ERR_SHAPE;
+  if (n_top > ansdev::kDistillMaxTop) return ANS_ERR_UNSUPPORTED;
+  // (2^-40 to 2^40: its products with fp32 sums and logits stay within fp32)
+  if (!(inverse_temperature >= 0x1p-40f && inverse_temperature <= 0x1p40f)) return ANS_ERR_ARG;
+  if (M == 0) return ANS_OK;
+  if (M > kMaxTokens) return ANS_ERR_UNSUPPORTED;
+  if (!d_X || !d_ids || !d_logits || !d_loss || !d_lse || !d_status || misaligned16(d_X) || misaligned16(d_dX) ||
+      misaligned16(d_scales))
+    return ANS_ERR_ARG;
+  for (const void* p : {static_cast<const void*>(d_ids), static_cast<const void*>(d_logits),
+                        static_cast<const void*>(d_teacher_lse), static_cast<const void*>(d_loss),
+                        static_cast<const void*>(d_lse), static_cast<const void*>(d_weight)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return ANS_ERR_ARG;
+  if (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0) return ANS_ERR_ARG;
+  int sms = 0;
+  st = device_info(&sms);
+  if (st != ANS_OK) return st;
+  ansdev::LayerDev L;
+  fill_layer(W, &L);
+  ansdev::DistillPlan plan;
+  ansdev::make_distill_plan(L, M, n_top, d_dX != nullptr, sms, &plan);
+  if (ws_bytes < plan.bytes) return ANS_ERR_BUFFER_TOO_SMALL;
+  const ansdev::DistillArgs a{d_X, static_cast<uint32_t>(scale_kind), d_scales, group_k, vocab, inverse_temperature,
+                              d_ids, d_logits, d_teacher_lse, d_loss, d_lse, d_weight, d_dX, d_status};
+  cudaError_t e = ansdev::launch_distill(plan, L, a, d_ws, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ANS_OK : cuda_fail(e, "ans_distill");
 }
 
 }  // extern "C"

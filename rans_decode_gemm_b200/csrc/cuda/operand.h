@@ -97,6 +97,17 @@ struct XentEpilogue {
   uint32_t stride;
   uint16_t* probs;
   uint32_t n0, vocab;
+  // Lists in place of targets (listed given, targets and zt not): per token up to
+  // `top` rows of W, ascending (-1: none), whose logits go to z_listed, in the same
+  // places.  listed: bit b % 32 of word [(b / 32) * listed_stride + m] is set where
+  // block b of 32 rows (of the whole vocabulary) holds rows of token m's list.  Logits
+  // are times per_t (probs are not).
+  // probs then have probs_ld columns.
+  const uint32_t* listed;
+  uint32_t listed_stride, top, probs_ld;
+  const int32_t* ids;
+  float* z_listed;
+  float per_t;
 };
 
 // A second layer of the same shape in a transposed product, whose sum runs over

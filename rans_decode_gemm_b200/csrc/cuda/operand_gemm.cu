@@ -98,15 +98,23 @@ __device__ __forceinline__ float across_lanes(float (&x)[32], uint32_t lane, Op 
 // m + lane's reference, target and factor come in tok.
 struct XentToken {
   float ref, factor;
-  int32_t target;
+  int32_t target;  // (lists: 0 where this block holds rows of the token's, else -1)
 };
-__device__ __forceinline__ XentToken xent_token(const XentEpilogue& E, uint32_t m, bool in) {
+template <bool kLists>
+__device__ __forceinline__ XentToken xent_token(const XentEpilogue& E, uint32_t c, uint32_t m, bool in) {
   XentToken t;
   t.ref = in ? __ldcg(E.ref_in + m) : 0.0f;
-  t.target = in ? __ldg(E.targets + m) : -1;
+  if constexpr (kLists) {
+    const uint32_t b = (E.n0 + c) / 32;
+    const uint32_t word = in ? __ldcg(E.listed + static_cast<uint64_t>(b / 32) * E.listed_stride + m) : 0u;
+    t.target = (word >> (b % 32)) & 1u ? 0 : -1;
+  } else {
+    t.target = in ? __ldg(E.targets + m) : -1;
+  }
   t.factor = E.factor != nullptr && in ? __ldcg(E.factor + m) : 1.0f;
   return t;
 }
+template <bool kLists>
 __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, uint32_t rows, const uint32_t (&v)[32],
                                           float scale, float lift, uint32_t c, uint32_t m, uint32_t n_tok,
                                           uint32_t lane, const XentToken& tok) {
@@ -115,29 +123,57 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
   const float ref_in = tok.ref, factor = tok.factor;
   const int32_t target = tok.target;
   const bool n_in = E.n0 + c < E.vocab;
+  const float z_scale = kLists ? scale * E.per_t : scale;
   float z[32], x[32];
 #pragma unroll
   for (uint32_t j = 0; j < 32; ++j) {
-    z[j] = __uint_as_float(v[j]) * scale;
+    z[j] = __uint_as_float(v[j]) * z_scale;
     if (E.factor != nullptr) z[j] *= __shfl_sync(0xFFFFFFFFu, factor, j);
     if (!n_in) z[j] = -INFINITY;
   }
   // targets among this warp's rows (one that is past the vocabulary is none): few
   // and far between, so that the loops above and below carry no test for them
   const uint32_t first = E.n0 + c - lane;
-  const bool hit = target >= 0 && static_cast<uint32_t>(target) < E.vocab && static_cast<uint32_t>(target) - first < 32u;
-  for (uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit); hits != 0; hits &= hits - 1) {
-    const uint32_t k = __ffs(hits) - 1;
-    if (lane == static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, target, k)) - first) {
+  if constexpr (kLists) {
+    for (uint32_t hits = __ballot_sync(0xFFFFFFFFu, target >= 0); hits != 0; hits &= hits - 1) {
+      const uint32_t k = __ffs(hits) - 1;
+      float zk = 0.0f;
 #pragma unroll
-      for (uint32_t j = 0; j < 32; ++j) {
-        if (j == k) {
-          E.zt[m + j] = z[j];
-          z[j] = -INFINITY;
+      for (uint32_t j = 0; j < 32; ++j)
+        if (j == k) zk = z[j];
+      // the list, 32 entries at a time; those of this block take their row's logit
+      uint32_t mine = 0;
+      const uint64_t at = static_cast<uint64_t>(m + k) * E.top;
+      for (uint32_t q = 0; q < E.top; q += 32) {
+        const uint32_t row = q + lane < E.top ? static_cast<uint32_t>(__ldcg(E.ids + at + q + lane)) - first : 32u;
+        const float zr = __shfl_sync(0xFFFFFFFFu, zk, row & 31u);
+        if (row < 32u) {
+          E.z_listed[at + q + lane] = zr;
+          mine |= 1u << row;
         }
       }
+      mine = __reduce_or_sync(0xFFFFFFFFu, mine);
+      if ((mine >> lane) & 1u) {
+#pragma unroll
+        for (uint32_t j = 0; j < 32; ++j)
+          if (j == k) z[j] = -INFINITY;
+      }
     }
-    __syncwarp();
+  } else {
+    const bool hit = target >= 0 && static_cast<uint32_t>(target) < E.vocab && static_cast<uint32_t>(target) - first < 32u;
+    for (uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit); hits != 0; hits &= hits - 1) {
+      const uint32_t k = __ffs(hits) - 1;
+      if (lane == static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, target, k)) - first) {
+#pragma unroll
+        for (uint32_t j = 0; j < 32; ++j) {
+          if (j == k) {
+            E.zt[m + j] = z[j];
+            z[j] = -INFINITY;
+          }
+        }
+      }
+      __syncwarp();
+    }
   }
 #pragma unroll
   for (uint32_t j = 0; j < 32; ++j) x[j] = z[j];
@@ -152,11 +188,12 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
   }
   const float ps = n_in ? scale * lift : 0.0f;  // (a padding row's scale may be anything)
   if (E.probs != nullptr) {
-    uint16_t* p = E.probs + static_cast<uint64_t>(m) * rows + c;
+    const uint32_t ld = kLists ? E.probs_ld : rows;
+    uint16_t* p = E.probs + static_cast<uint64_t>(m) * ld + c;
     auto store = [&](uint32_t j) {
       const float q = x[j] * ps;
       *p = f16 ? __half_as_ushort(__float2half_rn(q)) : __bfloat16_as_ushort(__float2bfloat16_rn(q));
-      p += rows;
+      p += ld;
     };
     if (n_tok == 32) {
 #pragma unroll
@@ -171,7 +208,8 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
   if (m_in) E.blocks[static_cast<uint64_t>(c / 32) * E.stride + m + lane] = make_float2(ref, sum);
 }
 
-template <bool kTrans>
+// kLists: logits with lists in place of targets.
+template <bool kTrans, bool kLists = false>
 __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __grid_constant__ OperandGemmDev P) {
   extern __shared__ __align__(1024) uint8_t dsmem_raw[];
   __shared__ __align__(8) uint64_t full[kOgMaxStages], empty[kOgMaxStages];
@@ -349,7 +387,7 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
         const uint32_t m = m0 + c0 + lane;
         const bool m_in = c0 + lane < cols;
         if constexpr (!kTrans) {
-          tok = xent_token(P.xent, m, m_in);
+          tok = xent_token<kLists>(P.xent, c, m, m_in);
           return;
         }
         if (rmw) my_alpha = m_in ? __ldcg(O.alpha + m) : 0.0f;
@@ -386,7 +424,7 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
         if constexpr (!kTrans) {
           const XentToken now = tok;
           if (c0 + 64 < cols) ask(c0 + 64);
-          xent_fold(P.xent, P.f16, P.out_cols, v, scale, lift, c, m0 + c0, min(32u, cols - c0), lane, now);
+          xent_fold<kLists>(P.xent, P.f16, P.out_cols, v, scale, lift, c, m0 + c0, min(32u, cols - c0), lane, now);
         } else if (cut) {
           const uint64_t at = static_cast<uint64_t>(ab * P.m_blocks + mb) * P.splits + sp;
           float* part = P.parts + (at * P.bn + c0) * kOgBM + 32 * quad + lane;
@@ -562,7 +600,8 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
   if (e == cudaSuccess && pair) e = tokens(&P.tmap_b2, pair->rows16);
   if (e == cudaSuccess && pair) e = weights(&P.tmap_a2, pair->images);
   if (e != cudaSuccess) return e;
-  auto kern = plan.trans ? operand_gemm_kernel<true> : operand_gemm_kernel<false>;
+  auto kern = plan.trans ? operand_gemm_kernel<true>
+              : P.xent.listed != nullptr ? operand_gemm_kernel<false, true> : operand_gemm_kernel<false>;
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   e = cudaGetDevice(&dev);
@@ -571,6 +610,8 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
     e = cudaFuncSetAttribute(operand_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(operand_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(operand_gemm_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }

@@ -47,12 +47,6 @@ namespace ansdev {
 constexpr uint32_t kXentThreads = 256;
 constexpr float kLn2 = 0.69314718055994531f, kLog2E = 1.4426950408889634f;
 
-// Running state of M rows: reference r, sum l of the others, target logit,
-// and this piece's factors of the gradient's sum.  lift: one value.
-struct XentState {
-  float *ref, *sum, *zt, *alpha, *beta, *lift;
-};
-
 // 2^e for a whole e; 0 below the normal range.
 __device__ __forceinline__ float pow2(float e) {
   return e < -126.0f ? 0.0f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(fminf(e, 127.0f)) + 127) << 23);
@@ -105,20 +99,6 @@ __global__ void __launch_bounds__(1024) xent_begin_kernel(XentState st, uint32_t
   }
   griddep_beside_end();
 }
-
-struct XentJoin {
-  XentState st;
-  const float2* blocks;    // (reference, sum): [n_blocks][stride], tokens m0 .. m0 + m - 1 from column 0
-  uint32_t stride, n_blocks, m0, m, rows, f16;
-  uint32_t beside;         // runs beside the next piece's decoding
-  uint32_t* moved;         // one bit a token, in order: has blocks under another reference
-  uint16_t* probs;         // m x rows, or null
-  // the targets' rows of W
-  const int32_t* targets;
-  const uint8_t* images;
-  uint16_t* target_rows;   // M x K in operand form
-  uint32_t n0, vocab, K;
-};
 
 // kTok tokens a CTA (32, or 8 where there are few), one a lane of each of a warp's
 // 32 / kTok shares; the shares of all warps take the blocks in turn, 8 loads in
@@ -261,8 +241,11 @@ __global__ void __launch_bounds__(256) xent_piece_kernel(const __grid_constant__
   }
 }
 
-// Zeros in the images of rows [first, rows): padding behind the vocabulary, whose
-// probabilities are 0, and 0 times an infinity or a NaN is not.
+cudaError_t launch_xent_join(const XentJoin& j, cudaStream_t stream) {
+  return j.m <= 128 ? launch_pdl(xent_join_kernel<8>, dim3((j.m + 7) / 8), dim3(32 * kJoinWarps), 0, stream, j)
+                    : launch_pdl(xent_join_kernel<32>, dim3((j.m + 31) / 32), dim3(32 * kJoinWarps), 0, stream, j);
+}
+
 __global__ void __launch_bounds__(256) xent_blank_kernel(uint8_t* images, uint32_t first, uint32_t rows, uint32_t k_slabs) {
   griddep_wait();
   griddep_launch_dependents();
@@ -273,6 +256,12 @@ __global__ void __launch_bounds__(256) xent_blank_kernel(uint8_t* images, uint32
     *reinterpret_cast<uint4*>(images + ((row >> 7) * static_cast<uint64_t>(k_slabs) + slab) * kSlabBytes + (row & 127u) * 32u +
                               16 * (i & 1)) = make_uint4(0, 0, 0, 0);
   }
+}
+
+cudaError_t launch_xent_blank(uint8_t* images, uint32_t first, uint32_t rows, uint32_t K, cudaStream_t stream) {
+  const uint64_t items = static_cast<uint64_t>(rows - first) * (K / 8);
+  return launch_pdl(xent_blank_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((items + 255) / 256, 1024))), dim3(256), 0,
+                    stream, images, first, rows, K / 16);
 }
 
 struct XentFinish {
@@ -441,10 +430,6 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
   float* x_factor = reinterpret_cast<float*>(w + p.off_factor);
   const uint16_t* x = p.f16 ? x16 : a.X;
   const float* factor = p.f16 ? x_factor : nullptr;
-  auto launch_join = [&](const XentJoin& j) {
-    return j.m <= 128 ? launch_pdl(xent_join_kernel<8>, dim3((j.m + 7) / 8), dim3(32 * kJoinWarps), 0, stream, j)
-                      : launch_pdl(xent_join_kernel<32>, dim3((j.m + 31) / 32), dim3(32 * kJoinWarps), 0, stream, j);
-  };
   XentJoin j;
   bool pending = false;  // j is still to be joined
   cudaError_t e;
@@ -453,10 +438,7 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
     e = launch_operand_decode(L, n0, rows, a.scale_kind, a.scales, a.group_k, images, a.status, p.sms, stream);
     if (e != cudaSuccess) return e;
     if (p.grad && n0 + rows > a.vocab) {
-      const uint32_t first = a.vocab - n0;
-      const uint64_t items = static_cast<uint64_t>(rows - first) * (p.K / 8);
-      e = launch_pdl(xent_blank_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((items + 255) / 256, 1024))), dim3(256), 0,
-                     stream, images, first, rows, p.K / 16);
+      e = launch_xent_blank(images, a.vocab - n0, rows, p.K, stream);
       if (e != cudaSuccess) return e;
     }
     if (n0 == 0) {
@@ -467,13 +449,13 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
     }
     if (pending) {
       j.beside = 1;
-      e = launch_join(j);
+      e = launch_xent_join(j, stream);
       if (e != cudaSuccess) return e;
       pending = false;
     }
     for (uint32_t m0 = 0; m0 < p.M; m0 += p.chunk) {
       const uint32_t m = std::min(p.chunk, p.M - m0);
-      XentEpilogue f;
+      XentEpilogue f = {};
       f.factor = factor ? factor + m0 : nullptr;
       f.scale_kind = a.scale_kind;
       f.scales = a.scale_kind == 1 ? static_cast<const void*>(static_cast<const uint16_t*>(a.scales) + n0)
@@ -512,7 +494,7 @@ cudaError_t launch_xent(const XentPlan& p, const LayerDev& L, const XentArgs& a,
       // piece's decoding
       pending = !p.grad && m0 + m == p.M && n0 + p.piece < a.vocab;
       if (pending) break;
-      e = launch_join(j);
+      e = launch_xent_join(j, stream);
       if (e != cudaSuccess) return e;
       if (!p.grad) continue;
       // as many CTAs a group as its blocks take, or as the copies of rows can use

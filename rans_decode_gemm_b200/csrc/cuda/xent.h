@@ -34,6 +34,32 @@ struct XentArgs {
   uint32_t* status;
 };
 
+// Running state of M rows: reference r (units of log 2), sum l of the others, target
+// logit, and this piece's factors of the gradient's sum.  lift: one value.
+struct XentState {
+  float *ref, *sum, *zt, *alpha, *beta, *lift;
+};
+
+// A piece's blocks joined into the state of tokens m0 .. m0 + m - 1.
+struct XentJoin {
+  XentState st;
+  const float2* blocks;    // (reference, sum): [n_blocks][stride], tokens m0 .. m0 + m - 1 from column 0
+  uint32_t stride, n_blocks, m0, m, rows, f16;
+  uint32_t beside;         // runs beside the next piece's decoding
+  uint32_t* moved;         // one bit a token, in order: has blocks under another reference
+  uint16_t* probs;         // m x rows, or null
+  // the targets' rows of W
+  const int32_t* targets;
+  const uint8_t* images;
+  uint16_t* target_rows;   // M x K in operand form
+  uint32_t n0, vocab, K;
+};
+cudaError_t launch_xent_join(const XentJoin& j, cudaStream_t stream);
+
+// Zeros in the images of rows [first, rows): padding behind the vocabulary, whose
+// probabilities are 0, and 0 times an infinity or a NaN is not.
+cudaError_t launch_xent_blank(uint8_t* images, uint32_t first, uint32_t rows, uint32_t K, cudaStream_t stream);
+
 void make_xent_plan(const LayerDev& L, uint32_t M, bool grad, int sms, XentPlan* plan);
 cudaError_t launch_xent(const XentPlan& plan, const LayerDev& L, const XentArgs& a, void* ws, cudaStream_t stream);
 

@@ -72,6 +72,46 @@ __device__ __forceinline__ double distance(double z, double c, double ref) {
   return __dsub_rn(__dmul_rn(z, c), ref);
 }
 
+// The same for logits up to 500 above a reference of no more than 2^30 (those that lie
+// more than 900 below count as there), in nine instructions of 64 bits and six others
+// in place of eleven and sixteen: one fused product rounds z c - ref to sixteenths, a
+// second has what is left of it, and the table holds its high words less the index that
+// comes with the exponent (in `whole`, which the caller adds to the exponent's bits).
+constexpr double kSixteenth = 422212465065984.0;  // 1.5 * 2^48
+struct Near {
+  double c, from, back;  // log2(e) / T;  kSixteenth - ref;  -from
+  float low, high;       // the logits of distance -900 and 500, to 2^-24 of themselves
+};
+__device__ __forceinline__ Near near_of(double c, double ref) {
+  Near r;
+  r.c = c;
+  r.from = kSixteenth - ref;
+  r.back = -r.from;
+  r.low = static_cast<float>((ref - 900.0) / c);
+  r.high = static_cast<float>((ref + 500.0) / c);
+  return r;
+}
+__device__ __forceinline__ bool is_near(double ref) { return fabs(ref) <= 1073741824.0; }
+__device__ __forceinline__ void near_parts(float z, const Near& r, const double* table, double& value, double& scale) {
+  const double x = fmaxf(z, r.low);
+  const double a = fma(x, r.c, r.from);
+  const int q = __double2loint(a);
+  const double f = fma(x, r.c, -(a + r.back));
+  value = fma(f, 0.0013333558146428441, 0.009618129107628477);
+  value = fma(value, f, 0.055504108664821576);
+  value = fma(value, f, 0.2402265069591007);
+  value = fma(value, f, 0.6931471805599453);
+  value = fma(value, f, 1.0);
+  const double s = table[q & 15];
+  scale = __hiloint2double(__double2hiint(s) + (q << 16), __double2loint(s));
+}
+
+__device__ __forceinline__ void fill_tables(uint32_t i, double* sixteenths, double* near_table) {
+  const double s = g_sixteenths[i];
+  sixteenths[i] = s;
+  near_table[i] = __hiloint2double(__double2hiint(s) - static_cast<int>(i << 16), __double2loint(s));
+}
+
 // log2(e) / T; 0 for a greedy sequence.  (T from 1e30 on leaves all finite logits alike already.)
 __device__ __forceinline__ double per_temperature(const float* temperature, uint32_t b) {
   const float t = temperature == nullptr ? 1.0f : __ldg(temperature + b);
@@ -102,11 +142,11 @@ struct VerifyDev {
 
 // One part of one row.
 __global__ void __launch_bounds__(kVerifyThreads) verify_sums_kernel(const __grid_constant__ VerifyDev P) {
-  __shared__ double sixteenths[16];
+  __shared__ double sixteenths[16], near_table[16];
   __shared__ double part_ref[kVerifyWarps], part_sum[kVerifyWarps];
   const VerifyArgs& A = P.a;
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  if (threadIdx.x < 16) sixteenths[threadIdx.x] = g_sixteenths[threadIdx.x];
+  if (threadIdx.x < 16) fill_tables(threadIdx.x, sixteenths, near_table);
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t row = blockIdx.x / P.n_chunks, part = blockIdx.x - row * P.n_chunks;
@@ -126,41 +166,40 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_sums_kernel(const __gri
   const uint32_t g0 = part * (P.chunk / 4), g1 = part + 1 == P.n_chunks ? groups : min(groups, g0 + P.chunk / 4);
   const float* base = z - off;
   constexpr uint32_t kDeep = 4;
-  bool bad = false;
+  bool bad = false, near = false;
   double ref = kNoRef, sum = 0.0;
+  Near at_ref = {};
+  at_ref.high = -INFINITY;
   float best = -INFINITY;
   uint32_t best_at = 0xFFFFFFFFu;
+  // groups that lie within the row; the first and the last may not
+  const uint32_t in0 = off == 0 ? 0u : 1u, in1 = (A.vocab + off) / 4;
   for (uint32_t g = g0 + threadIdx.x; g < g1; g += kDeep * kVerifyThreads) {
     float x[4 * kDeep];
+    if (g >= in0 && g + (kDeep - 1) * kVerifyThreads < min(g1, in1)) {
 #pragma unroll
-    for (uint32_t k = 0; k < kDeep; ++k) {
-      const uint32_t at = g + k * kVerifyThreads;
-      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (at < g1) {
-        const uint32_t n = 4 * at - off;  // (wraps below 0 in the first group)
-        if (n < A.vocab && n + 3 < A.vocab) {
-          q = __ldcs(reinterpret_cast<const float4*>(base + 4ull * at));
-        } else {
-          // (places in 32 bits throughout: the sum has wrapped back before it meets the pointer)
-          const uint32_t n1 = n + 1, n2 = n + 2, n3 = n + 3;
-          if (n < A.vocab) q.x = __ldg(z + n);
-          if (n1 < A.vocab) q.y = __ldg(z + n1);
-          if (n2 < A.vocab) q.z = __ldg(z + n2);
-          if (n3 < A.vocab) q.w = __ldg(z + n3);
-        }
+      for (uint32_t k = 0; k < kDeep; ++k) {
+        const float4 q = __ldcs(reinterpret_cast<const float4*>(base + 4ull * g) + k * kVerifyThreads);
+        x[4 * k] = q.x;
+        x[4 * k + 1] = q.y;
+        x[4 * k + 2] = q.z;
+        x[4 * k + 3] = q.w;
       }
-      x[4 * k] = q.x;
-      x[4 * k + 1] = q.y;
-      x[4 * k + 2] = q.z;
-      x[4 * k + 3] = q.w;
-    }
-    float top = x[0];
+    } else {
 #pragma unroll
-    for (uint32_t k = 0; k < 4 * kDeep; ++k) {
-      bad = bad || !(x[k] <= 3.402823466e38f);
-      top = fmaxf(top, x[k]);
+      for (uint32_t k = 0; k < 4 * kDeep; ++k) {
+        // (places in 32 bits: the first group's wrap below 0, and are none)
+        const uint32_t at = g + (k / 4) * kVerifyThreads, n = 4 * at - off + k % 4;
+        x[k] = at < g1 && n < A.vocab ? __ldg(z + n) : -INFINITY;
+      }
     }
     if (greedy) {
+      float top = x[0];
+#pragma unroll
+      for (uint32_t k = 0; k < 4 * kDeep; ++k) {
+        bad = bad || !(x[k] <= 3.402823466e38f);
+        top = fmaxf(top, x[k]);
+      }
       if (top > best) {
         best = top;
 #pragma unroll
@@ -169,19 +208,43 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_sums_kernel(const __gri
       }
       continue;
     }
-    // (64 bits reach 2^1000 above a reference, so that it hardly ever moves)
-    const double d = __dmul_rn(top, c);
-    if (d > ref + 500.0 && top >= -3.402823466e38f) {
-      const double next = rint(d);
-      sum *= pow2_whole(fmax(ref - next, -2000.0));
-      ref = next;
-    }
-    const double from = ref == kNoRef ? 0.0 : ref;
+    // (64 bits reach 2^500 above a reference and more, so that it hardly ever moves)
+    bool odd = false;
 #pragma unroll
-    for (uint32_t k = 0; k < 4 * kDeep; ++k) {
-      double value, scale;
-      exp2_parts(distance(x[k], c, from), sixteenths, value, scale);
-      sum = fma(value, scale, sum);
+    for (uint32_t k = 0; k < 4 * kDeep; ++k) odd = odd || !(x[k] <= at_ref.high);
+    if (odd) {
+      float top = x[0];
+#pragma unroll
+      for (uint32_t k = 0; k < 4 * kDeep; ++k) {
+        bad = bad || !(x[k] <= 3.402823466e38f);
+        top = fmaxf(top, x[k]);
+      }
+      const double d = __dmul_rn(top, c);
+      if (d > ref + 500.0 && fabsf(top) <= 3.402823466e38f) {
+        const double next = rint(d);
+        sum *= pow2_whole(fmax(ref - next, -2000.0));
+        ref = next;
+        at_ref = near_of(c, ref);
+        near = is_near(ref);
+      }
+    }
+    if (near) {
+#pragma unroll
+      for (uint32_t k = 0; k < 4 * kDeep; ++k) {
+        double value, scale;
+        near_parts(x[k], at_ref, near_table, value, scale);
+        sum = fma(value, scale, sum);
+      }
+    } else if (ref != kNoRef) {
+#pragma unroll 1
+      for (uint32_t k = 0; k < 4 * kDeep; ++k) {
+        double value, scale;
+        float xk = x[0];
+#pragma unroll
+        for (uint32_t j = 1; j < 4 * kDeep; ++j) xk = j == k ? x[j] : xk;
+        exp2_parts(distance(xk, c, ref), sixteenths, value, scale);
+        sum = fma(value, scale, sum);
+      }
     }
   }
   double2* out = P.parts + static_cast<uint64_t>(row) * P.n_chunks + part;
@@ -308,32 +371,60 @@ __device__ __forceinline__ uint32_t first_past(double aim, double& before, F sum
   return last;
 }
 
+// w of the row that the next token is drawn from.
 struct VerifyRows {
   const float *p, *q;    // the last row, and the draft's (null: none)
-  double c, p_ref, p_per, q_ref, q_per;  // value = 2^(z c - ref) * per
+  double c, p_ref, q_ref, p_per, q_per;  // a probability is 2^(z c - ref) * per
+  Near p_near, q_near;
+  bool near;
   uint32_t without;      // a token that counts for nothing (a draft without logits), or -1
 };
-__device__ __forceinline__ double verify_weight(const VerifyRows& R, uint32_t n, const double* sixteenths) {
-  double w = exp2_of(distance(__ldg(R.p + n), R.c, R.p_ref), sixteenths) * R.p_per;
-  if (R.q != nullptr) {
-    const double q = exp2_of(distance(__ldg(R.q + n), R.c, R.q_ref), sixteenths) * R.q_per;
-    w = fmax(w - q, 0.0);
+__device__ __forceinline__ double probability(float z, const VerifyRows& R, bool of_q, const double* sixteenths,
+                                              const double* near_table) {
+  double value, scale;
+  if (R.near) {
+    const Near& r = of_q ? R.q_near : R.p_near;
+    near_parts(z, r, near_table, value, scale);
+    return z >= r.low ? value * scale * (of_q ? R.q_per : R.p_per) : 0.0;
   }
-  return n == R.without ? 0.0 : w;
+  return exp2_of(distance(z, R.c, of_q ? R.q_ref : R.p_ref), sixteenths) * (of_q ? R.q_per : R.p_per);
+}
+// kMany rows of 32 logits from n on (a lane's: n, n + 32, ...; 0 from `end` on).
+template <uint32_t kMany>
+__device__ __forceinline__ void verify_weights(const VerifyRows& R, uint32_t n, uint32_t end, const double* sixteenths,
+                                               const double* near_table, double (&w)[kMany]) {
+  float zp[kMany], zq[kMany];
+#pragma unroll
+  for (uint32_t k = 0; k < kMany; ++k) {
+    zp[k] = n + 32 * k < end ? __ldg(R.p + n + 32 * k) : -INFINITY;
+    zq[k] = R.q != nullptr && n + 32 * k < end ? __ldg(R.q + n + 32 * k) : -INFINITY;
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < kMany; ++k) w[k] = probability(zp[k], R, false, sixteenths, near_table);
+  if (R.q != nullptr) {
+#pragma unroll
+    for (uint32_t k = 0; k < kMany; ++k) w[k] = fmax(w[k] - probability(zq[k], R, true, sixteenths, near_table), 0.0);
+  }
+  if (R.without != 0xFFFFFFFFu) {
+#pragma unroll
+    for (uint32_t k = 0; k < kMany; ++k)
+      if (n + 32 * k == R.without) w[k] = 0.0;
+  }
 }
 
 // A cluster a sequence.  Every CTA decides where the sequence stops; for the next
 // token the vocabulary is cut into 64 runs, one a warp.
-__global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerifyThreads, 2)
+__global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerifyThreads, 4)
     verify_decide_kernel(const __grid_constant__ VerifyDev P) {
-  __shared__ double sixteenths[16];
+  __shared__ double sixteenths[16], near_table[16];
   __shared__ double run_sum[kVerifyWarps], cta_sum[2], piece_sum[kVerifyWarps];
   __shared__ double2 row_join[2];
   __shared__ uint32_t first;
+  __shared__ int32_t last_some;
   const VerifyArgs& A = P.a;
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const uint32_t b = blockIdx.x / kVerifyCluster, rank = blockIdx.x % kVerifyCluster;
-  if (threadIdx.x < 16) sixteenths[threadIdx.x] = g_sixteenths[threadIdx.x];
+  if (threadIdx.x < 16) fill_tables(threadIdx.x, sixteenths, near_table);
   griddep_wait();
   griddep_launch_dependents();
   // (whatever starts hold, rows stay within the logits)
@@ -345,7 +436,10 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
   const uint64_t n_target = static_cast<uint64_t>(A.n_drafted) + A.n_seqs;
   const double c = per_temperature(A.temperature, b);
   const bool greedy = c == 0.0;
-  if (threadIdx.x == 0) first = count;
+  if (threadIdx.x == 0) {
+    first = count;
+    last_some = -1;
+  }
   __syncthreads();
   // a warp a draft, in turn
   for (uint32_t i = warp; i < count; i += kVerifyWarps) {
@@ -414,21 +508,26 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
   R.q = has_draft ? A.draft + static_cast<uint64_t>(s0 + stop) * A.draft_stride : nullptr;
   R.q_ref = row_join[1].x;
   R.q_per = 1.0 / row_join[1].y;
+  R.near = is_near(R.p_ref) && is_near(R.q_ref);
+  R.p_near = near_of(c, R.p_ref);
+  R.q_near = near_of(c, R.q_ref);
   R.without = 0xFFFFFFFFu;
   if (refused && A.draft == nullptr) {
     const int32_t x = __ldg(A.tokens + s0 + stop);
     if (x >= 0 && static_cast<uint32_t>(x) < A.vocab) R.without = static_cast<uint32_t>(x);
   }
-  // runs are whole numbers of 32 logits for each of eight warps
+  // runs are whole numbers of 256 logits
   const uint32_t run = (A.vocab + 64 * 256 - 1) / (64 * 256) * 256;
   const double v = __ldg(A.v + b);
   for (uint32_t turn = 0;; ++turn) {
     const uint64_t n0 = static_cast<uint64_t>(rank * kVerifyWarps + warp) * run;
     const uint32_t end = static_cast<uint32_t>(min(static_cast<uint64_t>(A.vocab), n0 + run));
     double s = 0.0;
-    if (n0 < end) {
-#pragma unroll 4
-      for (uint32_t n = static_cast<uint32_t>(n0) + lane; n < end; n += 32) s += verify_weight(R, n, sixteenths);
+    for (uint64_t n = n0; n < end; n += 256) {
+      double w[8];
+      verify_weights(R, static_cast<uint32_t>(n) + lane, end, sixteenths, near_table, w);
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) s += w[k];
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
@@ -455,40 +554,70 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
     cluster_sync();  // (every CTA's sums have been read: it may end)
     if (at != rank) return;
     const uint32_t w_at = first_past(aim, before, [&](uint32_t k) { return run_sum[k]; });
-    // that run once more, an eighth a warp
-    const uint32_t piece = run / kVerifyWarps, r0 = (rank * kVerifyWarps + w_at) * run;
-    const uint32_t p0 = r0 + warp * piece, p1 = min(A.vocab, p0 + piece);
-    s = 0.0;
-    for (uint32_t n = p0 + lane; n < p1; n += 32) s += verify_weight(R, n, sixteenths);
+    // that run once more, 256 logits a warp at a time, kept until it is known which hold
+    // the token
+    const uint32_t r0 = (rank * kVerifyWarps + w_at) * run, r1 = min(A.vocab, r0 + run);
+    int32_t behind = -1;
+    for (uint32_t n8 = r0;; n8 += 256 * kVerifyWarps) {
+      const bool last = n8 + 256 * kVerifyWarps >= r1;
+      const uint32_t p0 = n8 + 256 * warp;
+      double w[8];
+      verify_weights(R, p0 + lane, r1, sixteenths, near_table, w);
+      s = 0.0;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    if (lane == 0) piece_sum[warp] = s;
-    __syncthreads();
-    const uint32_t p_at = first_past(aim, before, [&](uint32_t k) { return piece_sum[k]; });
-    if (p_at != warp) return;
-    uint32_t token = 0xFFFFFFFFu;
-    bool done = false;
-    for (uint32_t n32 = p0; n32 < p1 && !done; n32 += 32) {
-      const uint32_t n = n32 + lane;
-      const double w = n < p1 ? verify_weight(R, n, sixteenths) : 0.0;
-      double upto = w;
+      for (uint32_t k = 0; k < 8; ++k) s += w[k];
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-        if (lane >= static_cast<uint32_t>(d)) upto += o;
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+      __syncthreads();  // (the sums of the round before have been read)
+      if (lane == 0) piece_sum[warp] = s;
+      __syncthreads();
+      double all8 = 0.0;
+#pragma unroll
+      for (uint32_t k = 0; k < kVerifyWarps; ++k) all8 += piece_sum[k];
+      double after = before;
+      const uint32_t p_at = first_past(aim, after, [&](uint32_t k) { return piece_sum[k]; });
+      // (behind the last round there is nothing: what the rounding of sums has left over
+      // goes to the last token that has some)
+      if (!(before + all8 > aim) && !last) {
+        before += all8;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+          const uint32_t some = __ballot_sync(0xFFFFFFFFu, w[k] > 0.0);
+          if (some != 0) behind = p0 + 32 * k + 31 - __clz(some);
+        }
+        continue;
       }
-      const uint32_t some = __ballot_sync(0xFFFFFFFFu, w > 0.0);
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, w > 0.0 && before + upto > aim);
-      if (past != 0) {
-        token = n32 + __ffs(past) - 1;
-        done = true;
-      } else if (some != 0) {
-        token = n32 + 31 - __clz(some);
+      if (p_at == 8) {
+        // (nothing in the last round)
+        if (lane == 0) atomicMax(&last_some, behind);
+        __syncthreads();
+        if (threadIdx.x == 0) A.out[row] = last_some;
+        return;
       }
-      before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+      if (p_at != warp) return;
+      uint32_t token = 0xFFFFFFFFu;
+      bool done = false;
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+        double upto = w[k];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const double o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+          if (lane >= static_cast<uint32_t>(d)) upto += o;
+        }
+        const uint32_t some = __ballot_sync(0xFFFFFFFFu, w[k] > 0.0);
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, w[k] > 0.0 && after + upto > aim);
+        if (!done && past != 0) {
+          token = p0 + 32 * k + __ffs(past) - 1;
+          done = true;
+        } else if (!done && some != 0) {
+          token = p0 + 32 * k + 31 - __clz(some);
+        }
+        after += __shfl_sync(0xFFFFFFFFu, upto, 31);
+      }
+      if (lane == 0) A.out[row] = static_cast<int32_t>(token);
+      return;
     }
-    if (lane == 0) A.out[row] = static_cast<int32_t>(token);
-    return;
   }
 }
 

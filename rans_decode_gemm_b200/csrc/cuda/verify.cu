@@ -33,10 +33,24 @@ constexpr double kLog2E64 = 1.4426950408889634;
 constexpr double kNoRef = -1.0e300;              // the reference of a part without a finite logit
 constexpr double kNoMass = 1.0 / (1ull << 40);   // p - q is rounding from here down
 
-__constant__ double g_sixteenths[16] = {
-    1.0, 1.0442737824274138, 1.0905077326652577, 1.1387886347566916, 1.189207115002721, 1.241857812073484,
-    1.2968395546510096, 1.3542555469368927, 1.4142135623730951, 1.4768261459394993, 1.5422108254079407,
-    1.6104903319492543, 1.681792830507429, 1.7562521603732995, 1.8340080864093424, 1.9152065613971474};
+// 2^(i / 64)
+__constant__ double g_powers[64] = {
+    1.0, 1.0108892860517005, 1.0218971486541166, 1.0330248790212284,
+    1.0442737824274138, 1.0556451783605572, 1.0671404006768237, 1.0787607977571199,
+    1.0905077326652577, 1.102382583307841, 1.1143867425958924, 1.1265216186082418,
+    1.1387886347566916, 1.1511892299529827, 1.1637248587775775, 1.1763969916502812,
+    1.189207115002721, 1.202156731452703, 1.215247359980469, 1.22848053610687,
+    1.241857812073484, 1.255380757024691, 1.2690509571917332, 1.2828700160787783,
+    1.2968395546510096, 1.3109612115247644, 1.3252366431597413, 1.339667524053303,
+    1.3542555469368927, 1.3690024229745905, 1.383909881963832, 1.3989796725383112,
+    1.4142135623730951, 1.42961333839197, 1.4451808069770467, 1.460917794180647,
+    1.4768261459394993, 1.4929077282912648, 1.5091644275934228, 1.5255981507445384,
+    1.5422108254079407, 1.559004400237837, 1.5759808451078865, 1.593142151342267,
+    1.6104903319492543, 1.6280274218573478, 1.645755478153965, 1.6636765803267364,
+    1.681792830507429, 1.7001063537185235, 1.718619298122478, 1.7373338352737062,
+    1.7562521603732995, 1.7753764925265212, 1.7947090750031072, 1.8142521755003989,
+    1.8340080864093424, 1.8539791250833855, 1.8741676341103, 1.8945759815869656,
+    1.9152065613971474, 1.9360617934922943, 1.9571441241754002, 1.978456026387951};
 
 // 2^d as value * scale (scale a power of two times a sixteenth power of two; 0 for
 // d below -1020 and for -infinity).  d at most 1000.
@@ -72,44 +86,42 @@ __device__ __forceinline__ double distance(double z, double c, double ref) {
   return __dsub_rn(__dmul_rn(z, c), ref);
 }
 
-// The same for logits up to 500 above a reference of no more than 2^30 (those that lie
-// more than 900 below count as there), in nine instructions of 64 bits and six others
-// in place of eleven and sixteen: one fused product rounds z c - ref to sixteenths, a
-// second has what is left of it, and the table holds its high words less the index that
-// comes with the exponent (in `whole`, which the caller adds to the exponent's bits).
-constexpr double kSixteenth = 422212465065984.0;  // 1.5 * 2^48
+// The same for logits up to 500 above a reference of no more than 2^30 and no more than
+// 900 below it, in six instructions of 64 bits (of which an SM issues one a cycle) and
+// six others in place of eleven and sixteen: one fused product rounds z c - ref to 64ths,
+// a second has what is left of it, the polynomial is one of degree 3 that is off by
+// 4.5e-12 of the value at most, and the table holds its high words less the index that
+// comes with the exponent.
+constexpr double k64th = 105553116266496.0;  // 1.5 * 2^46
 struct Near {
-  double c, from, back;  // log2(e) / T;  kSixteenth - ref;  -from
-  float low, high;       // the logits of distance -900 and 500, to 2^-24 of themselves
+  double c, from;      // log2(e) / T;  k64th - ref
+  float low, within;   // the logit of distance -900; and up to which magnitude all are near
 };
+__device__ __forceinline__ bool is_near(double ref) { return fabs(ref) <= 1073741824.0; }
 __device__ __forceinline__ Near near_of(double c, double ref) {
   Near r;
   r.c = c;
-  r.from = kSixteenth - ref;
-  r.back = -r.from;
+  r.from = k64th - ref;
   r.low = static_cast<float>((ref - 900.0) / c);
-  r.high = static_cast<float>((ref + 500.0) / c);
+  r.within = static_cast<float>(fmin(ref + 500.0, 900.0 - ref) / c);
   return r;
 }
-__device__ __forceinline__ bool is_near(double ref) { return fabs(ref) <= 1073741824.0; }
 __device__ __forceinline__ void near_parts(float z, const Near& r, const double* table, double& value, double& scale) {
-  const double x = fmaxf(z, r.low);
+  const double x = z;
   const double a = fma(x, r.c, r.from);
   const int q = __double2loint(a);
-  const double f = fma(x, r.c, -(a + r.back));
-  value = fma(f, 0.0013333558146428441, 0.009618129107628477);
-  value = fma(value, f, 0.055504108664821576);
-  value = fma(value, f, 0.2402265069591007);
-  value = fma(value, f, 0.6931471805599453);
-  value = fma(value, f, 1.0);
-  const double s = table[q & 15];
-  scale = __hiloint2double(__double2hiint(s) + (q << 16), __double2loint(s));
+  const double f = fma(x, r.c, r.from - a);
+  value = fma(f, 0.05550402724235489, 0.2402270940024159);
+  value = fma(value, f, 0.6931471805667776);
+  value = fma(value, f, 0.9999999999955212);
+  const double s = table[q & 63];
+  scale = __hiloint2double(__double2hiint(s) + (q << 14), __double2loint(s));
 }
 
 __device__ __forceinline__ void fill_tables(uint32_t i, double* sixteenths, double* near_table) {
-  const double s = g_sixteenths[i];
-  sixteenths[i] = s;
-  near_table[i] = __hiloint2double(__double2hiint(s) - static_cast<int>(i << 16), __double2loint(s));
+  const double s = g_powers[i];
+  if (i % 4 == 0) sixteenths[i / 4] = s;
+  near_table[i] = __hiloint2double(__double2hiint(s) - static_cast<int>(i << 14), __double2loint(s));
 }
 
 // log2(e) / T; 0 for a greedy sequence.  (T from 1e30 on leaves all finite logits alike already.)
@@ -141,42 +153,30 @@ struct VerifyDev {
 };
 
 // One part of one row.
-__global__ void __launch_bounds__(kVerifyThreads) verify_sums_kernel(const __grid_constant__ VerifyDev P) {
-  __shared__ double sixteenths[16], near_table[16];
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_sums_kernel(const __grid_constant__ VerifyDev P) {
+  __shared__ double sixteenths[16], near_table[64];
   __shared__ double part_ref[kVerifyWarps], part_sum[kVerifyWarps];
   const VerifyArgs& A = P.a;
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  if (threadIdx.x < 16) fill_tables(threadIdx.x, sixteenths, near_table);
+  if (threadIdx.x < 64) fill_tables(threadIdx.x, sixteenths, near_table);
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t row = blockIdx.x / P.n_chunks, part = blockIdx.x - row * P.n_chunks;
   const uint32_t n_target = A.n_drafted + A.n_seqs;
   const bool is_target = row < n_target;
   const uint32_t r = is_target ? row : row - n_target;
-  const uint32_t b = sequence_of(A.starts, A.n_seqs, r, is_target ? 1u : 0u, lane);
-  const double c = per_temperature(A.temperature, b);
   const float* z = is_target ? A.target + static_cast<uint64_t>(r) * A.target_stride
                              : A.draft + static_cast<uint64_t>(r) * A.draft_stride;
-  const bool greedy = c == 0.0;
-  if (greedy && !is_target) return;  // (all that a greedy sequence asks is the target's largest)
-  __syncthreads();
   // groups of four logits on 16-byte boundaries: group g holds logits 4 g - off .. + 3
   const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z) >> 2) & 3u;
   const uint32_t groups = (A.vocab + off + 3) / 4;
   const uint32_t g0 = part * (P.chunk / 4), g1 = part + 1 == P.n_chunks ? groups : min(groups, g0 + P.chunk / 4);
   const float* base = z - off;
-  constexpr uint32_t kDeep = 4;
-  bool bad = false, near = false;
-  double ref = kNoRef, sum = 0.0;
-  Near at_ref = {};
-  at_ref.high = -INFINITY;
-  float best = -INFINITY;
-  uint32_t best_at = 0xFFFFFFFFu;
   // groups that lie within the row; the first and the last may not
-  const uint32_t in0 = off == 0 ? 0u : 1u, in1 = (A.vocab + off) / 4;
-  for (uint32_t g = g0 + threadIdx.x; g < g1; g += kDeep * kVerifyThreads) {
-    float x[4 * kDeep];
-    if (g >= in0 && g + (kDeep - 1) * kVerifyThreads < min(g1, in1)) {
+  constexpr uint32_t kDeep = 4, kStep = kDeep * kVerifyThreads;
+  const uint32_t in0 = off == 0 ? 0u : 1u, in1 = min(g1, (A.vocab + off) / 4);
+  auto load = [&](uint32_t g, float (&x)[4 * kDeep]) {
+    if (g >= in0 && g + (kDeep - 1) * kVerifyThreads < in1) {
 #pragma unroll
       for (uint32_t k = 0; k < kDeep; ++k) {
         const float4 q = __ldcs(reinterpret_cast<const float4*>(base + 4ull * g) + k * kVerifyThreads);
@@ -193,6 +193,23 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_sums_kernel(const __gri
         x[k] = at < g1 && n < A.vocab ? __ldg(z + n) : -INFINITY;
       }
     }
+  };
+  // (the first are on their way while the row's sequence is looked up)
+  float x[4 * kDeep];
+  load(g0 + threadIdx.x, x);
+  const uint32_t b = sequence_of(A.starts, A.n_seqs, r, is_target ? 1u : 0u, lane);
+  const double c = per_temperature(A.temperature, b);
+  const bool greedy = c == 0.0;
+  if (greedy && !is_target) return;  // (all that a greedy sequence asks is the target's largest)
+  __syncthreads();
+  bool bad = false, near = false;
+  double ref = kNoRef, sum = 0.0;
+  Near at_ref = {};
+  at_ref.within = -1.0f;  // (none is)
+  float best = -INFINITY;
+  uint32_t best_at = 0xFFFFFFFFu;
+  for (uint32_t g = g0 + threadIdx.x; g < g1; g += kStep) {
+    if (g >= g0 + kStep) load(g, x);
     if (greedy) {
       float top = x[0];
 #pragma unroll
@@ -208,17 +225,18 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_sums_kernel(const __gri
       }
       continue;
     }
-    // (64 bits reach 2^500 above a reference and more, so that it hardly ever moves)
-    bool odd = false;
+    // one comparison a logit finds NaN, infinities, and what lies far from the reference
+    bool all_near = true;
 #pragma unroll
-    for (uint32_t k = 0; k < 4 * kDeep; ++k) odd = odd || !(x[k] <= at_ref.high);
-    if (odd) {
+    for (uint32_t k = 0; k < 4 * kDeep; ++k) all_near = all_near && fabsf(x[k]) <= at_ref.within;
+    if (!all_near) {
       float top = x[0];
 #pragma unroll
       for (uint32_t k = 0; k < 4 * kDeep; ++k) {
         bad = bad || !(x[k] <= 3.402823466e38f);
         top = fmaxf(top, x[k]);
       }
+      // (64 bits reach 2^500 above a reference and more, so that it hardly ever moves)
       const double d = __dmul_rn(top, c);
       if (d > ref + 500.0 && fabsf(top) <= 3.402823466e38f) {
         const double next = rint(d);
@@ -226,25 +244,28 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_sums_kernel(const __gri
         ref = next;
         at_ref = near_of(c, ref);
         near = is_near(ref);
+        if (!near) at_ref.within = -1.0f;
       }
-    }
-    if (near) {
-#pragma unroll
-      for (uint32_t k = 0; k < 4 * kDeep; ++k) {
-        double value, scale;
-        near_parts(x[k], at_ref, near_table, value, scale);
-        sum = fma(value, scale, sum);
-      }
-    } else if (ref != kNoRef) {
+      if (!near && ref != kNoRef) {
 #pragma unroll 1
-      for (uint32_t k = 0; k < 4 * kDeep; ++k) {
-        double value, scale;
-        float xk = x[0];
+        for (uint32_t k = 0; k < 4 * kDeep; ++k) {
+          double value, scale;
+          float xk = x[0];
 #pragma unroll
-        for (uint32_t j = 1; j < 4 * kDeep; ++j) xk = j == k ? x[j] : xk;
-        exp2_parts(distance(xk, c, ref), sixteenths, value, scale);
-        sum = fma(value, scale, sum);
+          for (uint32_t j = 1; j < 4 * kDeep; ++j) xk = j == k ? x[j] : xk;
+          exp2_parts(distance(xk, c, ref), sixteenths, value, scale);
+          sum = fma(value, scale, sum);
+        }
       }
+      if (!near) continue;
+#pragma unroll
+      for (uint32_t k = 0; k < 4 * kDeep; ++k) x[k] = fmaxf(x[k], at_ref.low);  // (2^-900 is as good as nothing)
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 4 * kDeep; ++k) {
+      double value, scale;
+      near_parts(x[k], at_ref, near_table, value, scale);
+      sum = fma(value, scale, sum);
     }
   }
   double2* out = P.parts + static_cast<uint64_t>(row) * P.n_chunks + part;
@@ -371,24 +392,15 @@ __device__ __forceinline__ uint32_t first_past(double aim, double& before, F sum
   return last;
 }
 
-// w of the row that the next token is drawn from.
+// w of the row that the next token is drawn from, times what the exponentials of p sum to.
 struct VerifyRows {
-  const float *p, *q;    // the last row, and the draft's (null: none)
-  double c, p_ref, q_ref, p_per, q_per;  // a probability is 2^(z c - ref) * per
+  const float *p, *q;      // the last row, and the draft's (null: none)
+  double c, p_ref, q_ref;
+  double ratio;            // the sum of p's exponentials over that of q's
   Near p_near, q_near;
   bool near;
-  uint32_t without;      // a token that counts for nothing (a draft without logits), or -1
+  uint32_t without;        // a token that counts for nothing (a draft without logits), or -1
 };
-__device__ __forceinline__ double probability(float z, const VerifyRows& R, bool of_q, const double* sixteenths,
-                                              const double* near_table) {
-  double value, scale;
-  if (R.near) {
-    const Near& r = of_q ? R.q_near : R.p_near;
-    near_parts(z, r, near_table, value, scale);
-    return z >= r.low ? value * scale * (of_q ? R.q_per : R.p_per) : 0.0;
-  }
-  return exp2_of(distance(z, R.c, of_q ? R.q_ref : R.p_ref), sixteenths) * (of_q ? R.q_per : R.p_per);
-}
 // kMany rows of 32 logits from n on (a lane's: n, n + 32, ...; 0 from `end` on).
 template <uint32_t kMany>
 __device__ __forceinline__ void verify_weights(const VerifyRows& R, uint32_t n, uint32_t end, const double* sixteenths,
@@ -399,11 +411,42 @@ __device__ __forceinline__ void verify_weights(const VerifyRows& R, uint32_t n, 
     zp[k] = n + 32 * k < end ? __ldg(R.p + n + 32 * k) : -INFINITY;
     zq[k] = R.q != nullptr && n + 32 * k < end ? __ldg(R.q + n + 32 * k) : -INFINITY;
   }
+  if (R.near) {
+    // (what is masked came out between 2^-970 and 2^-830; less than that, and less than 0, is none)
+    constexpr int kSome = (1023 - 830) << 20;
 #pragma unroll
-  for (uint32_t k = 0; k < kMany; ++k) w[k] = probability(zp[k], R, false, sixteenths, near_table);
-  if (R.q != nullptr) {
+    for (uint32_t k = 0; k < kMany; ++k) {
+      double value, scale;
+      near_parts(fmaxf(zp[k], R.p_near.low), R.p_near, near_table, value, scale);
+      w[k] = __dmul_rn(value, scale);
+    }
+    if (R.q != nullptr) {
 #pragma unroll
-    for (uint32_t k = 0; k < kMany; ++k) w[k] = fmax(w[k] - probability(zq[k], R, true, sixteenths, near_table), 0.0);
+      for (uint32_t k = 0; k < kMany; ++k) {
+        double value, scale;
+        near_parts(fmaxf(zq[k], R.q_near.low), R.q_near, near_table, value, scale);
+        // (both products rounded alike, so that equal probabilities leave 0)
+        w[k] = fma(-R.ratio, __dmul_rn(value, scale), w[k]);
+      }
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kMany; ++k)
+      if (__double2hiint(w[k]) < kSome) w[k] = 0.0;
+  } else {
+#pragma unroll 1
+    for (uint32_t k = 0; k < kMany; ++k) {
+      float xp = zp[0], xq = zq[0];
+#pragma unroll
+      for (uint32_t j = 1; j < kMany; ++j) {
+        xp = j == k ? zp[j] : xp;
+        xq = j == k ? zq[j] : xq;
+      }
+      double v = exp2_of(distance(xp, R.c, R.p_ref), sixteenths);
+      if (R.q != nullptr) v = fmax(fma(-R.ratio, exp2_of(distance(xq, R.c, R.q_ref), sixteenths), v), 0.0);
+#pragma unroll
+      for (uint32_t j = 0; j < kMany; ++j)
+        if (j == k) w[j] = v;
+    }
   }
   if (R.without != 0xFFFFFFFFu) {
 #pragma unroll
@@ -416,7 +459,7 @@ __device__ __forceinline__ void verify_weights(const VerifyRows& R, uint32_t n, 
 // token the vocabulary is cut into 64 runs, one a warp.
 __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerifyThreads, 4)
     verify_decide_kernel(const __grid_constant__ VerifyDev P) {
-  __shared__ double sixteenths[16], near_table[16];
+  __shared__ double sixteenths[16], near_table[64];
   __shared__ double run_sum[kVerifyWarps], cta_sum[2], piece_sum[kVerifyWarps];
   __shared__ double2 row_join[2];
   __shared__ uint32_t first;
@@ -424,7 +467,7 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
   const VerifyArgs& A = P.a;
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const uint32_t b = blockIdx.x / kVerifyCluster, rank = blockIdx.x % kVerifyCluster;
-  if (threadIdx.x < 16) fill_tables(threadIdx.x, sixteenths, near_table);
+  if (threadIdx.x < 64) fill_tables(threadIdx.x, sixteenths, near_table);
   griddep_wait();
   griddep_launch_dependents();
   // (whatever starts hold, rows stay within the logits)
@@ -504,10 +547,9 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
   R.c = c;
   R.p = A.target + static_cast<uint64_t>(row) * A.target_stride;
   R.p_ref = row_join[0].x;
-  R.p_per = 1.0 / row_join[0].y;
   R.q = has_draft ? A.draft + static_cast<uint64_t>(s0 + stop) * A.draft_stride : nullptr;
   R.q_ref = row_join[1].x;
-  R.q_per = 1.0 / row_join[1].y;
+  R.ratio = row_join[0].y / row_join[1].y;
   R.near = is_near(R.p_ref) && is_near(R.q_ref);
   R.p_near = near_of(c, R.p_ref);
   R.q_near = near_of(c, R.q_ref);
@@ -542,7 +584,7 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
     double all = 0.0;
 #pragma unroll
     for (uint32_t k = 0; k < kVerifyCluster; ++k) all += cluster_read(&cta_sum[turn], k);
-    if (turn == 0 && refused && all <= kNoMass) {
+    if (turn == 0 && refused && all <= kNoMass * row_join[0].y) {
       // nothing that p has more of than q: p itself
       R.q = nullptr;
       R.without = 0xFFFFFFFFu;

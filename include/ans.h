@@ -514,11 +514,13 @@ typedef enum {
 ans_status ans_gated_workspace(const ans_layout* layout, uint32_t M, ans_scale_kind scale_kind,
                                size_t* bytes);
 
-/* H bf16 M x N from X bf16 M x K, row-major, 16-byte aligned.  Up to 32 tokens for
- * 128-row tiles and 16 for 256-row ones no decoded weight reaches global memory,
- * and G and U are ans_gemm_batched's (X beyond f16's range, and X of 2^-17 and
- * less, as there); above, both layers are decoded once into the workspace
- * (4 N K bytes), and X enters under a power of two of its row.  M == 0 is a no-op. */
+/* H bf16 M x N from X bf16 M x K, row-major, 16-byte aligned.  With few tokens (up to
+ * 32; 16 on layers of 2^25 weights and more, and none there where a tile holds 16,384
+ * symbols) no decoded weight reaches global memory, and G and U are those of
+ * ans_gemm_batched, which takes X in f16 as it is for the formats whose values are
+ * exact in f16 (infinite from 65,520 on; 2^-17 and less lose bits); otherwise both
+ * layers are decoded once into the workspace (4 N K bytes), and X enters under a
+ * power of two of its row.  M == 0 is a no-op. */
 ans_status ans_gated(const uint16_t* d_X, uint32_t M, const ans_tiles* gate, const ans_tiles* up,
                      ans_scale_kind scale_kind, const void* d_gate_scales,
                      const void* d_up_scales, uint32_t group_k, ans_act act, uint16_t* d_H,
@@ -529,7 +531,11 @@ ans_status ans_gated_grad_workspace(const ans_layout* layout, uint32_t M,
 
 /* The gradients of ans_gated from dH (bf16 M x N); G and U are computed again:
  *   dG = dH * U * act'(G),  dU = dH * act(G)        bf16 M x N
- *   dX = dG Wg + dU Wu, of dG and dU as returned    bf16 M x K; d_dX NULL: not computed
+ *   dX = dG Wg + dU Wu                              bf16 M x K; d_dX NULL: not computed
+ * dG and dU enter dX as bf16 (times the row scales, where there are) beside bf16
+ * weights, and as f16 beside the others, under a power of two of the token's that
+ * their bound max |dH| 1.14 |x| sqrt(K) (largest |w|) is met with: with 11 bits down
+ * to 2^-28 of that bound, and off by at most 2^-38 of it below.
  * dG and dU are what ans_gemm_lora_grad takes as d_dY of the two projections
  * (d_dX NULL there) for the gradients of their adapters.  The workspace is the
  * same size with and without d_dX.  M == 0 is a no-op. */

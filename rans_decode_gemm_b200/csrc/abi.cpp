@@ -1141,7 +1141,12 @@ namespace {
 
 // A call through operand images, or, while both layers' products take the small-M
 // schedule on half of the SMs each, ans_gemm_batched's one launch of both and their
-// products joined: no weight reaches global memory.
+// products joined: no weight reaches global memory.  The images' decoder has more
+// warps, but needs a second launch and a product: it serves large layers where the
+// other's tiles meet more than 16 tokens or hold 16,384 symbols (two layers of 14336 x
+// 4096, images against the one launch: 24 tokens int8 189 us against 199, int4 153
+// against 204; one token fp8 190 against 204, bf16 191 against 187, int4 153 against
+// 141; of 4096 x 4096, 32 tokens: bf16 97 against 75, int4 97 against 81).
 struct GatedChoice {
   bool few;
   size_t off_y, bytes;
@@ -1156,6 +1161,9 @@ ans_status choose_gated(const ans_tiles* gate, const ans_tiles* up, uint32_t M, 
   if (!grad) {
     const ans_gemm_job jobs[2] = {{nullptr, gate, nullptr, nullptr}, {nullptr, up, nullptr, nullptr}};
     if (batch_plan(jobs, 2, M, kind, sms, c->share, c->full, c->ws_off, &c->few) != ANS_OK) c->few = false;
+    const ans_layout& ly = gate->layout;
+    const uint32_t symbols = ly.tile_n * ly.tile_k / (ly.dtype == ANS_INT4_PAIRS || ly.dtype == ANS_FP4_PAIRS ? 2 : 1);
+    if (static_cast<uint64_t>(ly.N) * ly.K >= (32u << 20) && (M > 16 || symbols >= 16384)) c->few = false;
   }
   if (c->few) {
     c->off_y = up1024(c->ws_off[2]);

@@ -55,51 +55,62 @@ __device__ __forceinline__ double warp_max(double x) {
 struct DistillBegin {
   const int32_t* ids;
   const float *logits, *teacher_lse;
-  const void* scales;
   XentState st;
   uint32_t* words;     // [vocab_words][M]
   int32_t* sorted;     // [M][top]: the list in order, every row once, then -1
   double* t;           // [M][top]: what the teacher has on them
   double2* held;       // [M]: (S, sum_j t_j log t_j)
   uint32_t* status;
-  uint32_t M, top, vocab, vocab_words, scale_kind, f16;
+  uint32_t M, top, vocab, vocab_words;
   float per_t;
 };
 
-// Beside the decoding.  A CTA a token puts its list in order, and one more sets lift:
-// f16 exponentials carry the row scale of W and are stored under a power of two that
+// Beside the decoding: sets lift.  f16 exponentials carry the row scale of W and are stored under a power of two that
 // puts the largest scale in [1, 2), so that those of e^4 (kXentSlack) times it lie at
 // 2^7, and what is listed may be 2^14 above 1 before the token's row is moved.
+__global__ void __launch_bounds__(1024) distill_lift_kernel(float* lift, uint32_t vocab, uint32_t f16, uint32_t kind,
+                                                            const void* scales) {
+  __shared__ float part[32];
+  griddep_beside();
+  float top = 0.0f;
+  if (f16 && (kind == 1 || kind == 2)) {
+    // (there are scales up to the next multiple of 128)
+#pragma unroll 4
+    for (uint32_t n = 4 * threadIdx.x; n < vocab; n += 4096) {
+      float4 v;
+      if (kind == 1) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(scales) + n));
+        v = make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u), __uint_as_float(q.y << 16),
+                        __uint_as_float(q.y & 0xFFFF0000u));
+      } else {
+        v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(scales) + n));
+      }
+      uint32_t at = n;
+      for (const float s : {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)})
+        if (at++ < vocab && s <= 3.402823466e38f) top = fmaxf(top, s);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < 32; ++k) top = fmaxf(top, part[k]);
+    const int ex = top == 0.0f ? 0 : static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    *lift = f16 ? pow2f_whole(static_cast<float>(min(126, max(-118, -ex)))) : 1.0f;
+  }
+  griddep_beside_end();
+}
+
+// Beside the decoding.  A CTA a token puts its list in order.
 __global__ void __launch_bounds__(kDiThreads) distill_begin_kernel(const __grid_constant__ DistillBegin P) {
   __shared__ int32_t id[kDistillMaxTop];
   __shared__ double a[kDistillMaxTop], t[kDistillMaxTop];
   __shared__ bool head[kDistillMaxTop];
   __shared__ uint32_t bits[kDiWords];
   __shared__ double part[kDiThreads / 32][2];
-  __shared__ float top_part[kDiThreads / 32];
   griddep_beside();
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, m = blockIdx.x;
-  if (m == P.M) {
-    float top = 0.0f;
-    if (P.f16 && (P.scale_kind == 1 || P.scale_kind == 2)) {
-#pragma unroll 8
-      for (uint32_t n = threadIdx.x; n < P.vocab; n += kDiThreads) {
-        const float s = fabsf(P.scale_kind == 1 ? bf16_to_f32(__ldg(static_cast<const uint16_t*>(P.scales) + n))
-                                                : __ldg(static_cast<const float*>(P.scales) + n));
-        if (s <= 3.402823466e38f) top = fmaxf(top, s);
-      }
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    if (lane == 0) top_part[warp] = top;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (uint32_t k = 1; k < kDiThreads / 32; ++k) top = fmaxf(top, top_part[k]);
-      const int ex = top == 0.0f ? 0 : static_cast<int>(__float_as_uint(top) >> 23) - 127;
-      *P.st.lift = P.f16 ? pow2f_whole(static_cast<float>(min(126, max(-118, -ex)))) : 1.0f;
-    }
-    return;
-  }
   bool bad = false;
   double top = -INFINITY;
   const uint64_t at = static_cast<uint64_t>(m) * P.top;
@@ -228,16 +239,10 @@ struct DistillCoef {
 constexpr int32_t kDropRow = 0x7FFFFFFF;
 constexpr uint32_t kCoefWarps = 4;
 
-__global__ void __launch_bounds__(32 * kCoefWarps) distill_coef_kernel(const __grid_constant__ DistillCoef P) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const uint32_t lane = threadIdx.x % 32, m = blockIdx.x * kCoefWarps + threadIdx.x / 32;
-  if (m >= P.M) return;
+__device__ __forceinline__ void distill_coefs(const DistillCoef& P, uint32_t m, float ref_raw, double l, uint32_t lane) {
   constexpr uint32_t kEach = kDistillMaxTop / 32;
   const uint64_t at = static_cast<uint64_t>(m) * P.top;
   const double2 held = __ldcg(P.held + m);
-  const float ref_raw = __ldcg(P.st.ref + m);
-  const double l = __ldcg(P.st.sum + m);
   double z[kEach], t[kEach];
   bool in[kEach];
   double top = -INFINITY;
@@ -311,6 +316,70 @@ __global__ void __launch_bounds__(32 * kCoefWarps) distill_coef_kernel(const __g
 #pragma unroll
   for (uint32_t k = 0; k < kEach; ++k)
     if (in[k]) P.z[at + 32 * k + lane] = static_cast<float>(ldexp(c[k], up));
+}
+
+__global__ void __launch_bounds__(32 * kCoefWarps) distill_coef_kernel(const __grid_constant__ DistillCoef P) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t m = blockIdx.x * kCoefWarps + threadIdx.x / 32;
+  if (m < P.M) distill_coefs(P, m, __ldcg(P.st.ref + m), __ldcg(P.st.sum + m), threadIdx.x % 32);
+}
+
+// Few tokens' blocks joined into their state, a CTA a token (xent.cu's kernel takes 8
+// or 32 of them, and is two CTAs for 16: 8.7 us for 592 blocks where this takes 4), and,
+// behind the last piece, their final numbers in the same launch.
+struct DistillJoin {
+  DistillCoef coef;        // (M: the tokens)
+  const float2* blocks;    // [n_blocks][stride]
+  uint32_t stride, n_blocks, beside, last;
+};
+constexpr uint32_t kFewTokens = 128;
+__global__ void __launch_bounds__(256) distill_join_kernel(const __grid_constant__ DistillJoin P) {
+  __shared__ float part_ref[8], part_sum[8];
+  if (P.beside == 0) griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t m = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const float ref_old = __ldcg(P.coef.st.ref + m), l = __ldcg(P.coef.st.sum + m);
+  float ref = kXentNone, s = 0.0f;
+  for (uint32_t b0 = threadIdx.x; b0 < P.n_blocks; b0 += 4 * 256) {
+    float2 u[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k)
+      u[k] = b0 + 256 * k < P.n_blocks ? __ldcg(P.blocks + static_cast<uint64_t>(b0 + 256 * k) * P.stride + m)
+                                       : make_float2(kXentNone, 0.0f);
+    const float top = fmaxf(fmaxf(fmaxf(u[0].x, u[1].x), fmaxf(u[2].x, u[3].x)), ref);
+    s = s == 0.0f ? 0.0f : s * pow2f_whole(ref - top);
+    ref = top;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k)
+      if (u[k].y != 0.0f) s += u[k].y * pow2f_whole(u[k].x - ref);
+  }
+  float top = ref;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  s = s == 0.0f ? 0.0f : s * pow2f_whole(ref - top);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+  if (lane == 0) {
+    part_ref[warp] = top;
+    part_sum[warp] = s;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // (every lane does the same)
+    ref = ref_old;
+    for (uint32_t k = 0; k < 8; ++k) ref = fmaxf(ref, part_ref[k]);
+    s = 0.0f;
+    for (uint32_t k = 0; k < 8; ++k) s += part_sum[k] == 0.0f ? 0.0f : part_sum[k] * pow2f_whole(part_ref[k] - ref);
+    const float keep = ref_old == kXentNone ? 0.0f : pow2f_whole(ref_old - ref);
+    s = fmaf(l, keep, s);  // (NaN stays NaN)
+    if (lane == 0) {
+      P.coef.st.ref[m] = ref;
+      P.coef.st.sum[m] = s;
+    }
+    if (P.last != 0) distill_coefs(P.coef, m, ref, s, lane);
+  }
+  if (P.beside != 0) griddep_beside_end();
 }
 
 // The exponentials of a chunk as the second product takes them: blocks under another
@@ -487,14 +556,16 @@ cudaError_t launch_distill(const DistillPlan& p, const LayerDev& L, const Distil
   const uint32_t all = (a.vocab + L.tile_n - 1) / L.tile_n * L.tile_n;
   cudaError_t e;
   auto begin = [&]() {
-    const DistillBegin q{a.ids, a.logits, a.teacher_lse, a.scales, st, words, ids, t, held, a.status, p.M, p.top, a.vocab,
-                         p.vocab_words, a.scale_kind, p.f16, a.per_t};
-    cudaError_t r = launch_pdl(distill_begin_kernel, dim3(p.M + 1), dim3(kDiThreads), 0, stream, q);
+    const DistillBegin q{a.ids, a.logits, a.teacher_lse, st, words, ids, t, held, a.status, p.M, p.top, a.vocab,
+                         p.vocab_words, a.per_t};
+    cudaError_t r = launch_pdl(distill_lift_kernel, dim3(1), dim3(1024), 0, stream, st.lift, a.vocab, p.f16, a.scale_kind,
+                               a.scales);
+    if (r == cudaSuccess) r = launch_pdl(distill_begin_kernel, dim3(p.M), dim3(kDiThreads), 0, stream, q);
     if (r == cudaSuccess && p.f16) r = launch_row_prep(a.X, p.M, p.K, 0, nullptr, true, x16, x_factor, stream);
     return r;
   };
   // the logits of rows n0 .. n0 + rows - 1 (images from `from` on) for tokens m0 ..,
-  // folded into blocks from block b0 on and joined into the tokens' state
+  // folded into blocks from block b0 on
   auto logits = [&](uint32_t n0, uint32_t rows, const uint8_t* from, uint32_t b0, uint32_t m0, uint32_t m) {
     XentEpilogue f = {};
     f.factor = factor ? factor + m0 : nullptr;
@@ -515,33 +586,55 @@ cudaError_t launch_distill(const DistillPlan& p, const LayerDev& L, const Distil
     f.ids = ids + static_cast<uint64_t>(m0) * p.top;
     f.z_listed = z + static_cast<uint64_t>(m0) * p.top;
     f.per_t = a.per_t;
-    cudaError_t r = launch_operand_gemm(plan_operand_gemm(false, p.f16, m, rows, p.K, p.sms), from,
-                                        x + static_cast<uint64_t>(m0) * p.K, nullptr, &f, w + p.off_gemm, a.status, stream);
-    if (r != cudaSuccess) return r;
+    return launch_operand_gemm(plan_operand_gemm(false, p.f16, m, rows, p.K, p.sms), from,
+                               x + static_cast<uint64_t>(m0) * p.K, nullptr, &f, w + p.off_gemm, a.status, stream);
+  };
+  auto coefs_of = [&](uint32_t m0, uint32_t m) {
+    const uint64_t at = static_cast<uint64_t>(m0) * p.top;
+    return DistillCoef{XentState{st.ref + m0, st.sum + m0, nullptr, nullptr, nullptr, st.lift}, t + at, held + m0, ids + at,
+                       z + at, a.scales, a.weight ? a.weight + m0 : nullptr, a.loss + m0, a.lse + m0, shift + m0, beta + m0,
+                       m, p.top, a.scale_kind, p.f16, p.grad, a.per_t};
+  };
+  // their blocks joined into the tokens' state, and, behind the last rows, the tokens'
+  // final numbers
+  auto join = [&](uint32_t rows, uint32_t b0, uint32_t m0, uint32_t m, bool beside, bool last) {
+    const float2* from = blocks + static_cast<uint64_t>(b0) * p.stride;
+    if (m <= kFewTokens) {
+      const DistillJoin j{coefs_of(m0, m), from, p.stride, rows / 32, beside, last};
+      return launch_pdl(distill_join_kernel, dim3(m), dim3(256), 0, stream, j);
+    }
     XentJoin j = {};
     j.st = st;
-    j.blocks = f.blocks;
+    j.blocks = from;
     j.stride = p.stride;
     j.n_blocks = rows / 32;
     j.m0 = m0;
     j.m = m;
-    return launch_xent_join(j, stream);
-  };
-  auto coefs = [&]() {
-    const DistillCoef q{st, t, held, ids, z, a.scales, a.weight, a.loss, a.lse, shift, beta, p.M, p.top, a.scale_kind, p.f16,
-                        p.grad, a.per_t};
-    return launch_pdl(distill_coef_kernel, dim3((p.M + kCoefWarps - 1) / kCoefWarps), dim3(32 * kCoefWarps), 0, stream, q);
+    j.beside = beside;
+    cudaError_t r = launch_xent_join(j, stream);
+    if (r != cudaSuccess || !last) return r;
+    return launch_pdl(distill_coef_kernel, dim3((m + kCoefWarps - 1) / kCoefWarps), dim3(32 * kCoefWarps), 0, stream,
+                      coefs_of(m0, m));
   };
   if (!p.grad) {
+    // the last tokens' blocks of a piece are joined beside the decoding of the next
+    const uint32_t m_last = (p.M - 1) / p.chunk * p.chunk;
+    uint32_t before = 0;  // rows of the piece before
     for (uint32_t n0 = 0; n0 < a.vocab; n0 += p.piece) {
       const uint32_t rows = std::min(p.piece, all - n0);
+      const bool last = n0 + p.piece >= a.vocab;
       e = launch_operand_decode(L, n0, rows, a.scale_kind, a.scales, a.group_k, images, a.status, p.sms, stream);
       if (e == cudaSuccess && n0 == 0) e = begin();
-      for (uint32_t m0 = 0; e == cudaSuccess && m0 < p.M; m0 += p.chunk)
-        e = logits(n0, rows, images, 0, m0, std::min(p.chunk, p.M - m0));
+      if (e == cudaSuccess && n0 != 0) e = join(before, 0, m_last, p.M - m_last, true, false);
+      for (uint32_t m0 = 0; e == cudaSuccess && m0 < p.M; m0 += p.chunk) {
+        const uint32_t m = std::min(p.chunk, p.M - m0);
+        e = logits(n0, rows, images, 0, m0, m);
+        if (e == cudaSuccess && (last || m0 != m_last)) e = join(rows, 0, m0, m, false, last);
+      }
       if (e != cudaSuccess) return e;
+      before = rows;
     }
-    return coefs();
+    return cudaSuccess;
   }
   e = launch_operand_decode(L, 0, all, a.scale_kind, a.scales, a.group_k, images, a.status, p.sms, stream);
   if (e == cudaSuccess) e = begin();
@@ -552,17 +645,12 @@ cudaError_t launch_distill(const DistillPlan& p, const LayerDev& L, const Distil
     for (uint32_t n0 = 0; n0 < all;) {
       const uint32_t rows = std::min(n0 == 0 ? p.first : p.piece, all - n0);
       e = logits(n0, rows, images + static_cast<uint64_t>(n0 / 128) * (p.K / 16) * kSlabBytes, n0 / 32, m0, m);
+      if (e == cudaSuccess) e = join(rows, n0 / 32, m0, m, false, n0 + rows == all);
       if (e != cudaSuccess) return e;
       n0 += rows;
     }
-    // (the tokens of this chunk: their coefficients take the place of their listed logits)
-    const DistillCoef q{XentState{st.ref + m0, st.sum + m0, nullptr, nullptr, nullptr, st.lift},
-                        t + static_cast<uint64_t>(m0) * p.top, held + m0, ids + static_cast<uint64_t>(m0) * p.top,
-                        z + static_cast<uint64_t>(m0) * p.top, a.scales, a.weight ? a.weight + m0 : nullptr, a.loss + m0,
-                        a.lse + m0, shift + m0, beta + m0, m, p.top, a.scale_kind, p.f16, p.grad, a.per_t};
-    e = launch_pdl(distill_coef_kernel, dim3((m + kCoefWarps - 1) / kCoefWarps), dim3(32 * kCoefWarps), 0, stream, q);
-    if (e != cudaSuccess) return e;
-    const DistillRows d{st.ref + m0, shift + m0, q.sorted, q.z, blocks, probs, m, p.top, all, all / 32, p.stride, p.f16};
+    const uint64_t at = static_cast<uint64_t>(m0) * p.top;
+    const DistillRows d{st.ref + m0, shift + m0, ids + at, z + at, blocks, probs, m, p.top, all, all / 32, p.stride, p.f16};
     e = launch_pdl(distill_rows_kernel, dim3((m + 31) / 32, (all / 32 + 31) / 32), dim3(256), 0, stream, d);
     if (e != cudaSuccess) return e;
     OperandGemmOut back = {};

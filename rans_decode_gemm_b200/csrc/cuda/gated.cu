@@ -12,7 +12,9 @@
 //
 // A stage holds 64 steps of the sum: 16 KB of tokens by TMA (128-byte swizzle) and
 // 32 KB of images by one copy.  An image's rows are K-major under the 32-byte
-// swizzle, so 8 KB of a gate and an up image are one 256-row operand.
+// swizzle, so 8 KB of a gate and an up image are one 256-row operand.  Where the tiles
+// would leave SMs idle they are of 64 or 32 rows: a box of that part of each of eight
+// images.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,13 +31,13 @@
 
 namespace ansdev {
 
-constexpr uint32_t kGaBM = 128, kGaBN = 128, kGaBK = 64;
+constexpr uint32_t kGaBM = 128, kGaBK = 64;
 constexpr uint32_t kGaABytes = kGaBM * kGaBK * 2;           // 16 KB of tokens
-constexpr uint32_t kGaBBytes = 2 * kGaBN * kGaBK * 2;       // 32 KB of both layers
-constexpr uint32_t kGaStageBytes = kGaABytes + kGaBBytes;
-constexpr uint32_t kGaStages = 4;
-constexpr uint32_t kGaSmem = kGaStages * kGaStageBytes + 1024;
-constexpr uint32_t kGaEpiWarps = 8;
+// kBN rows of both layers
+__host__ __device__ constexpr uint32_t ga_stage_bytes(uint32_t bn) { return kGaABytes + 2 * bn * kGaBK * 2; }
+__host__ __device__ constexpr uint32_t ga_stages(uint32_t bn) { return 192 * 1024 / ga_stage_bytes(bn); }
+constexpr uint32_t kGaSmem = 192 * 1024 + 1024;
+constexpr uint32_t kGaEpiWarps = 16;
 constexpr uint32_t kGaThreads = (2 + kGaEpiWarps) * 32;
 
 // act(g) and, where asked, its derivative.  Sigmoids for tanh and erfc for 1 + erf:
@@ -58,24 +60,40 @@ __device__ __forceinline__ void activation(uint32_t act, float g, float& value, 
       if (kSlope) dy = kA * fmaf(3.0f, q, 1.0f);
     }
     const float e = __expf(-y);
-    const float p = 1.0f / (1.0f + e);
+    const float p = __fdividef(1.0f, 1.0f + e);  // (0 from 2^126 on)
     value = g * p;
     // p' = p (1 - p) y', and 1 - p = e p
     if (kSlope) slope = e > 1e30f ? 0.0f : fmaf(g * dy, p * (e * p), p);
   }
 }
 
+// Rows of the transposed product: dG and dU times the row scales, before they are
+// rounded to bf16.  In f16 they come under a power of two of the token's that no value
+// of its can pass 2^15 with: |dG s| <= max |dH| * 1.13 |x| sqrt(K) * (the largest weight,
+// scale and all) * (the largest scale), and |dU s| likewise (|act'| < 1.13, |act(g)| <=
+// |g|).  A bound need not be met: it is some 2^7 above what a trained layer's values
+// come to, and f16 holds 11 bits of them down to 2^-28 of it, so 2^-21 of the largest.
+struct GatedRows {
+  uint16_t *gate, *up;      // null: dG and dU themselves are the rows
+  const float* bound;       // [M]: max |dH| * 1.13 |x| sqrt(K) * (the largest code); null: no power of two
+  const float* scale_parts; // kScaleParts largest scales
+  float* factor;            // [M]: 2^-e, for the product's sums
+};
+constexpr uint32_t kScaleParts = 64;
+
 struct GatedDev {
   const uint8_t* images;
   CUtensorMap tmap_x;       // tokens: 64 x b_rows boxes, 128-byte swizzle
+  CUtensorMap tmap_w;       // narrow tiles: images as rows of 512 eight-byte words, boxes of 4 bn x 8
   const float* factor;      // a token's factor, or null: 1
   const void *gate_scales, *up_scales;
   uint32_t scale_kind, act;
   uint16_t* H;
   const uint16_t* dH;
   uint16_t *dG, *dU;
+  GatedRows rows;
   uint32_t* status;
-  uint32_t M, N, m_blocks, n_tiles, k_slabs, n_kb, box_rows, idesc;
+  uint32_t M, N, m_blocks, n_tiles, k_slabs, n_kb, box_rows, f16;
 };
 
 // Eight row scales from n on.
@@ -101,8 +119,14 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool kGrad>
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <bool kGrad, uint32_t kBN>
 __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_constant__ GatedDev P) {
+  constexpr uint32_t kGaStages = ga_stages(kBN), kGaStageBytes = ga_stage_bytes(kBN);
   extern __shared__ __align__(1024) uint8_t dsmem_raw[];
   __shared__ __align__(8) uint64_t full[kGaStages], empty[kGaStages];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_done;
@@ -130,6 +154,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
     tmem_relinquish();
   } else if (warp == 0 && lane == 0) {
     prefetch_tmap(&P.tmap_x);
+    if (kBN < 128) prefetch_tmap(&P.tmap_w);
   }
   tc_fence_before();
   __syncthreads();
@@ -139,7 +164,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
   griddep_wait();
   griddep_launch_dependents();
 
-  // tile t: rows 128 ab of both layers, tokens 128 mb; row block major, so that the
+  // tile t: rows kBN ab of both layers, tokens 128 mb; row block major, so that the
   // CTAs running at one time share the weights through L2
   if (warp == 0) {
     // ======================= loads =======================
@@ -155,9 +180,19 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
           }
           const uint32_t bar = smem_u32(&full[s]);
           const uint32_t a_s = smem_s + s * kGaStageBytes, b_s = a_s + kGaABytes;
-          const uint32_t bytes = min(4u, P.k_slabs - 4 * kb) * 2 * kSlabBytes;
-          mbar_arrive_expect_tx_s(bar, bytes + P.box_rows * kGaBK * 2);
-          bulk_g2s_s(b_s, P.images + (static_cast<uint64_t>(ab) * P.k_slabs + 4 * kb) * 2 * kSlabBytes, bytes, bar);
+          if constexpr (kBN == 128) {
+            const uint32_t bytes = min(4u, P.k_slabs - 4 * kb) * 2 * kSlabBytes;
+            mbar_arrive_expect_tx_s(bar, bytes + P.box_rows * kGaBK * 2);
+            bulk_g2s_s(b_s, P.images + (static_cast<uint64_t>(ab) * P.k_slabs + 4 * kb) * 2 * kSlabBytes, bytes, bar);
+          } else {
+            // (where the last block of k holds fewer images, the box runs into the next
+            // row block's, or is filled with zeros: operands that no MMA takes)
+            constexpr uint32_t kParts = 128 / kBN;
+            const uint32_t block = ab / kParts, part = ab - block * kParts;
+            mbar_arrive_expect_tx_s(bar, kGaStageBytes - kGaABytes + P.box_rows * kGaBK * 2);
+            tma_load_2d_s(b_s, &P.tmap_w, static_cast<int32_t>(part * kBN * 4),
+                          static_cast<int32_t>(2 * (block * P.k_slabs + 4 * kb)), bar);
+          }
           tma_load_2d_s(a_s, &P.tmap_x, static_cast<int32_t>(kb * kGaBK), static_cast<int32_t>(mb * kGaBM), bar);
           if (++s == kGaStages) {
             s = 0;
@@ -184,7 +219,8 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
         const uint32_t b = acc & 1u;
         if (acc >= 2 && !wait_live(&acc_empty[b], ((acc >> 1) + 1) & 1u, abort, P.status, 21)) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + b * 256;
+        const uint32_t d_tmem = tmem_base + b * 2 * kBN;
+        const uint32_t idesc = idesc_f16(P.f16 ? 0u : 1u, 128, 2 * kBN);
         for (uint32_t kb = 0; kb < P.n_kb; ++kb) {
           if (!wait_live(&full[s], ph, abort, P.status, 22)) {
             live = false;
@@ -196,7 +232,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j)
             if (j < cnt)
-              umma_f16(d_tmem, da | (a16 + 2 * j), db | (b16 + j * (2 * kSlabBytes >> 4)), P.idesc,
+              umma_f16(d_tmem, da | (a16 + 2 * j), db | (b16 + j * (kBN * 64 >> 4)), idesc,
                        (kb != 0 || j != 0) ? 1u : 0u);
           umma_commit(&empty[s]);
           if (++s == kGaStages) {
@@ -212,9 +248,17 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
     __syncwarp();
   } else {
     // ======================= epilogue (warps 2-9) =======================
-    // a token a lane; two warps for each quarter of TMEM's lanes, 64 of the tile's
-    // rows each, 32 at a time
-    const uint32_t quad = warp & 3u, half = (warp - 2) >> 2;
+    // a token a lane; four warps for each quarter of TMEM's lanes, which take the tile's
+    // rows in turn, 16 at a time
+    const uint32_t quad = warp & 3u, turn = (warp - 2) >> 2;
+    float top_scale = 1.0f;
+    if (kGrad && P.rows.bound != nullptr && P.scale_kind != 0) {
+      top_scale = fmaxf(__ldcg(P.rows.scale_parts + lane), __ldcg(P.rows.scale_parts + 32 + lane));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top_scale = fmaxf(top_scale, __shfl_xor_sync(0xFFFFFFFFu, top_scale, d));
+      // (row scales come in G or U and in the row itself)
+      if (P.scale_kind != 3) top_scale *= top_scale;
+    }
     uint32_t acc = 0;
     for (uint32_t t = blockIdx.x; t < P.n_tiles; t += gridDim.x, ++acc) {
       const uint32_t ab = t / P.m_blocks, mb = t - ab * P.m_blocks;
@@ -222,32 +266,42 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
       const uint32_t m = mb * kGaBM + 32 * quad + lane;
       const bool m_in = m < P.M;
       const float f = P.factor != nullptr && m_in ? __ldcg(P.factor + m) : 1.0f;
+      float up = 1.0f;
+      if (kGrad && P.rows.bound != nullptr && m_in) {
+        // 2^e with the bound times 2^e in [2^14, 2^15); both powers stay normal numbers
+        const float bound = __ldcg(P.rows.bound + m) * top_scale;
+        const int ex = static_cast<int>(__float_as_uint(bound) >> 23) - 127;
+        const int e = bound == 0.0f ? 0 : min(126, max(-113, 14 - ex));
+        up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        if (ab == 0 && turn == 0) P.rows.factor[m] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      }
       const uint64_t row = static_cast<uint64_t>(m) * P.N;
       const bool ok = wait_live(&acc_full[b], (acc >> 1) & 1u, abort, P.status, 23, 64);
       tc_fence_after();
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (16 * turn >= kBN && lane == 0) mbar_arrive(&acc_empty[b]);
 #pragma unroll
-      for (uint32_t step = 0; step < 2; ++step) {
-        const uint32_t c0 = 64 * half + 32 * step, n0 = ab * kGaBN + c0;
-        uint32_t g[32], u[32];
-        const uint32_t at = tmem_base + ((32 * quad) << 16) + b * 256 + c0;
-        tmem_ld32(at, g);
-        tmem_ld32(at + kGaBN, u);
-        uint4 d[4];
+      for (uint32_t c0 = 16 * turn; c0 < kBN; c0 += 64) {
+        const uint32_t n0 = ab * kBN + c0;
+        uint32_t g[16], u[16];
+        const uint32_t at = tmem_base + ((32 * quad) << 16) + b * 2 * kBN + c0;
+        tmem_ld16(at, g);
+        tmem_ld16(at + kBN, u);
+        uint4 d[2];
         if (kGrad) {
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k)
+          for (uint32_t k = 0; k < 2; ++k)
             d[k] = m_in ? __ldg(reinterpret_cast<const uint4*>(P.dH + row + n0) + k) : make_uint4(0, 0, 0, 0);
         }
         tmem_ld_wait();
-        if (step == 1) {
+        if (c0 + 64 >= kBN) {
           // this warp has read its last of the tile's sums
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_empty[b]);
         }
 #pragma unroll
-        for (uint32_t k = 0; k < 4; ++k) {
+        for (uint32_t k = 0; k < 2; ++k) {
           float sg[8], su[8];
           if (P.scale_kind == 1 || P.scale_kind == 2) {
             row_scales8(P.scale_kind, P.gate_scales, n0 + 8 * k, sg);
@@ -256,7 +310,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
 #pragma unroll
             for (int i = 0; i < 8; ++i) sg[i] = su[i] = 1.0f;
           }
-          uint32_t o[4], o2[4];
+          uint32_t o[4], o2[4], q[4], q2[4];
           const uint32_t dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w};
 #pragma unroll
           for (uint32_t i = 0; i < 4; ++i) {
@@ -277,12 +331,25 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
               }
             }
             o[i] = bf16x2(r[0], r[1]);
-            if (kGrad) o2[i] = bf16x2(r2[0], r2[1]);
+            if (kGrad) {
+              o2[i] = bf16x2(r2[0], r2[1]);
+              if (P.rows.gate != nullptr) {
+                const float s0 = sg[2 * i] * up, s1 = sg[2 * i + 1] * up, t0 = su[2 * i] * up, t1 = su[2 * i + 1] * up;
+                q[i] = P.f16 ? f16x2(r[0] * s0, r[1] * s1) : bf16x2(r[0] * s0, r[1] * s1);
+                q2[i] = P.f16 ? f16x2(r2[0] * t0, r2[1] * t1) : bf16x2(r2[0] * t0, r2[1] * t1);
+              }
+            }
           }
           if (m_in) {
-            uint16_t* out = (kGrad ? P.dG : P.H) + row + n0 + 8 * k;
-            *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
-            if (kGrad) *reinterpret_cast<uint4*>(P.dU + row + n0 + 8 * k) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+            const uint64_t to = row + n0 + 8 * k;
+            *reinterpret_cast<uint4*>((kGrad ? P.dG : P.H) + to) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (kGrad) {
+              *reinterpret_cast<uint4*>(P.dU + to) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+              if (P.rows.gate != nullptr) {
+                *reinterpret_cast<uint4*>(P.rows.gate + to) = make_uint4(q[0], q[1], q[2], q[3]);
+                *reinterpret_cast<uint4*>(P.rows.up + to) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
+              }
+            }
           }
         }
       }
@@ -325,81 +392,119 @@ cudaError_t launch_gated_join(const float* G, const float* U, uint64_t n, uint32
                     stream, G, U, n8, act, H);
 }
 
-// ---- dG and dU as rows of the transposed product --------------------------------
-// As row_prep_kernel (operand_gemm.cu), for two rows under one power of two: both
-// products add into one sum.  A CTA a token.
-struct GatedPrep {
-  const uint16_t *dG, *dU;
-  const void *gate_scales, *up_scales;
-  uint32_t N, scale_kind, f16;
-  uint16_t* rows;   // [2][M][N]
-  uint64_t second;  // elements from the first to the second
-  float* factor;
-};
-__device__ __forceinline__ void prep_values(const GatedPrep& P, uint32_t which, uint64_t row, uint32_t c, float (&v)[8]) {
-  const uint4 q = __ldcg(reinterpret_cast<const uint4*>((which ? P.dU : P.dG) + row + c));
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    v[2 * k] = __uint_as_float(w[k] << 16);
-    v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-  }
-  if (P.scale_kind == 1 || P.scale_kind == 2) {
-    float s[8];
-    row_scales8(P.scale_kind, which ? P.up_scales : P.gate_scales, c, s);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= s[k];
-  }
-}
-constexpr uint32_t kGaPrepThreads = 256;
-__global__ void __launch_bounds__(kGaPrepThreads) gated_prep_kernel(const __grid_constant__ GatedPrep P) {
-  __shared__ float part[kGaPrepThreads / 32];
+// ---- bounds of the gradient's rows ----------------------------------------------
+// The largest scales of both layers, in kScaleParts parts.  (Group scales are part of
+// the images' values and bound those; row scales are met once more by the rows.)
+__global__ void __launch_bounds__(256) gated_scales_kernel(const void* gate, const void* up, uint32_t kind, uint64_t count,
+                                                           float* parts) {
+  __shared__ float part[8];
   griddep_wait();
   griddep_launch_dependents();
-  const uint64_t row = static_cast<uint64_t>(blockIdx.x) * P.N;
   float top = 0.0f;
-  if (P.f16) {
-    for (uint32_t c = threadIdx.x * 8; c < 2 * P.N; c += kGaPrepThreads * 8) {
-      float v[8];
-      prep_values(P, c >= P.N, row, c >= P.N ? c - P.N : c, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float a = fabsf(v[k]);
-        if (a <= 3.402823466e38f) top = fmaxf(top, a);
-      }
-    }
+  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < 2 * count; i += kScaleParts * 256) {
+    const void* from = i < count ? gate : up;
+    const uint64_t n = i < count ? i : i - count;
+    const float s = fabsf(kind == 2 ? __ldg(static_cast<const float*>(from) + n)
+                                    : bf16_to_f32(__ldg(static_cast<const uint16_t*>(from) + n)));
+    if (s <= 3.402823466e38f) top = fmaxf(top, s);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
   __syncthreads();
-#pragma unroll
-  for (uint32_t k = 0; k < kGaPrepThreads / 32; ++k) top = fmaxf(top, part[k]);
-  // 2^e with top * 2^e in [2^14, 2^15); both powers stay normal numbers
-  const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-  const int e = top == 0.0f ? 0 : min(126, max(-113, 14 - ex));
-  const float scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-  if (threadIdx.x == 0) P.factor[blockIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  for (uint32_t c = threadIdx.x * 8; c < 2 * P.N; c += kGaPrepThreads * 8) {
-    const bool which = c >= P.N;
-    const uint32_t cc = which ? c - P.N : c;
-    float v[8];
-    prep_values(P, which, row, cc, v);
-    uint32_t o[4];
+  if (threadIdx.x != 0) return;
+  for (int k = 1; k < 8; ++k) top = fmaxf(top, part[k]);
+  parts[blockIdx.x] = top;
+}
+
+// Beside the decoding: 1.13 max |dH| |x| sqrt(K) times the largest code, of finite
+// values.  A CTA a token.
+__global__ void __launch_bounds__(256) gated_bound_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ dH,
+                                                          uint32_t N, uint32_t K, float per, float* __restrict__ bound) {
+  __shared__ float part[8][2];
+  griddep_beside();
+  auto values = [&](const uint16_t* p, float (&v)[8]) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (P.f16) {
-        const __half2 h = __floats2half2_rn(v[2 * k] * scale, v[2 * k + 1] * scale);
-        o[k] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        o[k] = bf16x2(v[2 * k], v[2 * k + 1]);
-      }
+      v[2 * k] = fabsf(__uint_as_float(w[k] << 16));
+      v[2 * k + 1] = fabsf(__uint_as_float(w[k] & 0xFFFF0000u));
     }
-    *reinterpret_cast<uint4*>(P.rows + (which ? P.second : 0) + row + cc) = make_uint4(o[0], o[1], o[2], o[3]);
+  };
+  // (the norm under the row's largest, so that no square passes fp32)
+  const uint64_t m = blockIdx.x;
+  float top_h = 0.0f, top_x = 0.0f, v[8];
+  for (uint32_t c = threadIdx.x * 8; c < N; c += 2048) {
+    values(dH + m * N + c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top_h = v[k] <= 3.402823466e38f ? fmaxf(top_h, v[k]) : top_h;
   }
+  for (uint32_t c = threadIdx.x * 8; c < K; c += 2048) {
+    values(X + m * K + c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top_x = v[k] <= 3.402823466e38f ? fmaxf(top_x, v[k]) : top_x;
+  }
+  auto across = [&](float x, uint32_t slot, bool sum) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const float o = __shfl_xor_sync(0xFFFFFFFFu, x, d);
+      x = sum ? x + o : fmaxf(x, o);
+    }
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32][slot] = x;
+    return x;
+  };
+  across(top_h, 0, false);
+  across(top_x, 1, false);
+  __syncthreads();
+  for (int k = 0; k < 8; ++k) {
+    top_h = fmaxf(top_h, part[k][0]);
+    top_x = fmaxf(top_x, part[k][1]);
+  }
+  const float down = top_x > 0.0f ? 1.0f / top_x : 0.0f;
+  float sum = 0.0f;
+  for (uint32_t c = threadIdx.x * 8; c < K; c += 2048) {
+    values(X + m * K + c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float y = v[k] <= 3.402823466e38f ? v[k] * down : 0.0f;
+      sum = fmaf(y, y, sum);
+    }
+  }
+  __syncthreads();
+  across(sum, 0, true);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0.0f;
+    for (int k = 0; k < 8; ++k) sum += part[k][0];
+    // (the largest fp32 in place of what is past it)
+    bound[m] = fminf(top_h * sqrtf(sum * static_cast<float>(K)) * top_x * per, 3.0e38f);
+  }
+  griddep_beside_end();
 }
 
 static size_t aligned(size_t n) { return (n + 1023) / 1024 * 1024; }
+
+// The tile's rows: rounds of tiles over the SMs, at 395, 345 and 335 ns a stage (a
+// narrow tile's hardly take less, so that it only serves to fill the SMs), and the
+// last epilogue, which nothing hides: 16, 8 and 5 us with the gradient.  (4096 x 4096
+// int4 with the gradient: 200 tokens 140, 128 and 141 us by tiles of 128, 64 and 32
+// rows; 301 tokens 152, 157 and 176; 1024 x 1024, 40 tokens: 87, 76 and 76.)
+static uint32_t gated_rows_of_tile(uint32_t M, uint32_t N, uint32_t K, bool grad, uint32_t sms) {
+  const uint64_t m_blocks = (M + kGaBM - 1) / kGaBM, n_kb = (K + kGaBK - 1) / kGaBK;
+  uint64_t least = ~0ull;
+  uint32_t best = 128;
+  for (const uint32_t bn : {128u, 64u, 32u}) {
+    const uint64_t rounds = (N / bn * m_blocks + sms - 1) / sms;
+    const uint64_t last = bn == 128 ? 16000 : bn == 64 ? 8000 : 5000;
+    const uint64_t cost = rounds * n_kb * (bn == 128 ? 395 : bn == 64 ? 345 : 335) + (grad ? last : last / 4);
+    if (cost < least) {
+      least = cost;
+      best = bn;
+    }
+  }
+  return best;
+}
 
 void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool grad, int sms, GatedPlan* p) {
   p->M = M;
@@ -420,24 +525,38 @@ void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool gr
   p->off_x16 = take(p->f16 ? static_cast<size_t>(M) * L.K * 2 : 0);
   p->off_factor = take(p->f16 ? static_cast<size_t>(M) * 4 : 0);
   p->off_rows = take(grad && p->prep ? static_cast<size_t>(M) * L.N * 4 : 0);
-  p->off_rows_factor = take(grad && p->prep ? static_cast<size_t>(M) * 4 : 0);
+  p->off_rows_factor = take(grad && p->f16 ? (static_cast<size_t>(M) * 2 + kScaleParts) * 4 : 0);
   p->off_gemm = take(grad ? operand_gemm_workspace(p->back) : 0);
   p->bytes = at;
 }
 
-template <bool kGrad>
-static cudaError_t launch_gated_gemm(const GatedDev& P, int sms, cudaStream_t stream) {
+template <bool kGrad, uint32_t kBN>
+static cudaError_t launch_gated_tiles(GatedDev& P, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(attr_set.load() & (1ull << dev))) {
-    e = cudaFuncSetAttribute(gated_gemm_kernel<kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGaSmem);
+    e = cudaFuncSetAttribute(gated_gemm_kernel<kGrad, kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGaSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }
-  return launch_pdl(gated_gemm_kernel<kGrad>, dim3(std::min(P.n_tiles, static_cast<uint32_t>(sms))), dim3(kGaThreads),
+  P.n_tiles = P.N / kBN * P.m_blocks;
+  if (kBN < 128) {
+    e = encode_tmap(&P.tmap_w, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, P.images, kSlabBytes / 8,
+                    static_cast<uint64_t>(P.N / 128) * P.k_slabs * 2, kSlabBytes, kBN * 4, 8, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(gated_gemm_kernel<kGrad, kBN>, dim3(std::min(P.n_tiles, static_cast<uint32_t>(sms))), dim3(kGaThreads),
                     kGaSmem, stream, P);
+}
+template <bool kGrad>
+static cudaError_t launch_gated_gemm(GatedDev& P, uint32_t K, int sms, cudaStream_t stream) {
+  switch (gated_rows_of_tile(P.M, P.N, K, kGrad, static_cast<uint32_t>(sms))) {
+    case 128: return launch_gated_tiles<kGrad, 128>(P, sms, stream);
+    case 64: return launch_gated_tiles<kGrad, 64>(P, sms, stream);
+    default: return launch_gated_tiles<kGrad, 32>(P, sms, stream);
+  }
 }
 
 cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDev& up, const GatedArgs& a, void* ws,
@@ -446,12 +565,27 @@ cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDe
   uint8_t* images = w + p.off_images;
   uint16_t* x16 = reinterpret_cast<uint16_t*>(w + p.off_x16);
   float* factor = reinterpret_cast<float*>(w + p.off_factor);
-  cudaError_t e = launch_operand_decode(gate, 0, p.N, a.scale_kind, a.gate_scales, a.group_k, images, a.status, p.sms,
+  float* rows_factor = reinterpret_cast<float*>(w + p.off_rows_factor);
+  float* bound = rows_factor + p.M;
+  float* scale_parts = bound + p.M;
+  const bool bounds = p.grad && p.f16 && a.dX != nullptr;
+  cudaError_t e = cudaSuccess;
+  if (bounds && a.scale_kind != 0)
+    e = launch_pdl(gated_scales_kernel, dim3(kScaleParts), dim3(256), 0, stream, a.gate_scales, a.up_scales, a.scale_kind,
+                   a.scale_kind == 3 ? static_cast<uint64_t>(p.N) * (p.K / a.group_k) : static_cast<uint64_t>(p.N),
+                   scale_parts);
+  if (e != cudaSuccess) return e;
+  e = launch_operand_decode(gate, 0, p.N, a.scale_kind, a.gate_scales, a.group_k, images, a.status, p.sms,
                                         stream, 2 * kOperandImage);
   if (e == cudaSuccess)
     e = launch_operand_decode(up, 0, p.N, a.scale_kind, a.up_scales, a.group_k, images + kOperandImage, a.status, p.sms,
                               stream, 2 * kOperandImage);
   if (e == cudaSuccess && p.f16) e = launch_row_prep(a.X, p.M, p.K, 0, nullptr, true, x16, factor, stream);
+  if (e == cudaSuccess && bounds) {
+    const uint32_t dt = gate.dtype;
+    const float code = dt == kDtInt8 ? 128.0f : dt == kDtFp8 ? 448.0f : dt == kDtInt4 || dt == kDtInt4Pairs ? 8.0f : 6.0f;
+    e = launch_pdl(gated_bound_kernel, dim3(p.M), dim3(256), 0, stream, a.X, a.dH, p.N, p.K, 1.14f * code, bound);
+  }
   if (e != cudaSuccess) return e;
   GatedDev P;
   std::memset(&P, 0, sizeof(P));
@@ -469,33 +603,33 @@ cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDe
   P.M = p.M;
   P.N = p.N;
   P.m_blocks = (p.M + kGaBM - 1) / kGaBM;
-  P.n_tiles = p.N / kGaBN * P.m_blocks;
   P.k_slabs = p.K / 16;
   P.n_kb = (p.K + kGaBK - 1) / kGaBK;
   P.box_rows = std::min(p.M, kGaBM);
-  P.idesc = idesc_f16(p.f16 ? 0u : 1u, 128, 256);
+  P.f16 = p.f16;
   e = encode_tmap(&P.tmap_x, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.f16 ? x16 : a.X, p.K, p.M, static_cast<uint64_t>(p.K) * 2,
                   kGaBK, P.box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  if (!p.grad) return launch_gated_gemm<false>(P, p.sms, stream);
-  e = launch_gated_gemm<true>(P, p.sms, stream);
+  if (!p.grad) return launch_gated_gemm<false>(P, p.K, p.sms, stream);
+  const uint16_t *rows = a.dG, *rows2 = a.dU;
+  if (p.prep && a.dX != nullptr) {
+    P.rows.gate = reinterpret_cast<uint16_t*>(w + p.off_rows);
+    P.rows.up = P.rows.gate + static_cast<uint64_t>(p.M) * p.N;
+    if (bounds) {
+      P.rows.bound = bound;
+      P.rows.scale_parts = scale_parts;
+      P.rows.factor = rows_factor;
+    }
+    rows = P.rows.gate;
+    rows2 = P.rows.up;
+  }
+  e = launch_gated_gemm<true>(P, p.K, p.sms, stream);
   if (e != cudaSuccess || a.dX == nullptr) return e;
   OperandGemmOut out;
   std::memset(&out, 0, sizeof(out));
   out.out16 = a.dX;
   out.ld = p.K;
-  const uint16_t *rows = a.dG, *rows2 = a.dU;
-  if (p.prep) {
-    uint16_t* r = reinterpret_cast<uint16_t*>(w + p.off_rows);
-    float* f = reinterpret_cast<float*>(w + p.off_rows_factor);
-    const GatedPrep q{a.dG, a.dU, a.gate_scales, a.up_scales, p.N, a.scale_kind, p.f16, r,
-                      static_cast<uint64_t>(p.M) * p.N, f};
-    e = launch_pdl(gated_prep_kernel, dim3(p.M), dim3(kGaPrepThreads), 0, stream, q);
-    if (e != cudaSuccess) return e;
-    rows = r;
-    rows2 = r + q.second;
-    out.beta = f;
-  }
+  out.beta = bounds ? rows_factor : nullptr;
   const OperandPair pair{images + kOperandImage, rows2, 2 * kOperandImage};
   return launch_operand_gemm(p.back, images, rows, &out, nullptr, w + p.off_gemm, a.status, stream, &pair);
 }

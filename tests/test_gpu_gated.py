@@ -93,14 +93,31 @@ def check_grad(B, x, dh, act):
     bu = iu + BF16 * (want_u.abs() + iu) + 2.0 ** -133
     within(dg, want_g, bg, "dg")
     within(du, want_u, bu, "du")
-    # dX of dG and dU as they came back
-    g64, u64, wg, wu = dg.cpu().double(), du.cpu().double(), B.gate.w, B.up.w
+    wg, wu = B.gate.w, B.up.w
+    if B.gate.dtype == ans.BF16_SPLIT:
+        # dX of dG and dU as they came back, or, under row scales, of those times the scales, rounded once
+        g64, u64 = dg.cpu().double(), du.cpu().double()
+        eg, eu, eps = 0.0, 0.0, 0.0
+        if B.kind != ans.SCALE_NONE:
+            g64, u64, eg, eu, eps = want_g, want_u, ig, iu, BF16
+        floor = 0.0
+    else:
+        # of the values before they are rounded, in f16 under the token's bound: 11 bits, and 2^-25 of
+        # the unit below its normal range, 2^-39 of the bound (2^-38: its power of two)
+        g64, u64, eg, eu, eps = want_g, want_u, ig, iu, 2.0 ** -11
+        code = {ans.INT8: 128, ans.FP8_E4M3: 448, ans.INT4: 8, ans.INT4_PAIRS: 8}.get(B.gate.dtype, 6)
+        rowed = B.kind in (ans.SCALE_ROW_BF16, ans.SCALE_ROW_F32)
+        tops = [1.0 if L.scales is None else L.scales.double().max().item() for L in (B.gate, B.up)]
+        bound = 1.14 * d.abs().amax(1) * x.double().norm(dim=1) * B.K ** 0.5 * code * max(tops) ** (2 if rowed else 1)
+        codes = [L.w.abs() / (L.scales.cpu().double()[:, None] if rowed else 1.0) for L in (B.gate, B.up)]
+        floor = 2.0 ** -38 * bound[:, None] * (codes[0].sum(0) + codes[1].sum(0))[None, :]
     mass = g64.abs() @ wg.abs() + u64.abs() @ wu.abs()
-    row = torch.maximum(g64.abs().amax(1, keepdim=True) * wg.abs().max(), u64.abs().amax(1, keepdim=True) * wu.abs().max())
-    inner = (B.gate.factor_eps + sum_eps(2 * B.N)) * mass + 2.0 ** -37 * 2 * B.N * row
+    inner = (eps + sum_eps(2 * B.N)) * mass + floor
+    if B.gate.dtype != ans.BF16_SPLIT or B.kind != ans.SCALE_NONE:
+        inner = inner + (1 + eps) * (eg @ wg.abs() + eu @ wu.abs())
     want = g64 @ wg + u64 @ wu
     within(dx, want, inner + BF16 * (want.abs() + inner) + 2.0 ** -133, "dx")
-    # and of the formula's
+    # and, beside weights in bf16, of the formula's own
     want = want_g @ wg + want_u @ wu
     inner = inner + bg @ wg.abs() + bu @ wu.abs()
     within(dx, want, inner + BF16 * (want.abs() + inner) + 2.0 ** -133, "dx of exact dG and dU")

@@ -29,7 +29,7 @@ namespace ansdev {
 constexpr uint32_t kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr uint32_t kVerifyCluster = 8;
 constexpr uint32_t kVerifyMaxChunks = 64;
-constexpr double kLog2E64 = 1.4426950408889634;
+constexpr double kLog2E64 = 1.4426950408889634, kLn2_64 = 0.69314718055994531;
 constexpr double kNoRef = -1.0e300;              // the reference of a part without a finite logit
 constexpr double kNoMass = 1.0 / (1ull << 40);   // p - q is rounding from here down
 
@@ -98,12 +98,13 @@ struct Near {
   float low, within;   // the logit of distance -900; and up to which magnitude all are near
 };
 __device__ __forceinline__ bool is_near(double ref) { return fabs(ref) <= 1073741824.0; }
-__device__ __forceinline__ Near near_of(double c, double ref) {
+// per: 1 / c
+__device__ __forceinline__ Near near_of(double c, double per, double ref) {
   Near r;
   r.c = c;
   r.from = k64th - ref;
-  r.low = static_cast<float>((ref - 900.0) / c);
-  r.within = static_cast<float>(fmin(ref + 500.0, 900.0 - ref) / c);
+  r.low = static_cast<float>((ref - 900.0) * per);
+  r.within = static_cast<float>(fmin(ref + 500.0, 900.0 - ref) * per);
   return r;
 }
 __device__ __forceinline__ void near_parts(float z, const Near& r, const double* table, double& value, double& scale) {
@@ -125,9 +126,13 @@ __device__ __forceinline__ void fill_tables(uint32_t i, double* sixteenths, doub
 }
 
 // log2(e) / T; 0 for a greedy sequence.  (T from 1e30 on leaves all finite logits alike already.)
-__device__ __forceinline__ double per_temperature(const float* temperature, uint32_t b) {
+struct Heat {
+  double c, per;  // log2(e) / T and its inverse
+};
+__device__ __forceinline__ Heat heat_of(const float* temperature, uint32_t b) {
   const float t = temperature == nullptr ? 1.0f : __ldg(temperature + b);
-  return t > 0.0f ? kLog2E64 / static_cast<double>(fminf(t, 1e30f)) : 0.0;
+  const double t64 = fminf(t, 1e30f);
+  return t > 0.0f ? Heat{kLog2E64 / t64, kLn2_64 * t64} : Heat{0.0, 0.0};
 }
 
 // The last sequence whose first row (its drafts' rows and, for a target, one more
@@ -198,7 +203,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_sums_kernel(const __
   float x[4 * kDeep];
   load(g0 + threadIdx.x, x);
   const uint32_t b = sequence_of(A.starts, A.n_seqs, r, is_target ? 1u : 0u, lane);
-  const double c = per_temperature(A.temperature, b);
+  const Heat heat = heat_of(A.temperature, b);
+  const double c = heat.c;
   const bool greedy = c == 0.0;
   if (greedy && !is_target) return;  // (all that a greedy sequence asks is the target's largest)
   __syncthreads();
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_sums_kernel(const __
         const double next = rint(d);
         sum *= pow2_whole(fmax(ref - next, -2000.0));
         ref = next;
-        at_ref = near_of(c, ref);
+        at_ref = near_of(c, heat.per, ref);
         near = is_near(ref);
         if (!near) at_ref.within = -1.0f;
       }
@@ -316,53 +322,60 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_sums_kernel(const __
   *out = make_double2(ref, sum);
 }
 
-// A row's parts joined: (reference, sum), or (value, index) of the largest; sum NaN
-// (index -1) where the row has no distribution.  By whole warps.
-__device__ __forceinline__ double2 join_row(const VerifyDev& P, uint64_t row, bool greedy, uint32_t lane) {
-  double ref = greedy ? -INFINITY : kNoRef, sum = greedy ? 4294967295.0 : 0.0;
+// A row's parts, two a lane, and those joined: (reference, sum), or (value, index) of
+// the largest; sum NaN (index -1) where the row has no distribution.  By whole warps.
+struct RowParts {
   double2 u[kVerifyMaxChunks / 32];
-  bool bad = false;
+};
+__device__ __forceinline__ RowParts row_parts(const VerifyDev& P, uint64_t row, bool greedy, uint32_t lane) {
+  RowParts r;
 #pragma unroll
   for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k) {
     const uint32_t at = lane + 32 * k;
-    u[k] = at < P.n_chunks ? __ldcg(P.parts + row * P.n_chunks + at) : make_double2(ref, sum);
-    bad = bad || isnan(u[k].y);
+    r.u[k] = at < P.n_chunks ? __ldcg(P.parts + row * P.n_chunks + at)
+                             : (greedy ? make_double2(-INFINITY, 4294967295.0) : make_double2(kNoRef, 0.0));
   }
+  return r;
+}
+__device__ __forceinline__ double2 join_parts(const RowParts& r, bool greedy) {
+  bool bad = false;
+#pragma unroll
+  for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k) bad = bad || isnan(r.u[k].y);
   bad = __any_sync(0xFFFFFFFFu, bad);
   if (greedy) {
+    double top = -INFINITY, at = 4294967295.0;
 #pragma unroll
     for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k)
-      if (u[k].x > ref || (u[k].x == ref && u[k].y < sum)) {
-        ref = u[k].x;
-        sum = u[k].y;
+      if (r.u[k].x > top || (r.u[k].x == top && r.u[k].y < at)) {
+        top = r.u[k].x;
+        at = r.u[k].y;
       }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-      const double v = __shfl_xor_sync(0xFFFFFFFFu, ref, d), at = __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-      if (v > ref || (v == ref && at < sum)) {
-        ref = v;
-        sum = at;
+      const double v = __shfl_xor_sync(0xFFFFFFFFu, top, d), w = __shfl_xor_sync(0xFFFFFFFFu, at, d);
+      if (v > top || (v == top && w < at)) {
+        top = v;
+        at = w;
       }
     }
-    if (bad || ref == -INFINITY) sum = -1.0;
-    return make_double2(ref, sum);
+    if (bad || top == -INFINITY) at = -1.0;
+    return make_double2(top, at);
   }
-  double top = kNoRef;
+  double top = kNoRef, sum = 0.0;
 #pragma unroll
-  for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k) top = fmax(top, u[k].x);
+  for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k) top = fmax(top, r.u[k].x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmax(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
 #pragma unroll
-  for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k) sum += u[k].y * pow2_whole(fmax(u[k].x - top, -2000.0));
+  for (uint32_t k = 0; k < kVerifyMaxChunks / 32; ++k) sum += r.u[k].y * pow2_whole(fmax(r.u[k].x - top, -2000.0));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
   if (bad || sum == 0.0) sum = __longlong_as_double(0x7FF8000000000000ll);
   return make_double2(top, sum);
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ double cluster_read(const double* p, uint32_t rank) {
   uint32_t at;
   double v;
@@ -455,13 +468,16 @@ __device__ __forceinline__ void verify_weights(const VerifyRows& R, uint32_t n, 
   }
 }
 
+// Drafts of a sequence whose rows' sums are kept until it is known which one is drawn from.
+constexpr uint32_t kKnown = 32;
+
 // A cluster a sequence.  Every CTA decides where the sequence stops; for the next
 // token the vocabulary is cut into 64 runs, one a warp.
 __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerifyThreads, 4)
     verify_decide_kernel(const __grid_constant__ VerifyDev P) {
   __shared__ double sixteenths[16], near_table[64];
   __shared__ double run_sum[kVerifyWarps], cta_sum[2], piece_sum[kVerifyWarps];
-  __shared__ double2 row_join[2];
+  __shared__ double2 row_join[2], known[kKnown][2];
   __shared__ uint32_t first;
   __shared__ int32_t last_some;
   const VerifyArgs& A = P.a;
@@ -477,35 +493,48 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
   bool wrong = s0 != raw0 || s1 != raw1 || (b == 0 && raw0 != 0) || (b + 1 == A.n_seqs && raw1 != drafted);
   const uint32_t count = static_cast<uint32_t>(s1 - s0), t0 = static_cast<uint32_t>(s0) + b;
   const uint64_t n_target = static_cast<uint64_t>(A.n_drafted) + A.n_seqs;
-  const double c = per_temperature(A.temperature, b);
+  const Heat heat = heat_of(A.temperature, b);
+  const double c = heat.c, v = __ldg(A.v + b);
   const bool greedy = c == 0.0;
   if (threadIdx.x == 0) {
     first = count;
     last_some = -1;
   }
   __syncthreads();
-  // a warp a draft, in turn
-  for (uint32_t i = warp; i < count; i += kVerifyWarps) {
+  // a warp a draft, in turn, and one the row behind the last
+  for (uint32_t i = warp; i <= count; i += kVerifyWarps) {
     if (i > *static_cast<volatile uint32_t*>(&first)) break;
-    const double2 t = join_row(P, t0 + i, greedy, lane);
-    const int32_t x = __ldg(A.tokens + s0 + i);
+    const bool has_q = A.draft != nullptr && !greedy && i < count;
+    const RowParts pt = row_parts(P, t0 + i, greedy, lane);
+    RowParts pd = pt;
+    if (has_q) pd = row_parts(P, n_target + s0 + i, false, lane);
+    int32_t x = -1;
+    float u = 0.0f, zx = 0.0f, yx = 0.0f;
+    if (i < count) {
+      x = __ldg(A.tokens + s0 + i);
+      u = __ldg(A.u + s0 + i);
+    }
     const bool in = x >= 0 && static_cast<uint32_t>(x) < A.vocab;
+    if (in && !greedy) {
+      zx = __ldg(A.target + (t0 + i) * A.target_stride + x);
+      if (A.draft != nullptr) yx = __ldg(A.draft + static_cast<uint64_t>(s0 + i) * A.draft_stride + x);
+    }
+    const double2 t = join_parts(pt, greedy);
+    double2 d = make_double2(0.0, 1.0);
+    if (has_q) d = join_parts(pd, false);
+    if (i < kKnown && lane == 0) {
+      known[i][0] = t;
+      known[i][1] = d;
+    }
+    if (i == count) break;
     bool keep = false;
     if (greedy) {
       keep = in && t.y == static_cast<double>(x);
-    } else {
-      double2 d = make_double2(0.0, 1.0);
-      if (A.draft != nullptr) d = join_row(P, n_target + s0 + i, false, lane);
-      if (in) {
-        const double zx = __ldg(A.target + (t0 + i) * A.target_stride + x);
-        const double px = exp2_of(distance(zx, c, t.x), sixteenths) / t.y;
-        double qx = 1.0;
-        if (A.draft != nullptr) {
-          const double yx = __ldg(A.draft + static_cast<uint64_t>(s0 + i) * A.draft_stride + x);
-          qx = exp2_of(distance(yx, c, d.x), sixteenths) / d.y;
-        }
-        keep = static_cast<double>(__ldg(A.u + s0 + i)) * qx < px;  // (false where a row has no distribution)
-      }
+    } else if (in) {
+      // u q < p, both times both sums (false where a row has no distribution)
+      const double ep = exp2_of(distance(zx, c, t.x), sixteenths);
+      const double eq = has_q ? exp2_of(distance(yx, c, d.x), sixteenths) : 1.0;
+      keep = u * eq * t.y < ep * d.y;
     }
     if (!keep && lane == 0) atomicMin(&first, i);
   }
@@ -522,21 +551,17 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
     }
     if (wrong) atomicOr(A.status, kStatusBadIndex);
   }
-  if (greedy) {
-    if (rank == 0 && warp == 0) {
-      const double2 t = join_row(P, row, true, lane);
-      if (lane == 0) A.out[row] = static_cast<int32_t>(t.y);
-    }
-    return;
-  }
-  const bool has_draft = refused && A.draft != nullptr;
-  if (warp == 0) {
-    const double2 t = join_row(P, row, false, lane);
-    if (lane == 0) row_join[0] = t;
-  } else if (warp == 1) {
+  const bool has_draft = refused && A.draft != nullptr && !greedy;
+  if (warp < 2) {
     double2 t = make_double2(0.0, 1.0);
-    if (has_draft) t = join_row(P, n_target + s0 + stop, false, lane);
-    if (lane == 0) row_join[1] = t;
+    if (stop < kKnown) t = known[stop][warp];
+    else if (warp == 0) t = join_parts(row_parts(P, row, greedy, lane), greedy);
+    else if (has_draft) t = join_parts(row_parts(P, n_target + s0 + stop, false, lane), false);
+    if (lane == 0) row_join[warp] = t;
+  }
+  if (greedy) {
+    if (rank == 0 && threadIdx.x == 0) A.out[row] = static_cast<int32_t>(row_join[0].y);
+    return;
   }
   __syncthreads();
   if (isnan(row_join[0].y) || isnan(row_join[1].y)) {
@@ -551,8 +576,8 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
   R.q_ref = row_join[1].x;
   R.ratio = row_join[0].y / row_join[1].y;
   R.near = is_near(R.p_ref) && is_near(R.q_ref);
-  R.p_near = near_of(c, R.p_ref);
-  R.q_near = near_of(c, R.q_ref);
+  R.p_near = near_of(c, heat.per, R.p_ref);
+  R.q_near = near_of(c, heat.per, R.q_ref);
   R.without = 0xFFFFFFFFu;
   if (refused && A.draft == nullptr) {
     const int32_t x = __ldg(A.tokens + s0 + stop);
@@ -560,7 +585,6 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
   }
   // runs are whole numbers of 256 logits
   const uint32_t run = (A.vocab + 64 * 256 - 1) / (64 * 256) * 256;
-  const double v = __ldg(A.v + b);
   for (uint32_t turn = 0;; ++turn) {
     const uint64_t n0 = static_cast<uint64_t>(rank * kVerifyWarps + warp) * run;
     const uint32_t end = static_cast<uint32_t>(min(static_cast<uint64_t>(A.vocab), n0 + run));
@@ -580,7 +604,8 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
       for (uint32_t k = 0; k < kVerifyWarps; ++k) all += run_sum[k];
       cta_sum[turn] = all;
     }
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     double all = 0.0;
 #pragma unroll
     for (uint32_t k = 0; k < kVerifyCluster; ++k) all += cluster_read(&cta_sum[turn], k);
@@ -593,8 +618,12 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
     const double aim = v * all;
     double before = 0.0;
     const uint32_t at = first_past(aim, before, [&](uint32_t k) { return cluster_read(&cta_sum[turn], k); });
-    cluster_sync();  // (every CTA's sums have been read: it may end)
-    if (at != rank) return;
+    // (every CTA's sums have been read: it may end when all have come here)
+    cluster_arrive();
+    if (at != rank) {
+      cluster_wait();
+      return;
+    }
     const uint32_t w_at = first_past(aim, before, [&](uint32_t k) { return run_sum[k]; });
     // that run once more, 256 logits a warp at a time, kept until it is known which hold
     // the token
@@ -634,9 +663,13 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
         if (lane == 0) atomicMax(&last_some, behind);
         __syncthreads();
         if (threadIdx.x == 0) A.out[row] = last_some;
+        cluster_wait();
         return;
       }
-      if (p_at != warp) return;
+      if (p_at != warp) {
+        cluster_wait();
+        return;
+      }
       uint32_t token = 0xFFFFFFFFu;
       bool done = false;
 #pragma unroll
@@ -658,17 +691,18 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
         after += __shfl_sync(0xFFFFFFFFu, upto, 31);
       }
       if (lane == 0) A.out[row] = static_cast<int32_t>(token);
+      cluster_wait();
       return;
     }
   }
 }
 
 void make_verify_plan(uint32_t n_seqs, uint32_t n_drafted, uint32_t vocab, VerifyPlan* p) {
-  // parts of 2,048 to 32,768 logits, so that a few rows fill the SMs and many rows
-  // have few ends; 64 of them at most
+  // parts of 1,024 to 32,768 logits: one round of the SMs, at four CTAs each, or many
+  // of long parts; 64 of a row at most
   const uint64_t rows = 2ull * n_drafted + n_seqs, all = rows * vocab;
-  uint64_t chunk = (all / (148 * 16) + 1023) / 1024 * 1024;
-  chunk = std::max<uint64_t>(2048, std::min<uint64_t>(chunk, 32768));
+  uint64_t chunk = (all / (148 * 4) + 1023) / 1024 * 1024;
+  chunk = std::max<uint64_t>(1024, std::min<uint64_t>(chunk, 32768));
   // (a row that starts off a 16-byte boundary has up to three places more)
   const uint64_t places = static_cast<uint64_t>(vocab) + 3;
   chunk = std::max(chunk, ((places + kVerifyMaxChunks - 1) / kVerifyMaxChunks + 1023) / 1024 * 1024);

@@ -579,7 +579,7 @@ cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDe
                                         stream, 2 * kOperandImage);
   if (e == cudaSuccess)
     e = launch_operand_decode(up, 0, p.N, a.scale_kind, a.up_scales, a.group_k, images + kOperandImage, a.status, p.sms,
-                              stream, 2 * kOperandImage);
+                              stream, 2 * kOperandImage, true);
   if (e == cudaSuccess && p.f16) e = launch_row_prep(a.X, p.M, p.K, 0, nullptr, true, x16, factor, stream);
   if (e == cudaSuccess && bounds) {
     const uint32_t dt = gate.dtype;

@@ -51,6 +51,7 @@ struct OperandDev {
   uint32_t block0;               // its first 128-row block
   uint8_t* images;
   uint32_t step;                 // bytes from an image to the next
+  uint32_t beside;               // does not wait for the kernel before it
   uint32_t* status;
 };
 
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kOpThreads, 1) operand_decode_kernel(const __g
   if (!single) build_lut(lut, L, warp, cta_warps, lane);
   __syncthreads();
   // the prologue above read only kernel parameters
-  griddep_wait();
+  if (P.beside == 0) griddep_wait();
   griddep_launch_dependents();
 
   volatile uint32_t* abort = &abort_flag;
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(kOpThreads, 1) operand_decode_kernel(const __g
   }
   rp_drain(pipe, P.status);
   if (lane == 0) bulk_wait_all();
+  if (P.beside != 0) griddep_beside_end();
 }
 
 template <uint32_t DT, bool kWide>
@@ -285,7 +287,8 @@ uint32_t operand_decode_rounds(uint32_t tiles, uint32_t ctas) {
 
 cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t rows, uint32_t scale_kind,
                                   const void* scales, uint32_t group_k, uint8_t* images,
-                                  uint32_t* status, int sms, cudaStream_t stream, uint32_t step) {
+                                  uint32_t* status, int sms, cudaStream_t stream, uint32_t step,
+                                  bool beside) {
   if (rows == 0) return cudaSuccess;
   OperandDev P;
   std::memset(&P, 0, sizeof(P));
@@ -300,6 +303,7 @@ cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t row
   P.block0 = row0 / 128;
   P.images = images;
   P.step = step;
+  P.beside = beside ? 1u : 0u;
   P.status = status;
   // one CTA an SM (with fewer tiles than that, one tile a CTA), and the fewest
   // warps that need no more rounds of tiles than the most warps would

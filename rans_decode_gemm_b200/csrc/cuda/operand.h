@@ -24,12 +24,14 @@ inline bool operand_is_f16(uint32_t dtype) { return dtype != 1; }
 inline size_t operand_bytes(uint64_t rows, uint32_t K) { return static_cast<size_t>(rows) * K * 2; }
 
 // Decodes row blocks [row0, row0 + rows) (multiples of tile_n) into images, one
-// every `step` bytes (two layers' images may lie side by side).
+// every `step` bytes (two layers' images may lie side by side).  beside: starts as the
+// decoding before it leaves SMs free and does not wait for it (griddep_beside() in
+// ptx.cuh), whose images it does not touch.
 constexpr uint32_t kOperandImage = 4096;
 cudaError_t launch_operand_decode(const LayerDev& L, uint32_t row0, uint32_t rows,
                                   uint32_t scale_kind, const void* scales, uint32_t group_k,
                                   uint8_t* images, uint32_t* status, int sms, cudaStream_t stream,
-                                  uint32_t step = kOperandImage);
+                                  uint32_t step = kOperandImage, bool beside = false);
 
 // Rounds of tiles that decoding them takes on that many SMs.
 uint32_t operand_decode_rounds(uint32_t tiles, uint32_t ctas);

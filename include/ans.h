@@ -568,8 +568,8 @@ ans_status ans_distill_workspace(const ans_layout* layout, uint32_t M, ans_scale
  * (S = 1).  A row that is listed more than once has the sum of its shares.
  * X bf16 M x K; loss and lse fp32 [M]; dX bf16 M x K (NULL: loss only), the gradient
  * of sum_m g[m] loss[m] with g = d_weight fp32 [M] (NULL: 1; read with d_dX only); it
- * is not times T^2.  A token that lists nothing has loss 0 and a zero dX; its lse is
- * written.  An entry whose t_j is 0 (v_j = -infinity) has no part in the loss.  A
+ * is not times T^2.  A token that lists nothing (or nothing above -infinity) has loss 0 and a
+ * zero dX; its lse is written.  An entry whose t_j is 0 (v_j = -infinity) has no part in the loss.  A
  * token whose lse is not finite has NaN in dX, if it lists anything.  An index of
  * vocab or more sets ANS_STATUS_BAD_INDEX and lists nothing.  Probabilities and
  * listed coefficients S p - t (taken in 64 bits) are rounded once, to 16 bits, as

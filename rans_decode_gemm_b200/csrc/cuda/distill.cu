@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kDiThreads) distill_begin_kernel(const __grid_
     __syncthreads();
     s = 0.0;
     for (uint32_t k = 0; k < kDiThreads / 32; ++k) s += part[k][1];
-    norm = from + log(s);
+    norm = top == -INFINITY ? 0.0 : from + log(s);  // (nothing above -infinity: all shares are 0)
   }
   // every entry's share, and its part of sum t log t
   double sum = 0.0, self = 0.0;
@@ -412,12 +412,21 @@ __global__ void __launch_bounds__(256) distill_rows_kernel(const __grid_constant
     const float4 u = __ldcg(q), v = __ldcg(q + 1);
     r[0] = u.x; r[1] = u.z; r[2] = v.x; r[3] = v.z;
   }
+  // what the four tokens need is asked for together: their references and shifts, a lane
+  // each, and their lists' first 32 entries
+  const bool mine = lane < 4 && row0 + lane < P.m;
+  const float my_ref = mine ? __ldcg(P.ref + row0 + lane) : 0.0f;
+  const int32_t my_shift = mine ? __ldcg(P.shift + row0 + lane) : 0;
+  int32_t list[4];
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k)
+    list[k] = lane < P.top && row0 + k < P.m ? __ldcg(P.sorted + static_cast<uint64_t>(row0 + k) * P.top + lane) : -1;
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k) {
     const uint32_t col = row0 + k;
     if (col >= P.m) break;
-    const float ref = __ldcg(P.ref + col);
-    const int32_t shift = __ldcg(P.shift + col);
+    const float ref = __shfl_sync(0xFFFFFFFFu, my_ref, k);
+    const int32_t shift = __shfl_sync(0xFFFFFFFFu, my_shift, k);
     const bool drop = shift == kDropRow;
     const float f = !b_in ? 1.0f : drop ? 0.0f : pow2f_whole(r[k] - ref - static_cast<float>(shift));
     const uint64_t at = static_cast<uint64_t>(col) * P.rows + 1024ull * blockIdx.y;
@@ -462,9 +471,12 @@ __global__ void __launch_bounds__(256) distill_rows_kernel(const __grid_constant
     __syncwarp();
     for (uint32_t q = 0; q < P.top; q += 32) {
       const uint32_t j = q + lane;
-      const int32_t n = j < P.top ? __ldcg(P.sorted + static_cast<uint64_t>(col) * P.top + j) : -1;
+      int32_t n = list[k];
+      if (q != 0) n = j < P.top ? __ldcg(P.sorted + static_cast<uint64_t>(col) * P.top + j) : -1;
       const uint32_t c = static_cast<uint32_t>(n) - 1024u * blockIdx.y;
       if (n >= 0 && c < 1024u) P.probs[at + c] = to_operand(__ldcg(P.coef + static_cast<uint64_t>(col) * P.top + j), P.f16);
+      // (in order: the rest lie behind these columns)
+      if (__any_sync(0xFFFFFFFFu, n < 0 || (n >= 0 && static_cast<uint32_t>(n) >= 1024u * (blockIdx.y + 1)))) break;
     }
   }
 }

@@ -62,8 +62,8 @@ __device__ __forceinline__ void activation(uint32_t act, float g, float& value, 
     const float e = __expf(-y);
     const float p = __fdividef(1.0f, 1.0f + e);  // (0 from 2^126 on)
     value = g * p;
-    // p' = p (1 - p) y', and 1 - p = e p
-    if (kSlope) slope = e > 1e30f ? 0.0f : fmaf(g * dy, p * (e * p), p);
+    // p' = p (1 - p) y', and 1 - p = e p (far out there is nothing of it, and g y' may be infinite)
+    if (kSlope) slope = e > 1e30f || e < 1e-30f ? p : fmaf(g * dy, p * (e * p), p);
   }
 }
 
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
               activation<kGrad>(P.act, gv, value, slope);
               if (kGrad) {
                 const float dh = __uint_as_float(h ? dw[i] & 0xFFFF0000u : dw[i] << 16);
-                r[h] = dh * uv * slope;
+                r[h] = dh * (uv * slope);
                 r2[h] = dh * value;
               } else {
                 r[h] = value * uv;

@@ -174,13 +174,16 @@ def test_entries_of_no_mass_and_far_logits(cuda):
     ids[6, 0], logits[6, 0] = 9, 0.0
     rest = torch.full((24,), 1.0)
     x = leaning(L, rng, 24, ids)
-    # (a token whose entries all are -infinity has no shares to speak of without the teacher's lse)
     ids[1] = -1
     check(L, x, 384, 1.0, ids, logits)
     logits[5] -= 3e4
     ids[1, 4] = 7
     logits[1] = -torch.inf
     check(L, x, 384, 1.0, ids, logits, rest)
+    # nothing above -infinity: nothing is listed, with the teacher's lse and without
+    for lse in (rest, None):
+        loss, _, dx = run(L, x, 384, 1.0, ids, logits, lse)
+        assert loss[1] == 0 and not dx[1].any()
 
 
 @pytest.mark.parametrize("dtype", [ans.BF16_SPLIT, ans.INT8, ans.FP4_PAIRS])

@@ -207,6 +207,28 @@ def test_large_and_small_values(cuda):
 
 
 @pytest.mark.parametrize("M", [6, 50])
+def test_slopes_far_out(cuda, M):
+    """G of 1e13 to 1e20 either way: the activations are g or 0 there, and their slopes 1 or 0."""
+    B = Block(ans.BF16_SPLIT, 128, 16, seed=9)
+    x, dh = inputs(B, M, 9)
+    for size in (1e15, 1e18, 1e20):
+        big = (x.float() * size).bfloat16()
+        small = (dh.float() * 1e-20).bfloat16()
+        for act in ACTS:
+            _, dg, du = run_grad(B, big, small, act)
+            g, u = big.double() @ B.gate.w.T, big.double() @ B.up.w.T
+            d = small.double()
+            clear = g.abs() > size * 0.02   # (away from 0, whose slopes are between)
+            rel = 2 * BF16
+            for got, want in ((dg, torch.where(g > 0, d * u, 0.0)), (du, torch.where(g > 0, d * g, 0.0))):
+                got = got.cpu().double()
+                assert torch.isfinite(got).all()
+                off = (got - want).abs()
+                # G and U: fp32 sums of 16 products
+                assert (off <= rel * want.abs() + d.abs() * size * 2.0 ** -16)[clear].all()
+
+
+@pytest.mark.parametrize("M", [6, 50])
 def test_not_finite_stays_with_its_token(cuda, M):
     B = Block(ans.FP8_E4M3, 256, 128)
     x, dh = inputs(B, M, 6)

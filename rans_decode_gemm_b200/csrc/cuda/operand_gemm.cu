@@ -64,6 +64,7 @@ struct OperandGemmDev {
   CUtensorMap tmap_a;  // transposed: images as rows of 512 eight-byte words, boxes of 256 x 8
   CUtensorMap tmap_b2, tmap_a2;  // transposed: the second layer's, from stage half_kb on
   uint32_t half_kb;
+  uint32_t seg_kb;       // lists: stages that one of 256 / bn accumulators takes
   OperandGemmOut out;
   XentEpilogue xent;
   uint32_t f16;
@@ -323,7 +324,8 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
         const uint32_t b = acc & 1u;
         if (acc >= 2 && !wait_live(&acc_empty[b], ((acc >> 1) + 1) & 1u, abort, P.status, 21)) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + b * 256;
+        uint32_t d_tmem = tmem_base + b * 256;
+        [[maybe_unused]] uint32_t seg_end = P.seg_kb;
         // the last token block is narrower when M is not a multiple of bn
         const uint32_t idesc = mb == P.m_blocks - 1 ? P.idesc_tail : P.idesc;
         for (uint32_t kb = kb0; kb < kb1; ++kb) {
@@ -333,12 +335,22 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
           }
           tc_fence_after();
           const uint32_t a16 = (smem_s + s * P.stage_bytes) >> 4, b16 = a16 + (kOgABytes >> 4);
+          bool fresh = kb == kb0;
+          if constexpr (kLists) {
+            // narrow tiles leave columns free: a sum in several accumulators, which the
+            // epilogue adds, loses less to the truncation of each step
+            if (kb == seg_end) {
+              fresh = true;
+              seg_end += P.seg_kb;
+              d_tmem += P.bn;
+            }
+          }
           const uint32_t cnt = kTrans ? 4u : min(4u, P.k_slabs - 4 * kb);
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j)
             if (j < cnt)
               umma_f16(d_tmem, da | (a16 + j * ((kTrans ? 512u : kSlabBytes) >> 4)), db | (b16 + 2 * j), idesc,
-                       (kb != kb0 || j != 0) ? 1u : 0u);
+                       (!fresh || j != 0) ? 1u : 0u);
           umma_commit(&empty[s]);
           if (++s == n_st) {
             s = 0;
@@ -415,6 +427,15 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
         uint32_t v[32];
         tmem_ld32(tmem_base + ((32 * quad) << 16) + b * 256 + c0, v);
         tmem_ld_wait();
+        if constexpr (kLists) {
+          for (uint32_t q = P.seg_kb, at = P.bn; q < P.n_kb; q += P.seg_kb, at += P.bn) {
+            uint32_t more[32];
+            tmem_ld32(tmem_base + ((32 * quad) << 16) + b * 256 + at + c0, more);
+            tmem_ld_wait();
+#pragma unroll
+            for (uint32_t j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(more[j]));
+          }
+        }
         if (c0 + 64 >= cols) {
           // this warp has read its last of the tile's sums
           tc_fence_before();
@@ -576,6 +597,7 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
   const uint32_t red = plan.trans ? plan.rows : plan.K;
   P.n_kb = (red + kOgBK - 1) / kOgBK;
   P.n_tiles = (P.out_cols + kOgBM - 1) / kOgBM * P.m_blocks * P.splits;
+  P.seg_kb = (P.n_kb + 256 / plan.bn - 1) / (256 / plan.bn);
   P.b_box_rows = std::min(plan.M, plan.bn);
   P.stage_bytes = kOgABytes + plan.bn * kOgBK * 2;
   P.stages = std::min(kOgMaxStages, kOgSmemTiles / P.stage_bytes);

@@ -10,7 +10,7 @@
 // dG_n and dU_n, take.  G and U never reach memory; the gradient computes them
 // again.  dX is one transposed product over both layers' rows (operand_gemm.cu).
 //
-// A stage holds 64 steps of the sum: 16 KB of tokens by TMA (128-byte swizzle) and
+// A stage of a wide tile holds 64 steps of the sum: 16 KB of tokens by TMA (128-byte swizzle) and
 // 32 KB of images by one copy.  An image's rows are K-major under the 32-byte
 // swizzle, so 8 KB of a gate and an up image are one 256-row operand.  Where the tiles
 // would leave SMs idle they are of 64 or 32 rows: a box of that part of each of eight
@@ -33,8 +33,12 @@ namespace ansdev {
 
 constexpr uint32_t kGaBM = 128, kGaBK = 64;
 constexpr uint32_t kGaABytes = kGaBM * kGaBK * 2;           // 16 KB of tokens
-// kBN rows of both layers
-__host__ __device__ constexpr uint32_t ga_stage_bytes(uint32_t bn) { return kGaABytes + 2 * bn * kGaBK * 2; }
+// kBN rows of both layers; narrow tiles take two blocks of 64 a stage, whose MMAs are as
+// short as a stage's barriers are long (int4 14336 x 4096, 2048 tokens in tiles of 64 rows:
+// 539 us, with a block a stage 699)
+__host__ __device__ constexpr uint32_t ga_block_bytes(uint32_t bn) { return kGaABytes + 2 * bn * kGaBK * 2; }
+__host__ __device__ constexpr uint32_t ga_blocks(uint32_t bn) { return bn == 128 ? 1u : 2u; }
+__host__ __device__ constexpr uint32_t ga_stage_bytes(uint32_t bn) { return ga_blocks(bn) * ga_block_bytes(bn); }
 __host__ __device__ constexpr uint32_t ga_stages(uint32_t bn) { return 192 * 1024 / ga_stage_bytes(bn); }
 constexpr uint32_t kGaSmem = 192 * 1024 + 1024;
 constexpr uint32_t kGaEpiWarps = 16;
@@ -127,6 +131,7 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
 template <bool kGrad, uint32_t kBN>
 __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_constant__ GatedDev P) {
   constexpr uint32_t kGaStages = ga_stages(kBN), kGaStageBytes = ga_stage_bytes(kBN);
+  constexpr uint32_t kBlocks = ga_blocks(kBN), kBlockBytes = ga_block_bytes(kBN);
   extern __shared__ __align__(1024) uint8_t dsmem_raw[];
   __shared__ __align__(8) uint64_t full[kGaStages], empty[kGaStages];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_done;
@@ -173,27 +178,35 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
       bool live = true;
       for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x) {
         const uint32_t ab = t / P.m_blocks, mb = t - ab * P.m_blocks;
-        for (uint32_t kb = 0; kb < P.n_kb; ++kb, ++it) {
+        for (uint32_t kb0 = 0; kb0 < P.n_kb; kb0 += kBlocks, ++it) {
           if (it >= kGaStages && !wait_live(&empty[s], ph, abort, P.status, 20)) {
             live = false;
             break;
           }
           const uint32_t bar = smem_u32(&full[s]);
-          const uint32_t a_s = smem_s + s * kGaStageBytes, b_s = a_s + kGaABytes;
+          const uint32_t here = min(kBlocks, P.n_kb - kb0);
           if constexpr (kBN == 128) {
-            const uint32_t bytes = min(4u, P.k_slabs - 4 * kb) * 2 * kSlabBytes;
+            const uint32_t bytes = min(4u, P.k_slabs - 4 * kb0) * 2 * kSlabBytes;
             mbar_arrive_expect_tx_s(bar, bytes + P.box_rows * kGaBK * 2);
-            bulk_g2s_s(b_s, P.images + (static_cast<uint64_t>(ab) * P.k_slabs + 4 * kb) * 2 * kSlabBytes, bytes, bar);
+            bulk_g2s_s(smem_s + s * kGaStageBytes + kGaABytes,
+                       P.images + (static_cast<uint64_t>(ab) * P.k_slabs + 4 * kb0) * 2 * kSlabBytes, bytes, bar);
           } else {
-            // (where the last block of k holds fewer images, the box runs into the next
-            // row block's, or is filled with zeros: operands that no MMA takes)
-            constexpr uint32_t kParts = 128 / kBN;
-            const uint32_t block = ab / kParts, part = ab - block * kParts;
-            mbar_arrive_expect_tx_s(bar, kGaStageBytes - kGaABytes + P.box_rows * kGaBK * 2);
-            tma_load_2d_s(b_s, &P.tmap_w, static_cast<int32_t>(part * kBN * 4),
-                          static_cast<int32_t>(2 * (block * P.k_slabs + 4 * kb)), bar);
+            mbar_arrive_expect_tx_s(bar, here * (kBlockBytes - kGaABytes + P.box_rows * kGaBK * 2));
           }
-          tma_load_2d_s(a_s, &P.tmap_x, static_cast<int32_t>(kb * kGaBK), static_cast<int32_t>(mb * kGaBM), bar);
+#pragma unroll
+          for (uint32_t q = 0; q < kBlocks; ++q) {
+            if (q >= here) break;
+            const uint32_t kb = kb0 + q, a_s = smem_s + s * kGaStageBytes + q * kBlockBytes;
+            if constexpr (kBN < 128) {
+              // (where the last block of k holds fewer images, the box runs into the next
+              // row block's, or is filled with zeros: operands that no MMA takes)
+              constexpr uint32_t kParts = 128 / kBN;
+              const uint32_t block = ab / kParts, part = ab - block * kParts;
+              tma_load_2d_s(a_s + kGaABytes, &P.tmap_w, static_cast<int32_t>(part * kBN * 4),
+                            static_cast<int32_t>(2 * (block * P.k_slabs + 4 * kb)), bar);
+            }
+            tma_load_2d_s(a_s, &P.tmap_x, static_cast<int32_t>(kb * kGaBK), static_cast<int32_t>(mb * kGaBM), bar);
+          }
           if (++s == kGaStages) {
             s = 0;
             ph ^= 1u;
@@ -221,19 +234,23 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + b * 2 * kBN;
         const uint32_t idesc = idesc_f16(P.f16 ? 0u : 1u, 128, 2 * kBN);
-        for (uint32_t kb = 0; kb < P.n_kb; ++kb) {
+        for (uint32_t kb0 = 0; kb0 < P.n_kb; kb0 += kBlocks) {
           if (!wait_live(&full[s], ph, abort, P.status, 22)) {
             live = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a16 = (smem_s + s * kGaStageBytes) >> 4, b16 = a16 + (kGaABytes >> 4);
-          const uint32_t cnt = min(4u, P.k_slabs - 4 * kb);
 #pragma unroll
-          for (uint32_t j = 0; j < 4; ++j)
-            if (j < cnt)
-              umma_f16(d_tmem, da | (a16 + 2 * j), db | (b16 + j * (kBN * 64 >> 4)), idesc,
-                       (kb != 0 || j != 0) ? 1u : 0u);
+          for (uint32_t q = 0; q < kBlocks; ++q) {
+            if (kb0 + q >= P.n_kb) break;
+            const uint32_t a16 = (smem_s + s * kGaStageBytes + q * kBlockBytes) >> 4, b16 = a16 + (kGaABytes >> 4);
+            const uint32_t cnt = min(4u, P.k_slabs - 4 * (kb0 + q));
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+              if (j < cnt)
+                umma_f16(d_tmem, da | (a16 + 2 * j), db | (b16 + j * (kBN * 64 >> 4)), idesc,
+                         (kb0 + q != 0 || j != 0) ? 1u : 0u);
+          }
           umma_commit(&empty[s]);
           if (++s == kGaStages) {
             s = 0;
@@ -247,7 +264,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
     }
     __syncwarp();
   } else {
-    // ======================= epilogue (warps 2-9) =======================
+    // ======================= epilogue (warps 2-17) =======================
     // a token a lane; four warps for each quarter of TMEM's lanes, which take the tile's
     // rows in turn, 16 at a time
     const uint32_t quad = warp & 3u, turn = (warp - 2) >> 2;
@@ -485,11 +502,12 @@ __global__ void __launch_bounds__(256) gated_bound_kernel(const uint16_t* __rest
 
 static size_t aligned(size_t n) { return (n + 1023) / 1024 * 1024; }
 
-// The tile's rows: rounds of tiles over the SMs, at 395, 345 and 335 ns a stage (a
-// narrow tile's hardly take less, so that it only serves to fill the SMs), and the
-// last epilogue, which nothing hides: 16, 8 and 5 us with the gradient.  (4096 x 4096
-// int4 with the gradient: 200 tokens 140, 128 and 141 us by tiles of 128, 64 and 32
-// rows; 301 tokens 152, 157 and 176; 1024 x 1024, 40 tokens: 87, 76 and 76.)
+// The tile's rows: rounds of tiles over the SMs, at 395, 277 and 259 ns for 64 steps of
+// the sum (a narrow tile's take more a row, so that it only serves to fill the SMs), and
+// the last epilogue, which nothing hides: 16, 8 and 5 us with the gradient.  (int4 with
+// the gradient, by tiles of 128, 64 and 32 rows: 4096 x 4096, 200 tokens 120, 101 and
+// 111 us, 301 tokens 130, 126 and 139; 14336 x 4096, 2048 tokens 921, 997 and 1,321;
+// 1024 x 1024, 40 tokens 70, 57 and 57.)
 static uint32_t gated_rows_of_tile(uint32_t M, uint32_t N, uint32_t K, bool grad, uint32_t sms) {
   const uint64_t m_blocks = (M + kGaBM - 1) / kGaBM, n_kb = (K + kGaBK - 1) / kGaBK;
   uint64_t least = ~0ull;
@@ -497,7 +515,7 @@ static uint32_t gated_rows_of_tile(uint32_t M, uint32_t N, uint32_t K, bool grad
   for (const uint32_t bn : {128u, 64u, 32u}) {
     const uint64_t rounds = (N / bn * m_blocks + sms - 1) / sms;
     const uint64_t last = bn == 128 ? 16000 : bn == 64 ? 8000 : 5000;
-    const uint64_t cost = rounds * n_kb * (bn == 128 ? 395 : bn == 64 ? 345 : 335) + (grad ? last : last / 4);
+    const uint64_t cost = rounds * n_kb * (bn == 128 ? 395 : bn == 64 ? 277 : 259) + (grad ? last : last / 4);
     if (cost < least) {
       least = cost;
       best = bn;

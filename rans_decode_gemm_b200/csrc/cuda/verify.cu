@@ -503,7 +503,8 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
   __syncthreads();
   // a warp a draft, in turn, and one the row behind the last
   for (uint32_t i = warp; i <= count; i += kVerifyWarps) {
-    if (i > *static_cast<volatile uint32_t*>(&first)) break;
+    // (another warp may write it meanwhile: all lanes go by what one of them read)
+    if (i > __shfl_sync(0xFFFFFFFFu, *static_cast<volatile uint32_t*>(&first), 0)) break;
     const bool has_q = A.draft != nullptr && !greedy && i < count;
     const RowParts pt = row_parts(P, t0 + i, greedy, lane);
     RowParts pd = pt;
@@ -537,6 +538,7 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
       keep = u * eq * t.y < ep * d.y;
     }
     if (!keep && lane == 0) atomicMin(&first, i);
+    __syncwarp();
   }
   __syncthreads();
   const uint32_t stop = first;
@@ -560,7 +562,9 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
     if (lane == 0) row_join[warp] = t;
   }
   if (greedy) {
-    if (rank == 0 && threadIdx.x == 0) A.out[row] = static_cast<int32_t>(row_join[0].y);
+    // (rows that wrong starts give to sequences of other temperatures may hold sums)
+    const double at = row_join[0].y;
+    if (rank == 0 && threadIdx.x == 0) A.out[row] = at >= 0.0 && at < A.vocab ? static_cast<int32_t>(at) : -1;
     return;
   }
   __syncthreads();
@@ -618,6 +622,8 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
     const double aim = v * all;
     double before = 0.0;
     const uint32_t at = first_past(aim, before, [&](uint32_t k) { return cluster_read(&cta_sum[turn], k); });
+    // (a row has some mass, but for one that wrong starts left without sums)
+    if (at == 8 && rank == 0 && threadIdx.x == 0) A.out[row] = -1;
     // (every CTA's sums have been read: it may end when all have come here)
     cluster_arrive();
     if (at != rank) {

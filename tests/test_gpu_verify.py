@@ -269,6 +269,30 @@ def test_tokens_outside_and_starts_that_fall(cuda):
         assert out[6:].tolist() == [-7, -7] and accepted[2] == -7
 
 
+@pytest.mark.parametrize("starts", [[0, 5, 4, 6], [0, 4, 2, 6], [3, 0, 6, 6], [0, -3, 9, 1], [6, 6, 6, 6]])
+@pytest.mark.parametrize("temperature", [[0.0, 1.0, 0.0], [1.0, 0.0, 0.5], [0.0, 0.0, 2.0]])
+def test_wrong_starts_of_greedy_and_other_sequences(cuda, starts, temperature):
+    """Rows that the starts give to two sequences: flagged, and what comes out is a token or -1."""
+    rng = np.random.default_rng(12)
+    vocab = 700
+    target, draft, tokens, u, v = batch(rng, [2, 2, 2], vocab)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    size = ans.ans_verify_workspace(3, 6, vocab)
+    for lookup in (False, True):
+        for fill in (0, 0x7E):
+            out = torch.full((9,), -1, dtype=torch.int32, device="cuda")
+            accepted = torch.zeros(3, dtype=torch.int32, device="cuda")
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+            ans.ans_verify(dev(target), vocab, None if lookup else dev(draft), vocab, 3, 6, vocab,
+                           dev(np.array(starts, np.int32)), dev(tokens.astype(np.int32)), dev(u), dev(v),
+                           dev(np.array(temperature, np.float32)), accepted, out, ws, size, st)
+            torch.cuda.synchronize()
+            assert int(st.item()) == ans.STATUS_BAD_INDEX
+            assert out.min() >= -1 and out.max() < vocab
+            assert accepted.min() >= 0 and accepted.max() <= 6
+
+
 def test_what_comes_out_is_distributed_as_the_target(cuda):
     """Over a grid of u and v and all drafts with their chances, the first token's distribution is p."""
     vocab, grid = 5, 64

@@ -669,6 +669,7 @@ cudaError_t launch_distill(const DistillPlan& p, const LayerDev& L, const Distil
     back.out16 = a.dX + static_cast<uint64_t>(m0) * p.K;
     back.ld = p.K;
     back.beta = beta + m0;
+    back.drops = 1;
     // (the plan that the workspace was made for; fewer rows are cut into no more parts)
     OperandGemmPlan g = plan_operand_gemm(true, p.f16, m, p.N, p.K, p.sms);
     g.rows = all;

@@ -66,6 +66,7 @@ struct OperandGemmOut {
   //   taken for rows with 0 <= ids[m] < n_ids only (add may be null).
   // out32: out32[m * ld + k] = alpha[m] * (its old value) + beta[m] * v;
   //   alpha null: the old value is not read.  beta null: 1.
+  // drops: where beta[m] is 0 the row is, whatever v is (NaN beside infinite weights).
   float* out32;
   uint16_t* out16;
   uint32_t ld;
@@ -74,6 +75,7 @@ struct OperandGemmOut {
   const float* add;
   const int32_t* ids;
   uint32_t n_ids;
+  uint32_t drops;
 };
 
 // What happens to the logits: they are folded into softmax sums, 32 rows of W

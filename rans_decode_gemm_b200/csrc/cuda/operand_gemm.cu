@@ -457,7 +457,10 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
 #pragma unroll
           for (uint32_t j = 0; j < 32; ++j) {
             x[j] = __uint_as_float(v[j]);
-            if (O.beta != nullptr) x[j] *= __shfl_sync(0xFFFFFFFFu, my_beta, j);
+            if (O.beta != nullptr) {
+              const float f = __shfl_sync(0xFFFFFFFFu, my_beta, j);
+              x[j] = O.drops && f == 0.0f ? 0.0f : x[j] * f;
+            }
             if (rmw) x[j] = fmaf(__shfl_sync(0xFFFFFFFFu, my_alpha, j), old[j], x[j]);
             else if (adds) x[j] += old[j];
           }
@@ -522,6 +525,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
   if (O.beta != nullptr) {
     const float f = __ldcg(O.beta + m);
     v.x *= f; v.y *= f; v.z *= f; v.w *= f;
+    if (O.drops && f == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
   if (adds) {
     v.x = fmaf(alpha, old.x, v.x); v.y = fmaf(alpha, old.y, v.y); v.z = fmaf(alpha, old.z, v.z); v.w = fmaf(alpha, old.w, v.w);

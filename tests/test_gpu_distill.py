@@ -268,6 +268,22 @@ def test_not_finite_stays_with_its_token(cuda):
             check(L, x, 500, 1.0, ids, logits)
 
 
+@pytest.mark.parametrize("M", [3, 300])
+def test_nothing_listed_beside_infinite_weights(cuda, M):
+    """A token that lists nothing has a zero gradient whatever the rows of W hold."""
+    rng = np.random.default_rng(21)
+    L = usual(ans.BF16_SPLIT, 256, 64, seed=21)
+    L.codes[17, 5] = 0x7F80
+    L.layer = ans.CompressedLayer.from_weights(L.codes.reshape(-1), L.layout)
+    L.tiles = L.layer.tiles
+    ids, logits = teacher(rng, M, 256, 4)
+    x = leaning(usual(ans.BF16_SPLIT, 256, 64, seed=21), rng, M, ids)
+    ids[0, 0], ids[1] = 7, -1
+    loss, lse, dx = run(L, x, 256, 1.0, ids, logits)
+    assert loss[1] == 0 and (dx[1] == 0).all()
+    assert torch.isnan(dx[0, 5])
+
+
 def test_same_bits_and_capture(cuda):
     rng = np.random.default_rng(13)
     L = usual(ans.FP8_E4M3, 1024, 128, seed=13)

@@ -54,7 +54,23 @@ constexpr uint32_t kOgBM = 128, kOgBK = 64;
 constexpr uint32_t kOgABytes = kOgBM * kOgBK * 2;  // 16 KB
 constexpr uint32_t kOgEpiWarps = 8;
 constexpr uint32_t kOgThreads = (2 + kOgEpiWarps) * 32;
+// Parts: warps 4-11 are the epilogue's, whose sums of 128 tokens stay in registers: 224 a
+// thread, and 56 for the warps before them (128 x 56 + 256 x 224 = 384 x 168, which is what
+// the block is launched with; launch_operand_gemm checks that it is).
+constexpr uint32_t kOgPartThreads = 384, kOgPartRegs = 168;
 constexpr uint32_t kOgMaxStages = 8;
+// The tensor unit truncates each step of a sum: 4096 products in one accumulator are off
+// by 1.5e-6 of a loss where fp32 has 4e-7.  Narrow tiles leave columns of TMEM free and
+// take several accumulators a sum.  Wide tiles of a loss without a gradient take one after
+// another, which the epilogue adds to sums of its own: the first two of 24 stages, which
+// serve while it folds the tile before, the others of 8.  (A loss over 32000 x 4096 bf16,
+// 1000 tokens: off by 4.7e-7 in 497 us, in one accumulator 1.5e-6 in 412; the first two of
+// 16 and 32 stages: 2.6e-7 in 530, 7.5e-7 in 466.)
+constexpr uint32_t kOgFirst = 24, kOgPart = 8;
+__device__ __forceinline__ uint32_t part_end(uint32_t kb, uint32_t n_kb) {
+  return min(n_kb, kb < 2 * kOgFirst ? kb + kOgFirst : kb + kOgPart);
+}
+enum : uint32_t { kOgTargets = 0, kOgLists = 1, kOgListsInParts = 2 };
 constexpr uint32_t kOgSmemTiles = 200 * 1024;  // stages
 constexpr uint32_t kOgSmem = kOgSmemTiles + 1024;
 
@@ -64,7 +80,7 @@ struct OperandGemmDev {
   CUtensorMap tmap_a;  // transposed: images as rows of 512 eight-byte words, boxes of 256 x 8
   CUtensorMap tmap_b2, tmap_a2;  // transposed: the second layer's, from stage half_kb on
   uint32_t half_kb;
-  uint32_t seg_kb;       // lists: stages that one of 256 / bn accumulators takes
+  uint32_t seg_kb;       // lists: stages that one of 256 / bn accumulators takes (narrow tiles)
   OperandGemmOut out;
   XentEpilogue xent;
   uint32_t f16;
@@ -101,11 +117,11 @@ struct XentToken {
   float ref, factor;
   int32_t target;  // (lists: 0 where this block holds rows of the token's, else -1)
 };
-template <bool kLists>
+template <uint32_t kLists>
 __device__ __forceinline__ XentToken xent_token(const XentEpilogue& E, uint32_t c, uint32_t m, bool in) {
   XentToken t;
   t.ref = in ? __ldcg(E.ref_in + m) : 0.0f;
-  if constexpr (kLists) {
+  if constexpr (kLists != kOgTargets) {
     const uint32_t b = (E.n0 + c) / 32;
     const uint32_t word = in ? __ldcg(E.listed + static_cast<uint64_t>(b / 32) * E.listed_stride + m) : 0u;
     t.target = (word >> (b % 32)) & 1u ? 0 : -1;
@@ -115,8 +131,8 @@ __device__ __forceinline__ XentToken xent_token(const XentEpilogue& E, uint32_t 
   t.factor = E.factor != nullptr && in ? __ldcg(E.factor + m) : 1.0f;
   return t;
 }
-template <bool kLists>
-__device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, uint32_t rows, const uint32_t (&v)[32],
+template <uint32_t kLists, typename V>
+__device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, uint32_t rows, const V (&v)[32],
                                           float scale, float lift, uint32_t c, uint32_t m, uint32_t n_tok,
                                           uint32_t lane, const XentToken& tok) {
   constexpr float kLog2E = 1.4426950408889634f;
@@ -128,14 +144,15 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
   float z[32], x[32];
 #pragma unroll
   for (uint32_t j = 0; j < 32; ++j) {
-    z[j] = __uint_as_float(v[j]) * z_scale;
+    if constexpr (kLists == kOgListsInParts) z[j] = v[j] * z_scale;
+    else z[j] = __uint_as_float(v[j]) * z_scale;
     if (E.factor != nullptr) z[j] *= __shfl_sync(0xFFFFFFFFu, factor, j);
     if (!n_in) z[j] = -INFINITY;
   }
   // targets among this warp's rows (one that is past the vocabulary is none): few
   // and far between, so that the loops above and below carry no test for them
   const uint32_t first = E.n0 + c - lane;
-  if constexpr (kLists) {
+  if constexpr (kLists != kOgTargets) {
     for (uint32_t hits = __ballot_sync(0xFFFFFFFFu, target >= 0); hits != 0; hits &= hits - 1) {
       const uint32_t k = __ffs(hits) - 1;
       float zk = 0.0f;
@@ -188,7 +205,7 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x[j]) : "f"(fmaf(z[j], kLog2E, -r)));
   }
   const float ps = n_in ? scale * lift : 0.0f;  // (a padding row's scale may be anything)
-  if (E.probs != nullptr) {
+  if (kLists != kOgListsInParts && E.probs != nullptr) {
     const uint32_t ld = kLists ? E.probs_ld : rows;
     uint16_t* p = E.probs + static_cast<uint64_t>(m) * ld + c;
     auto store = [&](uint32_t j) {
@@ -210,14 +227,17 @@ __device__ __forceinline__ void xent_fold(const XentEpilogue& E, uint32_t f16, u
 }
 
 // kLists: logits with lists in place of targets.
-template <bool kTrans, bool kLists = false>
-__global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __grid_constant__ OperandGemmDev P) {
+template <bool kTrans, uint32_t kLists = kOgTargets>
+__global__ void __launch_bounds__(kLists == kOgListsInParts ? kOgPartThreads : kOgThreads, 1)
+    operand_gemm_kernel(const __grid_constant__ OperandGemmDev P) {
   extern __shared__ __align__(1024) uint8_t dsmem_raw[];
   __shared__ __align__(8) uint64_t full[kOgMaxStages], empty[kOgMaxStages];
   __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t abort_flag;
 
+  constexpr bool kParts = kLists == kOgListsInParts;
+  constexpr uint32_t kFirstEpi = kParts ? 4 : 2;
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // stages on a 1024-byte boundary (the 128-byte swizzle atom)
   const uint32_t smem_s = (smem_u32(dsmem_raw) + 1023u) & ~1023u;
@@ -263,114 +283,132 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
     kb1 = cta_begin(P.n_kb, P.splits, sp + 1);
   };
 
-  if (warp == 0) {
-    // ======================= loads =======================
-    if (lane == 0) {
-      uint32_t it = 0, s = 0, ph = 1;  // the first pass over the ring finds it free
-      bool live = true;
-      for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x) {
-        uint32_t ab, mb, sp, kb0, kb1;
-        tile_of(t, ab, mb, sp, kb0, kb1);
-        for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
-          if (it >= n_st && !wait_live(&empty[s], ph, abort, P.status, 20)) {
-            live = false;
-            break;
-          }
-          const uint32_t bar = smem_u32(&full[s]);
-          const uint32_t a_s = smem_s + s * P.stage_bytes, b_s = a_s + kOgABytes;
-          const bool second = kTrans && kb >= P.half_kb;
-          const uint32_t kl = second ? kb - P.half_kb : kb;
-          if (kTrans) {
-            // half of each of eight images in one box.  Where the last block
-            // of k holds fewer, the box runs into the next row block's (or, at
-            // the end, is filled with zeros): rows of D that are never stored.
-            mbar_arrive_expect_tx_s(bar, kOgABytes + P.b_box_rows * kOgBK * 2);
-            tma_load_2d_s(a_s, second ? &P.tmap_a2 : &P.tmap_a, static_cast<int32_t>((kl & 1u) * 256u),
-                          static_cast<int32_t>((kl >> 1) * P.k_slabs + 8 * ab), bar);
-          } else {
-            const uint32_t cnt = min(4u, P.k_slabs - 4 * kb);
-            mbar_arrive_expect_tx_s(bar, cnt * kSlabBytes + P.b_box_rows * kOgBK * 2);
-            bulk_g2s_s(a_s, P.images + (static_cast<uint64_t>(ab) * P.k_slabs + 4 * kb) * kSlabBytes,
-                       cnt * kSlabBytes, bar);
-          }
-          tma_load_2d_s(b_s, second ? &P.tmap_b2 : &P.tmap_b, static_cast<int32_t>(kl * kOgBK),
-                        static_cast<int32_t>(mb * P.bn), bar);
-          if (++s == n_st) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-      }
-      // loads still in flight (only after an abort) land before exit
-      const uint32_t first = it > n_st ? it - n_st : 0;
-      for (uint32_t q = first; q < it; ++q) wait_drain(&full[q % n_st], (q / n_st) & 1u, P.status);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ======================= MMA issue =======================
-    if (lane == 0) {
-      // logits A: K-major, 8-row groups 256 B apart (SBO), image j of a stage
-      // is its K = 16 slice j.  Transposed A: MN-major, atoms of 16 k 2 KB
-      // apart (LBO), 8-row groups of n 256 B apart (SBO); the K = 16 slice j
-      // starts 16 rows (512 B) further.  B: 128-byte swizzle, 8-row groups
-      // 1024 B apart, slice j 32 j bytes into each row.
-      const uint64_t da = (kTrans ? (128ull << 16) : (1ull << 16)) | (16ull << 32) | (1ull << 46) | (6ull << 61);
-      const uint64_t db = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-      uint32_t s = 0, ph = 0, acc = 0;
-      bool live = true;
-      for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x, ++acc) {
-        uint32_t ab, mb, sp, kb0, kb1;
-        tile_of(t, ab, mb, sp, kb0, kb1);
-        const uint32_t b = acc & 1u;
-        if (acc >= 2 && !wait_live(&acc_empty[b], ((acc >> 1) + 1) & 1u, abort, P.status, 21)) break;
-        tc_fence_after();
-        uint32_t d_tmem = tmem_base + b * 256;
-        [[maybe_unused]] uint32_t seg_end = P.seg_kb;
-        // the last token block is narrower when M is not a multiple of bn
-        const uint32_t idesc = mb == P.m_blocks - 1 ? P.idesc_tail : P.idesc;
-        for (uint32_t kb = kb0; kb < kb1; ++kb) {
-          if (!wait_live(&full[s], ph, abort, P.status, 22)) {
-            live = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a16 = (smem_s + s * P.stage_bytes) >> 4, b16 = a16 + (kOgABytes >> 4);
-          bool fresh = kb == kb0;
-          if constexpr (kLists) {
-            // narrow tiles leave columns free: a sum in several accumulators, which the
-            // epilogue adds, loses less to the truncation of each step
-            if (kb == seg_end) {
-              fresh = true;
-              seg_end += P.seg_kb;
-              d_tmem += P.bn;
+  if (warp < kFirstEpi) {
+    if constexpr (kParts) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // ======================= loads =======================
+      if (lane == 0) {
+        uint32_t it = 0, s = 0, ph = 1;  // the first pass over the ring finds it free
+        bool live = true;
+        for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x) {
+          uint32_t ab, mb, sp, kb0, kb1;
+          tile_of(t, ab, mb, sp, kb0, kb1);
+          for (uint32_t kb = kb0; kb < kb1; ++kb, ++it) {
+            if (it >= n_st && !wait_live(&empty[s], ph, abort, P.status, 20)) {
+              live = false;
+              break;
+            }
+            const uint32_t bar = smem_u32(&full[s]);
+            const uint32_t a_s = smem_s + s * P.stage_bytes, b_s = a_s + kOgABytes;
+            const bool second = kTrans && kb >= P.half_kb;
+            const uint32_t kl = second ? kb - P.half_kb : kb;
+            if (kTrans) {
+              // half of each of eight images in one box.  Where the last block
+              // of k holds fewer, the box runs into the next row block's (or, at
+              // the end, is filled with zeros): rows of D that are never stored.
+              mbar_arrive_expect_tx_s(bar, kOgABytes + P.b_box_rows * kOgBK * 2);
+              tma_load_2d_s(a_s, second ? &P.tmap_a2 : &P.tmap_a, static_cast<int32_t>((kl & 1u) * 256u),
+                            static_cast<int32_t>((kl >> 1) * P.k_slabs + 8 * ab), bar);
+            } else {
+              const uint32_t cnt = min(4u, P.k_slabs - 4 * kb);
+              mbar_arrive_expect_tx_s(bar, cnt * kSlabBytes + P.b_box_rows * kOgBK * 2);
+              bulk_g2s_s(a_s, P.images + (static_cast<uint64_t>(ab) * P.k_slabs + 4 * kb) * kSlabBytes,
+                         cnt * kSlabBytes, bar);
+            }
+            tma_load_2d_s(b_s, second ? &P.tmap_b2 : &P.tmap_b, static_cast<int32_t>(kl * kOgBK),
+                          static_cast<int32_t>(mb * P.bn), bar);
+            if (++s == n_st) {
+              s = 0;
+              ph ^= 1u;
             }
           }
-          const uint32_t cnt = kTrans ? 4u : min(4u, P.k_slabs - 4 * kb);
-#pragma unroll
-          for (uint32_t j = 0; j < 4; ++j)
-            if (j < cnt)
-              umma_f16(d_tmem, da | (a16 + j * ((kTrans ? 512u : kSlabBytes) >> 4)), db | (b16 + 2 * j), idesc,
-                       (!fresh || j != 0) ? 1u : 0u);
-          umma_commit(&empty[s]);
-          if (++s == n_st) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
-        if (live) umma_commit(&acc_full[b]);
+        // loads still in flight (only after an abort) land before exit
+        const uint32_t first = it > n_st ? it - n_st : 0;
+        for (uint32_t q = first; q < it; ++q) wait_drain(&full[q % n_st], (q / n_st) & 1u, P.status);
       }
-      umma_commit(&mma_done);
-      wait_drain(&mma_done, 0, P.status);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ======================= MMA issue =======================
+      if (lane == 0) {
+        // logits A: K-major, 8-row groups 256 B apart (SBO), image j of a stage
+        // is its K = 16 slice j.  Transposed A: MN-major, atoms of 16 k 2 KB
+        // apart (LBO), 8-row groups of n 256 B apart (SBO); the K = 16 slice j
+        // starts 16 rows (512 B) further.  B: 128-byte swizzle, 8-row groups
+        // 1024 B apart, slice j 32 j bytes into each row.
+        const uint64_t da = (kTrans ? (128ull << 16) : (1ull << 16)) | (16ull << 32) | (1ull << 46) | (6ull << 61);
+        const uint64_t db = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+        uint32_t s = 0, ph = 0, acc = 0;
+        bool live = true;
+        for (uint32_t t = blockIdx.x; t < P.n_tiles && live; t += gridDim.x, ++acc) {
+          uint32_t ab, mb, sp, kb0, kb1;
+          tile_of(t, ab, mb, sp, kb0, kb1);
+          uint32_t b = acc & 1u;
+          if (acc >= 2 && !wait_live(&acc_empty[b], ((acc >> 1) + 1) & 1u, abort, P.status, 21)) break;
+          tc_fence_after();
+          uint32_t d_tmem = tmem_base + b * 256;
+          [[maybe_unused]] uint32_t seg_end = kParts ? part_end(0, P.n_kb) : P.seg_kb;
+          // the last token block is narrower when M is not a multiple of bn
+          const uint32_t idesc = mb == P.m_blocks - 1 ? P.idesc_tail : P.idesc;
+          for (uint32_t kb = kb0; kb < kb1; ++kb) {
+            bool fresh = kb == kb0;
+            if constexpr (kParts) {
+              if (kb == seg_end) {
+                fresh = true;
+                seg_end = part_end(kb, kb1);
+                umma_commit(&acc_full[b]);
+                b = ++acc & 1u;
+                if (acc >= 2 && !wait_live(&acc_empty[b], ((acc >> 1) + 1) & 1u, abort, P.status, 21)) {
+                  live = false;
+                  break;
+                }
+                tc_fence_after();
+                d_tmem = tmem_base + b * 256;
+              }
+            }
+            if (!wait_live(&full[s], ph, abort, P.status, 22)) {
+              live = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a16 = (smem_s + s * P.stage_bytes) >> 4, b16 = a16 + (kOgABytes >> 4);
+            if constexpr (kLists == kOgLists) {
+              // narrow tiles leave columns free: a sum in several accumulators, which the
+              // epilogue adds, loses less to the truncation of each step
+              if (kb == seg_end) {
+                fresh = true;
+                seg_end += P.seg_kb;
+                d_tmem += P.bn;
+              }
+            }
+            const uint32_t cnt = kTrans ? 4u : min(4u, P.k_slabs - 4 * kb);
+  #pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+              if (j < cnt)
+                umma_f16(d_tmem, da | (a16 + j * ((kTrans ? 512u : kSlabBytes) >> 4)), db | (b16 + 2 * j), idesc,
+                         (!fresh || j != 0) ? 1u : 0u);
+            umma_commit(&empty[s]);
+            if (++s == n_st) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          if (live) umma_commit(&acc_full[b]);
+        }
+        umma_commit(&mma_done);
+        wait_drain(&mma_done, 0, P.status);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
-    // ======================= epilogue (warps 2-9) =======================
+    if constexpr (kParts) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ======================= epilogue (warps 2-9, in parts 4-11) =======================
     // 32 tokens at a time.  Transposed: what is read of global memory for them
     // (the old values or the addend, 32 independent loads; the tokens' factors,
     // one a lane) is asked for before the previous 32 are stored, and for a
     // tile's first 32 before its sums are ready.  Logits: likewise the tokens'
     // references, targets and factors.
-    const uint32_t quad = warp & 3u, turn = 32u * ((warp - 2) >> 2);
+    const uint32_t quad = warp & 3u, turn = 32u * ((warp - kFirstEpi) >> 2);
     const OperandGemmOut& O = P.out;
     // (a part of a sum that is cut goes to memory as it is)
     const bool cut = kTrans && P.splits > 1;
@@ -419,6 +457,42 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
         }
       };
       if (turn < cols) ask(turn);
+      if constexpr (kParts) {
+        // (32 tokens each: 64 apart, up to 256)
+        float held[4][32];
+        bool whole = true;
+        for (uint32_t kb = 0; kb < P.n_kb; kb = part_end(kb, P.n_kb)) {
+          if (kb != 0) ++acc;
+          const uint32_t p = acc & 1u;
+          whole = wait_live(&acc_full[p], (acc >> 1) & 1u, abort, P.status, 23, 64);
+          tc_fence_after();
+          whole = __all_sync(0xFFFFFFFFu, whole);
+          if (!whole) break;
+#pragma unroll
+          for (uint32_t q = 0; q < 4; ++q) {
+            if (turn + 64 * q >= cols) break;
+            uint32_t v[32];
+            tmem_ld32(tmem_base + ((32 * quad) << 16) + p * 256 + turn + 64 * q, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (uint32_t j = 0; j < 32; ++j)
+              held[q][j] = kb == 0 ? __uint_as_float(v[j]) : held[q][j] + __uint_as_float(v[j]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[p]);
+        }
+        if (!whole) break;
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) {
+          const uint32_t c0 = turn + 64 * q;
+          if (c0 >= cols) break;
+          const XentToken now = tok;
+          if (c0 + 64 < cols) ask(c0 + 64);
+          xent_fold<kLists>(P.xent, P.f16, P.out_cols, held[q], scale, lift, c, m0 + c0, min(32u, cols - c0), lane, now);
+        }
+        continue;
+      }
       const bool ok = wait_live(&acc_full[b], (acc >> 1) & 1u, abort, P.status, 23, 64);
       tc_fence_after();
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
@@ -427,7 +501,7 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
         uint32_t v[32];
         tmem_ld32(tmem_base + ((32 * quad) << 16) + b * 256 + c0, v);
         tmem_ld_wait();
-        if constexpr (kLists) {
+        if constexpr (kLists == kOgLists) {
           for (uint32_t q = P.seg_kb, at = P.bn; q < P.n_kb; q += P.seg_kb, at += P.bn) {
             uint32_t more[32];
             tmem_ld32(tmem_base + ((32 * quad) << 16) + b * 256 + at + c0, more);
@@ -445,7 +519,8 @@ __global__ void __launch_bounds__(kOgThreads, 1) operand_gemm_kernel(const __gri
         if constexpr (!kTrans) {
           const XentToken now = tok;
           if (c0 + 64 < cols) ask(c0 + 64);
-          xent_fold<kLists>(P.xent, P.f16, P.out_cols, v, scale, lift, c, m0 + c0, min(32u, cols - c0), lane, now);
+          if constexpr (!kParts)
+            xent_fold<kLists>(P.xent, P.f16, P.out_cols, v, scale, lift, c, m0 + c0, min(32u, cols - c0), lane, now);
         } else if (cut) {
           const uint64_t at = static_cast<uint64_t>(ab * P.m_blocks + mb) * P.splits + sp;
           float* part = P.parts + (at * P.bn + c0) * kOgBM + 32 * quad + lane;
@@ -626,8 +701,10 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
   if (e == cudaSuccess && pair) e = tokens(&P.tmap_b2, pair->rows16);
   if (e == cudaSuccess && pair) e = weights(&P.tmap_a2, pair->images);
   if (e != cudaSuccess) return e;
+  const bool parts = !plan.trans && P.xent.listed != nullptr && P.xent.probs == nullptr && plan.bn >= 128;
   auto kern = plan.trans ? operand_gemm_kernel<true>
-              : P.xent.listed != nullptr ? operand_gemm_kernel<false, true> : operand_gemm_kernel<false>;
+              : parts ? operand_gemm_kernel<false, kOgListsInParts>
+              : P.xent.listed != nullptr ? operand_gemm_kernel<false, kOgLists> : operand_gemm_kernel<false>;
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   e = cudaGetDevice(&dev);
@@ -637,12 +714,19 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(operand_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(operand_gemm_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem);
+      e = cudaFuncSetAttribute(operand_gemm_kernel<false, kOgLists>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(operand_gemm_kernel<false, kOgListsInParts>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kOgSmem);
+    cudaFuncAttributes built;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&built, operand_gemm_kernel<false, kOgListsInParts>);
+    // (with fewer, the epilogue's warps would wait for registers that there are not)
+    if (e == cudaSuccess && built.numRegs != kOgPartRegs) e = cudaErrorInvalidConfiguration;
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }
   const uint32_t grid = std::min(P.n_tiles, plan.sms);
-  e = launch_pdl(kern, dim3(grid), dim3(kOgThreads), kOgSmem, stream, P);
+  e = launch_pdl(kern, dim3(grid), dim3(parts ? kOgPartThreads : kOgThreads), kOgSmem, stream, P);
   if (e != cudaSuccess || plan.splits == 1) return e;
   // a CTA 8 tokens of a tile
   const JoinParts J{P.out, P.parts, plan.M, plan.bn, P.m_blocks, plan.splits, P.out_cols};

@@ -268,6 +268,20 @@ def test_not_finite_stays_with_its_token(cuda):
             check(L, x, 500, 1.0, ids, logits)
 
 
+@pytest.mark.parametrize("dtype", [ans.BF16_SPLIT, ans.INT8])
+@pytest.mark.parametrize("M", [300, 1000])
+def test_wide_tiles_of_long_sums(cuda, dtype, M):
+    """Tokens in tiles of 128 and 256, whose sums of K = 4160 come in several parts where there is no gradient."""
+    rng = np.random.default_rng(22)
+    L = usual(dtype, 4096, 4160, seed=22)
+    ids, logits = teacher(rng, M, 4090, 5)
+    x = leaning(L, rng, M, ids)
+    check(L, x, 4090, 1.0, ids, logits)
+    # the same bits again
+    a, b = run(L, x, 4090, 1.0, ids, logits, grad=False), run(L, x, 4090, 1.0, ids, logits, grad=False)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("M", [3, 300])
 def test_nothing_listed_beside_infinite_weights(cuda, M):
     """A token that lists nothing has a zero gradient whatever the rows of W hold."""

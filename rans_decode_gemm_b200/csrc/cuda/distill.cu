@@ -19,6 +19,12 @@
 // of 2 M V K operations in all.  Blocks under another reference than their token's
 // are rescaled before it: nearly all of the first rows of the vocabulary, which are
 // a piece of their own, and hardly any of the others.
+//
+// Measured alone (32000 x 4096 bf16, 2048 tokens of 64 listed, with the gradient): the
+// decoding 150 us, logits 50 + 401 (537 GFLOP, 1.19 PFLOP/s), joins 7 + 15, coefficients
+// 9, rows rescaled 24, the product back 399 (1.35 PFLOP/s); the lists (23 us) run beside the
+// decoding.  The products bound it.  Without a gradient and at 16 tokens the decoding does:
+// 91 + 63 of 217 us, the products, which read 262 MB of images, 32 + 30.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -10,11 +10,15 @@
 // dG_n and dU_n, take.  G and U never reach memory; the gradient computes them
 // again.  dX is one transposed product over both layers' rows (operand_gemm.cu).
 //
-// A stage of a wide tile holds 64 steps of the sum: 16 KB of tokens by TMA (128-byte swizzle) and
-// 32 KB of images by one copy.  An image's rows are K-major under the 32-byte
+// A stage of a wide tile holds 64 steps of the sum: 16 KB of tokens by TMA (128-byte
+// swizzle) and 32 KB of images by one copy.  An image's rows are K-major under the 32-byte
 // swizzle, so 8 KB of a gate and an up image are one 256-row operand.  Where the tiles
 // would leave SMs idle they are of 64 or 32 rows: a box of that part of each of eight
 // images.
+//
+// Measured alone (fp8 14336 x 4096, 2048 tokens): the decoding 67 us a layer, the product
+// 362 (481 GFLOP, 1.33 PFLOP/s).  int8 with the gradient: 67 a layer, the product 445, of
+// which its epilogue (58 MB of dH read, 235 MB written) adds some 80, dX 369.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -593,8 +597,8 @@ cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDe
                    a.scale_kind == 3 ? static_cast<uint64_t>(p.N) * (p.K / a.group_k) : static_cast<uint64_t>(p.N),
                    scale_parts);
   if (e != cudaSuccess) return e;
-  e = launch_operand_decode(gate, 0, p.N, a.scale_kind, a.gate_scales, a.group_k, images, a.status, p.sms,
-                                        stream, 2 * kOperandImage);
+  e = launch_operand_decode(gate, 0, p.N, a.scale_kind, a.gate_scales, a.group_k, images, a.status, p.sms, stream,
+                            2 * kOperandImage);
   if (e == cudaSuccess)
     e = launch_operand_decode(up, 0, p.N, a.scale_kind, a.up_scales, a.group_k, images + kOperandImage, a.status, p.sms,
                               stream, 2 * kOperandImage, true);

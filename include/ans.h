@@ -520,7 +520,9 @@ ans_status ans_gated_workspace(const ans_layout* layout, uint32_t M, ans_scale_k
  * ans_gemm_batched, which takes X in f16 as it is for the formats whose values are
  * exact in f16 (infinite from 65,520 on; 2^-17 and less lose bits); otherwise both
  * layers are decoded once into the workspace (4 N K bytes), and X enters under a
- * power of two of its row.  M == 0 is a no-op. */
+ * power of two of its row.  A workspace that was zero-filled once serves calls of
+ * any token counts of a layer, and of ans_gated_grad, in turn (it is as large as
+ * the largest of them asks for).  M == 0 is a no-op. */
 ans_status ans_gated(const uint16_t* d_X, uint32_t M, const ans_tiles* gate, const ans_tiles* up,
                      ans_scale_kind scale_kind, const void* d_gate_scales,
                      const void* d_up_scales, uint32_t group_k, ans_act act, uint16_t* d_H,

@@ -1147,8 +1147,11 @@ namespace {
 // 4096, images against the one launch: 24 tokens int8 189 us against 199, int4 153
 // against 204; one token fp8 190 against 204, bf16 191 against 187, int4 153 against
 // 141; of 4096 x 4096, 32 tokens: bf16 97 against 75, int4 97 against 81).
+// Both schedules leave the split-K counters of the one launch where they are for every
+// token count, so that one workspace serves them in turn.
 struct GatedChoice {
   bool few;
+  size_t counters[2];  // per layer, at the workspace's start
   size_t off_y, bytes;
   ansdev::GatedPlan images;
   ansdev::GemmPlan share[ANS_MAX_BATCH], full[ANS_MAX_BATCH];
@@ -1158,6 +1161,10 @@ struct GatedChoice {
 ans_status choose_gated(const ans_tiles* gate, const ans_tiles* up, uint32_t M, ans_scale_kind kind, bool grad, int sms,
                         GatedChoice* c) {
   c->few = false;
+  const size_t per_layer = (static_cast<size_t>(gate->layout.N / gate->layout.tile_n) * 4 + 255) / 256 * 256;
+  const size_t head = up1024(2 * per_layer);
+  c->counters[0] = 0;
+  c->counters[1] = per_layer;
   if (!grad) {
     const ans_gemm_job jobs[2] = {{nullptr, gate, nullptr, nullptr}, {nullptr, up, nullptr, nullptr}};
     if (batch_plan(jobs, 2, M, kind, sms, c->share, c->full, c->ws_off, &c->few) != ANS_OK) c->few = false;
@@ -1166,13 +1173,14 @@ ans_status choose_gated(const ans_tiles* gate, const ans_tiles* up, uint32_t M, 
     if (static_cast<uint64_t>(ly.N) * ly.K >= (32u << 20) && (M > 16 || symbols >= 16384)) c->few = false;
   }
   if (c->few) {
+    for (size_t& at : c->ws_off) at += head;
     c->off_y = up1024(c->ws_off[2]);
     c->bytes = c->off_y + 2 * up1024(static_cast<size_t>(M) * gate->layout.N * 4);
     return ANS_OK;
   }
   ansdev::LayerDev L;
   fill_layer_plain(&gate->layout, &L);
-  ansdev::make_gated_plan(L, M, kind, grad, sms, &c->images);
+  ansdev::make_gated_plan(L, M, kind, grad, sms, head, &c->images);
   c->bytes = c->images.bytes;
   return ANS_OK;
 }
@@ -1257,7 +1265,8 @@ ans_status ans_gated(const uint16_t* d_X, uint32_t M, const ans_tiles* gate, con
     const ansdev::LayerDev* Ls[2] = {&Lg, &Lu};
     const uint16_t* Xs[2] = {d_X, d_X};
     const void* Ss[2] = {d_gate_scales, d_up_scales};
-    e = ansdev::launch_gemm_batched(c.share, 2, Ls, Xs, Ss, scale_kind, group_k, Y, d_ws, c.ws_off, d_status, cs);
+    e = ansdev::launch_gemm_batched(c.share, 2, Ls, Xs, Ss, scale_kind, group_k, Y, d_ws, c.ws_off, d_status, cs,
+                                    c.counters);
     if (e == cudaSuccess)
       e = ansdev::launch_gated_join(Y[0], Y[1], static_cast<uint64_t>(M) * Lg.N, act, d_H, cs);
   } else {

@@ -528,7 +528,7 @@ static uint32_t gated_rows_of_tile(uint32_t M, uint32_t N, uint32_t K, bool grad
   return best;
 }
 
-void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool grad, int sms, GatedPlan* p) {
+void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool grad, int sms, size_t head, GatedPlan* p) {
   p->M = M;
   p->N = L.N;
   p->K = L.K;
@@ -537,7 +537,7 @@ void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool gr
   p->sms = sms;
   p->prep = p->f16 || scale_kind == 1 || scale_kind == 2;
   p->back = plan_operand_gemm(true, p->f16, M, 2 * L.N, L.K, sms);
-  size_t at = 0;
+  size_t at = head;
   auto take = [&](size_t n) {
     const size_t o = at;
     at += aligned(n);

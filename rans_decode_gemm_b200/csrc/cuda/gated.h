@@ -36,7 +36,8 @@ struct GatedArgs {
   uint32_t* status;
 };
 
-void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool grad, int sms, GatedPlan* plan);
+// (the workspace's first `head` bytes are not used)
+void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool grad, int sms, size_t head, GatedPlan* plan);
 // Through operand images, any M.
 cudaError_t launch_gated(const GatedPlan& plan, const LayerDev& gate, const LayerDev& up, const GatedArgs& a, void* ws,
                          cudaStream_t stream);

@@ -1255,7 +1255,8 @@ cudaError_t launch_gemm(const GemmPlan& plan, const LayerDev& L, bool decode, co
 cudaError_t launch_gemm_batched(const GemmPlan* plans, uint32_t n, const LayerDev* const* Ls,
                                 const uint16_t* const* Xs, const void* const* scales,
                                 uint32_t scale_kind, uint32_t group_k, float* const* Ys, void* ws,
-                                const size_t* ws_off, uint32_t* status, cudaStream_t stream) {
+                                const size_t* ws_off, uint32_t* status, cudaStream_t stream,
+                                const size_t* counters) {
   if (n == 0 || plans[0].M == 0) return cudaSuccess;
   if (n > kMaxBatch) return cudaErrorInvalidValue;
   static_assert(sizeof(BatchDev) <= 32000, "kernel parameter limit");
@@ -1268,6 +1269,8 @@ cudaError_t launch_gemm_batched(const GemmPlan* plans, uint32_t n, const LayerDe
     if (!plans[j].local || plans[j].dense || plans[j].fmt != plans[0].fmt) return cudaErrorInvalidValue;
     B.job[j] = make_gemm_dev(plans[j], *Ls[j], nullptr, Xs[j], scales[j], scale_kind, group_k,
                              Ys[j], static_cast<uint8_t*>(ws) + ws_off[j], status);
+    if (counters)
+      B.job[j].counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + counters[j]);
     B.job[j].cta0 = cta;
     cta += plans[j].grid;
     shape.D = std::max(shape.D, plans[j].D);

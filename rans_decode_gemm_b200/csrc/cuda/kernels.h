@@ -222,10 +222,13 @@ cudaError_t launch_gemm(const GemmPlan& plan, const LayerDev& L, bool decode, co
 // n layers in one launch of the small-M schedule: layer j runs plans[j]
 // (every plan local, one operand format) on CTAs [sum of the earlier grids,
 // + plans[j].grid), each with its own X, scales, Y and workspace
-// (ws + ws_off[j], round_up(plans[j].ws_bytes, 256) bytes at least).
+// (ws + ws_off[j], round_up(plans[j].ws_bytes, 256) bytes at least).  counters: byte
+// offsets of the layers' split-K counters (plans[j].ws_counters_bytes each), or null:
+// each at the start of its layer's workspace.
 cudaError_t launch_gemm_batched(const GemmPlan* plans, uint32_t n, const LayerDev* const* Ls,
                                 const uint16_t* const* Xs, const void* const* scales,
                                 uint32_t scale_kind, uint32_t group_k, float* const* Ys, void* ws,
-                                const size_t* ws_off, uint32_t* status, cudaStream_t stream);
+                                const size_t* ws_off, uint32_t* status, cudaStream_t stream,
+                                const size_t* counters = nullptr);
 
 }  // namespace ansdev

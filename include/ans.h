@@ -276,7 +276,8 @@ ans_status ans_decode_tiles16(const ans_layout* layout, const uint8_t* d_table, 
 /* Bytes of device workspace ans_gemm / ans_gemm_uncompressed need for a
  * layout, M tokens and a scale kind.  The workspace must be zero-filled once
  * before its first use; the kernels return it to all-zero counters on
- * completion (after a run that set *d_status, zero it again).  Above one
+ * completion (after a run that set *d_status, zero it again), so that one
+ * buffer serves any token counts of a layer in turn.  Above one
  * token pass (M > 512 for 128-row tiles, M > 256 for 256-row tiles, with K a
  * multiple of 64) it also holds a 16-bit copy of the decoded weights, 2 N K
  * bytes (see ans_gemm). */

@@ -1104,6 +1104,12 @@ static cudaError_t launch_single(const GemmPlan& plan, const LayerDev& L, bool d
                                  void* ws, uint16_t* w16, uint32_t* status, cudaStream_t stream) {
   GemmDev P = make_gemm_dev(plan, L, w_plain, X, scales, scale_kind, group_k, Y, ws, status);
   if (decode && w16) P.w16 = reinterpret_cast<uint8_t*>(w16);  // the decoded slabs' images
+  if (plan.n_pass > 1) {
+    // a counter for every pass: more than one pass has, in whose place calls of fewer
+    // tokens leave partial sums
+    const cudaError_t e = cudaMemsetAsync(P.counters, 0, plan.ws_counters_bytes, stream);
+    if (e != cudaSuccess) return e;
+  }
   if (!plan.local) {
     // X for the MMA as a tensor map: the caller's bf16 X, or its f16 copy
     const void* xsrc = X;

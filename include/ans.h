@@ -383,7 +383,8 @@ ans_status ans_gemm_batched_workspace(const ans_gemm_job* jobs, uint32_t n_jobs,
  * confined to G_j SMs (the split-K partition depends on the SM count, so it
  * may differ from ans_gemm's on the whole device in the last bits).  d_ws:
  * ans_gemm_batched_workspace bytes, zero-filled once before first use (the
- * kernels leave it that way); d_status as for ans_gemm. */
+ * kernels leave its counters that way: one buffer serves any M of the same layers
+ * in turn); d_status as for ans_gemm. */
 ans_status ans_gemm_batched(const ans_gemm_job* jobs, uint32_t n_jobs, uint32_t M,
                             ans_scale_kind scale_kind, uint32_t group_k, void* d_ws,
                             size_t ws_bytes, uint32_t* d_status, ans_stream_t stream);

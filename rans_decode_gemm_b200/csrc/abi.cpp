@@ -661,16 +661,24 @@ void batch_shares(const ans_gemm_job* jobs, uint32_t n, int sms, uint32_t* G) {
 
 // Plans of a batch: share[j] for job j on its share of the SMs (used when
 // every job takes the small-M schedule there: all jobs in one launch),
-// full[j] for job j on all SMs (consecutive launches otherwise); ws_off[j]
-// the byte offset of job j's workspace, ws_off[n] the total, each job's part
-// large enough for either plan.
+// full[j] for job j on all SMs (consecutive launches otherwise).  The workspace
+// starts with every job's split-K counters, counters[j], in places that do not depend
+// on M, so that one buffer serves any M in turn; ws_off[j] is the byte offset of the
+// rest of job j's, ws_off[n] the total, each job's part large enough for either plan.
 ans_status batch_plan(const ans_gemm_job* jobs, uint32_t n_jobs, uint32_t M,
                       ans_scale_kind scale_kind, int sms, ansdev::GemmPlan* share,
-                      ansdev::GemmPlan* full, size_t* ws_off, bool* one_launch) {
+                      ansdev::GemmPlan* full, size_t* counters, size_t* ws_off, bool* one_launch) {
   uint32_t G[ANS_MAX_BATCH];
   batch_shares(jobs, n_jobs, sms, G);
   *one_launch = true;
-  ws_off[0] = 0;
+  size_t at = 0;
+  for (uint32_t j = 0; j < n_jobs; ++j) {
+    // (one for each row block of a pass; more than one pass counts in the job's own part)
+    const ans_layout& ly = jobs[j].W->layout;
+    counters[j] = at;
+    at += (static_cast<size_t>(ly.N / ly.tile_n) * 4 + 255) / 256 * 256;
+  }
+  ws_off[0] = at;
   for (uint32_t j = 0; j < n_jobs; ++j) {
     ansdev::LayerDev L;
     fill_layer_plain(&jobs[j].W->layout, &L);
@@ -698,9 +706,9 @@ ans_status ans_gemm_batched_workspace(const ans_gemm_job* jobs, uint32_t n_jobs,
   if (st != ANS_OK) return st;
   if (M == 0) { *bytes = 0; return ANS_OK; }
   ansdev::GemmPlan share[ANS_MAX_BATCH], full[ANS_MAX_BATCH];
-  size_t ws_off[ANS_MAX_BATCH + 1];
+  size_t counters[ANS_MAX_BATCH], ws_off[ANS_MAX_BATCH + 1];
   bool one = false;
-  st = batch_plan(jobs, n_jobs, M, scale_kind, sms, share, full, ws_off, &one);
+  st = batch_plan(jobs, n_jobs, M, scale_kind, sms, share, full, counters, ws_off, &one);
   if (st != ANS_OK) return st;
   *bytes = ws_off[n_jobs];
   return ANS_OK;
@@ -734,22 +742,22 @@ ans_status ans_gemm_batched(const ans_gemm_job* jobs, uint32_t n_jobs, uint32_t 
   if (M == 0) return ANS_OK;
   if (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256 != 0) return ANS_ERR_ARG;
   ansdev::GemmPlan share[ANS_MAX_BATCH], full[ANS_MAX_BATCH];
-  size_t ws_off[ANS_MAX_BATCH + 1];
+  size_t counters[ANS_MAX_BATCH], ws_off[ANS_MAX_BATCH + 1];
   bool one = false;
-  st = batch_plan(jobs, n_jobs, M, scale_kind, sms, share, full, ws_off, &one);
+  st = batch_plan(jobs, n_jobs, M, scale_kind, sms, share, full, counters, ws_off, &one);
   if (st != ANS_OK) return st;
   if (ws_bytes < ws_off[n_jobs]) return ANS_ERR_BUFFER_TOO_SMALL;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (one) {
     cudaError_t e = ansdev::launch_gemm_batched(share, n_jobs, Lp, Xs, Ss, scale_kind, group_k, Ys,
-                                                d_ws, ws_off, d_status, s);
+                                                d_ws, counters, ws_off, d_status, s);
     if (e != cudaSuccess) return cuda_fail(e, "ans_gemm_batched");
     return ANS_OK;
   }
   for (uint32_t j = 0; j < n_jobs; ++j) {
+    uint8_t* ws = static_cast<uint8_t*>(d_ws);
     cudaError_t e = ansdev::launch_gemm(full[j], Ls[j], true, nullptr, Xs[j], Ss[j], scale_kind,
-                                        group_k, Ys[j], static_cast<uint8_t*>(d_ws) + ws_off[j],
-                                        d_status, s);
+                                        group_k, Ys[j], ws + ws_off[j], d_status, s, ws + counters[j]);
     if (e != cudaSuccess) return cuda_fail(e, "ans_gemm_batched");
   }
   return ANS_OK;
@@ -1147,40 +1155,36 @@ namespace {
 // 4096, images against the one launch: 24 tokens int8 189 us against 199, int4 153
 // against 204; one token fp8 190 against 204, bf16 191 against 187, int4 153 against
 // 141; of 4096 x 4096, 32 tokens: bf16 97 against 75, int4 97 against 81).
-// Both schedules leave the split-K counters of the one launch where they are for every
-// token count, so that one workspace serves them in turn.
+// Decoded weights lie behind the split-K counters of that launch, so that one workspace
+// serves both in turn.
 struct GatedChoice {
   bool few;
-  size_t counters[2];  // per layer, at the workspace's start
   size_t off_y, bytes;
   ansdev::GatedPlan images;
   ansdev::GemmPlan share[ANS_MAX_BATCH], full[ANS_MAX_BATCH];
-  size_t ws_off[ANS_MAX_BATCH + 1];
+  size_t counters[ANS_MAX_BATCH], ws_off[ANS_MAX_BATCH + 1];
 };
 
 ans_status choose_gated(const ans_tiles* gate, const ans_tiles* up, uint32_t M, ans_scale_kind kind, bool grad, int sms,
                         GatedChoice* c) {
+  const ans_gemm_job jobs[2] = {{nullptr, gate, nullptr, nullptr}, {nullptr, up, nullptr, nullptr}};
   c->few = false;
-  const size_t per_layer = (static_cast<size_t>(gate->layout.N / gate->layout.tile_n) * 4 + 255) / 256 * 256;
-  const size_t head = up1024(2 * per_layer);
-  c->counters[0] = 0;
-  c->counters[1] = per_layer;
-  if (!grad) {
-    const ans_gemm_job jobs[2] = {{nullptr, gate, nullptr, nullptr}, {nullptr, up, nullptr, nullptr}};
-    if (batch_plan(jobs, 2, M, kind, sms, c->share, c->full, c->ws_off, &c->few) != ANS_OK) c->few = false;
+  const bool planned =
+      batch_plan(jobs, 2, M, kind, sms, c->share, c->full, c->counters, c->ws_off, &c->few) == ANS_OK;
+  if (grad || !planned) c->few = false;
+  if (c->few) {
     const ans_layout& ly = gate->layout;
     const uint32_t symbols = ly.tile_n * ly.tile_k / (ly.dtype == ANS_INT4_PAIRS || ly.dtype == ANS_FP4_PAIRS ? 2 : 1);
     if (static_cast<uint64_t>(ly.N) * ly.K >= (32u << 20) && (M > 16 || symbols >= 16384)) c->few = false;
   }
   if (c->few) {
-    for (size_t& at : c->ws_off) at += head;
     c->off_y = up1024(c->ws_off[2]);
     c->bytes = c->off_y + 2 * up1024(static_cast<size_t>(M) * gate->layout.N * 4);
     return ANS_OK;
   }
   ansdev::LayerDev L;
   fill_layer_plain(&gate->layout, &L);
-  ansdev::make_gated_plan(L, M, kind, grad, sms, head, &c->images);
+  ansdev::make_gated_plan(L, M, kind, grad, sms, up1024(c->ws_off[0]), &c->images);
   c->bytes = c->images.bytes;
   return ANS_OK;
 }
@@ -1265,8 +1269,8 @@ ans_status ans_gated(const uint16_t* d_X, uint32_t M, const ans_tiles* gate, con
     const ansdev::LayerDev* Ls[2] = {&Lg, &Lu};
     const uint16_t* Xs[2] = {d_X, d_X};
     const void* Ss[2] = {d_gate_scales, d_up_scales};
-    e = ansdev::launch_gemm_batched(c.share, 2, Ls, Xs, Ss, scale_kind, group_k, Y, d_ws, c.ws_off, d_status, cs,
-                                    c.counters);
+    e = ansdev::launch_gemm_batched(c.share, 2, Ls, Xs, Ss, scale_kind, group_k, Y, d_ws, c.counters, c.ws_off, d_status,
+                                    cs);
     if (e == cudaSuccess)
       e = ansdev::launch_gated_join(Y[0], Y[1], static_cast<uint64_t>(M) * Lg.N, act, d_H, cs);
   } else {

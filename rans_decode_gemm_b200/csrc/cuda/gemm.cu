@@ -1101,7 +1101,8 @@ static cudaError_t convert_x(const uint16_t* X, uint32_t M, uint32_t K, uint8_t*
 static cudaError_t launch_single(const GemmPlan& plan, const LayerDev& L, bool decode,
                                  const void* w_plain, const uint16_t* X, const uint8_t* x16_ready,
                                  const void* scales, uint32_t scale_kind, uint32_t group_k, float* Y,
-                                 void* ws, uint16_t* w16, uint32_t* status, cudaStream_t stream) {
+                                 void* ws, uint16_t* w16, uint32_t* status, cudaStream_t stream,
+                                 void* counters) {
   GemmDev P = make_gemm_dev(plan, L, w_plain, X, scales, scale_kind, group_k, Y, ws, status);
   if (decode && w16) P.w16 = reinterpret_cast<uint8_t*>(w16);  // the decoded slabs' images
   if (plan.n_pass > 1) {
@@ -1109,6 +1110,8 @@ static cudaError_t launch_single(const GemmPlan& plan, const LayerDev& L, bool d
     // tokens leave partial sums
     const cudaError_t e = cudaMemsetAsync(P.counters, 0, plan.ws_counters_bytes, stream);
     if (e != cudaSuccess) return e;
+  } else if (counters) {
+    P.counters = static_cast<uint32_t*>(counters);
   }
   if (!plan.local) {
     // X for the MMA as a tensor map: the caller's bf16 X, or its f16 copy
@@ -1201,11 +1204,11 @@ static cudaError_t format_w16(uint32_t fmt, const void* w, const void* scales, c
 cudaError_t launch_gemm(const GemmPlan& plan, const LayerDev& L, bool decode, const void* w_plain,
                         const uint16_t* X, const void* scales, uint32_t scale_kind,
                         uint32_t group_k, float* Y, void* ws, uint32_t* status,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, void* counters) {
   if (plan.M == 0) return cudaSuccess;
   if (!plan.dense)
     return launch_single(plan, L, decode, w_plain, X, nullptr, scales, scale_kind, group_k, Y, ws,
-                         nullptr, status, stream);
+                         nullptr, status, stream, counters);
   // Large M: the first M_first tokens fused (the decode variant storing the
   // decoded weights into W16), then every other token in one dense GEMM on
   // W16 -- the uncompressed variant formats its codes into W16 the same way
@@ -1223,7 +1226,7 @@ cudaError_t launch_gemm(const GemmPlan& plan, const LayerDev& L, bool decode, co
   if (!make_gemm_plan(L, plan.M_first, scale_kind, decode, static_cast<int>(plan.sms), &first))
     return cudaErrorInvalidValue;
   e = launch_single(first, L, decode, w_plain, X, plan.ab_f16 ? x16 : nullptr, scales, scale_kind,
-                    group_k, Y, ws, decode ? w16 : nullptr, status, stream);
+                    group_k, Y, ws, decode ? w16 : nullptr, status, stream, counters);
   if (e != cudaSuccess) return e;
   if (!decode) {
     e = format_w16(plan.fmt, w_plain, scales, L, group_k, reinterpret_cast<uint8_t*>(w16), stream);
@@ -1261,8 +1264,8 @@ cudaError_t launch_gemm(const GemmPlan& plan, const LayerDev& L, bool decode, co
 cudaError_t launch_gemm_batched(const GemmPlan* plans, uint32_t n, const LayerDev* const* Ls,
                                 const uint16_t* const* Xs, const void* const* scales,
                                 uint32_t scale_kind, uint32_t group_k, float* const* Ys, void* ws,
-                                const size_t* ws_off, uint32_t* status, cudaStream_t stream,
-                                const size_t* counters) {
+                                const size_t* counters, const size_t* ws_off, uint32_t* status,
+                                cudaStream_t stream) {
   if (n == 0 || plans[0].M == 0) return cudaSuccess;
   if (n > kMaxBatch) return cudaErrorInvalidValue;
   static_assert(sizeof(BatchDev) <= 32000, "kernel parameter limit");
@@ -1275,8 +1278,7 @@ cudaError_t launch_gemm_batched(const GemmPlan* plans, uint32_t n, const LayerDe
     if (!plans[j].local || plans[j].dense || plans[j].fmt != plans[0].fmt) return cudaErrorInvalidValue;
     B.job[j] = make_gemm_dev(plans[j], *Ls[j], nullptr, Xs[j], scales[j], scale_kind, group_k,
                              Ys[j], static_cast<uint8_t*>(ws) + ws_off[j], status);
-    if (counters)
-      B.job[j].counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + counters[j]);
+    B.job[j].counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + counters[j]);
     B.job[j].cta0 = cta;
     cta += plans[j].grid;
     shape.D = std::max(shape.D, plans[j].D);

@@ -215,20 +215,20 @@ cudaError_t launch_decode_tiles(const LayerDev& L, void* out, uint32_t* status,
 cudaError_t launch_histogram(const void* w, uint64_t n_bytes, uint32_t dtype, uint64_t* hist,
                              cudaStream_t stream, int num_sms);
 // X: bf16 M x K.  ws must hold plan.ws_bytes (partials, counters, f16 X copy).
+// counters: where the split-K counters of a plan of one pass lie, if not in ws.
 cudaError_t launch_gemm(const GemmPlan& plan, const LayerDev& L, bool decode, const void* w_plain,
                         const uint16_t* X, const void* scales, uint32_t scale_kind,
                         uint32_t group_k, float* Y, void* ws, uint32_t* status,
-                        cudaStream_t stream);
+                        cudaStream_t stream, void* counters = nullptr);
 // n layers in one launch of the small-M schedule: layer j runs plans[j]
 // (every plan local, one operand format) on CTAs [sum of the earlier grids,
 // + plans[j].grid), each with its own X, scales, Y and workspace
-// (ws + ws_off[j], round_up(plans[j].ws_bytes, 256) bytes at least).  counters: byte
-// offsets of the layers' split-K counters (plans[j].ws_counters_bytes each), or null:
-// each at the start of its layer's workspace.
+// (ws + ws_off[j], round_up(plans[j].ws_bytes, 256) bytes at least) and split-K
+// counters (ws + counters[j], plans[j].ws_counters_bytes).
 cudaError_t launch_gemm_batched(const GemmPlan* plans, uint32_t n, const LayerDev* const* Ls,
                                 const uint16_t* const* Xs, const void* const* scales,
                                 uint32_t scale_kind, uint32_t group_k, float* const* Ys, void* ws,
-                                const size_t* ws_off, uint32_t* status, cudaStream_t stream,
-                                const size_t* counters = nullptr);
+                                const size_t* counters, const size_t* ws_off, uint32_t* status,
+                                cudaStream_t stream);
 
 }  // namespace ansdev

@@ -36,3 +36,28 @@ def test_gemm_of_one_pass_and_of_several(cuda, name, N, K, tile_k):
         assert int(st.item()) == 0
         same = torch.equal(y, want)
         assert same, f"M {M}, turn {turn}"
+
+
+@pytest.mark.parametrize("name,tile_n,shapes", [("bf16_4096", 128, [(1024, 1024), (512, 2048), (1024, 512)]),
+                                                ("int4_70b", 256, [(1024, 1024), (1024, 1024)]),
+                                                ("fp8_405b", 128, [(512, 1040), (8192, 80)])])
+def test_batched_layers(cuda, name, tile_n, shapes):
+    layers = [_layer(name, N, K, tile_n, 64 if K % 64 == 0 else 16, j) for j, (N, K) in enumerate(shapes)]
+    cfg = layers[0][0]
+    st = status_tensor()
+
+    def call(M, turn, ws):
+        jobs = [(x_dev(WL.make_x(c, M, lay.K, stream=turn)), layer.tiles, sc, torch.empty(M, lay.N, device="cuda"))
+                for c, sc, lay, layer in layers]
+        size = ans.ans_gemm_batched_workspace(jobs, M, cfg.scale_kind)
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda") if ws is None else ws
+        ans.ans_gemm_batched(jobs, M, cfg.scale_kind, cfg.group_k, ws, ws.numel(), st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        return size, [job[3] for job in jobs]
+    order = (8, 20, 300, 1, 1100, 32, 5, 300, 17)
+    want = [call(M, turn, None) for turn, M in enumerate(order)]
+    ws = torch.zeros(max(size for size, _ in want), dtype=torch.uint8, device="cuda")
+    for turn, M in enumerate(order):
+        same = all(torch.equal(a, b) for a, b in zip(call(M, turn, ws)[1], want[turn][1]))
+        assert same, f"M {M}, turn {turn}"

@@ -519,11 +519,11 @@ ans_status ans_gated_workspace(const ans_layout* layout, uint32_t M, ans_scale_k
 /* H bf16 M x N from X bf16 M x K, row-major, 16-byte aligned.  With few tokens (up to
  * 32; 16 on layers of 2^25 weights and more, and none there where a tile holds 16,384
  * symbols) no decoded weight reaches global memory, and G and U are those of
- * ans_gemm_batched, which takes X in f16 as it is for the formats whose values are
- * exact in f16 (infinite from 65,520 on; 2^-17 and less lose bits); otherwise both
- * layers are decoded once into the workspace (4 N K bytes), and X enters under a
- * power of two of its row.  A workspace that was zero-filled once serves calls of
- * any token counts of a layer, and of ans_gated_grad, in turn (it is as large as
+ * ans_gemm_batched; otherwise both layers are decoded once into the workspace
+ * (4 N K bytes).  Either way X enters products in f16 under a power of two of its
+ * row: rows of any size keep their values' 8 bits down to 2^-31 of the row's largest.
+ * A workspace that was zero-filled once serves calls of any token counts of a layer,
+ * and of ans_gated_grad, in turn (it is as large as
  * the largest of them asks for).  M == 0 is a no-op. */
 ans_status ans_gated(const uint16_t* d_X, uint32_t M, const ans_tiles* gate, const ans_tiles* up,
                      ans_scale_kind scale_kind, const void* d_gate_scales,

@@ -1159,7 +1159,7 @@ namespace {
 // serves both in turn.
 struct GatedChoice {
   bool few;
-  size_t off_y, bytes;
+  size_t off_y, off_x, off_factor, bytes;  // (X under a power of two of its row: where products take it in f16)
   ansdev::GatedPlan images;
   ansdev::GemmPlan share[ANS_MAX_BATCH], full[ANS_MAX_BATCH];
   size_t counters[ANS_MAX_BATCH], ws_off[ANS_MAX_BATCH + 1];
@@ -1179,7 +1179,9 @@ ans_status choose_gated(const ans_tiles* gate, const ans_tiles* up, uint32_t M, 
   }
   if (c->few) {
     c->off_y = up1024(c->ws_off[2]);
-    c->bytes = c->off_y + 2 * up1024(static_cast<size_t>(M) * gate->layout.N * 4);
+    c->off_x = c->off_y + 2 * up1024(static_cast<size_t>(M) * gate->layout.N * 4);
+    c->off_factor = c->off_x + (c->share[0].ab_f16 ? up1024(static_cast<size_t>(M) * gate->layout.K * 2) : 0);
+    c->bytes = c->off_factor + (c->share[0].ab_f16 ? up1024(static_cast<size_t>(M) * 4) : 0);
     return ANS_OK;
   }
   ansdev::LayerDev L;
@@ -1267,12 +1269,21 @@ ans_status ans_gated(const uint16_t* d_X, uint32_t M, const ans_tiles* gate, con
     Y[0] = reinterpret_cast<float*>(ws + c.off_y);
     Y[1] = reinterpret_cast<float*>(ws + c.off_y + up1024(static_cast<size_t>(M) * Lg.N * 4));
     const ansdev::LayerDev* Ls[2] = {&Lg, &Lu};
-    const uint16_t* Xs[2] = {d_X, d_X};
+    const uint16_t* x = d_X;
+    float* factor = nullptr;
+    e = cudaSuccess;
+    if (c.share[0].ab_f16) {
+      uint16_t* x_up = reinterpret_cast<uint16_t*>(ws + c.off_x);
+      factor = reinterpret_cast<float*>(ws + c.off_factor);
+      e = ansdev::launch_gated_x(d_X, M, Lg.K, x_up, factor, cs);
+      x = x_up;
+    }
+    const uint16_t* Xs[2] = {x, x};
     const void* Ss[2] = {d_gate_scales, d_up_scales};
-    e = ansdev::launch_gemm_batched(c.share, 2, Ls, Xs, Ss, scale_kind, group_k, Y, d_ws, c.counters, c.ws_off, d_status,
-                                    cs);
     if (e == cudaSuccess)
-      e = ansdev::launch_gated_join(Y[0], Y[1], static_cast<uint64_t>(M) * Lg.N, act, d_H, cs);
+      e = ansdev::launch_gemm_batched(c.share, 2, Ls, Xs, Ss, scale_kind, group_k, Y, d_ws, c.counters, c.ws_off, d_status,
+                                      cs);
+    if (e == cudaSuccess) e = ansdev::launch_gated_join(Y[0], Y[1], factor, M, Lg.N, act, d_H, cs);
   } else {
     const ansdev::GatedArgs a{d_X, static_cast<uint32_t>(scale_kind), d_gate_scales, d_up_scales, group_k,
                               static_cast<uint32_t>(act), d_H, nullptr, nullptr, nullptr, nullptr, d_status};

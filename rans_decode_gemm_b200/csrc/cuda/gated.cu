@@ -383,34 +383,81 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
 }
 
 // ---- products that are there ---------------------------------------------------
-__global__ void __launch_bounds__(256) gated_join_kernel(const float* __restrict__ G, const float* __restrict__ U,
-                                                         uint64_t n8, uint32_t act, uint16_t* __restrict__ H) {
+// X under a power of two of its row, for products that take it as f16: the row's largest
+// finite value lies in [2^14, 2^15), and f16 then holds all 8 bits of the others down to
+// 2^-31 of it and is off by 2^-39 of it below.  A CTA a token.
+__global__ void __launch_bounds__(256) gated_x_kernel(const uint16_t* __restrict__ X, uint32_t K, uint16_t* __restrict__ out,
+                                                      float* __restrict__ factor) {
+  __shared__ float part[8];
   griddep_wait();
   griddep_launch_dependents();
-  for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<uint64_t>(gridDim.x) * 256) {
-    uint32_t o[4];
-#pragma unroll
-    for (uint32_t k = 0; k < 2; ++k) {
-      const float4 g = __ldcg(reinterpret_cast<const float4*>(G) + 2 * i + k);
-      const float4 u = __ldcg(reinterpret_cast<const float4*>(U) + 2 * i + k);
-      const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
-      float r[4], slope;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        activation<false>(act, gv[j], r[j], slope);
-        r[j] *= uv[j];
+  const uint64_t row = static_cast<uint64_t>(blockIdx.x) * K;
+  auto load = [&](uint32_t c) { return __ldg(reinterpret_cast<const uint4*>(X + row + c)); };
+  float top = 0.0f;
+  for (uint32_t c = threadIdx.x * 8; c < K; c += 2048) {
+    const uint4 q = load(c);
+    for (const uint32_t w : {q.x, q.y, q.z, q.w})
+      for (const uint32_t h : {w << 16, w & 0xFFFF0000u}) {
+        const float a = fabsf(__uint_as_float(h));
+        if (a <= 3.402823466e38f) top = fmaxf(top, a);
       }
-      o[2 * k] = bf16x2(r[0], r[1]);
-      o[2 * k + 1] = bf16x2(r[2], r[3]);
-    }
-    reinterpret_cast<uint4*>(H)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
+  __syncthreads();
+#pragma unroll
+  for (uint32_t k = 0; k < 8; ++k) top = fmaxf(top, part[k]);
+  // (both powers stay normal numbers)
+  const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+  const int e = top == 0.0f ? 0 : min(126, max(-113, 14 - ex));
+  const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  if (threadIdx.x == 0) factor[blockIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  for (uint32_t c = threadIdx.x * 8; c < K; c += 2048) {
+    const uint4 q = load(c);
+    auto times = [&](uint32_t w) {
+      return bf16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+    };
+    *reinterpret_cast<uint4*>(out + row + c) = make_uint4(times(q.x), times(q.y), times(q.z), times(q.w));
   }
 }
 
-cudaError_t launch_gated_join(const float* G, const float* U, uint64_t n, uint32_t act, uint16_t* H, cudaStream_t stream) {
-  const uint64_t n8 = n / 8;
-  return launch_pdl(gated_join_kernel, dim3(static_cast<uint32_t>(std::min<uint64_t>((n8 + 255) / 256, 148 * 8))), dim3(256), 0,
-                    stream, G, U, n8, act, H);
+cudaError_t launch_gated_x(const uint16_t* X, uint32_t M, uint32_t K, uint16_t* out, float* factor, cudaStream_t stream) {
+  return launch_pdl(gated_x_kernel, dim3(M), dim3(256), 0, stream, X, K, out, factor);
+}
+
+// factor: of a token's G and U, or null.  Eight of a token's values a thread.
+__global__ void __launch_bounds__(256) gated_join_kernel(const float* __restrict__ G, const float* __restrict__ U,
+                                                         const float* factor, uint32_t n8, uint32_t act,
+                                                         uint16_t* __restrict__ H) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= n8) return;
+  const uint64_t i = static_cast<uint64_t>(blockIdx.y) * n8 + n;
+  const float f = factor != nullptr ? __ldcg(factor + blockIdx.y) : 1.0f;
+  uint32_t o[4];
+#pragma unroll
+  for (uint32_t k = 0; k < 2; ++k) {
+    const float4 g = __ldcg(reinterpret_cast<const float4*>(G) + 2 * i + k);
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(U) + 2 * i + k);
+    const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
+    float r[4], slope;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      activation<false>(act, gv[j] * f, r[j], slope);
+      r[j] *= uv[j] * f;
+    }
+    o[2 * k] = bf16x2(r[0], r[1]);
+    o[2 * k + 1] = bf16x2(r[2], r[3]);
+  }
+  reinterpret_cast<uint4*>(H)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+cudaError_t launch_gated_join(const float* G, const float* U, const float* factor, uint32_t M, uint32_t N, uint32_t act,
+                              uint16_t* H, cudaStream_t stream) {
+  const uint32_t n8 = N / 8;
+  return launch_pdl(gated_join_kernel, dim3((n8 + 255) / 256, M), dim3(256), 0, stream, G, U, factor, n8, act, H);
 }
 
 // ---- bounds of the gradient's rows ----------------------------------------------

@@ -41,8 +41,11 @@ void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool gr
 // Through operand images, any M.
 cudaError_t launch_gated(const GatedPlan& plan, const LayerDev& gate, const LayerDev& up, const GatedArgs& a, void* ws,
                          cudaStream_t stream);
-// H = act(G) * U of products that are there (fp32, M x N).
-cudaError_t launch_gated_join(const float* G, const float* U, uint64_t n, uint32_t act, uint16_t* H, cudaStream_t stream);
+// X (bf16, M x K) under a power of two of its row, and what its products are times then.
+cudaError_t launch_gated_x(const uint16_t* X, uint32_t M, uint32_t K, uint16_t* out, float* factor, cudaStream_t stream);
+// H = act(G) * U of products that are there (fp32, M x N), times factor[m] first (or null).  M up to 65535.
+cudaError_t launch_gated_join(const float* G, const float* U, const float* factor, uint32_t M, uint32_t N, uint32_t act,
+                              uint16_t* H, cudaStream_t stream);
 
 cudaError_t set_live_wait_budget_gated(long long cycles);
 

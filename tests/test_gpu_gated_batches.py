@@ -4,8 +4,8 @@ import torch
 
 from rans_decode_gemm_b200 import ans
 
-from _ops_util import status, workspace
-from test_gpu_gated import Block, inputs, run_forward, run_grad
+from _ops_util import status, within, workspace
+from test_gpu_gated import Block, forward_reference, inputs, run_forward, run_grad
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,21 @@ def test_one_workspace_serves_every_batch(cuda, dtype, N, K):
             torch.cuda.synchronize()
             assert int(st.item()) == 0
             assert all(torch.equal(a, b) for a, b in zip((dx, dg, du), run_grad(B, x, dh, ans.ACT_SILU)))
+
+
+@pytest.mark.parametrize("dtype", [ans.INT8, ans.FP8_E4M3, ans.INT4_PAIRS, ans.INT4, ans.FP4_E2M1, ans.BF16_SPLIT])
+@pytest.mark.parametrize("M", [1, 16, 32, 33])
+def test_rows_of_any_size_in_batches_of_any_size(cuda, dtype, M):
+    """Rows far outside f16's range, below and above: a token's result does not depend on how many come with it."""
+    B = Block(dtype, 512, 256, seed=7)
+    x, _ = inputs(B, M, 11)
+    sizes = torch.tensor([1e-7, 1e6, 1e-15, 1e12, 1.0, 7e4])
+    for first in range(6 if M == 1 else 1):
+        y = (x.float() * sizes[(torch.arange(M) + first) % 6][:, None]).bfloat16()
+        for act in (ans.ACT_SILU, ans.ACT_RELU):
+            h = run_forward(B, y, act)
+            within(h, *forward_reference(B, y, act), f"h {act} {first}")
+            # and within two roundings of those of a batch that is large enough to be decoded first
+            many = run_forward(B, torch.cat([y, y.new_zeros(64, B.K)]), act)[:M]
+            want, bound = forward_reference(B, y, act)
+            assert ((h.double() - many.double()).abs().cpu() <= 2 * bound).all()

@@ -287,14 +287,19 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
       const uint32_t m = mb * kGaBM + 32 * quad + lane;
       const bool m_in = m < P.M;
       const float f = P.factor != nullptr && m_in ? __ldcg(P.factor + m) : 1.0f;
-      float up = 1.0f;
+      float up = 1.0f, up2 = 1.0f;
       if (kGrad && P.rows.bound != nullptr && m_in) {
-        // 2^e with the bound times 2^e in [2^14, 2^15); both powers stay normal numbers
+        // 2^e with the bound times 2^e in [2^14, 2^15), in two steps: up to 2^141, which no
+        // fp32 holds, and a row scale times the first alone stays finite (|e| / 2 <= 71; the
+        // scale's square is in the bound)
         const float bound = __ldcg(P.rows.bound + m) * top_scale;
-        const int ex = static_cast<int>(__float_as_uint(bound) >> 23) - 127;
-        const int e = bound == 0.0f ? 0 : min(126, max(-113, 14 - ex));
-        up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-        if (ab == 0 && turn == 0) P.rows.factor[m] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const int ex = static_cast<int>(__float_as_uint(bound) >> 23) - 127;  // (-127: 2^-126 and less)
+        const int e = max(-113, 14 - ex);
+        up = __uint_as_float(static_cast<uint32_t>(e / 2 + 127) << 23);
+        up2 = __uint_as_float(static_cast<uint32_t>(e - e / 2 + 127) << 23);
+        // (2^-e is below the normal numbers from e = 127 on, and exact)
+        if (ab == 0 && turn == 0)
+          P.rows.factor[m] = __uint_as_float(e <= 126 ? static_cast<uint32_t>(127 - e) << 23 : 1u << (149 - e));
       }
       const uint64_t row = static_cast<uint64_t>(m) * P.N;
       const bool ok = wait_live(&acc_full[b], (acc >> 1) & 1u, abort, P.status, 23, 64);
@@ -356,8 +361,8 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
               o2[i] = bf16x2(r2[0], r2[1]);
               if (P.rows.gate != nullptr) {
                 const float s0 = sg[2 * i] * up, s1 = sg[2 * i + 1] * up, t0 = su[2 * i] * up, t1 = su[2 * i + 1] * up;
-                q[i] = P.f16 ? f16x2(r[0] * s0, r[1] * s1) : bf16x2(r[0] * s0, r[1] * s1);
-                q2[i] = P.f16 ? f16x2(r2[0] * t0, r2[1] * t1) : bf16x2(r2[0] * t0, r2[1] * t1);
+                q[i] = P.f16 ? f16x2(r[0] * s0 * up2, r[1] * s1 * up2) : bf16x2(r[0] * s0, r[1] * s1);
+                q2[i] = P.f16 ? f16x2(r2[0] * t0 * up2, r2[1] * t1 * up2) : bf16x2(r2[0] * t0, r2[1] * t1);
               }
             }
           }

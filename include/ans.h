@@ -538,8 +538,10 @@ ans_status ans_gated_grad_workspace(const ans_layout* layout, uint32_t M,
  *   dX = dG Wg + dU Wu                              bf16 M x K; d_dX NULL: not computed
  * dG and dU enter dX as bf16 (times the row scales, where there are) beside bf16
  * weights, and as f16 beside the others, under a power of two of the token's that
- * their bound max |dH| 1.14 |x| sqrt(K) (largest |w|) is met with: with 11 bits down
- * to 2^-28 of that bound, and off by at most 2^-38 of it below.
+ * their bound max |dH| 1.14 |x| sqrt(K) (largest |w|) is met with (times the largest
+ * row scale, where there are): with 11 bits down to 2^-28 of that bound, and off by at
+ * most 2^-38 of it below.  A token whose values are all 2^-27 of that bound and less
+ * has the roundings of dG and dU in them, under a power of two of their largest.
  * dG and dU are what ans_gemm_lora_grad takes as d_dY of the two projections
  * (d_dX NULL there) for the gradients of their adapters.  The workspace is the
  * same size with and without d_dX.  M == 0 is a no-op. */

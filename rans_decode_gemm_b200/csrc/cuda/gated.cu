@@ -81,11 +81,14 @@ __device__ __forceinline__ void activation(uint32_t act, float g, float& value, 
 // scale and all) * (the largest scale), and |dU s| likewise (|act'| < 1.13, |act(g)| <=
 // |g|).  A bound need not be met: it is some 2^7 above what a trained layer's values
 // come to, and f16 holds 11 bits of them down to 2^-28 of it, so 2^-21 of the largest.
+// Where a row of far larger scales has no part in a token's gradient the bound can be
+// 2^20 and more too large; gated_rows_kernel sees to such tokens.
 struct GatedRows {
   uint16_t *gate, *up;      // null: dG and dU themselves are the rows
   const float* bound;       // [M]: max |dH| * 1.13 |x| sqrt(K) * (the largest code); null: no power of two
   const float* scale_parts; // kScaleParts largest scales
   float* factor;            // [M]: 2^-e, for the product's sums
+  float* top;               // [M]: the largest magnitude that a token's rows hold
 };
 constexpr uint32_t kScaleParts = 64;
 
@@ -306,6 +309,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
       tc_fence_after();
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       if (16 * turn >= kBN && lane == 0) mbar_arrive(&acc_empty[b]);
+      [[maybe_unused]] float top = 0.0f;
 #pragma unroll
       for (uint32_t c0 = 16 * turn; c0 < kBN; c0 += 64) {
         const uint32_t n0 = ab * kBN + c0;
@@ -361,8 +365,11 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
               o2[i] = bf16x2(r2[0], r2[1]);
               if (P.rows.gate != nullptr) {
                 const float s0 = sg[2 * i] * up, s1 = sg[2 * i + 1] * up, t0 = su[2 * i] * up, t1 = su[2 * i + 1] * up;
-                q[i] = P.f16 ? f16x2(r[0] * s0 * up2, r[1] * s1 * up2) : bf16x2(r[0] * s0, r[1] * s1);
-                q2[i] = P.f16 ? f16x2(r2[0] * t0 * up2, r2[1] * t1 * up2) : bf16x2(r2[0] * t0, r2[1] * t1);
+                const float v[4] = {r[0] * s0 * up2, r[1] * s1 * up2, r2[0] * t0 * up2, r2[1] * t1 * up2};
+                q[i] = P.f16 ? f16x2(v[0], v[1]) : bf16x2(v[0], v[1]);
+                q2[i] = P.f16 ? f16x2(v[2], v[3]) : bf16x2(v[2], v[3]);
+#pragma unroll
+                for (const float a : v) top = fmaxf(top, fabsf(a));
               }
             }
           }
@@ -379,6 +386,9 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
           }
         }
       }
+      // (the order of maxima changes nothing)
+      if (kGrad && P.rows.bound != nullptr && m_in && top > 0.0f)
+        atomicMax(reinterpret_cast<int*>(P.rows.top + m), __float_as_int(top));
     }
   }
   tc_fence_before();
@@ -493,7 +503,8 @@ __global__ void __launch_bounds__(256) gated_scales_kernel(const void* gate, con
 // Beside the decoding: 1.13 max |dH| |x| sqrt(K) times the largest code, of finite
 // values.  A CTA a token.
 __global__ void __launch_bounds__(256) gated_bound_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ dH,
-                                                          uint32_t N, uint32_t K, float per, float* __restrict__ bound) {
+                                                          uint32_t N, uint32_t K, float per, float* __restrict__ bound,
+                                                          float* __restrict__ rows_top) {
   __shared__ float part[8][2];
   griddep_beside();
   auto values = [&](const uint16_t* p, float (&v)[8]) {
@@ -552,8 +563,80 @@ __global__ void __launch_bounds__(256) gated_bound_kernel(const uint16_t* __rest
     for (int k = 0; k < 8; ++k) sum += part[k][0];
     // (the largest fp32 in place of what is past it)
     bound[m] = fminf(top_h * sqrtf(sum * static_cast<float>(K)) * top_x * per, 3.0e38f);
+    rows_top[m] = 0.0f;
   }
   griddep_beside_end();
+}
+
+// Tokens whose largest row value lies below 2^-12, 2^26 and more below their bound: f16's
+// steps of 2^-24 there are 2^-12 of it, more than what bf16 leaves of a value.  Their rows
+// come of dG and dU as they are rounded, under a power of two of their own largest.  Where
+// no token is one the kernel takes 2 us (int8 14336 x 4096, 2048 tokens).
+constexpr float kRowsLow = 1.0f / 4096;
+struct GatedLowRows {
+  const uint16_t *dG, *dU;
+  const void *gate_scales, *up_scales;
+  GatedRows rows;
+  uint32_t scale_kind, M, N;
+};
+__global__ void __launch_bounds__(512) gated_rows_kernel(const __grid_constant__ GatedLowRows P) {
+  __shared__ float part[16][2];
+  griddep_wait();
+  griddep_launch_dependents();
+  for (uint32_t m = blockIdx.x; m < P.M; m += gridDim.x) {
+    const float held = __ldcg(P.rows.top + m);
+    if (held >= kRowsLow || held == 0.0f) continue;
+    const uint64_t row = static_cast<uint64_t>(m) * P.N;
+    // eight values of dG (half 0) or dU (half 1), and those times their scales
+    auto values = [&](uint32_t half, uint32_t n, float (&v)[8], float (&vs)[8]) {
+      const uint4 u = __ldcg(reinterpret_cast<const uint4*>((half ? P.dU : P.dG) + row + n));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      float s[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+      if (P.scale_kind == 1 || P.scale_kind == 2) row_scales8(P.scale_kind, half ? P.up_scales : P.gate_scales, n, s);
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+        v[k] = __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+        vs[k] = v[k] * s[k];
+      }
+    };
+    float top = 0.0f, top_v = 0.0f, v[8], vs[8];
+    for (uint32_t half = 0; half < 2; ++half)
+      for (uint32_t n = 8 * threadIdx.x; n < P.N; n += 4096) {
+        values(half, n, v, vs);
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+          top = fmaxf(top, fabsf(vs[k]));
+          top_v = fmaxf(top_v, fabsf(v[k]));
+        }
+      }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      top_v = fmaxf(top_v, __shfl_xor_sync(0xFFFFFFFFu, top_v, d));
+    }
+    __syncthreads();  // (the token before has been read)
+    if (threadIdx.x % 32 == 0) {
+      part[threadIdx.x / 32][0] = top;
+      part[threadIdx.x / 32][1] = top_v;
+    }
+    __syncthreads();
+    for (uint32_t k = 0; k < 16; ++k) {
+      top = fmaxf(top, part[k][0]);
+      top_v = fmaxf(top_v, part[k][1]);
+    }
+    // (near the end of bf16's own range dG and dU have fewer bits than the rows)
+    const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    if (!(top_v >= 0x1p-100f) || ex < -110 || ex > 126) continue;
+    const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+    if (threadIdx.x == 0) P.rows.factor[m] = __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
+    for (uint32_t half = 0; half < 2; ++half)
+      for (uint32_t n = 8 * threadIdx.x; n < P.N; n += 4096) {
+        values(half, n, v, vs);
+        *reinterpret_cast<uint4*>((half ? P.rows.up : P.rows.gate) + row + n) =
+            make_uint4(f16x2(vs[0] * up, vs[1] * up), f16x2(vs[2] * up, vs[3] * up), f16x2(vs[4] * up, vs[5] * up),
+                       f16x2(vs[6] * up, vs[7] * up));
+      }
+  }
 }
 
 static size_t aligned(size_t n) { return (n + 1023) / 1024 * 1024; }
@@ -599,7 +682,7 @@ void make_gated_plan(const LayerDev& L, uint32_t M, uint32_t scale_kind, bool gr
   p->off_x16 = take(p->f16 ? static_cast<size_t>(M) * L.K * 2 : 0);
   p->off_factor = take(p->f16 ? static_cast<size_t>(M) * 4 : 0);
   p->off_rows = take(grad && p->prep ? static_cast<size_t>(M) * L.N * 4 : 0);
-  p->off_rows_factor = take(grad && p->f16 ? (static_cast<size_t>(M) * 2 + kScaleParts) * 4 : 0);
+  p->off_rows_factor = take(grad && p->f16 ? (static_cast<size_t>(M) * 3 + kScaleParts) * 4 : 0);
   p->off_gemm = take(grad ? operand_gemm_workspace(p->back) : 0);
   p->bytes = at;
 }
@@ -641,7 +724,8 @@ cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDe
   float* factor = reinterpret_cast<float*>(w + p.off_factor);
   float* rows_factor = reinterpret_cast<float*>(w + p.off_rows_factor);
   float* bound = rows_factor + p.M;
-  float* scale_parts = bound + p.M;
+  float* rows_top = bound + p.M;
+  float* scale_parts = rows_top + p.M;
   const bool bounds = p.grad && p.f16 && a.dX != nullptr;
   cudaError_t e = cudaSuccess;
   if (bounds && a.scale_kind != 0)
@@ -658,7 +742,7 @@ cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDe
   if (e == cudaSuccess && bounds) {
     const uint32_t dt = gate.dtype;
     const float code = dt == kDtInt8 ? 128.0f : dt == kDtFp8 ? 448.0f : dt == kDtInt4 || dt == kDtInt4Pairs ? 8.0f : 6.0f;
-    e = launch_pdl(gated_bound_kernel, dim3(p.M), dim3(256), 0, stream, a.X, a.dH, p.N, p.K, 1.14f * code, bound);
+    e = launch_pdl(gated_bound_kernel, dim3(p.M), dim3(256), 0, stream, a.X, a.dH, p.N, p.K, 1.14f * code, bound, rows_top);
   }
   if (e != cudaSuccess) return e;
   GatedDev P;
@@ -693,12 +777,18 @@ cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDe
       P.rows.bound = bound;
       P.rows.scale_parts = scale_parts;
       P.rows.factor = rows_factor;
+      P.rows.top = rows_top;
     }
     rows = P.rows.gate;
     rows2 = P.rows.up;
   }
   e = launch_gated_gemm<true>(P, p.K, p.sms, stream);
   if (e != cudaSuccess || a.dX == nullptr) return e;
+  if (bounds) {
+    const GatedLowRows low{a.dG, a.dU, a.gate_scales, a.up_scales, P.rows, a.scale_kind, p.M, p.N};
+    e = launch_pdl(gated_rows_kernel, dim3(std::min(p.M, 2u * p.sms)), dim3(512), 0, stream, low);
+    if (e != cudaSuccess) return e;
+  }
   OperandGemmOut out;
   std::memset(&out, 0, sizeof(out));
   out.out16 = a.dX;

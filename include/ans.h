@@ -623,7 +623,8 @@ ans_status ans_verify_workspace(uint32_t n_seqs, uint32_t n_drafted, uint32_t vo
  * has no part in w), and starts are taken as the nearest that lie within the rows:
  * d_accepted and d_out then mean nothing, but what is written lies within n_drafted
  * and the vocabulary (or is -1).
- * All in 64 bits; the same bits for the same inputs.  vocab <= 2^24 and n_drafted +
+ * All in 64 bits (an exponential is right to 2.4e-15 of its value); the same bits for
+ * the same inputs.  vocab <= 2^24 and n_drafted +
  * n_seqs <= 2^20 (ANS_ERR_UNSUPPORTED above); strides (in logits) of vocab or more,
  * any alignment of 4 bytes; d_ws 256-byte aligned, with any contents.  n_seqs == 0
  * (with n_drafted == 0) is a no-op. */

@@ -8,8 +8,11 @@
 //
 // A decision compares numbers that may lie next to one another, so everything is
 // held in 64 bits: a running sum over a vocabulary has a border every 1 / vocab,
-// which sums in 32 bits would move.  2^d is a table of sixteenths times a polynomial
-// of degree 5 on |f| <= 1/32: (log(2) / 32)^6 / 720 = 1.4e-13 of the value.
+// which sums in 32 bits would move.  And p - q of models that agree is a difference of
+// like numbers: what an exponential is off by must be small against kNoMass, from which
+// on a difference counts.  2^d is a table of 64ths times the polynomial of degree 4 that
+// agrees with 2^f at the five Chebyshev points of |f| <= 1 / 128 (2.4e-15 of the value), or,
+// far from a row's reference, a table of sixteenths times that of degree 6 on |f| <= 1 / 32.
 //
 // Two kernels.  The first reads every row once and leaves a reference and a sum for
 // each part of it; the second, a cluster of eight CTAs a sequence, joins the parts
@@ -39,7 +42,9 @@ constexpr uint32_t kVerifyCluster = 8;
 constexpr uint32_t kVerifyMaxChunks = 64;
 constexpr double kLog2E64 = 1.4426950408889634, kLn2_64 = 0.69314718055994531;
 constexpr double kNoRef = -1.0e300;              // the reference of a part without a finite logit
-constexpr double kNoMass = 1.0 / (1ull << 40);   // p - q is rounding from here down
+// p - q is rounding from here down: 9.1e-13.  (Of p = q some 1e-14 is left: both polynomials'
+// 2.4e-15, and a sum of 2^17 exponentials, 128 of them one after another, another 1e-14 at most.)
+constexpr double kNoMass = 1.0 / (1ull << 40);
 
 // 2^(i / 64)
 __constant__ double g_powers[64] = {
@@ -69,10 +74,11 @@ __device__ __forceinline__ void exp2_parts(double d, const double* sixteenths, d
   const double a = d + kRound;
   const int q = __double2loint(a);
   const double f = d - (a - kRound);
-  value = fma(f, 0.0013333558146428441, 0.009618129107628477);
-  value = fma(value, f, 0.055504108664821576);
-  value = fma(value, f, 0.2402265069591007);
-  value = fma(value, f, 0.6931471805599453);
+  value = fma(f, 0.0001540375624545771, 0.001333381881538924);
+  value = fma(value, f, 0.009618129106525682);
+  value = fma(value, f, 0.05550410865209357);
+  value = fma(value, f, 0.24022650695910086);
+  value = fma(value, f, 0.6931471805599468);
   value = fma(value, f, 1.0);
   const double s = sixteenths[q & 15];
   scale = __hiloint2double(none ? 0 : __double2hiint(s) + ((q >> 4) << 20), none ? 0 : __double2loint(s));
@@ -95,11 +101,9 @@ __device__ __forceinline__ double distance(double z, double c, double ref) {
 }
 
 // The same for logits up to 500 above a reference of no more than 2^30 and no more than
-// 900 below it, in six instructions of 64 bits (of which an SM issues one a cycle) and
-// six others in place of eleven and sixteen: one fused product rounds z c - ref to 64ths,
-// a second has what is left of it, the polynomial is one of degree 3 that is off by
-// 4.5e-12 of the value at most, and the table holds its high words less the index that
-// comes with the exponent.
+// 900 below it, in fewer instructions: one fused product rounds z c - ref to 64ths, a
+// second has what is left of it, the polynomial is of degree 4 for 6, and the table holds
+// its high words less the index that comes with the exponent.
 constexpr double k64th = 105553116266496.0;  // 1.5 * 2^46
 struct Near {
   double c, from;      // log2(e) / T;  k64th - ref
@@ -120,9 +124,10 @@ __device__ __forceinline__ void near_parts(float z, const Near& r, const double*
   const double a = fma(x, r.c, r.from);
   const int q = __double2loint(a);
   const double f = fma(x, r.c, r.from - a);
-  value = fma(f, 0.05550402724235489, 0.2402270940024159);
-  value = fma(value, f, 0.6931471805667776);
-  value = fma(value, f, 0.9999999999955212);
+  value = fma(f, 0.009618140859595685, 0.05550421039186821);
+  value = fma(value, f, 0.2402265069589214);
+  value = fma(value, f, 0.6931471805583931);
+  value = fma(value, f, 1.0);
   const double s = table[q & 63];
   scale = __hiloint2double(__double2hiint(s) + (q << 14), __double2loint(s));
 }

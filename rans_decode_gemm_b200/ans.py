@@ -598,6 +598,16 @@ def _set_wait_budget(cycles: int = 0):
     _check(fn(int(cycles)), "ansdev_set_wait_budget")
 
 
+def _set_part_registers(least: int = 0):
+    """Internal test hook of libans.so: what the kernel of a loss's sums in parts
+    counts as needing of registers a thread (more than 255: it is taken for built
+    otherwise than it needs to be, and left out); 0 restores what it does need."""
+    fn = load().ansdev_set_part_registers
+    fn.argtypes = [C.c_uint32]
+    fn.restype = None
+    fn(int(least))
+
+
 def _wait_probe(d_status, stream=None):
     """Internal test hook: one bounded wait on a barrier nothing arrives on
     (leaves the TIMEOUT bit in d_status)."""

@@ -587,6 +587,10 @@ void ansdev_set_plan_limits(uint32_t max_ctas, uint32_t max_producers, uint32_t 
   ansdev::set_plan_limits(max_ctas, max_producers, force_shared);
 }
 
+// Internal test hook (not part of the public ABI): what the kernel of sums in parts
+// counts as needing of registers a thread (at least what it does); 0 restores that.
+void ansdev_set_part_registers(uint32_t least) { ansdev::set_part_registers(least); }
+
 // Internal test hook (not part of the public ABI): the launch plan that
 // ans_gemm (decode = 1) or ans_gemm_uncompressed (decode = 0) would use for a
 // layout, M and scale kind on a device with num_sms SMs, without touching a

@@ -128,6 +128,10 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
                                 const OperandGemmOut* out, const XentEpilogue* xent, void* ws, uint32_t* status,
                                 cudaStream_t stream, const OperandPair* pair = nullptr);
 
+// Internal test hook: sums in parts only where their kernel was built with that many
+// registers a thread (what it needs, or more).
+void set_part_registers(uint32_t least);
+
 cudaError_t set_live_wait_budget_operand(long long cycles);
 cudaError_t set_live_wait_budget_operand_gemm(long long cycles);
 

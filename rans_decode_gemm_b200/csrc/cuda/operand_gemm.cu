@@ -54,9 +54,9 @@ constexpr uint32_t kOgBM = 128, kOgBK = 64;
 constexpr uint32_t kOgABytes = kOgBM * kOgBK * 2;  // 16 KB
 constexpr uint32_t kOgEpiWarps = 8;
 constexpr uint32_t kOgThreads = (2 + kOgEpiWarps) * 32;
-// Parts: warps 4-11 are the epilogue's, whose sums of 128 tokens stay in registers: 224 a
+// Parts: warps 4-11 are the epilogue's, which keep sums of 128 tokens: 224 registers a
 // thread, and 56 for the warps before them (128 x 56 + 256 x 224 = 384 x 168, which is what
-// the block is launched with; launch_operand_gemm checks that it is).
+// the block has to be launched with: parts_fit()).
 constexpr uint32_t kOgPartThreads = 384, kOgPartRegs = 168;
 constexpr uint32_t kOgMaxStages = 8;
 // The tensor unit truncates each step of a sum: 4096 products in one accumulator are off
@@ -655,6 +655,25 @@ size_t operand_gemm_workspace(const OperandGemmPlan& p) {
   return tiles * p.splits * p.bn * kOgBM * 4;
 }
 
+// Whether the kernel of sums in parts was built with the registers that its warps share out
+// (with fewer its epilogue would wait for some that there are not); one accumulator a sum
+// serves in its place.
+static std::atomic<uint32_t> g_part_regs{kOgPartRegs};
+void set_part_registers(uint32_t least) { g_part_regs.store(std::max(least, kOgPartRegs)); }
+static cudaError_t parts_fit(int dev, bool* fit) {
+  static std::atomic<int> built[64];  // registers a thread; 0: not looked up
+  int regs = dev < 64 ? built[dev].load() : 0;
+  if (regs == 0) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, operand_gemm_kernel<false, kOgListsInParts>);
+    if (e != cudaSuccess) return e;
+    regs = a.numRegs;
+    if (dev < 64) built[dev].store(regs);
+  }
+  *fit = static_cast<uint32_t>(regs) >= g_part_regs.load();
+  return cudaSuccess;
+}
+
 cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* images, const void* rows16,
                                 const OperandGemmOut* out, const XentEpilogue* xent, void* ws, uint32_t* status,
                                 cudaStream_t stream, const OperandPair* pair) {
@@ -701,14 +720,16 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
   if (e == cudaSuccess && pair) e = tokens(&P.tmap_b2, pair->rows16);
   if (e == cudaSuccess && pair) e = weights(&P.tmap_a2, pair->images);
   if (e != cudaSuccess) return e;
-  const bool parts = !plan.trans && P.xent.listed != nullptr && P.xent.probs == nullptr && plan.bn >= 128;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  bool parts = !plan.trans && P.xent.listed != nullptr && P.xent.probs == nullptr && plan.bn >= 128;
+  if (parts) e = parts_fit(dev, &parts);
+  if (e != cudaSuccess) return e;
   auto kern = plan.trans ? operand_gemm_kernel<true>
               : parts ? operand_gemm_kernel<false, kOgListsInParts>
               : P.xent.listed != nullptr ? operand_gemm_kernel<false, kOgLists> : operand_gemm_kernel<false>;
   static std::atomic<uint64_t> attr_set{0};
-  int dev = 0;
-  e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
   if (dev >= 64 || !(attr_set.load() & (1ull << dev))) {
     e = cudaFuncSetAttribute(operand_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem);
     if (e == cudaSuccess)
@@ -718,10 +739,6 @@ cudaError_t launch_operand_gemm(const OperandGemmPlan& plan, const uint8_t* imag
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(operand_gemm_kernel<false, kOgListsInParts>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kOgSmem);
-    cudaFuncAttributes built;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&built, operand_gemm_kernel<false, kOgListsInParts>);
-    // (with fewer, the epilogue's warps would wait for registers that there are not)
-    if (e == cudaSuccess && built.numRegs != kOgPartRegs) e = cudaErrorInvalidConfiguration;
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set.fetch_or(1ull << dev);
   }

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kDiThreads) distill_begin_kernel(const __grid_
   double sum = 0.0, self = 0.0;
   for (uint32_t j = threadIdx.x; j < P.top; j += kDiThreads) {
     double v = 0.0;
-    if (id[j] >= 0) {
+    if (id[j] >= 0 && a[j] != -INFINITY) {  // (of -infinity there is nothing, whatever the teacher's lse)
       const double log_t = a[j] - norm;
       v = exp(log_t);
       sum += v;

@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(kDiThreads) distill_begin_kernel(const __grid_
 // All of it is stored in units of 2^r, in which the others already are, unless the
 // largest of the listed then passes 2^14 (f16; 2^100 in bf16): the row is shifted down by
 // as much as it does, whatever the others lose by that being below 2^-38 of the row's largest.
+// Where all are listed there is no r, and f16 would lose what is small of a student that has
+// learnt its teacher: the listed then are in units of their own largest.
 struct DistillCoef {
   XentState st;
   const double* t;
@@ -310,10 +312,13 @@ __device__ __forceinline__ void distill_coefs(const DistillCoef& P, uint32_t m, 
   most = warp_max(most);
   const int E = most == 0.0 ? -2000 : ilogb(most), limit = P.f16 ? 14 : 100;
   const bool over = E + D > limit;
-  const int up = over ? limit - E : static_cast<int>(D);       // the listed are times 2^up
-  const int back = -up;                                          // and beta 2^back
+  // the listed are times 2^up, and beta 2^-up.  Beside others without mass (l = 0: all their
+  // exponentials are 0) f16 holds the listed alone, the largest of them in [2^14, 2^15)
+  const bool alone = P.f16 && l == 0.0f;
+  const int up = alone ? min(limit - E, 100) : over ? limit - E : static_cast<int>(D);
+  const int back = -up;
   if (lane == 0) {
-    P.shift[m] = over ? static_cast<int32_t>(fmin(E + D - limit, 1e6)) : 0;
+    P.shift[m] = over && !alone ? static_cast<int32_t>(fmin(E + D - limit, 1e6)) : 0;
     const double g = P.weight != nullptr ? static_cast<double>(__ldg(P.weight + m)) : 1.0;
     double beta = ldexp(g * P.per_t * S / total / lift, back);
     if (!isfinite(lse)) beta = __longlong_as_double(0x7FF8000000000000ll);

@@ -17,8 +17,8 @@
 // images.
 //
 // Measured alone (fp8 14336 x 4096, 2048 tokens): the decoding 67 us a layer, the product
-// 362 (481 GFLOP, 1.33 PFLOP/s).  int8 with the gradient: 67 a layer, the product 445, of
-// which its epilogue (58 MB of dH read, 235 MB written) adds some 80, dX 369.
+// 362 (481 GFLOP, 1.33 PFLOP/s).  int8 with the gradient: 67 a layer, the product 447, of
+// which its epilogue (58 MB of dH read, 235 MB written) adds some 80, dX 373.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -77,7 +77,7 @@ __device__ __forceinline__ void activation(uint32_t act, float g, float& value, 
 
 // Rows of the transposed product: dG and dU times the row scales, before they are
 // rounded to bf16.  In f16 they come under a power of two of the token's that no value
-// of its can pass 2^15 with: |dG s| <= max |dH| * 1.13 |x| sqrt(K) * (the largest weight,
+// of its can pass 2^15 with: |dG s| <= max |dH| * 1.14 |x| sqrt(K) * (the largest weight,
 // scale and all) * (the largest scale), and |dU s| likewise (|act'| < 1.13, |act(g)| <=
 // |g|).  A bound need not be met: it is some 2^7 above what a trained layer's values
 // come to, and f16 holds 11 bits of them down to 2^-28 of it, so 2^-21 of the largest.
@@ -85,7 +85,7 @@ __device__ __forceinline__ void activation(uint32_t act, float g, float& value, 
 // 2^20 and more too large; gated_rows_kernel sees to such tokens.
 struct GatedRows {
   uint16_t *gate, *up;      // null: dG and dU themselves are the rows
-  const float* bound;       // [M]: max |dH| * 1.13 |x| sqrt(K) * (the largest code); null: no power of two
+  const float* bound;       // [M]: max |dH| * 1.14 |x| sqrt(K) * (the largest code); null: no power of two
   const float* scale_parts; // kScaleParts largest scales
   float* factor;            // [M]: 2^-e, for the product's sums
   float* top;               // [M]: the largest magnitude that a token's rows hold
@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(kGaThreads, 1) gated_gemm_kernel(const __grid_
 // ---- products that are there ---------------------------------------------------
 // X under a power of two of its row, for products that take it as f16: the row's largest
 // finite value lies in [2^14, 2^15), and f16 then holds all 8 bits of the others down to
-// 2^-31 of it and is off by 2^-39 of it below.  A CTA a token.
+// 2^-31 of it and is off by 2^-39 of it below.  A CTA a token; with it a call of few
+// tokens takes 2 to 4 us more (int8 14336 x 4096, 1 token: 181.8 to 184.7).
 __global__ void __launch_bounds__(256) gated_x_kernel(const uint16_t* __restrict__ X, uint32_t K, uint16_t* __restrict__ out,
                                                       float* __restrict__ factor) {
   __shared__ float part[8];
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(256) gated_scales_kernel(const void* gate, con
   parts[blockIdx.x] = top;
 }
 
-// Beside the decoding: 1.13 max |dH| |x| sqrt(K) times the largest code, of finite
+// Beside the decoding: 1.14 max |dH| |x| sqrt(K) times the largest code, of finite
 // values.  A CTA a token.
 __global__ void __launch_bounds__(256) gated_bound_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ dH,
                                                           uint32_t N, uint32_t K, float per, float* __restrict__ bound,
@@ -571,8 +572,10 @@ __global__ void __launch_bounds__(256) gated_bound_kernel(const uint16_t* __rest
 // Tokens whose largest row value lies below 2^-12, 2^26 and more below their bound: f16's
 // steps of 2^-24 there are 2^-12 of it, more than what bf16 leaves of a value.  Their rows
 // come of dG and dU as they are rounded, under a power of two of their own largest.  Where
-// no token is one the kernel takes 2 us (int8 14336 x 4096, 2048 tokens).
+// no token is one the call takes 2 us more (int8 4096 x 4096, 200 tokens: 111.6 to 113.7; the
+// kernel alone 5.5 us for 2048 tokens).
 constexpr float kRowsLow = 1.0f / 4096;
+constexpr uint32_t kRowsTokens = 8;  // a CTA
 struct GatedLowRows {
   const uint16_t *dG, *dU;
   const void *gate_scales, *up_scales;
@@ -583,9 +586,16 @@ __global__ void __launch_bounds__(512) gated_rows_kernel(const __grid_constant__
   __shared__ float part[16][2];
   griddep_wait();
   griddep_launch_dependents();
-  for (uint32_t m = blockIdx.x; m < P.M; m += gridDim.x) {
-    const float held = __ldcg(P.rows.top + m);
-    if (held >= kRowsLow || held == 0.0f) continue;
+  // (each thread the same: eight tokens' maxima at once)
+  const uint32_t m0 = blockIdx.x * kRowsTokens;
+  uint32_t low = 0;
+#pragma unroll
+  for (uint32_t k = 0; k < kRowsTokens; ++k) {
+    const float held = m0 + k < P.M ? __ldcg(P.rows.top + m0 + k) : 0.0f;
+    low |= (held < kRowsLow && held > 0.0f ? 1u : 0u) << k;
+  }
+  for (; low != 0; low &= low - 1) {
+    const uint32_t m = m0 + __ffs(low) - 1;
     const uint64_t row = static_cast<uint64_t>(m) * P.N;
     // eight values of dG (half 0) or dU (half 1), and those times their scales
     auto values = [&](uint32_t half, uint32_t n, float (&v)[8], float (&vs)[8]) {
@@ -786,7 +796,7 @@ cudaError_t launch_gated(const GatedPlan& p, const LayerDev& gate, const LayerDe
   if (e != cudaSuccess || a.dX == nullptr) return e;
   if (bounds) {
     const GatedLowRows low{a.dG, a.dU, a.gate_scales, a.up_scales, P.rows, a.scale_kind, p.M, p.N};
-    e = launch_pdl(gated_rows_kernel, dim3(std::min(p.M, 2u * p.sms)), dim3(512), 0, stream, low);
+    e = launch_pdl(gated_rows_kernel, dim3((p.M + kRowsTokens - 1) / kRowsTokens), dim3(512), 0, stream, low);
     if (e != cudaSuccess) return e;
   }
   OperandGemmOut out;

@@ -1158,7 +1158,10 @@ namespace {
 // other's tiles meet more than 16 tokens or hold 16,384 symbols (two layers of 14336 x
 // 4096, images against the one launch: 24 tokens int8 189 us against 199, int4 153
 // against 204; one token fp8 190 against 204, bf16 191 against 187, int4 153 against
-// 141; of 4096 x 4096, 32 tokens: bf16 97 against 75, int4 97 against 81).
+// 141; of 4096 x 4096, 32 tokens: bf16 97 against 75, int4 97 against 81).  Near the border
+// either is within 8 % of the other, as its rounds of tiles fall (24 tokens with the weights
+// in L2, images against the one launch: 8192 x 4096 bf16 123 against 114, int8 and fp8 123
+// against 118 and 120; 6144 x 4096 84 against 90, 84 against 94).
 // Decoded weights lie behind the split-K counters of that launch, so that one workspace
 // serves both in turn.
 struct GatedChoice {

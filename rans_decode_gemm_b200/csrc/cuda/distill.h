@@ -16,7 +16,6 @@ constexpr uint32_t kDistillMaxTop = 256;
 struct DistillPlan {
   uint32_t M, N, K, top, vocab_words;
   uint32_t grad, f16;
-  uint32_t rows;     // W rows that are decoded: the vocabulary in whole tiles
   uint32_t piece;    // loss only: W rows of a piece.  Gradient: of all but the first
   uint32_t first;    // of the first
   uint32_t chunk;    // tokens at a time

@@ -54,14 +54,16 @@ constexpr uint32_t kOgBM = 128, kOgBK = 64;
 constexpr uint32_t kOgABytes = kOgBM * kOgBK * 2;  // 16 KB
 constexpr uint32_t kOgEpiWarps = 8;
 constexpr uint32_t kOgThreads = (2 + kOgEpiWarps) * 32;
-// Parts: warps 4-11 are the epilogue's, which keep sums of 128 tokens: 224 registers a
+// Parts: warps 4-11 are the epilogue's, which keep sums of 128 tokens (of which, beside a
+// fold's own values, the compiler spills 552 bytes a thread to local memory): 224 registers a
 // thread, and 56 for the warps before them (128 x 56 + 256 x 224 = 384 x 168, which is what
 // the block has to be launched with: parts_fit()).
 constexpr uint32_t kOgPartThreads = 384, kOgPartRegs = 168;
 constexpr uint32_t kOgMaxStages = 8;
 // The tensor unit truncates each step of a sum: 4096 products in one accumulator are off
 // by 1.5e-6 of a loss where fp32 has 4e-7.  Narrow tiles leave columns of TMEM free and
-// take several accumulators a sum.  Wide tiles of a loss without a gradient take one after
+// take several accumulators a sum.  (With a gradient wide tiles keep one: parts took a call over
+// 32000 x 4096, 2048 tokens, from 1,036 to 1,256 us.)  Wide tiles of a loss alone take one after
 // another, which the epilogue adds to sums of its own: the first two of 24 stages, which
 // serve while it folds the tile before, the others of 8.  (A loss over 32000 x 4096 bf16,
 // 1000 tokens: off by 4.7e-7 in 497 us, in one accumulator 1.5e-6 in 412; the first two of

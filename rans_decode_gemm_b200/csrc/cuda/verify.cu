@@ -20,12 +20,13 @@
 // is drawn from once more.
 //
 // Measured, 64 sequences of 8 drafts with the draft's logits, vocabulary 130001 (500 MB):
-// the first kernel 114 us (4.2 TB/s: twelve instructions a logit, half of them of 64 bits,
-// at 61 % of the issue slots; the bytes alone would take 76), the second 36 (50 MB in two
-// passes, and five rounds of joins one behind another).  16 logits a thread at a time and
-// four CTAs an SM: 144 us for both; with 8 logits 154, three CTAs 157, five 155, and with
-// the next 16 asked for before these are summed 142.  One sequence of 5 drafts of 32000
-// logits: 8.6 and 14 us, each latency from end to end.
+// the first kernel 118 us alone (4.0 TB/s; the bytes alone would take 76): 18 instructions a
+// logit, 7.5 of them of 64 bits, at 61 % of the issue slots and 48 % of the 64-bit pipe.  The
+// second 36 (50 MB in two passes, and five rounds of joins one behind another).  16 logits a
+// thread at a time and four CTAs an SM: with a polynomial of degree 3, 144 us for both; with 8
+// logits 154, three CTAs 157, five 155; with the next 16 asked for before these are summed 142,
+// for 16 registers more, not taken for 1 %.  One sequence of 5 drafts of 32000 logits: 8.2 and
+// 14 us alone, each latency from end to end.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -717,8 +718,9 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
 }
 
 void make_verify_plan(uint32_t n_seqs, uint32_t n_drafted, uint32_t vocab, VerifyPlan* p) {
-  // parts of 1,024 to 32,768 logits: one round of the SMs, at four CTAs each, or many
-  // of long parts; 64 of a row at most
+  // parts of 1,024 to 32,768 logits: one round of 148 SMs, at four CTAs each, or many
+  // of long parts; 64 of a row at most.  (The size can be asked for without a device, so that
+  // the count of SMs is not one's; any other works the same.)
   const uint64_t rows = 2ull * n_drafted + n_seqs, all = rows * vocab;
   uint64_t chunk = (all / (148 * 4) + 1023) / 1024 * 1024;
   chunk = std::max<uint64_t>(1024, std::min<uint64_t>(chunk, 32768));

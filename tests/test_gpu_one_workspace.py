@@ -61,3 +61,25 @@ def test_batched_layers(cuda, name, tile_n, shapes):
     for turn, M in enumerate(order):
         same = all(torch.equal(a, b) for a, b in zip(call(M, turn, ws)[1], want[turn][1]))
         assert same, f"M {M}, turn {turn}"
+
+
+@pytest.mark.parametrize("K", [1024, 1040])
+def test_adapters(cuda, K):
+    N, rank = 8192, 16
+    cfg, sc, lay, layer = _layer("fp8_405b", N, K, 128, 64 if K % 64 == 0 else 16)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    A = ans.LoraAdapters(torch.randn(3, rank, K, generator=g, device="cuda").bfloat16(),
+                         torch.randn(3, N, rank, generator=g, device="cuda").bfloat16())
+    order = (1, 1100, 40, 200, 1, 700, 5)
+    size = max(ans.ans_gemm_lora_workspace(lay, M, cfg.scale_kind, A.lora) for M in order)
+    ws, st = torch.zeros(size, dtype=torch.uint8, device="cuda"), status_tensor()
+    for turn, M in enumerate(order):
+        x = x_dev(WL.make_x(cfg, M, K, stream=turn))
+        ids = torch.randint(-1, 3, (M,), generator=g, device="cuda", dtype=torch.int32)
+        y, want = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+        for to, buf in ((y, ws), (want, torch.zeros(size, dtype=torch.uint8, device="cuda"))):
+            ans.ans_gemm_lora(x, M, layer.tiles, cfg.scale_kind, sc, cfg.group_k, A.lora, ids, to, buf, size, st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        same = torch.equal(y, want)
+        assert same, f"M {M}, turn {turn}"
